@@ -43,6 +43,8 @@
 #include <type_traits>
 
 #include "attn_common.cuh"
+#include "attn_fp8.h"
+#include "rows.h"
 #include "turbo.h"
 
 using namespace dendrite;
@@ -220,7 +222,7 @@ struct ConsumerCtx {
     int warp, lane, c;
 };
 
-template <int P, bool PACKED>
+template <int P, bool PACKED, bool DRAFT>
 __device__ __forceinline__ void consume_chunk(const ConsumerCtx& x, const AttnUnit& U, int32_t t, int32_t cend,
                                               int32_t& stage) {
     constexpr int NCOL = D / P, NT = NCOL / 8;   // columns and 8-column n-tiles of this warp
@@ -233,6 +235,7 @@ __device__ __forceinline__ void consume_chunk(const ConsumerCtx& x, const AttnUn
     // query fragments of rows r*16 + lane/4 (+8), and their visibility limits
     uint32_t qa[8][4];
     int32_t lim0 = 0, lim1 = 0;
+    uint64_t mask0 = 0, mask1 = 0;   // draft trees: drafted positions seen from the limit on
     {
         const int row0 = r * 16 + (lane >> 2), row1 = row0 + 8;
         const bool v0 = row0 < U.n_rows, v1 = row1 < U.n_rows;
@@ -240,6 +243,10 @@ __device__ __forceinline__ void consume_chunk(const ConsumerCtx& x, const AttnUn
         const AttnRow R1 = v1 ? unit_row(pl, U, row1) : AttnRow{0, 0};
         lim0 = R0.limit;
         lim1 = R1.limit;
+        if (DRAFT) {
+            mask0 = v0 ? draft_mask(pl, U, row0) : 0;
+            mask1 = v1 ? draft_mask(pl, U, row1) : 0;
+        }
         const uint32_t* q0 = reinterpret_cast<const uint32_t*>(Q + (int64_t)R0.q_row * D);
         const uint32_t* q1 = reinterpret_cast<const uint32_t*>(Q + (int64_t)R1.q_row * D);
 #pragma unroll
@@ -299,14 +306,21 @@ __device__ __forceinline__ void consume_chunk(const ConsumerCtx& x, const AttnUn
             } else {
                 pos0 = (U.blk_start + (st - U.tile_off) + ti) * BS + (lane & 3) * 2;
             }
+            uint32_t see0 = 0, see1 = 0;   // draft trees: the lane's positions as bits
+            if (DRAFT) {
+                see0 = vl0 == INT_MIN ? 0u : (uint32_t)draft_visible(mask0, vl0 - pos0);
+                see1 = vl1 == INT_MIN ? 0u : (uint32_t)draft_visible(mask1, vl1 - pos0);
+            }
             float mx0 = NEG_INF, mx1 = NEG_INF;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int32_t pos = pos0 + nt * 8 + e;
-                    sc[nt][e] = pos < vl0 ? sc[nt][e] * a.scale_log2 : NEG_INF;
-                    sc[nt][2 + e] = pos < vl1 ? sc[nt][2 + e] * a.scale_log2 : NEG_INF;
+                    const bool on0 = DRAFT ? (see0 >> (nt * 8 + e)) & 1u : pos < vl0;
+                    const bool on1 = DRAFT ? (see1 >> (nt * 8 + e)) & 1u : pos < vl1;
+                    sc[nt][e] = on0 ? sc[nt][e] * a.scale_log2 : NEG_INF;
+                    sc[nt][2 + e] = on1 ? sc[nt][2 + e] * a.scale_log2 : NEG_INF;
                     mx0 = fmaxf(mx0, sc[nt][e]);
                     mx1 = fmaxf(mx1, sc[nt][2 + e]);
                 }
@@ -392,7 +406,8 @@ __device__ __forceinline__ void consume_chunk(const ConsumerCtx& x, const AttnUn
 // PACKED: the plan has packed units; the producer then writes every tile's
 // logical block and row mask into shared memory and the consumers mask by
 // them (plans without packed units run without that step or its memory).
-template <bool PACKED>
+// DRAFT: the rows are nodes of draft trees (masked by their ancestors too).
+template <bool PACKED, bool DRAFT>
 __global__ void __launch_bounds__(THREADS, 2)
 k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const AttnArgs a) {
@@ -552,8 +567,8 @@ k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const int32_t cend = min(t_end, uend);
         if (U.rt != 1) {
             // 32 or 64 rows: the warps of a row tile split head_dim (no exchange)
-            if (U.rt == 2) consume_chunk<2, PACKED>(ctx, U, t, cend, stage);
-            else consume_chunk<1, PACKED>(ctx, U, t, cend, stage);
+            if (U.rt == 2) consume_chunk<2, PACKED, DRAFT>(ctx, U, t, cend, stage);
+            else consume_chunk<1, PACKED, DRAFT>(ctx, U, t, cend, stage);
             t = cend;
             ++u;
             continue;
@@ -566,6 +581,7 @@ k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         // query fragments of rows r*16 + lane/4 (+8), and their visibility limits
         uint32_t qa[8][4];
         int32_t lim0 = 0, lim1 = 0;
+        uint64_t mask0 = 0, mask1 = 0;
         {
             const int row0 = r * 16 + (lane >> 2), row1 = row0 + 8;
             const bool v0 = row0 < U.n_rows, v1 = row1 < U.n_rows;
@@ -573,6 +589,10 @@ k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const AttnRow R1 = v1 ? unit_row(pl, U, row1) : AttnRow{0, 0};
             lim0 = R0.limit;
             lim1 = R1.limit;
+            if (DRAFT) {
+                mask0 = v0 ? draft_mask(pl, U, row0) : 0;
+                mask1 = v1 ? draft_mask(pl, U, row1) : 0;
+            }
             const uint32_t* q0 = reinterpret_cast<const uint32_t*>(Q + (int64_t)R0.q_row * D);
             const uint32_t* q1 = reinterpret_cast<const uint32_t*>(Q + (int64_t)R1.q_row * D);
 #pragma unroll
@@ -630,14 +650,21 @@ k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 } else {
                     pos0 = (U.blk_start + (st - U.tile_off) + ti) * BS + (lane & 3) * 2;
                 }
+                uint32_t see0 = 0, see1 = 0;
+                if (DRAFT) {
+                    see0 = vl0 == INT_MIN ? 0u : (uint32_t)draft_visible(mask0, vl0 - pos0);
+                    see1 = vl1 == INT_MIN ? 0u : (uint32_t)draft_visible(mask1, vl1 - pos0);
+                }
                 float mx0 = NEG_INF, mx1 = NEG_INF;
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int32_t pos = pos0 + nt * 8 + e;
-                        s[nt][e] = pos < vl0 ? s[nt][e] * a.scale_log2 : NEG_INF;
-                        s[nt][2 + e] = pos < vl1 ? s[nt][2 + e] * a.scale_log2 : NEG_INF;
+                        const bool on0 = DRAFT ? (see0 >> (nt * 8 + e)) & 1u : pos < vl0;
+                        const bool on1 = DRAFT ? (see1 >> (nt * 8 + e)) & 1u : pos < vl1;
+                        s[nt][e] = on0 ? s[nt][e] * a.scale_log2 : NEG_INF;
+                        s[nt][2 + e] = on1 ? s[nt][2 + e] * a.scale_log2 : NEG_INF;
                         mx0 = fmaxf(mx0, s[nt][e]);
                         mx1 = fmaxf(mx1, s[nt][2 + e]);
                     }
@@ -787,12 +814,14 @@ __global__ void __launch_bounds__(128) k_attn_partial_f32(const AttnArgs a) {
         const int32_t cend = min(t_end, uend);
         float q[4][8], acc[4][8], m[4], l[4];
         int32_t lim[4];
+        uint64_t dmask[4];
 #pragma unroll
         for (int rr = 0; rr < 4; ++rr) {
             const int row = warp + 4 * rr;
             const bool v = row < U.n_rows;
             const AttnRow R = v ? unit_row(pl, U, row) : AttnRow{0, 0};
             lim[rr] = R.limit;
+            dmask[rr] = v && pl.masks ? draft_mask(pl, U, row) : 0;
             m[rr] = -INFINITY;
             l[rr] = 0.f;
 #pragma unroll
@@ -820,7 +849,11 @@ __global__ void __launch_bounds__(128) k_attn_partial_f32(const AttnArgs a) {
             for (int rr = 0; rr < 4; ++rr) {
                 if (warp + 4 * rr >= U.n_rows) continue;
                 for (int tok = 0; tok < BS; ++tok) {
-                    if (lb * BS + tok >= lim[rr]) break;
+                    const int32_t past = lb * BS + tok - lim[rr];   // >= 0: seen only if the draft mask says so
+                    if (past >= 0) {
+                        if (past >= 64 || !(dmask[rr] >> past)) break;
+                        if (!((dmask[rr] >> past) & 1u)) continue;
+                    }
                     float dot = 0.f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -1487,6 +1520,7 @@ struct HostPlan {
     std::vector<Segment> psegs;
     std::vector<ExtraTile> pxt;      // the planner's extra tiles of packed segments
     std::vector<AttnXTile> xtiles;   // the same for the kernels (branch handles)
+    std::vector<uint64_t> masks;     // draft trees: drafted tokens each query sees
     std::vector<SegPlan> segplan;
     PlanHeader hdr{};
     bool device = false;       // units and CTA split left to the device
@@ -1494,7 +1528,7 @@ struct HostPlan {
     void clear() {   // keeps capacity: plans are rebuilt whenever the tree changes; the unit and
                      // member arrays keep their size too (build_plan resizes and fills them in place)
         segs.clear(); cta_begin.clear(); cta_unit.clear(); segplan.clear(); device = false; small_packed = false;
-        pxt.clear(); xtiles.clear();
+        pxt.clear(); xtiles.clear(); masks.clear();
         tc_cta_begin.clear(); tc_cta_unit.clear(); path_off.clear(); path.clear(); cuts.clear();
         tiles = unique_tiles = 0;
         n_tc_units = 0;
@@ -1642,8 +1676,12 @@ int32_t class_ctas(int64_t weight, int max_ctas, const ClassWeights& cw) {
 // (64: the CTA decodes each tile once for its four warps' row tiles) partial
 // kernels, and of the fp32 kernel (16).
 int unit_rows_small(const dendrite_pool* p) {
-    return p->dtype == DENDRITE_BF16 ? kMaxUnitRowsBf16 : p->dtype == DENDRITE_TURBO ? kMaxUnitRowsTurbo
-                                                                                    : kMaxUnitRowsF32;
+    switch (p->dtype) {
+        case DENDRITE_BF16: return kMaxUnitRowsBf16;
+        case DENDRITE_TURBO: return kMaxUnitRowsTurbo;
+        case DENDRITE_FP8: return kMaxUnitRowsFp8;
+        default: return kMaxUnitRowsF32;
+    }
 }
 
 // bf16 plans of at least this many units, with fewer tiles per unit than
@@ -1930,7 +1968,7 @@ int encode_pool_map(dendrite_pool* p, void* base, unsigned char* out) {
 // counts, which k_plan_expand writes when the plan is expanded on the device
 // (only the prefix before them is then uploaded).
 enum PlanSection {
-    SEC_SEGS, SEC_MEMBERS, SEC_PATH_OFF, SEC_PATH, SEC_SEGPLAN, SEC_HEADER, SEC_XTILES,
+    SEC_SEGS, SEC_MEMBERS, SEC_PATH_OFF, SEC_PATH, SEC_SEGPLAN, SEC_HEADER, SEC_XTILES, SEC_MASKS,
     SEC_UNITS, SEC_CTA_BEGIN, SEC_CTA_UNIT, SEC_TC_BEGIN, SEC_TC_UNIT, SEC_COUNTS, kPlanSections
 };
 constexpr int kPlanDeviceSection = SEC_UNITS;
@@ -1940,7 +1978,7 @@ size_t plan_layout(const HostPlan& hp, size_t (&off)[kPlanSections + 1]) {
         hp.path_off.size() * 4,               hp.path.size() * 4,
         hp.device ? hp.segplan.size() * sizeof(SegPlan) : 0,
         hp.device ? sizeof(PlanHeader) : 0,
-        hp.xtiles.size() * sizeof(AttnXTile),
+        hp.xtiles.size() * sizeof(AttnXTile), hp.masks.size() * sizeof(uint64_t),
         hp.units.size() * sizeof(AttnUnit),   hp.cta_begin.size() * 4,
         hp.cta_unit.size() * 4,               hp.tc_cta_begin.size() * 4,
         hp.tc_cta_unit.size() * 4,            hp.device ? 4 * sizeof(int32_t) : 0};
@@ -1967,6 +2005,7 @@ void plan_pack(const HostPlan& hp, const size_t (&off)[kPlanSections + 1], char*
     put(SEC_PATH_OFF, hp.path_off.data(), hp.path_off.size() * 4);
     put(SEC_PATH, hp.path.data(), hp.path.size() * 4);
     put(SEC_XTILES, hp.xtiles.data(), hp.xtiles.size() * sizeof(AttnXTile));
+    put(SEC_MASKS, hp.masks.data(), hp.masks.size() * sizeof(uint64_t));
     if (hp.device) {
         put(SEC_SEGPLAN, hp.segplan.data(), hp.segplan.size() * sizeof(SegPlan));
         put(SEC_HEADER, &hp.hdr, sizeof(PlanHeader));
@@ -1993,6 +2032,7 @@ AttnPlanDev plan_view(const HostPlan& hp, const size_t (&off)[kPlanSections + 1]
     v.tc_cta_begin = reinterpret_cast<const int32_t*>(d + off[SEC_TC_BEGIN]);
     v.tc_cta_unit = reinterpret_cast<const int32_t*>(d + off[SEC_TC_UNIT]);
     v.counts = hp.device ? reinterpret_cast<const int32_t*>(d + off[SEC_COUNTS]) : nullptr;
+    v.masks = hp.masks.empty() ? nullptr : reinterpret_cast<const uint64_t*>(d + off[SEC_MASKS]);
     v.packed = hp.small_packed ? 1 : 0;
     v.n_units = (int32_t)hp.units.size();
     v.n_ctas = (int32_t)hp.cta_unit.size();
@@ -2024,6 +2064,7 @@ AttnPlanDev plan_rebase(AttnPlanDev v, const char* from, const char* to) {
     mv(v.path);
     mv(v.xtiles);
     if (v.counts) mv(v.counts);
+    if (v.masks) mv(v.masks);
     return v;
 }
 
@@ -2046,6 +2087,21 @@ int launch_plan_expand(dendrite_pool* p, char* d, const size_t* off, int32_t n_u
     return DENDRITE_OK;
 }
 
+// Each query's drafted tokens: bit b of masks[i][j] is set if node b is node j
+// or an ancestor of it.
+void draft_masks(const int32_t* parents, int32_t n_trees, int32_t n, int32_t t, std::vector<uint64_t>& masks) {
+    masks.resize((size_t)n * t);
+    for (int32_t i = 0; i < n_trees; ++i)
+        for (int32_t j = 0; j < t; ++j) {
+            const int32_t up = parents[(size_t)i * t + j];
+            masks[(size_t)i * t + j] = (up < 0 ? 0ull : masks[(size_t)i * t + up]) | 1ull << j;
+        }
+    for (int32_t i = n_trees; i < n; ++i) std::copy(masks.begin(), masks.begin() + t, masks.begin() + (size_t)i * t);
+}
+
+int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads, int32_t q_len, const int32_t* branches,
+              int32_t n, const int32_t* parents, int32_t n_trees, void* out, void* stream);
+
 // CTAs the tensor-core kernel may use on this pool (0: not used).
 int tc_ctas(const dendrite_pool* p) {
     return (p->dtype == DENDRITE_BF16 && p->tc_ready && p->tc_min_rows >= 0) ? p->sm_count : 0;
@@ -2058,6 +2114,7 @@ int tc_ctas(const dendrite_pool* p) {
 // (griddepcontrol.wait) before reading anything.
 int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStream_t s) {
     const bool bf16 = p->dtype == DENDRITE_BF16;
+    const bool out16 = p->dtype != DENDRITE_FP32;   // outputs are bf16
     prof_begin(p, T_ATTN_PARTIAL, s);
     CUtensorMap mk{}, mv{};
     if (bf16) {
@@ -2086,10 +2143,12 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
     if (beside) {
         DENDRITE_CUDA(cudaStreamWaitEvent(p->side, p->ev_fork, 0));
         prof_begin(p, T_ATTN_MMA_SIDE, p->side);
-        if (a.plan.packed)
-            k_attn_partial_bf16<true><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16_PACKED, p->side>>>(mk, mv, a);
+        if (a.plan.masks)
+            k_attn_partial_bf16<true, true><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16_PACKED, p->side>>>(mk, mv, a);
+        else if (a.plan.packed)
+            k_attn_partial_bf16<true, false><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16_PACKED, p->side>>>(mk, mv, a);
         else
-            k_attn_partial_bf16<false><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16, p->side>>>(mk, mv, a);
+            k_attn_partial_bf16<false, false><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16, p->side>>>(mk, mv, a);
         DENDRITE_CUDA(cudaGetLastError());
         prof_end(p, T_ATTN_MMA_SIDE, p->side);
         DENDRITE_CUDA(cudaEventRecord(p->ev_join, p->side));
@@ -2102,14 +2161,19 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
         // launched above
     } else if (p->dtype == DENDRITE_TURBO) {
         DENDRITE_TRY(launch_turbo_partials(a, a.Q, n_out_rows, p->d_tq_signs, p->d_tq_S, p->d_tq_qs, s));
+    } else if (p->dtype == DENDRITE_FP8) {
+        DENDRITE_TRY(launch_attn_fp8(a, s));
     } else if (a.plan.n_ctas > 0) {
         if (bf16) {
-            if (a.plan.packed)
-                DENDRITE_CUDA(launch_pdl(k_attn_partial_bf16<true>, dim3(a.plan.n_ctas), dim3(THREADS),
+            if (a.plan.masks)
+                DENDRITE_CUDA(launch_pdl(k_attn_partial_bf16<true, true>, dim3(a.plan.n_ctas), dim3(THREADS),
+                                         SMEM_BF16_PACKED, s, mk, mv, a));
+            else if (a.plan.packed)
+                DENDRITE_CUDA(launch_pdl(k_attn_partial_bf16<true, false>, dim3(a.plan.n_ctas), dim3(THREADS),
                                          SMEM_BF16_PACKED, s, mk, mv, a));
             else
-                DENDRITE_CUDA(launch_pdl(k_attn_partial_bf16<false>, dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16,
-                                         s, mk, mv, a));
+                DENDRITE_CUDA(launch_pdl(k_attn_partial_bf16<false, false>, dim3(a.plan.n_ctas), dim3(THREADS),
+                                         SMEM_BF16, s, mk, mv, a));
         } else {
             DENDRITE_CUDA(launch_pdl(k_attn_partial_f32, dim3(a.plan.n_ctas), dim3(128),
                                      2 * BS * p->head_dim * sizeof(float), s, a));
@@ -2137,7 +2201,7 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
             DENDRITE_CUDA(mlaunch(k_attn_merge<__nv_bfloat16, true>, grid));
         } else if (p->head_dim == D && ng > 0 && (int64_t)n_out / ng >= (int64_t)16 * p->sm_count) {
             const unsigned ggrid = (unsigned)((n_out / ng + 7) / 8);
-            if (bf16) {
+            if (out16) {
                 if (ng == 4) DENDRITE_CUDA(mlaunch(k_attn_merge_grouped<__nv_bfloat16, 4>, ggrid));
                 else if (ng == 2) DENDRITE_CUDA(mlaunch(k_attn_merge_grouped<__nv_bfloat16, 2>, ggrid));
                 else DENDRITE_CUDA(mlaunch(k_attn_merge_grouped<__nv_bfloat16, 1>, ggrid));
@@ -2146,7 +2210,7 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
                 else if (ng == 2) DENDRITE_CUDA(mlaunch(k_attn_merge_grouped<float, 2>, ggrid));
                 else DENDRITE_CUDA(mlaunch(k_attn_merge_grouped<float, 1>, ggrid));
             }
-        } else if (bf16) DENDRITE_CUDA(mlaunch(k_attn_merge<__nv_bfloat16, true>, grid));
+        } else if (out16) DENDRITE_CUDA(mlaunch(k_attn_merge<__nv_bfloat16, true>, grid));
         else if (p->head_dim == D) DENDRITE_CUDA(mlaunch(k_attn_merge<float, true>, grid));
         else DENDRITE_CUDA(mlaunch(k_attn_merge<float, false>, grid));
     }
@@ -2223,18 +2287,25 @@ int attn_setup(dendrite_pool* p) {
             DENDRITE_TRY(encode_pool_map(p, static_cast<char*>(p->d_v) + off, p->tmap_v[l].bytes));
         }
         p->tmaps_ok = true;
-        DENDRITE_CUDA(cudaFuncSetAttribute(k_attn_partial_bf16<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        DENDRITE_CUDA(cudaFuncSetAttribute(k_attn_partial_bf16<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)SMEM_BF16));
-        DENDRITE_CUDA(cudaFuncSetAttribute(k_attn_partial_bf16<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        DENDRITE_CUDA(cudaFuncSetAttribute(k_attn_partial_bf16<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)SMEM_BF16_PACKED));
-        int occ = 0, occ_packed = 0;
-        DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_bf16<false>, THREADS, SMEM_BF16));
-        DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_packed, k_attn_partial_bf16<true>, THREADS,
+        DENDRITE_CUDA(cudaFuncSetAttribute(k_attn_partial_bf16<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)SMEM_BF16_PACKED));
+        int occ = 0, occ_packed = 0, occ_draft = 0;
+        DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_bf16<false, false>, THREADS,
+                                                                    SMEM_BF16));
+        DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_packed, k_attn_partial_bf16<true, false>, THREADS,
                                                                     SMEM_BF16_PACKED));
-        p->attn_ctas_per_sm = std::max(1, std::min(occ, occ_packed));
+        DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_draft, k_attn_partial_bf16<true, true>, THREADS,
+                                                                    SMEM_BF16_PACKED));
+        p->attn_ctas_per_sm = std::max(1, std::min({occ, occ_packed, occ_draft}));
         p->tc_ready = attn_tc_setup() == DENDRITE_OK;
         DENDRITE_CUDA(cudaFuncSetAttribute(k_plan_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kMaxExpandSegs * 16));
+    } else if (p->dtype == DENDRITE_FP8) {
+        DENDRITE_TRY(attn_fp8_setup(&p->attn_ctas_per_sm));
     } else if (p->dtype == DENDRITE_TURBO) {
         p->attn_ctas_per_sm = turbo_ctas_per_sm();
     } else {
@@ -2271,6 +2342,27 @@ extern "C" int dendrite_tree_attn_decode(dendrite_pool* p, const void* Q, int32_
 extern "C" int dendrite_tree_attn_decode_layer(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
                                                int32_t q_len, const int32_t* branches, int32_t n, void* out,
                                                void* stream) {
+    return attn_call(p, layer, Q, n_q_heads, q_len, branches, n, nullptr, 0, out, stream);
+}
+
+extern "C" int dendrite_tree_attn_draft(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
+                                        int32_t n_draft, const int32_t* branches, int32_t n, const int32_t* parents,
+                                        int32_t n_trees, void* out, void* stream) {
+    if (!p) return DENDRITE_EINVAL;
+    if (p->poisoned) return p->poisoned;
+    if (p->dtype == DENDRITE_TURBO) return DENDRITE_EDTYPE;
+    if (n <= 0) return DENDRITE_EINVAL;
+    DENDRITE_TRY(check_trees(parents, n_trees, n, n_draft));
+    DENDRITE_CUDA(cudaSetDevice(p->device));
+    DENDRITE_TRY(check_not_capturing((cudaStream_t)stream));
+    return attn_call(p, layer, Q, n_q_heads, n_draft, branches, n, parents, n_trees, out, stream);
+}
+
+namespace {
+
+// One attention call; parents: n_trees draft trees of q_len nodes, or null.
+int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads, int32_t q_len, const int32_t* branches,
+              int32_t n, const int32_t* parents, int32_t n_trees, void* out, void* stream) {
     if (!p) return DENDRITE_EINVAL;
     if (p->poisoned) return p->poisoned;
     if (layer < 0 || layer >= p->n_layers) return DENDRITE_EINVAL;
@@ -2295,8 +2387,9 @@ extern "C" int dendrite_tree_attn_decode_layer(dendrite_pool* p, int32_t layer, 
     bool began = false;
     const int max_ctas = p->sm_count * p->attn_ctas_per_sm;
     PlanCache& pc = p->plan;
-    const bool same_query = pc.valid && pc.q_len == q_len && pc.n_q_heads == n_q_heads &&
-                            (int32_t)pc.branches.size() == n && std::equal(branches, branches + n, pc.branches.begin());
+    const bool same_query = pc.valid && pc.q_len == q_len && pc.n_q_heads == n_q_heads && pc.n_trees == n_trees &&
+                            (int32_t)pc.branches.size() == n && std::equal(branches, branches + n, pc.branches.begin()) &&
+                            (!parents || std::equal(pc.parents.begin(), pc.parents.end(), parents));
     const bool hit = same_query && pc.version == p->version;
     // Only appends since the plan was built, and no queried branch reached a
     // new block: the segments, units and partition are unchanged, and only
@@ -2398,6 +2491,7 @@ extern "C" int dendrite_tree_attn_decode_layer(dendrite_pool* p, int32_t layer, 
         } else {
             DENDRITE_TRY(build_plan(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, true));
         }
+        if (parents) draft_masks(parents, n_trees, n, q_len, hp.masks);
         size_t off[kPlanSections + 1];
         const size_t b = plan_layout(hp, off);
         DENDRITE_TRY(ensure_capacity(p, b, hp.partial_rows));
@@ -2459,6 +2553,8 @@ extern "C" int dendrite_tree_attn_decode_layer(dendrite_pool* p, int32_t layer, 
         pc.q_len = q_len;
         pc.n_q_heads = n_q_heads;
         pc.branches.assign(branches, branches + n);
+        pc.n_trees = n_trees;
+        pc.parents.assign(parents, parents ? parents + (size_t)n_trees * q_len : nullptr);
         pc.stats.n_segments = (int32_t)hp.segs.size();
         pc.stats.n_units = (int32_t)hp.units.size();
         pc.stats.n_ctas = pc.dev.n_ctas;
@@ -2492,6 +2588,8 @@ extern "C" int dendrite_tree_attn_decode_layer(dendrite_pool* p, int32_t layer, 
     if (!began) prof_begin(p, T_ATTN_TOTAL, s);
     return launch_attention(p, layer, a, s);
 }
+
+}  // namespace
 
 extern "C" int dendrite_last_plan_stats(dendrite_pool* p, dendrite_plan_stats* out) {
     if (!p || !out) return DENDRITE_EINVAL;

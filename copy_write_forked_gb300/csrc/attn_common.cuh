@@ -21,7 +21,8 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 // Row r of unit U: segment row sr = row_lo + r belongs to member sr / (q_len G),
 // query token j = (sr % (q_len G)) / G and head group g = sr % G; it reads the
 // Q/out row (member, token, kv head, group) and sees positions
-// < len - q_len + j + 1.
+// < len - q_len + j + 1 (a row of a draft tree: < len - q_len, and what its
+// mask adds).
 // The two divisions use the divisors' fp32 reciprocals (the host limits
 // segment rows to 2^24, so sr converts exactly and the estimate is off by at
 // most one, which one remainder test corrects): integer division by a
@@ -40,7 +41,25 @@ __device__ __forceinline__ AttnRow unit_row(const AttnPlanDev& pl, const AttnUni
     const int32_t mi = div_rcp(sr, RM, pl.rcp_rows_per_member), rem = sr - mi * RM;
     const int32_t j = div_rcp(rem, G, pl.rcp_group), g = rem - j * G;
     const AttnMember M = pl.members[U.mem_off + mi];
-    return AttnRow{(M.qi * pl.q_len + j) * pl.n_q_heads + U.kv_head * G + g, M.len - pl.q_len + j + 1, mi};
+    const int32_t limit = M.len - pl.q_len + (pl.masks ? 0 : j + 1);
+    return AttnRow{(M.qi * pl.q_len + j) * pl.n_q_heads + U.kv_head * G + g, limit, mi};
+}
+
+// Draft trees (pl.masks set): a row sees every position below its limit, the
+// first drafted one, and drafted position limit + b where bit b of its mask is
+// set.
+__device__ __forceinline__ uint64_t draft_mask(const AttnPlanDev& pl, const AttnUnit& U, int32_t r) {
+    const int32_t G = pl.group, RM = pl.q_len * G;
+    const int32_t sr = U.row_lo + r;
+    const int32_t mi = div_rcp(sr, RM, pl.rcp_rows_per_member), rem = sr - mi * RM;
+    const int32_t j = div_rcp(rem, G, pl.rcp_group);
+    return pl.masks[(int64_t)pl.members[U.mem_off + mi].qi * pl.q_len + j];
+}
+// Bit i: position p + i is seen, for off = limit - p.
+__device__ __forceinline__ uint64_t draft_visible(uint64_t mask, int32_t off) {
+    if (off >= 64) return ~0ull;
+    if (off > 0) return mask << off | ((1ull << off) - 1ull);
+    return off > -64 ? mask >> -off : 0ull;
 }
 
 struct AttnArgs {

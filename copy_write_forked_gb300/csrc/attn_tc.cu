@@ -208,6 +208,8 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     }
 }
 
+// DRAFT: the rows are nodes of draft trees (masked by their ancestors too).
+template <bool DRAFT>
 __global__ void __launch_bounds__(TC_THREADS, 1)
 k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const AttnArgs a) {
@@ -504,8 +506,16 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 if (ti0 + ntiles <= U.n_shared) {
                     const int32_t vis = min(ntiles * BS, R.limit - (U.blk_start + ti0) * BS);
                     if (!__all_sync(0xffffffffu, vis >= TC_TOK)) {
+                        if constexpr (DRAFT) {
+                            // draft trees: the stage's seen positions as bits
+                            uint64_t see = valid ? draft_visible(draft_mask(pl, U, row), R.limit - (U.blk_start + ti0) * BS) : 0;
+                            if (ntiles < 4) see &= (1ull << (ntiles * BS)) - 1ull;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) s[i] = i < vis ? s[i] : -INFINITY;
+                            for (int i = 0; i < 64; ++i) s[i] = (see >> i) & 1ull ? s[i] : -INFINITY;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) s[i] = i < vis ? s[i] : -INFINITY;
+                        }
                     }
                 } else {
                     // a stage with a packed unit's extra tiles: each tile counts
@@ -522,8 +532,15 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                             seen = ((uint32_t)e.y >> (mi & 31)) & 1u;
                         }
                         const int32_t v = seen ? min(BS, R.limit - lb * BS) : 0;
+                        if constexpr (DRAFT) {
+                            const uint32_t see =
+                                seen && valid ? (uint32_t)draft_visible(draft_mask(pl, U, row), R.limit - lb * BS) : 0u;
 #pragma unroll
-                        for (int c = 0; c < BS; ++c) s[BS * j + c] = c < v ? s[BS * j + c] : -INFINITY;
+                            for (int c = 0; c < BS; ++c) s[BS * j + c] = (see >> c) & 1u ? s[BS * j + c] : -INFINITY;
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < BS; ++c) s[BS * j + c] = c < v ? s[BS * j + c] : -INFINITY;
+                        }
                     }
                 }
                 // row max of the raw scores (eight independent chains), then
@@ -641,19 +658,29 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
 namespace dendrite {
 
-int attn_tc_setup() {
-    if (cudaFuncSetAttribute(k_attn_partial_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TC) !=
+template <bool DRAFT>
+static int setup_one() {
+    if (cudaFuncSetAttribute(k_attn_partial_tc<DRAFT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TC) !=
         cudaSuccess)
         return DENDRITE_ECUDA;
     int occ = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_tc, TC_THREADS, SMEM_TC) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_tc<DRAFT>, TC_THREADS, SMEM_TC) !=
+            cudaSuccess ||
         occ != 1)
         return DENDRITE_ECUDA;   // the kernel's 512 TMEM columns need exactly one CTA per SM
     return DENDRITE_OK;
 }
 
+int attn_tc_setup() {
+    DENDRITE_TRY(setup_one<false>());
+    return setup_one<true>();
+}
+
 int launch_attn_tc(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, cudaStream_t s) {
-    k_attn_partial_tc<<<n_ctas, TC_THREADS, SMEM_TC, s>>>(mk, mv, a);
+    if (a.plan.masks)
+        k_attn_partial_tc<true><<<n_ctas, TC_THREADS, SMEM_TC, s>>>(mk, mv, a);
+    else
+        k_attn_partial_tc<false><<<n_ctas, TC_THREADS, SMEM_TC, s>>>(mk, mv, a);
     return cudaGetLastError() == cudaSuccess ? DENDRITE_OK : DENDRITE_ECUDA;
 }
 

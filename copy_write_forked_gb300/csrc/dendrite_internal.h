@@ -20,6 +20,7 @@ constexpr int kBlockSize = 16;        // tokens per block (= attention tile heig
 constexpr int kMaxUnitRowsBf16 = 64;  // rows per mma.sync attention unit (4 row tiles of 16)
 constexpr int kMaxUnitRowsF32 = 16;
 constexpr int kMaxUnitRowsTurbo = 64;  // rows per compressed-pool unit (4 warps x 16 rows)
+constexpr int kMaxUnitRowsFp8 = 64;    // rows per 8-bit-pool unit (4 warps x 16 rows)
 constexpr int kMaxUnitRowsTc = 256;   // rows per tcgen05 attention unit (2 row tiles of 128)
 constexpr int kTcMinRowsDefault = 64; // segments with more rows per kv head use the tcgen05 kernel
 constexpr int32_t kFoldPctDefault = 100;  // fold a segment when that is estimated cheaper
@@ -130,6 +131,7 @@ struct AttnPlanDev {
     int32_t group;                 // G = n_q_heads / n_kv
     float rcp_rows_per_member;     // 1 / (q_len G)
     float rcp_group;               // 1 / G
+    const uint64_t* masks;         // [n_queried][q_len] drafted tokens each query sees (draft trees), or null
     int32_t packed;                // some unit reads extra tiles (the mma.sync kernel then needs its tile info)
 };
 
@@ -228,6 +230,8 @@ struct PlanCache {
     int32_t n_segplan = 0;           // segments of the device expansion's list
     size_t upload_bytes = 0;         // host-written prefix of the packed plan
     size_t sec_off[16] = {};         // section offsets of the packed plan
+    std::vector<int32_t> parents;    // draft trees the plan's masks were made from (empty: none)
+    int32_t n_trees = 0;
     uint64_t version = 0, shape_version = 0;
     int32_t q_len = 0, n_q_heads = 0;
     std::vector<int32_t> branches;

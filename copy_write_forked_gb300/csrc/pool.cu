@@ -20,11 +20,13 @@
 // and the free stack are bit-for-bit reproducible.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <unordered_set>
 
 #include "dendrite_internal.h"
+#include "rows.h"
 #include "turbo.h"
 
 using namespace dendrite;
@@ -953,10 +955,11 @@ int append_check(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n
 // Launches the metadata kernel (meta) and/or the copy kernel (copy) of an
 // append whose branches had lengths lens[] before it.  The copy writes layers
 // [layer0, layer0 + n_layers_in) from K/V (layer y's rows in_layer 16-byte
-// words after layer y - 1's).
+// words after layer y - 1's).  rotate: rotary positions and queries of the
+// rows (its q_*, rope, depth and n_trees fields), or null.
 int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens, int32_t n, int32_t n_new,
                   int64_t touched, bool copy, const void* K, const void* V, int32_t layer0, int32_t n_layers_in,
-                  int64_t in_layer, cudaStream_t s, bool meta = true) {
+                  int64_t in_layer, cudaStream_t s, bool meta = true, const RowsCall* rotate = nullptr) {
     const int32_t bs = p->block_size;
     // args: branch[n], len[n], tile prefix[n]
     constexpr int CAP = 768;
@@ -989,7 +992,22 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
                                      p->d_stack, p->d_holders, p->d_last, p->d_call_i32, p->d_meta));
             prof_end(p, T_APPEND_META, s);
         }
-        if (copy && p->dtype == DENDRITE_TURBO) {
+        if (copy && (rotate || p->dtype == DENDRITE_FP8)) {
+            RowsCall c = rotate ? *rotate : RowsCall{};
+            c.branches = branches;
+            c.lens = lens;
+            c.n = n;
+            c.n_new = n_new;
+            c.touched = touched;
+            c.K = K;
+            c.V = V;
+            c.layer0 = layer0;
+            c.n_layers_in = n_layers_in;
+            c.kv_layer = in_layer * (16 / p->elt);
+            prof_begin(p, T_APPEND_COPY, s);
+            DENDRITE_TRY(launch_append_rows(p, c, s));
+            prof_end(p, T_APPEND_COPY, s);
+        } else if (copy && p->dtype == DENDRITE_TURBO) {
             prof_begin(p, T_APPEND_COPY, s);
             TurboAppend t{};
             t.args = args.dev_ptr();
@@ -1047,6 +1065,43 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
     return p->staging.release(s);
 }
 
+// Host checks of a rotating append of n x n_new tokens in n_layers layers;
+// fills the rotation fields of `c` (depth holds the draft tree depths it
+// points to).
+int check_rotation(dendrite_pool* p, int32_t n, int32_t n_new, const int32_t* parents, int32_t n_trees, const void* Q,
+                   int32_t n_q_heads, void* q_out, const dendrite_rope* rope, int32_t n_layers, RowsCall& c,
+                   std::vector<uint8_t>& depth) {
+    if (!rope || rope->rot_dim < 16 || rope->rot_dim > p->head_dim || rope->rot_dim % 16) return DENDRITE_EINVAL;
+    if (rope->interleaved != 0 && rope->interleaved != 1) return DENDRITE_EINVAL;
+    if (!std::isfinite(rope->scale)) return DENDRITE_EINVAL;
+    for (int32_t r : rope->reserved)
+        if (r) return DENDRITE_EINVAL;
+    for (int32_t i = 0; i < rope->rot_dim / 2; ++i)
+        if (!std::isfinite(rope->inv_freq[i])) return DENDRITE_EINVAL;
+    if (Q) {
+        if (n_q_heads < 1 || !q_out || (((uintptr_t)Q | (uintptr_t)q_out) & 15)) return DENDRITE_EINVAL;
+        const int64_t rows = (int64_t)n * n_new * n_q_heads;
+        if (rows * n_layers >= INT32_MAX / 2) return DENDRITE_ELIMIT;
+        // in place, or apart
+        const uintptr_t x = (uintptr_t)Q, y = (uintptr_t)q_out, bytes = (uintptr_t)(rows * n_layers * p->head_dim * p->elt);
+        if (x != y && x < y + bytes && y < x + bytes) return DENDRITE_EINVAL;
+        c.Q = Q;
+        c.q_out = q_out;
+        c.n_q_heads = n_q_heads;
+        c.q_layer = rows * p->head_dim;
+    }
+    if (parents) {
+        DENDRITE_TRY(check_trees(parents, n_trees, n, n_new));
+        tree_depths(parents, n_trees, n_new, depth);
+        c.depth = depth.data();
+        c.n_trees = n_trees;
+    } else if (n_trees != 0) {
+        return DENDRITE_EINVAL;
+    }
+    c.rope = rope;
+    return DENDRITE_OK;
+}
+
 void append_commit_lengths(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n_new) {
     for (int32_t i = 0; i < n; ++i) {
         Branch& b = p->br[branches[i]];
@@ -1077,7 +1132,7 @@ int pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads, int3
         if (!tq_signs || !tq_S) return DENDRITE_EINVAL;
         for (int i = 0; i < kTurboDim; ++i)
             if (tq_signs[i] != 1.f && tq_signs[i] != -1.f) return DENDRITE_EINVAL;
-    } else if (dtype == DENDRITE_BF16) {
+    } else if (dtype == DENDRITE_BF16 || dtype == DENDRITE_FP8) {
         if (head_dim != 128) return DENDRITE_EDTYPE;
     } else if (dtype == DENDRITE_FP32) {
         if (head_dim <= 0 || head_dim > 256 || head_dim % 32) return DENDRITE_EDTYPE;
@@ -1103,7 +1158,7 @@ int pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads, int3
     p->n_kv = n_kv_heads;
     p->head_dim = head_dim;
     p->dtype = dtype;
-    p->elt = dtype == DENDRITE_FP32 ? 4 : 2;   // compressed pools take bf16 rows
+    p->elt = dtype == DENDRITE_FP32 ? 4 : 2;   // compressed and 8-bit pools take bf16 rows
     p->max_branches = max_branches;
     p->bpb = bpb;
     if (opts && opts->tc_min_rows) p->tc_min_rows = opts->tc_min_rows;
@@ -1123,6 +1178,8 @@ int pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads, int3
     if (dtype == DENDRITE_TURBO) {
         p->layer_bytes = slots * kTurboKeyBytes;
         p->layer_bytes_v = slots * kTurboValueBytes;
+    } else if (dtype == DENDRITE_FP8) {
+        p->layer_bytes = p->layer_bytes_v = (size_t)num_blocks * n_kv_heads * kFp8TileBytes;
     } else {
         p->layer_bytes = p->layer_bytes_v = slots * head_dim * p->elt;
     }
@@ -1355,6 +1412,51 @@ int dendrite_append_layer(dendrite_pool* p, int32_t layer, const void* K, const 
     const int32_t n = (int32_t)pa.branches.size();
     DENDRITE_TRY(append_launch(p, pa.branches.data(), pa.lens.data(), n, pa.n_new, pa.touched, true, K, V, layer, 1,
                                0, s, /*meta=*/false));
+    pa.layer_done[layer] = 1;
+    if (++pa.n_done == p->n_layers) pa.active = false;
+    return DENDRITE_OK;
+}
+
+int dendrite_append_rope(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n_new, const int32_t* parents,
+                         int32_t n_trees, const void* K, const void* V, const void* Q, int32_t n_q_heads, void* q_out,
+                         const dendrite_rope* rope, void* stream) {
+    DENDRITE_TRY(prelude(p));
+    if (p->dtype == DENDRITE_TURBO) return DENDRITE_EDTYPE;
+    if (p->pending.active) return DENDRITE_EINVAL;
+    if (n < 0 || n_new < 0 || (n > 0 && !branches)) return DENDRITE_EINVAL;
+    if (n == 0 || n_new == 0) return DENDRITE_OK;
+    if (!K || !V || (((uintptr_t)K | (uintptr_t)V) & 15)) return DENDRITE_EINVAL;
+    RowsCall c{};
+    std::vector<uint8_t> depth;
+    DENDRITE_TRY(check_rotation(p, n, n_new, parents, n_trees, Q, n_q_heads, q_out, rope, p->n_layers, c, depth));
+    int64_t touched = 0;
+    DENDRITE_TRY(append_check(p, branches, n, n_new, &touched));
+    cudaStream_t s = (cudaStream_t)stream;
+    DENDRITE_TRY(check_not_capturing(s));
+    std::vector<int32_t> lens(n);
+    for (int32_t i = 0; i < n; ++i) lens[i] = p->br[branches[i]].len;
+    const int64_t in_layer = (int64_t)n * n_new * p->n_kv * p->head_dim * p->elt / 16;
+    DENDRITE_TRY(append_launch(p, branches, lens.data(), n, n_new, touched, true, K, V, 0, p->n_layers, in_layer, s,
+                               /*meta=*/true, &c));
+    append_commit_lengths(p, branches, n, n_new);
+    return DENDRITE_OK;
+}
+
+int dendrite_append_layer_rope(dendrite_pool* p, int32_t layer, const int32_t* parents, int32_t n_trees,
+                               const void* K, const void* V, const void* Q, int32_t n_q_heads, void* q_out,
+                               const dendrite_rope* rope, void* stream) {
+    DENDRITE_TRY(prelude(p));
+    if (p->dtype == DENDRITE_TURBO) return DENDRITE_EDTYPE;
+    PendingAppend& pa = p->pending;
+    if (!pa.active || layer < 0 || layer >= p->n_layers || pa.layer_done[layer]) return DENDRITE_EINVAL;
+    if (!K || !V || (((uintptr_t)K | (uintptr_t)V) & 15)) return DENDRITE_EINVAL;
+    const int32_t n = (int32_t)pa.branches.size();
+    RowsCall c{};
+    std::vector<uint8_t> depth;
+    DENDRITE_TRY(check_rotation(p, n, pa.n_new, parents, n_trees, Q, n_q_heads, q_out, rope, 1, c, depth));
+    DENDRITE_TRY(check_not_capturing((cudaStream_t)stream));
+    DENDRITE_TRY(append_launch(p, pa.branches.data(), pa.lens.data(), n, pa.n_new, pa.touched, true, K, V, layer, 1, 0,
+                               (cudaStream_t)stream, /*meta=*/false, &c));
     pa.layer_done[layer] = 1;
     if (++pa.n_done == p->n_layers) pa.active = false;
     return DENDRITE_OK;

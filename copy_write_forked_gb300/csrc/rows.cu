@@ -1,0 +1,815 @@
+// Rows into and out of the blocks.
+//
+// k_append_rows writes the new rows of an append and, on the way, applies
+// rotary positions and the 8-bit quantisation, so that a row is read once and
+// written once.
+//
+// Rotary positions.  Pair i of a head (elements (i, i + r/2), or (2 i, 2 i + 1)
+// when interleaved; r = rot_dim) turns by a = position * inv_freq[i]:
+//     y1 = m (x1 cos a - x2 sin a),   y2 = m (x2 cos a + x1 sin a).
+// The angle is kept in turns, as a 64-bit fixed-point fraction: position *
+// fraction wraps at whole turns, so the range reduction is one integer
+// product and exact however far the position is (an fp32 angle at position
+// 10^6 would be off by 2^-4 rad).  The top 32 bits, a signed fraction of half
+// a turn, go to sincospif: an error of about 2^-24 of half a turn, below the
+// rounding of fp32 products.
+//
+// 8-bit rows.  e is the least integer >= -127 with max|x| <= 448 * 2^e (over
+// the finite elements) and element k is stored as the e4m3 number nearest to
+// x_k * 2^-e, ties to even (with e = 120 at most 240, which is finite when read
+// back); a NaN or an infinity is stored as NaN.  The scale
+// is a power of two: x * 2^-e is exact in fp32, so a code depends on its
+// row's bits alone, and code * 2^e is again a bf16 number, exactly.
+//
+// A thread owns 16 elements (two 8-element chunks that hold whole pairs) of
+// the row of one token and walks the heads with them: the 8 angles are
+// computed once per thread, not once per head.  All of a tile's tokens and
+// heads are spread over 128 threads; tiles are (branch, block) pairs, and few
+// tiles are split over their heads (grid.z) until about 8 CTAs per SM exist.
+// The kernel is bound by HBM at large sizes and by its chain of dependent
+// reads (table, row) at small ones.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <type_traits>
+
+#include "rows.h"
+
+using namespace dendrite;
+
+namespace {
+
+__device__ __forceinline__ void pdl_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Per-call argument words: as kernel parameters up to CAP words, staged in
+// device memory beyond.
+template <int CAP>
+struct ParamWords {
+    int32_t v[CAP];
+    __device__ __forceinline__ int32_t operator[](int64_t i) const { return v[i]; }
+};
+struct GlobalWords {
+    const int32_t* p;
+    __device__ __forceinline__ int32_t operator[](int64_t i) const { return __ldg(p + i); }
+};
+constexpr int kRowsCap = 1536;
+
+template <typename A>
+__device__ __forceinline__ int32_t byte_of(const A& args, int64_t word0, int64_t i) {
+    return (int32_t)((uint32_t)args[word0 + (i >> 2)] >> (8 * (int)(i & 3))) & 255;
+}
+
+// Branch holding entry t of the concatenated per-branch ranges that start at
+// args[off + i] (ascending), and its range's start: a division when every
+// branch has `uniform` entries.
+template <typename A>
+__device__ __forceinline__ int32_t find_branch(const A& args, int64_t off, int32_t n, int32_t t, int32_t uniform,
+                                               int32_t& first) {
+    if (uniform > 0) {
+        const int32_t i = t / uniform;
+        first = i * uniform;
+        return i;
+    }
+    int32_t lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (args[off + mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    first = args[off + lo];
+    return lo;
+}
+
+struct RowsArgs {
+    int32_t n, n_new, bpb, n_kv, nq, dim, rot, interleaved, n_blocks, uniform, n_tiles, has_depth, one_tree;
+    float m;
+    const int32_t* table;
+    const int32_t* call;    // the metadata kernel's scratch: copy-on-write sources at [n, 2 n)
+    const void* K;
+    const void* V;
+    const void* Q;
+    void* q_out;
+    char* kp;
+    char* vp;
+    int64_t kv_layer, q_layer;   // elements
+    int64_t pool_layer;          // bytes
+    DevMeta* meta;
+    uint64_t freq[128];          // turns per position, as a fraction of 2^64
+};
+
+// Eight consecutive elements as fp32, and back.  Input rows are read once,
+// through L2 and not the read-only path: the queries may be rotated in place.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = __uint_as_float(w[k] << 16);
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// max|x| over the finite elements.
+__device__ __forceinline__ float finite_max(const float (&x)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float a = fabsf(x[k]);
+        m = fmaxf(m, a < INFINITY ? a : 0.f);
+    }
+    return m;
+}
+// The least e >= -127 with top <= 448 * 2^e: top = (1 + f) 2^(E - 127), and
+// 448 = 1.75 * 2^8.
+__device__ __forceinline__ int fp8_exponent(float top) {
+    const uint32_t b = __float_as_uint(top);
+    return max(-127, (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0));
+}
+// Eight codes of x * 2^-e.
+__device__ __forceinline__ uint2 fp8_codes(const float (&x)[8], int e) {
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);   // e in [-127, 120]
+    const float top = e == 120 ? 240.f : 448.f;   // 256 * 2^120 would read back as an infinity
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a = x[2 * k], b = x[2 * k + 1];
+        a = fabsf(a) < INFINITY ? fminf(fmaxf(a * inv, -top), top) : __uint_as_float(0x7fffffffu);
+        b = fabsf(b) < INFINITY ? fminf(fmaxf(b * inv, -top), top) : __uint_as_float(0x7fffffffu);
+        w[k] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+// Byte offset of element d (a multiple of 8) of slot s in an 8-bit tile.
+__device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
+    return s * kFp8Dim + (((d >> 4) ^ (s & 7)) << 4) + (d & 8);
+}
+
+// args: branch[n], length[n], prefix of touched blocks[n], then the draft
+// tree depths as bytes.
+// T: the rows' type; FP8: the blocks hold 8-bit rows (else rows of T).
+template <typename T, bool FP8, typename A>
+__global__ void __launch_bounds__(128) k_append_rows(const __grid_constant__ A args, const __grid_constant__ RowsArgs a) {
+    pdl_wait();
+    constexpr int bs = kBlockSize;
+    const int32_t n = a.n, dim = a.dim;
+    const int32_t items = dim >> 4;                     // threads per row
+    const int32_t lanes = 128 / items;                  // rows in flight, cut to a power of two
+    const int32_t lp2 = 1 << (31 - __clz(lanes));
+    const int32_t item = threadIdx.x % items, lane = threadIdx.x / items;
+    // this thread's two chunks, whether they turn, and their first pair
+    int32_t c0, c1;
+    if (a.interleaved || a.rot == 0) {
+        c0 = 8 * item;
+        c1 = dim / 2 + 8 * item;
+    } else if (16 * item < a.rot) {
+        c0 = 8 * item;
+        c1 = a.rot / 2 + 8 * item;
+    } else {
+        c0 = a.rot + 8 * (item - a.rot / 16);
+        c1 = c0 + (dim - a.rot) / 2;
+    }
+    const bool turn0 = c0 < a.rot, turn1 = c1 < a.rot;
+    const int32_t n_rows = 2 * a.n_kv + a.nq;           // rows per token: K heads, V heads, Q heads
+    const int32_t status = a.meta->status;
+    const T* K = static_cast<const T*>(a.K) + blockIdx.y * a.kv_layer;
+    const T* V = static_cast<const T*>(a.V) + blockIdx.y * a.kv_layer;
+    const T* Q = static_cast<const T*>(a.Q) + blockIdx.y * a.q_layer;
+    T* q_out = static_cast<T*>(a.q_out) + blockIdx.y * a.q_layer;
+    char* kp = a.kp + blockIdx.y * a.pool_layer;
+    char* vp = a.vp + blockIdx.y * a.pool_layer;
+    const int64_t tile_bytes = FP8 ? kFp8TileBytes : (int64_t)bs * dim * (int)sizeof(T);
+    if (__any_sync(0xffffffffu, status)) return;   // a whole warp leaves: shuffles below
+    for (int32_t t = blockIdx.x; t < a.n_tiles; t += gridDim.x) {
+        int32_t first;
+        const int32_t i = find_branch(args, 2 * (int64_t)n, n, t, a.uniform, first);
+        const int32_t L = args[n + i];
+        const int32_t lblk = L / bs + (t - first);
+        const int32_t s0 = lblk == L / bs ? L % bs : 0;
+        const int32_t s1 = min(bs, L + a.n_new - lblk * bs);
+        const int32_t dst = a.table[(int64_t)args[i] * a.bpb + lblk];
+        const int32_t csrc = lblk == L / bs ? a.call[n + i] : -1;
+        if ((uint32_t)dst >= (uint32_t)a.n_blocks || csrc >= a.n_blocks) {
+            if (threadIdx.x == 0) atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
+            return;
+        }
+        // tokens side by side over the lanes, as many as there are (to a power of two)
+        const int32_t nt = s1 - s0;
+        const int32_t tp = min(lp2, nt <= 1 ? 1 : 1 << (32 - __clz(nt - 1)));
+        const int32_t r0 = lane / tp, rstep = lp2 / tp;
+        const bool worker = lane < lp2;
+        for (int32_t k0 = 0; k0 < nt; k0 += tp) {
+            const int32_t k = k0 + lane % tp;
+            const bool live = worker && k < nt;
+            const int32_t slot = s0 + (live ? k : 0);
+            const int32_t tok = lblk * bs + slot - L;       // 0 .. n_new - 1
+            float cs[8], sn[8];
+            if (a.rot) {
+                const int32_t pos = L + (a.has_depth ? byte_of(args, 3 * (int64_t)n, (int64_t)(a.one_tree ? 0 : i) * a.n_new + tok) : tok);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int32_t pair = a.interleaved ? (q < 4 ? c0 / 2 + q : c1 / 2 + q - 4) : c0 + q;
+                    const bool on = a.interleaved ? (q < 4 ? turn0 : turn1) : turn0;
+                    cs[q] = 1.f;
+                    sn[q] = 0.f;
+                    if (on) {
+                        const uint64_t f = a.freq[pair & 127] * (uint64_t)(uint32_t)pos;
+                        const float half_turns = (float)(int32_t)(uint32_t)(f >> 32) * 4.656612873077393e-10f;   // 2^-31
+                        sincospif(half_turns, &sn[q], &cs[q]);
+                        cs[q] *= a.m;
+                        sn[q] *= a.m;
+                    }
+                }
+            }
+            const int64_t in_row = (int64_t)i * a.n_new + tok;
+            const int32_t n_iter = (n_rows + rstep * (int)gridDim.z - 1) / (rstep * (int)gridDim.z);
+#pragma unroll 2
+            for (int32_t it = 0; it < n_iter; ++it) {
+                const int32_t rr = (it * (int)gridDim.z + (int)blockIdx.z) * rstep + r0;
+                const bool act = live && rr < n_rows;
+                const int32_t kind = rr < a.n_kv ? 0 : rr < 2 * a.n_kv ? 1 : 2;   // K, V, Q
+                const int32_t h = rr - (kind == 0 ? 0 : kind == 1 ? a.n_kv : 2 * a.n_kv);
+                const T* src = kind == 0 ? K : kind == 1 ? V : Q;
+                src += (in_row * (kind == 2 ? a.nq : a.n_kv) + h) * dim;
+                float x[8], y[8];
+                if (act) {
+                    load8(src + c0, x);
+                    load8(src + c1, y);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) x[q] = y[q] = 0.f;
+                }
+                if (a.rot && kind != 1) {
+                    if (a.interleaved) {
+                        if (turn0) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float u = x[2 * q], v = x[2 * q + 1];
+                                x[2 * q] = u * cs[q] - v * sn[q];
+                                x[2 * q + 1] = v * cs[q] + u * sn[q];
+                            }
+                        }
+                        if (turn1) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float u = y[2 * q], v = y[2 * q + 1];
+                                y[2 * q] = u * cs[4 + q] - v * sn[4 + q];
+                                y[2 * q + 1] = v * cs[4 + q] + u * sn[4 + q];
+                            }
+                        }
+                    } else if (turn0) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float u = x[q], v = y[q];
+                            x[q] = u * cs[q] - v * sn[q];
+                            y[q] = v * cs[q] + u * sn[q];
+                        }
+                    }
+                }
+                char* tile = (kind == 0 ? kp : vp) + ((int64_t)dst * a.n_kv + (kind == 2 ? 0 : h)) * tile_bytes;
+                if constexpr (FP8) {
+                    // the row's largest element: its eight threads are eight neighbouring lanes
+                    float top = fmaxf(finite_max(x), finite_max(y));
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    if (act && kind != 2) {
+                        const int e = fp8_exponent(top);
+                        *reinterpret_cast<uint2*>(tile + fp8_at(slot, c0)) = fp8_codes(x, e);
+                        *reinterpret_cast<uint2*>(tile + fp8_at(slot, c1)) = fp8_codes(y, e);
+                        if (item == 0) tile[bs * kFp8Dim + slot] = (char)(e + 127);
+                    }
+                } else if (act && kind != 2) {
+                    T* out = reinterpret_cast<T*>(tile) + slot * dim;
+                    store8(out + c0, x);
+                    store8(out + c1, y);
+                }
+                if (act && kind == 2) {
+                    T* out = q_out + (in_row * a.nq + h) * dim;
+                    store8(out + c0, x);
+                    store8(out + c1, y);
+                }
+            }
+        }
+        // the valid slots of a copied-on-write tail, stored rows as they are
+        if (csrc >= 0 && s0 > 0) {
+            const int32_t words = FP8 ? kFp8Dim / 16 : dim * (int)sizeof(T) / 16;
+            for (int32_t r = blockIdx.z; r < 2 * a.n_kv; r += gridDim.z) {
+                char* pool = r < a.n_kv ? kp : vp;
+                const int32_t h = r < a.n_kv ? r : r - a.n_kv;
+                const char* from = pool + ((int64_t)csrc * a.n_kv + h) * tile_bytes;
+                char* to = pool + ((int64_t)dst * a.n_kv + h) * tile_bytes;
+                for (int32_t w = threadIdx.x; w < s0 * words; w += 128)
+                    reinterpret_cast<uint4*>(to)[w] = reinterpret_cast<const uint4*>(from)[w];
+                if (FP8 && (int32_t)threadIdx.x < s0) to[bs * kFp8Dim + threadIdx.x] = from[bs * kFp8Dim + threadIdx.x];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gather
+// args: branch[n], first position[n], output row[n], prefix of touched blocks[n],
+// row count[n].  One CTA per (branch, block) and share of the heads; a thread
+// moves 8 elements, so that a warp's stores cover whole 128-byte lines.
+struct ReadArgs {
+    int32_t n, bpb, n_kv, dim, n_blocks, uniform, n_tiles;
+    const int32_t* table;
+    const char* kp;
+    const char* vp;
+    void* K;
+    void* V;
+    DevMeta* meta;
+};
+
+template <typename T, bool FP8, typename A>
+__global__ void __launch_bounds__(128) k_read_rows(const __grid_constant__ A args, const __grid_constant__ ReadArgs a) {
+    pdl_wait();
+    constexpr int bs = kBlockSize;
+    const int32_t n = a.n, dim = a.dim, chunks = dim >> 3;
+    if (a.meta->status) return;
+    const int64_t tile_bytes = FP8 ? kFp8TileBytes : (int64_t)bs * dim * (int)sizeof(T);
+    for (int32_t t = blockIdx.x; t < a.n_tiles; t += gridDim.x) {
+        int32_t first;
+        const int32_t i = find_branch(args, 3 * (int64_t)n, n, t, a.uniform, first);
+        const int32_t p0 = args[n + i], count = args[4 * (int64_t)n + i];
+        const int32_t lblk = p0 / bs + (t - first);
+        const int32_t s0 = max(0, p0 - lblk * bs), s1 = min(bs, p0 + count - lblk * bs);
+        const int32_t src = a.table[(int64_t)args[i] * a.bpb + lblk];
+        if ((uint32_t)src >= (uint32_t)a.n_blocks) {
+            if (threadIdx.x == 0) atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
+            return;
+        }
+        const int64_t row0 = (int64_t)args[2 * (int64_t)n + i] + lblk * bs - p0;   // output row of slot 0
+        const int32_t per_slot = 2 * a.n_kv * chunks;       // K then V, head, chunk
+        const int32_t total = (s1 - s0) * per_slot;
+#pragma unroll 4
+        for (int32_t e = blockIdx.z * 128 + threadIdx.x; e < total; e += 128 * gridDim.z) {
+            const int32_t slot = s0 + e / per_slot;
+            int32_t r = e % per_slot;
+            const bool v = r >= a.n_kv * chunks;
+            r -= v ? a.n_kv * chunks : 0;
+            const int32_t h = r / chunks, d = 8 * (r % chunks);
+            const char* tile = (v ? a.vp : a.kp) + ((int64_t)src * a.n_kv + h) * tile_bytes;
+            T* out = static_cast<T*>(v ? a.V : a.K) + ((row0 + slot) * a.n_kv + h) * dim + d;
+            if constexpr (FP8) {
+                const uint2 w = *reinterpret_cast<const uint2*>(tile + fp8_at(slot, d));
+                // 2^(byte - 127), a denormal for byte 0
+                const uint32_t b = (unsigned char)tile[bs * kFp8Dim + slot];
+                const float s = __uint_as_float(b ? b << 23 : 0x400000u);
+                const uint32_t q[2] = {w.x, w.y};
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+                    const float2 f = __half22float2(__half2(hr));
+                    x[2 * k] = f.x * s;
+                    x[2 * k + 1] = f.y * s;
+                }
+                store8(out, x);
+            } else {
+                constexpr int W = 8 * sizeof(T) / 16;
+                const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(tile) + slot * dim + d);
+#pragma unroll
+                for (int k = 0; k < W; ++k) reinterpret_cast<uint4*>(out)[k] = from[k];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------- kept drafts
+// args: branch[n], base length[n], kept rows[n], prefix of kept nodes[n], then
+// the kept nodes as bytes.  Row base + node[k] moves to base + k.  Nodes are
+// ascending (node[k] >= k), so a write to row k never hits a row that a later
+// k still reads, and every thread moves its own 16-byte column: the order of
+// the loop is all the synchronisation it needs.  CTA (branch, kv head, layer).
+struct KeepArgs {
+    int32_t n, bpb, n_kv, n_blocks, words;   // words: 16-byte words of a stored row
+    int64_t tile_bytes, pool_layer;
+    int32_t fp8;
+    const int32_t* table;
+    char* kp;
+    char* vp;
+    DevMeta* meta;
+};
+
+template <typename A>
+__global__ void __launch_bounds__(128) k_keep_rows(const __grid_constant__ A args, const __grid_constant__ KeepArgs a) {
+    pdl_wait();
+    constexpr int bs = kBlockSize;
+    __shared__ int32_t blocks[kMaxDraft / bs + 1];
+    __shared__ int32_t bad;
+    const int32_t n = a.n, i = blockIdx.x, h = blockIdx.y;
+    if (a.meta->status) return;
+    const int32_t base = args[n + i], kept = args[2 * n + i], off = args[3 * n + i];
+    if (kept == 0) return;
+    const int32_t b0 = base / bs;
+    const int32_t top = base + byte_of(args, 4 * (int64_t)n, off + kept - 1);   // the last row read
+    const int32_t nb = top / bs - b0 + 1;
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    if ((int32_t)threadIdx.x < nb) {
+        const int32_t blk = a.table[(int64_t)args[i] * a.bpb + b0 + threadIdx.x];
+        blocks[threadIdx.x] = blk;
+        if ((uint32_t)blk >= (uint32_t)a.n_blocks) {
+            bad = 1;
+            atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
+        }
+    }
+    __syncthreads();
+    if (bad) return;
+    const int32_t cols = 2 * a.words + (a.fp8 ? 2 : 0);   // K words, V words, then the two exponent columns
+    for (int32_t c = threadIdx.x; c < cols; c += blockDim.x) {
+        const bool v = c < 2 * a.words ? c >= a.words : c - 2 * a.words == 1;
+        char* pool = (v ? a.vp : a.kp) + blockIdx.z * a.pool_layer;
+        if (c < 2 * a.words) {
+            const int32_t w = v ? c - a.words : c;
+            auto at = [&](int32_t pos) {
+                const int32_t s = pos % bs;
+                return reinterpret_cast<uint4*>(pool + ((int64_t)blocks[pos / bs - b0] * a.n_kv + h) * a.tile_bytes) +
+                       s * a.words + (a.fp8 ? w ^ (s & 7) : w);
+            };
+            constexpr int U = 8;
+            for (int32_t k0 = 0; k0 < kept; k0 += U) {
+                uint4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (k0 + u < kept) x[u] = *at(base + byte_of(args, 4 * (int64_t)n, off + k0 + u));
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (k0 + u < kept) *at(base + k0 + u) = x[u];
+            }
+        } else {
+            auto at = [&](int32_t pos) {
+                return pool + ((int64_t)blocks[pos / bs - b0] * a.n_kv + h) * a.tile_bytes + bs * kFp8Dim + pos % bs;
+            };
+            for (int32_t k = 0; k < kept; ++k) *at(base + k) = *at(base + byte_of(args, 4 * (int64_t)n, off + k));
+        }
+    }
+}
+
+// Calls `go` with the argument words: as kernel parameters, or staged.
+template <typename Fill, typename Go>
+int with_words(dendrite_pool* p, size_t words, cudaStream_t s, Fill fill, Go go) {
+    if (words <= (size_t)kRowsCap) {
+        ParamWords<kRowsCap> a;
+        fill(a.v);
+        return go(a);
+    }
+    char *h, *d;
+    DENDRITE_TRY(p->staging.reserve(words * 4, &h, &d));
+    fill(reinterpret_cast<int32_t*>(h));
+    DENDRITE_TRY(p->staging.upload(s, h, words * 4));
+    DENDRITE_TRY(go(GlobalWords{reinterpret_cast<const int32_t*>(d)}));
+    return p->staging.release(s);
+}
+
+// CTAs along the heads so that `tiles` tiles make about 8 per SM, at most `most`.
+unsigned head_splits(const dendrite_pool* p, int64_t tiles, int64_t most) {
+    const int64_t want = (8 * (int64_t)p->sm_count + tiles - 1) / std::max<int64_t>(tiles, 1);
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), 64));
+}
+
+}  // namespace
+
+namespace dendrite {
+
+// Captured calls would be replayed with the lengths, tables and staged
+// arguments of the capture: refused.
+int check_not_capturing(cudaStream_t s) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+        cudaGetLastError();
+        return DENDRITE_EINVAL;
+    }
+    return st == cudaStreamCaptureStatusNone ? DENDRITE_OK : DENDRITE_EINVAL;
+}
+
+}  // namespace dendrite
+
+namespace {
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+namespace dendrite {
+
+int check_trees(const int32_t* parents, int32_t n_trees, int32_t n, int32_t t) {
+    if (!parents || (n_trees != 1 && n_trees != n)) return DENDRITE_EINVAL;
+    if (t < 1 || t > kMaxDraft) return DENDRITE_EINVAL;
+    for (int64_t i = 0; i < n_trees; ++i)
+        for (int32_t j = 0; j < t; ++j) {
+            const int32_t up = parents[i * t + j];
+            if (up < -1 || up >= j) return DENDRITE_EINVAL;
+        }
+    return DENDRITE_OK;
+}
+
+void tree_depths(const int32_t* parents, int32_t n_trees, int32_t t, std::vector<uint8_t>& depth) {
+    depth.resize((size_t)n_trees * t);
+    for (int64_t i = 0; i < n_trees; ++i)
+        for (int32_t j = 0; j < t; ++j) {
+            const int32_t up = parents[i * t + j];
+            depth[i * t + j] = up < 0 ? 0 : (uint8_t)(depth[i * t + up] + 1);
+        }
+}
+
+int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s) {
+    const int32_t bs = p->block_size, n = c.n, n_new = c.n_new;
+    RowsArgs a{};
+    a.n = n;
+    a.n_new = n_new;
+    a.bpb = p->bpb;
+    a.n_kv = p->n_kv;
+    a.nq = c.Q ? c.n_q_heads : 0;
+    a.dim = p->head_dim;
+    a.n_blocks = (int32_t)p->num_blocks;
+    a.n_tiles = (int32_t)c.touched;
+    a.table = p->d_table;
+    a.call = p->d_call_i32;
+    a.K = c.K;
+    a.V = c.V;
+    a.Q = c.Q;
+    a.q_out = c.q_out;
+    a.kp = static_cast<char*>(p->d_k) + (size_t)c.layer0 * p->layer_bytes;
+    a.vp = static_cast<char*>(p->d_v) + (size_t)c.layer0 * p->layer_bytes_v;
+    a.kv_layer = c.kv_layer;
+    a.q_layer = c.q_layer;
+    a.pool_layer = (int64_t)p->layer_bytes;
+    a.meta = p->d_meta;
+    a.m = 1.f;
+    if (c.rope) {
+        a.rot = c.rope->rot_dim;
+        a.interleaved = c.rope->interleaved;
+        a.m = (float)c.rope->scale;
+        for (int k = 0; k < a.rot / 2; ++k) {
+            // turns per position modulo one: whole turns change nothing at whole positions
+            const double turns = c.rope->inv_freq[k] * 0.15915494309189533577;   // 1 / (2 pi)
+            const double frac = turns - std::floor(turns);
+            a.freq[k] = frac >= 1.0 ? 0 : (uint64_t)std::ldexp(frac, 64);
+        }
+        a.has_depth = c.depth != nullptr;
+        a.one_tree = c.n_trees == 1;
+    }
+    int32_t uniform = -1;
+    for (int32_t i = 0; i < n && uniform != 0; ++i) {
+        const int32_t k = (c.lens[i] + n_new - 1) / bs - c.lens[i] / bs + 1;
+        uniform = uniform < 0 ? k : (uniform == k ? k : 0);
+    }
+    a.uniform = std::max(uniform, 0);
+    const size_t n_depth = a.has_depth ? (size_t)c.n_trees * n_new : 0;
+    const size_t words = 3 * (size_t)n + (n_depth + 3) / 4;
+    auto fill = [&](int32_t* w) {
+        int32_t acc = 0;
+        for (int32_t i = 0; i < n; ++i) {
+            w[i] = c.branches[i];
+            w[n + i] = c.lens[i];
+            w[2 * (size_t)n + i] = acc;
+            acc += (c.lens[i] + n_new - 1) / bs - c.lens[i] / bs + 1;
+        }
+        if (n_depth) {
+            w[words - 1] = 0;   // the bytes after the last depth
+            std::memcpy(w + 3 * (size_t)n, c.depth, n_depth);
+        }
+    };
+    // rows side by side in a CTA: 128 / (dim / 16) threads over a tile's tokens, the rest over heads
+    const int32_t n_rows = 2 * a.n_kv + a.nq;
+    int32_t lanes = 128 / (a.dim / 16), tp = 1;
+    while (lanes & (lanes - 1)) lanes &= lanes - 1;
+    while (tp < lanes && tp < std::min(n_new, bs)) tp *= 2;
+    const unsigned z = head_splits(p, c.touched * c.n_layers_in, (n_rows + lanes / tp - 1) / (lanes / tp));
+    const dim3 grid((unsigned)std::min<int64_t>(c.touched, (int64_t)p->sm_count * 64), (unsigned)c.n_layers_in, z);
+    return with_words(p, words, s, fill, [&](auto args) -> int {
+        using A = decltype(args);
+        if (p->dtype == DENDRITE_FP8)
+            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, A>, grid, dim3(128), 0, s, args, a));
+        else if (p->dtype == DENDRITE_BF16)
+            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, false, A>, grid, dim3(128), 0, s, args, a));
+        else
+            DENDRITE_CUDA(launch_pdl(k_append_rows<float, false, A>, grid, dim3(128), 0, s, args, a));
+        return DENDRITE_OK;
+    });
+}
+
+}  // namespace dendrite
+
+extern "C" {
+
+int dendrite_rope_init(dendrite_rope* r, int32_t rot_dim, int32_t interleaved, double base, int32_t scaling,
+                       double factor, double original_len, double turns_low, double turns_high) {
+    if (!r || rot_dim < 16 || rot_dim > 256 || rot_dim % 16) return DENDRITE_EINVAL;
+    if (interleaved != 0 && interleaved != 1) return DENDRITE_EINVAL;
+    if (!(base > 1.0) || !std::isfinite(base)) return DENDRITE_EINVAL;
+    if (scaling < DENDRITE_ROPE_PLAIN || scaling > DENDRITE_ROPE_BANDS) return DENDRITE_EINVAL;
+    if (scaling != DENDRITE_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return DENDRITE_EINVAL;
+    const bool banded = scaling == DENDRITE_ROPE_YARN || scaling == DENDRITE_ROPE_BANDS;
+    if (banded && (!(original_len > 0.0) || !std::isfinite(original_len) || !(turns_low > 0.0) ||
+                   !(turns_high > turns_low) || !std::isfinite(turns_high)))
+        return DENDRITE_EINVAL;
+    std::memset(r, 0, sizeof(*r));
+    r->rot_dim = rot_dim;
+    r->interleaved = interleaved;
+    r->scale = scaling == DENDRITE_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    const double two_pi = 6.283185307179586476925;
+    const double b = scaling == DENDRITE_ROPE_NTK ? base * std::pow(factor, rot_dim / (rot_dim - 2.0)) : base;
+    // the pair that makes `turns` turns over the original length, as a real index
+    auto pair_of = [&](double turns) { return rot_dim * std::log(original_len / (turns * two_pi)) / (2.0 * std::log(base)); };
+    double low = 0.0, high = 0.0;
+    if (scaling == DENDRITE_ROPE_YARN) {
+        low = std::max(std::floor(pair_of(turns_high)), 0.0);
+        high = std::min(std::ceil(pair_of(turns_low)), rot_dim - 1.0);
+    }
+    for (int32_t i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(b, -2.0 * i / rot_dim);
+        double stretched = 0.0;   // share of the pair that is slowed down by factor
+        if (scaling == DENDRITE_ROPE_LINEAR) stretched = 1.0;
+        if (scaling == DENDRITE_ROPE_YARN)
+            stretched = std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+        if (scaling == DENDRITE_ROPE_BANDS) {
+            const double turns = original_len * f / two_pi;
+            stretched = 1.0 - std::min(std::max((turns - turns_low) / (turns_high - turns_low), 0.0), 1.0);
+        }
+        r->inv_freq[i] = stretched > 0.0 ? stretched * f / factor + (1.0 - stretched) * f : f;
+    }
+    return DENDRITE_OK;
+}
+
+int dendrite_read_kv(dendrite_pool* p, int32_t layer, const int32_t* branches, const int32_t* starts,
+                     const int32_t* counts, int32_t n, void* K, void* V, void* stream) {
+    if (!p) return DENDRITE_EINVAL;
+    if (p->poisoned) return p->poisoned;
+    if (p->dtype == DENDRITE_TURBO) return DENDRITE_EDTYPE;
+    if (layer < 0 || layer >= p->n_layers) return DENDRITE_EINVAL;
+    if (p->pending.active && !p->pending.layer_done[layer]) return DENDRITE_EINVAL;
+    if (n < 0 || (n > 0 && (!branches || !starts || !counts))) return DENDRITE_EINVAL;
+    const int32_t bs = p->block_size;
+    int64_t rows = 0, tiles = 0;
+    int32_t uniform = -1;
+    for (int32_t i = 0; i < n; ++i) {
+        DENDRITE_TRY(check_live(p, branches[i]));
+        if (starts[i] < 0 || counts[i] < 0 || (int64_t)starts[i] + counts[i] > p->br[branches[i]].len) return DENDRITE_EINVAL;
+        const int32_t k = counts[i] ? (starts[i] + counts[i] - 1) / bs - starts[i] / bs + 1 : 0;
+        rows += counts[i];
+        tiles += k;
+        uniform = uniform < 0 ? k : (uniform == k ? k : 0);
+    }
+    if (rows == 0) return DENDRITE_OK;
+    if (rows > INT32_MAX / 2 || tiles > INT32_MAX / 2) return DENDRITE_ELIMIT;
+    if (!K || !V || (((uintptr_t)K | (uintptr_t)V) & 15)) return DENDRITE_EINVAL;
+    const size_t bytes = (size_t)rows * p->n_kv * p->head_dim * p->elt;
+    if (overlap(K, bytes, V, bytes)) return DENDRITE_EINVAL;
+    DENDRITE_CUDA(cudaSetDevice(p->device));
+    cudaStream_t s = (cudaStream_t)stream;
+    DENDRITE_TRY(check_not_capturing(s));
+    ReadArgs a{};
+    a.n = n;
+    a.bpb = p->bpb;
+    a.n_kv = p->n_kv;
+    a.dim = p->head_dim;
+    a.n_blocks = (int32_t)p->num_blocks;
+    a.uniform = std::max(uniform, 0);
+    a.n_tiles = (int32_t)tiles;
+    a.table = p->d_table;
+    a.kp = static_cast<const char*>(p->d_k) + (size_t)layer * p->layer_bytes;
+    a.vp = static_cast<const char*>(p->d_v) + (size_t)layer * p->layer_bytes_v;
+    a.K = K;
+    a.V = V;
+    a.meta = p->d_meta;
+    auto fill = [&](int32_t* w) {
+        int32_t row = 0, tile = 0;
+        for (int32_t i = 0; i < n; ++i) {
+            w[i] = branches[i];
+            w[n + i] = starts[i];
+            w[2 * (size_t)n + i] = row;
+            w[3 * (size_t)n + i] = tile;
+            w[4 * (size_t)n + i] = counts[i];
+            row += counts[i];
+            tile += counts[i] ? (starts[i] + counts[i] - 1) / bs - starts[i] / bs + 1 : 0;
+        }
+    };
+    const int64_t per_tile = (int64_t)bs * 2 * p->n_kv * p->head_dim / 8;   // 8-element moves
+    const dim3 grid((unsigned)std::min<int64_t>(tiles, (int64_t)p->sm_count * 64), 1,
+                    head_splits(p, tiles, std::max<int64_t>(1, per_tile / 256)));
+    return with_words(p, 5 * (size_t)n, s, fill, [&](auto args) -> int {
+        using A = decltype(args);
+        if (p->dtype == DENDRITE_FP8)
+            DENDRITE_CUDA(launch_pdl(k_read_rows<__nv_bfloat16, true, A>, grid, dim3(128), 0, s, args, a));
+        else if (p->dtype == DENDRITE_BF16)
+            DENDRITE_CUDA(launch_pdl(k_read_rows<__nv_bfloat16, false, A>, grid, dim3(128), 0, s, args, a));
+        else
+            DENDRITE_CUDA(launch_pdl(k_read_rows<float, false, A>, grid, dim3(128), 0, s, args, a));
+        return DENDRITE_OK;
+    });
+}
+
+int dendrite_accept_draft(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n_draft,
+                          const int32_t* n_keep, const int32_t* nodes, void* stream) {
+    if (!p) return DENDRITE_EINVAL;
+    if (p->poisoned) return p->poisoned;
+    if (p->dtype == DENDRITE_TURBO) return DENDRITE_EDTYPE;
+    if (p->pending.active) return DENDRITE_EINVAL;
+    if (n < 0 || n_draft < 0 || n_draft > kMaxDraft || (n > 0 && (!branches || !n_keep))) return DENDRITE_EINVAL;
+    if (n == 0) return DENDRITE_OK;
+    int64_t total = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        DENDRITE_TRY(check_live(p, branches[i]));
+        const Branch& b = p->br[branches[i]];
+        if (b.len < n_draft || n_keep[i] < 0 || n_keep[i] > n_draft) return DENDRITE_EINVAL;
+        total += n_keep[i];
+    }
+    {
+        std::vector<int32_t> o(branches, branches + n);
+        std::sort(o.begin(), o.end());
+        if (std::adjacent_find(o.begin(), o.end()) != o.end()) return DENDRITE_EINVAL;
+    }
+    if (total > 0 && !nodes) return DENDRITE_EINVAL;
+    std::vector<int32_t> new_lens(n);
+    bool moves = false;
+    const int32_t* nd = nodes;
+    for (int32_t i = 0; i < n; ++i) {
+        const Branch& b = p->br[branches[i]];
+        const int32_t base = b.len - n_draft;
+        bool mine = false;
+        for (int32_t k = 0; k < n_keep[i]; ++k) {
+            if (nd[k] < 0 || nd[k] >= n_draft || (k && nd[k] <= nd[k - 1])) return DENDRITE_EINVAL;
+            mine |= nd[k] != k;
+        }
+        if (mine) {
+            // rows move in place: the drafted blocks must be this branch's
+            // own, so no fork may stand behind the base (this branch forked
+            // or rolled back there, or a child forked there)
+            const Node& nde = p->nodes[b.node];
+            if (nde.fork_len > base) return DENDRITE_EINVAL;
+            for (int32_t c = nde.first_child; c >= 0; c = p->nodes[c].next_sib)
+                if (p->nodes[c].fork_len > base) return DENDRITE_EINVAL;
+        }
+        moves |= mine;
+        new_lens[i] = base + n_keep[i];
+        nd += n_keep[i];
+    }
+    DENDRITE_CUDA(cudaSetDevice(p->device));
+    cudaStream_t s = (cudaStream_t)stream;
+    DENDRITE_TRY(check_not_capturing(s));
+    if (moves) {
+        KeepArgs a{};
+        a.n = n;
+        a.bpb = p->bpb;
+        a.n_kv = p->n_kv;
+        a.n_blocks = (int32_t)p->num_blocks;
+        a.fp8 = p->dtype == DENDRITE_FP8;
+        a.words = a.fp8 ? kFp8Dim / 16 : p->head_dim * p->elt / 16;
+        a.tile_bytes = (int64_t)(p->layer_bytes / p->num_blocks / p->n_kv);
+        a.pool_layer = (int64_t)p->layer_bytes;
+        a.table = p->d_table;
+        a.kp = static_cast<char*>(p->d_k);
+        a.vp = static_cast<char*>(p->d_v);
+        a.meta = p->d_meta;
+        const size_t words = 4 * (size_t)n + (size_t)(total + 3) / 4;
+        auto fill = [&](int32_t* w) {
+            int32_t acc = 0;
+            w[words - 1] = 0;
+            uint8_t* bytes = reinterpret_cast<uint8_t*>(w + 4 * (size_t)n);
+            for (int32_t i = 0; i < n; ++i) {
+                w[i] = branches[i];
+                w[n + i] = p->br[branches[i]].len - n_draft;
+                w[2 * (size_t)n + i] = n_keep[i];
+                w[3 * (size_t)n + i] = acc;
+                for (int32_t k = 0; k < n_keep[i]; ++k) bytes[acc + k] = (uint8_t)nodes[acc + k];
+                acc += n_keep[i];
+            }
+        };
+        DENDRITE_TRY(with_words(p, words, s, fill, [&](auto args) -> int {
+            DENDRITE_CUDA(launch_pdl(k_keep_rows<decltype(args)>, dim3((unsigned)n, (unsigned)p->n_kv, (unsigned)p->n_layers),
+                                     dim3(128), 0, s, args, a));
+            return DENDRITE_OK;
+        }));
+    }
+    return dendrite_truncate(p, branches, new_lens.data(), n, stream);
+}
+
+}  // extern "C"

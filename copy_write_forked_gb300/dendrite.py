@@ -17,7 +17,7 @@ import torch
 
 from . import _build
 
-__all__ = ["lib", "Pool", "DendriteError", "ERRORS", "plan_segments", "TIMING_NAMES"]
+__all__ = ["lib", "Pool", "Rope", "DendriteError", "ERRORS", "plan_segments", "TIMING_NAMES"]
 
 ERRORS = {
     -1: "EINVAL", -2: "ENOMEM", -3: "EBADHANDLE", -4: "ELIMIT", -5: "EDTYPE",
@@ -25,8 +25,11 @@ ERRORS = {
 }
 TIMING_NAMES = ("fork", "append_meta", "append_copy", "attn_partial", "attn_merge", "free", "attn_total",
                 "attn_tc", "attn_mma_side")
-FP32, BF16, TURBO = 0, 1, 2
+FP32, BF16, TURBO, FP8 = 0, 1, 2, 3
 TURBO_KEY_BYTES, TURBO_VALUE_BYTES = 96, 64
+FP8_TILE_BYTES = 16 * 128 + 16   # 16 slots of 128 codes, then their exponent bytes
+MAX_DRAFT = 64
+ROPE_SCALINGS = ("none", "linear", "ntk", "yarn", "bands")
 
 _LIB = None
 _i32 = ctypes.c_int32
@@ -46,6 +49,11 @@ class _Opts(ctypes.Structure):
     _fields_ = [("max_branches", _i32), ("max_blocks_per_branch", _i32), ("tc_min_rows", _i32),
                 ("n_layers", _i32), ("fold_segments", _i32), ("device_planning", _i32), ("tc_sms", _i32), ("pack_segments", _i32),
                 ("reserved", _i32 * 1)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", _i32), ("interleaved", _i32), ("reserved", _i32 * 2), ("scale", ctypes.c_double),
+                ("inv_freq", ctypes.c_double * 128)]
 
 
 class _PlanStats(ctypes.Structure):
@@ -73,6 +81,13 @@ _SIGS = {
     "dendrite_append_kv": [_p, _pi32, _i32, _i32, _p, _p, _p],
     "dendrite_append_begin": [_p, _pi32, _i32, _i32, _p],
     "dendrite_append_layer": [_p, _i32, _p, _p, _p],
+    "dendrite_rope_init": [ctypes.POINTER(_Rope), _i32, _i32, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double,
+                           ctypes.c_double, ctypes.c_double],
+    "dendrite_append_rope": [_p, _pi32, _i32, _i32, _pi32, _i32, _p, _p, _p, _i32, _p, _p, _p],
+    "dendrite_append_layer_rope": [_p, _i32, _pi32, _i32, _p, _p, _p, _i32, _p, _p, _p],
+    "dendrite_tree_attn_draft": [_p, _i32, _p, _i32, _i32, _pi32, _i32, _pi32, _i32, _p, _p],
+    "dendrite_accept_draft": [_p, _pi32, _i32, _i32, _pi32, _pi32, _p],
+    "dendrite_read_kv": [_p, _i32, _pi32, _pi32, _pi32, _i32, _p, _p, _p],
     "dendrite_tree_attn_decode_layer": [_p, _i32, _p, _i32, _i32, _pi32, _i32, _p, _p],
     "dendrite_read_block_layer": [_p, _i32, _i32, _p, _p, _p],
     "dendrite_pool_layers": [_p, _pi32],
@@ -150,7 +165,64 @@ def _stream_ptr(stream, device_index: int = 0) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-_DT = {torch.float32: FP32, torch.bfloat16: BF16}
+_DT = {torch.float32: FP32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8}
+
+
+def _trees(parents, n: int, t: int):
+    """Draft trees as (keep-alive buffer, address, n_trees): int32 CPU tensor, or
+    sequence, of t parents (one tree for every branch) or n lists of t."""
+    if parents is None:
+        return None, None, 0
+    if not isinstance(parents, torch.Tensor):
+        parents = torch.tensor(parents, dtype=torch.int32)
+    if parents.is_cuda or parents.dtype != torch.int32 or not parents.is_contiguous():
+        raise DendriteError(-1, "parents must be a contiguous int32 CPU tensor")
+    shape = tuple(parents.shape)
+    if shape == (t,):
+        return parents, parents.data_ptr(), 1
+    if shape == (n, t):
+        return parents, parents.data_ptr(), n
+    raise DendriteError(-1, f"parents shape {shape}")
+
+
+class Rope:
+    """Rotary positions for :meth:`Pool.append_rope` (``dendrite_rope``).
+
+    The first ``rot_dim`` elements of a head turn in pairs (i, i + rot_dim/2),
+    or (2 i, 2 i + 1) with ``interleaved``.  ``scaling`` stretches the
+    frequencies for long contexts: "linear", "ntk", "yarn" or "bands" (by
+    ``factor``; the last two from ``original_len`` positions, with a ramp
+    between ``turns_low`` and ``turns_high`` turns, by default 1 and 32 for
+    "yarn", 1 and 4 for "bands").  ``inv_freq``: radians per position of each
+    pair instead; ``scale``: the factor on turned elements."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, original_len: float = 0.0, turns_low: float = 1.0,
+                 turns_high: Optional[float] = None, inv_freq: Optional[Sequence[float]] = None,
+                 scale: Optional[float] = None):
+        if scaling not in ROPE_SCALINGS:
+            raise DendriteError(-1, f"scaling {scaling!r}")
+        self._c = _Rope()
+        high = turns_high if turns_high is not None else (32.0 if scaling == "yarn" else 4.0)
+        _check(lib().dendrite_rope_init(ctypes.byref(self._c), int(rot_dim), 1 if interleaved else 0, float(base),
+                                        ROPE_SCALINGS.index(scaling), float(factor), float(original_len),
+                                        float(turns_low), float(high)), "rope_init")
+        if inv_freq is not None:
+            if len(inv_freq) != self._c.rot_dim // 2:
+                raise DendriteError(-1, "inv_freq length")
+            for i, f in enumerate(inv_freq):
+                self._c.inv_freq[i] = float(f)
+        if scale is not None:
+            self._c.scale = float(scale)
+        self._ptr = ctypes.addressof(self._c)
+
+    @property
+    def inv_freq(self) -> List[float]:
+        return list(self._c.inv_freq[:self._c.rot_dim // 2])
+
+    @property
+    def scale(self) -> float:
+        return self._c.scale
 
 
 class Pool:
@@ -163,16 +235,21 @@ class Pool:
                  pack_segments: int = 0):
         """``turbo``: (rotation signs [128], QJL matrix [128][128]) to store
         compressed blocks (dendrite_pool_create_turbo); the calls then take
-        bf16 tensors."""
+        bf16 tensors.  ``dtype=torch.float8_e4m3fn``: 8-bit blocks
+        (DENDRITE_FP8); the calls take bf16 tensors too."""
         if dtype not in _DT or (turbo is not None and dtype != torch.bfloat16):
             raise DendriteError(-5, f"dtype {dtype}")
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None else
                                    torch.device(device).index or 0)
         self.num_blocks, self.block_size = int(num_blocks), int(block_size)
-        self.n_kv_heads, self.head_dim, self.dtype = int(n_kv_heads), int(head_dim), dtype
+        # the dtype of the calls' tensors: an 8-bit pool takes bf16
+        self.fp8 = dtype == torch.float8_e4m3fn
+        self.n_kv_heads, self.head_dim = int(n_kv_heads), int(head_dim)
+        self.dtype = torch.bfloat16 if self.fp8 else dtype
         opts = _Opts(int(max_branches), int(max_blocks_per_branch), int(tc_min_rows), int(n_layers),
                      int(fold_segments), int(device_planning), int(tc_sms), int(pack_segments))
         self.n_layers = int(n_layers)
+        self._max_len = int(max_blocks_per_branch or 4096) * self.block_size
         self.turbo = turbo is not None
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
@@ -255,6 +332,8 @@ class Pool:
     def _check_tensor(self, t: torch.Tensor, name: str) -> None:
         if not t.is_cuda or t.dtype != self.dtype or not t.is_contiguous():
             raise DendriteError(-1, f"{name} must be a contiguous {self.dtype} CUDA tensor")
+        if t.get_device() != self._dev:
+            raise DendriteError(-1, f"{name} is on another device than the pool")
 
     def append_kv(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, stream=None) -> None:
         """K, V: ``[n_branches][n_new][n_kv_heads][head_dim]``; for a pool of
@@ -286,6 +365,104 @@ class Pool:
             raise DendriteError(-1, f"K/V shape {tuple(K.shape)}")
         _check(lib().dendrite_append_layer(self._h, int(layer), K.data_ptr(), V.data_ptr(),
                                            _stream_ptr(stream, self._dev)), "append_layer")
+
+    def _rotated(self, K, V, rope, Q, out, lead, n, n_new):
+        """Shapes of a rotating append; returns (Q address, query heads, output)."""
+        self._check_tensor(K, "K")
+        self._check_tensor(V, "V")
+        if not isinstance(rope, Rope):
+            raise DendriteError(-1, "rope must be a Rope")
+        want = lead + (n, n_new, self.n_kv_heads, self.head_dim)
+        if tuple(K.shape) != want or K.shape != V.shape:
+            raise DendriteError(-1, f"K/V shape {tuple(K.shape)}")
+        if Q is None:
+            return None, 0, None
+        self._check_tensor(Q, "Q")
+        if Q.dim() != len(want) or Q.shape[:-2] != K.shape[:-2] or Q.shape[-1] != self.head_dim:
+            raise DendriteError(-1, f"Q shape {tuple(Q.shape)}")
+        if out is None:
+            out = torch.empty_like(Q)
+        self._check_tensor(out, "out")
+        if out.shape != Q.shape:
+            raise DendriteError(-1, "out shape")
+        return Q.data_ptr(), Q.shape[-2], out
+
+    def append_rope(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, rope: Rope,
+                    Q: Optional[torch.Tensor] = None, parents=None, out: Optional[torch.Tensor] = None,
+                    stream=None) -> Optional[torch.Tensor]:
+        """:meth:`append_kv` with K turned by its positions; Q
+        ``[n_branches][n_new][n_q_heads][head_dim]`` (layers first in a pool of
+        several) is turned too and returned (``out`` may be Q).  ``parents``:
+        the new tokens are draft trees (int32 ``[n_new]`` for every branch or
+        ``[n_branches][n_new]``, -1 or an earlier index), token j at its depth."""
+        nb, n_new = len(branches), K.shape[-3] if K.dim() >= 4 else 0
+        lead = () if self.n_layers == 1 else (self.n_layers,)
+        qp, nq, out = self._rotated(K, V, rope, Q, out, lead, nb, n_new)
+        keep, pp, nt = _trees(parents, nb, n_new)
+        ba = _arr(branches)
+        _check(lib().dendrite_append_rope(self._h, _ptr(ba), nb, n_new, pp, nt, K.data_ptr(), V.data_ptr(), qp, nq,
+                                          out.data_ptr() if qp is not None else None, rope._ptr,
+                                          _stream_ptr(stream, self._dev)), "append_rope")
+        return out
+
+    def append_layer_rope(self, layer: int, K: torch.Tensor, V: torch.Tensor, rope: Rope,
+                          Q: Optional[torch.Tensor] = None, parents=None, out: Optional[torch.Tensor] = None,
+                          stream=None) -> Optional[torch.Tensor]:
+        """:meth:`append_layer` with the rotation of :meth:`append_rope`."""
+        nb, n_new = (K.shape[0], K.shape[1]) if K.dim() == 4 else (0, 0)
+        qp, nq, out = self._rotated(K, V, rope, Q, out, (), nb, n_new)
+        keep, pp, nt = _trees(parents, nb, n_new)
+        _check(lib().dendrite_append_layer_rope(self._h, int(layer), pp, nt, K.data_ptr(), V.data_ptr(), qp, nq,
+                                                out.data_ptr() if qp is not None else None, rope._ptr,
+                                                _stream_ptr(stream, self._dev)), "append_layer_rope")
+        return out
+
+    def tree_attn_draft(self, Q: torch.Tensor, branches: Sequence[int], parents, out: Optional[torch.Tensor] = None,
+                        stream=None, layer: int = 0) -> torch.Tensor:
+        """Attention of draft trees: Q ``[n_branches][n_draft][n_q_heads][head_dim]``
+        are each branch's last n_draft tokens; token j sees what stands before
+        the drafts, its ancestors and itself (``parents`` as in :meth:`append_rope`)."""
+        self._check_tensor(Q, "Q")
+        if Q.dim() != 4 or Q.shape[0] != len(branches) or Q.shape[3] != self.head_dim:
+            raise DendriteError(-1, f"Q shape {tuple(Q.shape)}")
+        if out is None:
+            out = torch.empty_like(Q)
+        self._check_tensor(out, "out")
+        if out.shape != Q.shape:
+            raise DendriteError(-1, "out shape")
+        keep, pp, nt = _trees(parents, len(branches), Q.shape[1])
+        ba = _arr(branches)
+        _check(lib().dendrite_tree_attn_draft(self._h, int(layer), Q.data_ptr(), Q.shape[2], Q.shape[1], _ptr(ba),
+                                              len(branches), pp, nt, out.data_ptr(), _stream_ptr(stream, self._dev)),
+               "tree_attn_draft")
+        return out
+
+    def accept_draft(self, branches: Sequence[int], n_draft: int, keep: Sequence[Sequence[int]], stream=None) -> None:
+        """Of each branch's last ``n_draft`` tokens keep the nodes ``keep[i]``
+        (ascending: an accepted path) as its next tokens and drop the others."""
+        if len(keep) != len(branches):
+            raise DendriteError(-1, "branches / keep length")
+        ba, ca = _arr(branches), _arr([len(k) for k in keep])
+        na = _arr([j for k in keep for j in k])
+        _check(lib().dendrite_accept_draft(self._h, _ptr(ba), len(branches), int(n_draft), _ptr(ca), _ptr(na),
+                                           _stream_ptr(stream, self._dev)), "accept_draft")
+
+    def read_kv(self, branches: Sequence[int], starts: Sequence[int], counts: Sequence[int], stream=None,
+                layer: int = 0):
+        """K and V of positions ``starts[i] .. starts[i] + counts[i] - 1`` of each
+        branch, one branch after the other: two ``[sum counts][n_kv_heads][head_dim]``."""
+        if len(branches) != len(starts) or len(branches) != len(counts):
+            raise DendriteError(-1, "branches / starts / counts length")
+        ba, sa, ca = _arr(branches), _arr(starts), _arr(counts)
+        total = sum(counts)
+        if total > len(branches) * self._max_len:   # past any branch: refused before the rows are allocated
+            raise DendriteError(-1, "read_kv counts")
+        shape = (max(0, total), self.n_kv_heads, self.head_dim)
+        k = torch.empty(shape, dtype=self.dtype, device=self.device)
+        v = torch.empty(shape, dtype=self.dtype, device=self.device)
+        _check(lib().dendrite_read_kv(self._h, int(layer), _ptr(ba), _ptr(sa), _ptr(ca), len(branches), k.data_ptr(),
+                                      v.data_ptr(), _stream_ptr(stream, self._dev)), "read_kv")
+        return k, v
 
     def tree_attn_decode(self, Q: torch.Tensor, branches: Sequence[int], out: Optional[torch.Tensor] = None,
                          stream=None, layer: int = 0) -> torch.Tensor:
@@ -371,11 +548,14 @@ class Pool:
 
     def read_block(self, blk: int, stream=None, layer: int = 0):
         """K and V of a block: [n_kv_heads][block_size][head_dim] in the pool
-        dtype, or the raw records ([...][96] and [...][64] uint8) of a
-        compressed pool."""
+        dtype, the raw records ([...][96] and [...][64] uint8) of a
+        compressed pool, or the tiles ([n_kv_heads][2064] uint8) of an 8-bit one."""
         if self.turbo:
             k = torch.empty((self.n_kv_heads, self.block_size, TURBO_KEY_BYTES), dtype=torch.uint8)
             v = torch.empty((self.n_kv_heads, self.block_size, TURBO_VALUE_BYTES), dtype=torch.uint8)
+        elif self.fp8:
+            k = torch.empty((self.n_kv_heads, FP8_TILE_BYTES), dtype=torch.uint8)
+            v = torch.empty((self.n_kv_heads, FP8_TILE_BYTES), dtype=torch.uint8)
         else:
             shape = (self.n_kv_heads, self.block_size, self.head_dim)
             k = torch.empty(shape, dtype=self.dtype)

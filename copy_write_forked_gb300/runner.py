@@ -75,10 +75,10 @@ def _max_len(w) -> int:
     return top
 
 
-def pool_for(w, extra_blocks: int = 16, max_branches: Optional[int] = None, **kw) -> Pool:
-    """A pool sized for workload ``w``."""
+def pool_for(w, extra_blocks: int = 16, max_branches: Optional[int] = None, dtype=None, **kw) -> Pool:
+    """A pool sized for workload ``w`` (``dtype``: of the pool, where it is not the rows')."""
     nb = max(1, w.blocks_upper_bound() + extra_blocks)
     mb = max_branches or max(16, w.n_branch_ids() + 8)
     bpb = max(16, -(-_max_len(w) // w.block_size) + 4)
-    return Pool(nb, w.block_size, w.n_kv_heads, w.head_dim, w.dtype, max_branches=mb,
+    return Pool(nb, w.block_size, w.n_kv_heads, w.head_dim, dtype or w.dtype, max_branches=mb,
                 max_blocks_per_branch=bpb, **kw)

@@ -67,6 +67,8 @@ extern "C" {
 #define DENDRITE_BF16  1   /* bf16 K/V/Q/out; attention on tensor cores, fp32 accumulate */
 #define DENDRITE_TURBO 2   /* compressed blocks (dendrite_pool_create_turbo): bf16 K/V/Q/out
                             * in the calls, TurboQuant records in the pool               */
+#define DENDRITE_FP8   3   /* 8-bit blocks: bf16 K/V/Q/out in the calls, e4m3 codes with a  *
+                            * power-of-two scale per (token, KV head) row in the pool      */
 
 typedef struct dendrite_pool dendrite_pool;
 
@@ -119,12 +121,21 @@ typedef struct dendrite_pool_opts {
  *   num_blocks  > 0: number of KV blocks.
  *   block_size  tokens per block; 16 (the attention kernels' tile height).
  *   n_kv_heads  KV heads per token (1..64).
- *   head_dim    bf16: 128.  fp32: a multiple of 32, at most 256.
- *   dtype       DENDRITE_FP32 or DENDRITE_BF16.
+ *   head_dim    bf16 and fp8: 128.  fp32: a multiple of 32, at most 256.
+ *   dtype       DENDRITE_FP32, DENDRITE_BF16 or DENDRITE_FP8.
  * Device layout: K and V pools are [n_layers][num_blocks][n_kv_heads][block_size][head_dim]
  * (one (block, head) tile is contiguous); refcount int32[num_blocks]; the free
  * stack int32[num_blocks] starts as [num_blocks-1, ..., 0] so block 0 is handed
  * out first; block tables int32[max_branches][max_blocks_per_branch] (-1 = empty).
+ * 8-bit pools (DENDRITE_FP8) quantise every row of 128 as it is appended: e is
+ * the least integer >= -127 with max|x| <= 448 * 2^e over the row's finite
+ * elements, and x is stored as the e4m3 number nearest to x * 2^-e (ties to
+ * even; at most 240 where e = 120, so that it reads back finite; a NaN or an
+ * infinity as NaN).  A (block, head) tile is 2,064 bytes: 16
+ * slots of 128 codes, the 16-byte chunk c of slot s at chunk c ^ (s & 7), then
+ * the 16 slots' exponent bytes e + 127.  129 bytes per row instead of bf16's
+ * 256; a row reads back as code * 2^e, which bf16 holds exactly, and attention
+ * reads those values.
  * Synchronous.  Uses the current CUDA device.
  */
 int dendrite_pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads,
@@ -236,6 +247,71 @@ int dendrite_append_begin(dendrite_pool* pool, const int32_t* branches, int32_t 
 int dendrite_append_layer(dendrite_pool* pool, int32_t layer, const void* K, const void* V, void* stream);
 
 /*
+ * Rotary positions, applied as rows are appended (no counterpart on the
+ * pages).  Pair i of a head turns by position * inv_freq[i] radians:
+ *     y1 = scale (x1 cos a - x2 sin a),   y2 = scale (x2 cos a + x1 sin a),
+ * the pair being elements (i, i + rot_dim/2) of the head, or (2 i, 2 i + 1)
+ * when interleaved.  Elements from rot_dim on pass unchanged.  Angles are
+ * reduced exactly (64-bit fixed point), however far the position.
+ * The struct is plain data: fill it by hand or with dendrite_rope_init.
+ */
+typedef struct dendrite_rope {
+    int32_t rot_dim;      /* leading elements of each head that turn: a multiple of 16, at most head_dim */
+    int32_t interleaved;  /* 0: halves, 1: neighbours                                          */
+    int32_t reserved[2];  /* must be zero                                                       */
+    double  scale;        /* factor on the turned elements of K and of Q (1 = none)             */
+    double  inv_freq[128];/* radians per position of pair i < rot_dim / 2                       */
+} dendrite_rope;
+
+#define DENDRITE_ROPE_PLAIN  0  /* f_i = base^(-2 i / rot_dim)                                   */
+#define DENDRITE_ROPE_LINEAR 1  /* f_i / factor                                                  */
+#define DENDRITE_ROPE_NTK    2  /* base * factor^(rot_dim / (rot_dim - 2)) in place of base      */
+#define DENDRITE_ROPE_YARN   3  /* between f_i / factor and f_i by a ramp over the pair index,   *
+                                 * from the pair of turns_high turns (rounded down) to that of   *
+                                 * turns_low (rounded up); scale = 0.1 ln(factor) + 1            */
+#define DENDRITE_ROPE_BANDS  4  /* between f_i / factor and f_i by a ramp over the pair's turns, *
+                                 * from turns_low to turns_high                                  */
+
+/*
+ * Fills *rope.  base > 1; factor >= 1 for every scaling but PLAIN; original_len
+ * (positions the model was trained on) and 0 < turns_low < turns_high (turns a
+ * pair makes over original_len) for YARN and BANDS: usually 1 and 32, 1 and 4.
+ * rot_dim: a multiple of 16 up to 256.  Host only.
+ */
+int dendrite_rope_init(dendrite_rope* rope, int32_t rot_dim, int32_t interleaved, double base, int32_t scaling,
+                       double factor, double original_len, double turns_low, double turns_high);
+
+/*
+ * dendrite_append_kv with K (not V) turned on the way into the blocks, and the
+ * step's queries turned beside it: token j of branch i is at position
+ * len_i + j, or, with draft trees, len_i + depth of node j (0 for a child of
+ * the last accepted token).
+ *   parents:  host int32[n_trees][n_new], or NULL with n_trees = 0.  n_trees is
+ *             1 (one tree for every branch) or n_branches; parents[j] is the
+ *             index of token j's parent, in [-1, j), -1 for the last accepted
+ *             token; n_new <= 64 (DENDRITE_MAX_DRAFT).  A batch whose trees
+ *             differ in size is padded with nodes that nothing hangs on.
+ *   Q, q_out: device, [n_layers][n_branches][n_new][n_q_heads][head_dim] in the
+ *             dtype of K (no layer dimension in a one-layer pool); q_out may be
+ *             Q itself, but may not overlap it otherwise.  Q NULL: keys alone.
+ *   rope:     host; read during the call.
+ * Products are taken in fp32 and rounded once, to the row's stored type.
+ * DENDRITE_TURBO pools return DENDRITE_EDTYPE.  Otherwise as dendrite_append_kv.
+ * dendrite_append_layer_rope is dendrite_append_layer's turn of the same: layer
+ * `layer` of the pending append (Q without a layer dimension).
+ * These two and the draft and read calls below return DENDRITE_EINVAL on a
+ * stream that is being captured into a graph (a replay would use the lengths
+ * and tables of the capture).
+ */
+#define DENDRITE_MAX_DRAFT 64
+int dendrite_append_rope(dendrite_pool* pool, const int32_t* branches, int32_t n_branches, int32_t n_new,
+                         const int32_t* parents, int32_t n_trees, const void* K, const void* V, const void* Q,
+                         int32_t n_q_heads, void* q_out, const dendrite_rope* rope, void* stream);
+int dendrite_append_layer_rope(dendrite_pool* pool, int32_t layer, const int32_t* parents, int32_t n_trees,
+                               const void* K, const void* V, const void* Q, int32_t n_q_heads, void* q_out,
+                               const dendrite_rope* rope, void* stream);
+
+/*
  * Tree decode attention (Dendrite article, section 技术深度解析: attention
  * gathers keys and values from the shared ancestor path and the branch's own
  * leaf path).
@@ -278,6 +354,55 @@ int dendrite_tree_attn_decode(dendrite_pool* pool, const void* Q, int32_t n_q_he
 int dendrite_tree_attn_decode_layer(dendrite_pool* pool, int32_t layer, const void* Q, int32_t n_q_heads,
                                     int32_t q_len, const int32_t* branches, int32_t n_branches, void* out,
                                     void* stream);
+
+/*
+ * Attention of drafted tokens that form a tree (the verify step of speculative
+ * decoding, DSpark blog, section 第二层, with the drafts of a branch as one tree
+ * instead of one fork per draft path).  The last n_draft positions of every
+ * branch are its drafted tokens; query j sees every position before them, its
+ * ancestors and itself.
+ *   parents, n_trees: as for dendrite_append_rope (parents required); n_draft <= 64.
+ *   Q, out: device, [n_branches][n_draft][n_q_heads][head_dim].
+ * Otherwise as dendrite_tree_attn_decode_layer with q_len = n_draft; the trees
+ * are part of the cached plan.  A parents array of a chain (parents[j] = j - 1)
+ * gives that call's result.  As there, K and V rows have to be finite in every
+ * position a branch holds: a row a query does not see is weighed with zero.
+ * DENDRITE_TURBO pools return DENDRITE_EDTYPE.
+ */
+int dendrite_tree_attn_draft(dendrite_pool* pool, int32_t layer, const void* Q, int32_t n_q_heads, int32_t n_draft,
+                             const int32_t* branches, int32_t n_branches, const int32_t* parents, int32_t n_trees,
+                             void* out, void* stream);
+
+/*
+ * Keeps the accepted nodes of each branch's n_draft drafted tokens (its last
+ * n_draft positions) and rolls the others back: node nodes[k] of branch i's
+ * list becomes position len - n_draft + k, in every layer, and the branch then
+ * ends after its n_keep[i] kept rows.
+ *   n_keep: host int32[n_branches], 0 .. n_draft each.
+ *   nodes:  host int32[sum n_keep], the branches' lists one after the other,
+ *           each strictly ascending (a path from the root is), in [0, n_draft).
+ * Rows move in place.  A list that moves rows (nodes[k] != k) needs the drafted
+ * positions to be the branch's own: DENDRITE_EINVAL if this branch was forked
+ * or rolled back, or a live child was forked from it, at a length above
+ * len - n_draft.  n_draft <= 64.  Rotated keys keep their angles, which stay
+ * right for a path: node k of a path has depth k.
+ * DENDRITE_TURBO pools return DENDRITE_EDTYPE; not while an append is pending.
+ */
+int dendrite_accept_draft(dendrite_pool* pool, const int32_t* branches, int32_t n_branches, int32_t n_draft,
+                          const int32_t* n_keep, const int32_t* nodes, void* stream);
+
+/*
+ * Reads rows back: positions [starts[i], starts[i] + counts[i]) of each branch
+ * (any branch any number of times), one branch after the other.
+ *   K, V: device, [sum counts][n_kv_heads][head_dim] in the dtype of the append
+ *         calls (8-bit pools: code * 2^e as bf16, exactly); 16-byte aligned,
+ *         not overlapping.
+ * Layer `layer`; DENDRITE_EINVAL if a pending split append has not written it.
+ * DENDRITE_TURBO pools return DENDRITE_EDTYPE (dendrite_read_block gives their
+ * records).
+ */
+int dendrite_read_kv(dendrite_pool* pool, int32_t layer, const int32_t* branches, const int32_t* starts,
+                     const int32_t* counts, int32_t n_branches, void* K, void* V, void* stream);
 
 /*
  * Free branches (host int32[n_branches], no duplicates): every block of each
@@ -324,7 +449,7 @@ int dendrite_read_refcounts(dendrite_pool* pool, int32_t* out, void* stream);
 int dendrite_read_free_stack(dendrite_pool* pool, int32_t* out, int32_t* top_out, void* stream);
 
 /* Copy one block's K and V ([n_kv_heads][block_size][head_dim], pool dtype;
- * the records for DENDRITE_TURBO pools) to host buffers k_out / v_out
+ * the records for DENDRITE_TURBO pools, the tiles for DENDRITE_FP8) to host buffers k_out / v_out
  * (layer 0; dendrite_read_block_layer for any). */
 int dendrite_read_block(dendrite_pool* pool, int32_t block, void* k_out, void* v_out, void* stream);
 int dendrite_read_block_layer(dendrite_pool* pool, int32_t layer, int32_t block, void* k_out, void* v_out,
