@@ -1637,7 +1637,7 @@ int build_plan(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_l
     const int32_t RM = q_len * G;
     const bool bf16 = p->dtype == DENDRITE_BF16;
     const int small_rows = unit_rows_small(p);
-    const bool tc_on = bf16 && max_tc_ctas > 0 && p->tc_min_rows >= 0;
+    const bool tc_on = max_tc_ctas > 0 && p->tc_min_rows >= 0;
     const int32_t n_nodes = (int32_t)p->nodes.size();
     hp.parent.resize(n_nodes);
     hp.fork_len.resize(n_nodes);
@@ -1716,7 +1716,8 @@ int split_tc_sms(const dendrite_pool* p, int64_t w_tc, int64_t w_small, int64_t 
     constexpr double kTcNsPerWeight = 85.0, kSmallNsPerWeight = 30.0;   // SM ns
     constexpr double kHbmBytesPerNs = 6700.0;                           // measured copy bandwidth
     constexpr double kSmallBytesPerNsPerSm = 70.0;                      // one SM's two mma.sync CTAs
-    const double tile_bytes = 2.0 * p->block_size * p->head_dim * 2;   // K and V of one kv head, bf16
+    const double tile_bytes =   // K and V of one kv head
+        p->dtype == DENDRITE_FP8 ? 2.0 * kFp8TileBytes : 2.0 * p->block_size * p->head_dim * 2;
     const double A = (double)w_tc * kTcNsPerWeight, S = (double)w_small * kSmallNsPerWeight;
     const double Bt = (double)tiles_tc * tile_bytes, Bs = (double)tiles_small * tile_bytes;
     const double serial = std::max(A / sms, Bt / kHbmBytesPerNs) + std::max(S / sms, Bs / kHbmBytesPerNs);
@@ -1740,7 +1741,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
     const int32_t RM = q_len * G;
     const bool bf16 = p->dtype == DENDRITE_BF16;
     const int small_rows = unit_rows_small(p);
-    const bool tc_on = bf16 && max_tc_ctas > 0 && p->tc_min_rows >= 0;
+    const bool tc_on = max_tc_ctas > 0 && p->tc_min_rows >= 0;
     // Segments, their members and their units (kv head major, then row
     // group), tensor-core segments first: pass 0 takes the segments read by
     // more than tc_min_rows rows per kv head, pass 1 the rest.
@@ -2104,7 +2105,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
 
 // CTAs the tensor-core kernel may use on this pool (0: not used).
 int tc_ctas(const dendrite_pool* p) {
-    return (p->dtype == DENDRITE_BF16 && p->tc_ready && p->tc_min_rows >= 0) ? p->sm_count : 0;
+    return (p->tc_ready && p->tc_min_rows >= 0) ? p->sm_count : 0;
 }
 
 // The partial kernels of one attention call (tensor-core class, then the
@@ -2129,13 +2130,14 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
     // kernel's CTAs fit on their own SMs at once and the two run side by
     // side; without one the mma.sync CTAs take the SMs the tcgen05 CTAs
     // leave as they finish.
-    const bool beside = bf16 && a.plan.n_tc_ctas > 0 && a.plan.n_ctas > 0 && p->side;
+    const bool f8 = p->dtype == DENDRITE_FP8;
+    const bool beside = a.plan.n_tc_ctas > 0 && a.plan.n_ctas > 0 && p->side;
     if (beside) DENDRITE_CUDA(cudaEventRecord(p->ev_fork, s));
     // the tcgen05 kernel is submitted first, so that its CTAs are placed
     // before the side stream's
     if (a.plan.n_tc_ctas > 0) {
         prof_begin(p, T_ATTN_TC, s);
-        DENDRITE_TRY(launch_attn_tc(mk, mv, a, a.plan.n_tc_ctas, s));
+        DENDRITE_TRY(launch_attn_tc(mk, mv, a, a.plan.n_tc_ctas, f8, s));
         prof_end(p, T_ATTN_TC, s);
     } else {
         p->ev_recorded[T_ATTN_TC] = false;   // this call ran no tensor-core kernel
@@ -2143,7 +2145,9 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
     if (beside) {
         DENDRITE_CUDA(cudaStreamWaitEvent(p->side, p->ev_fork, 0));
         prof_begin(p, T_ATTN_MMA_SIDE, p->side);
-        if (a.plan.masks)
+        if (f8)
+            DENDRITE_TRY(launch_attn_fp8(a, true, p->side));
+        else if (a.plan.masks)
             k_attn_partial_bf16<true, true><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16_PACKED, p->side>>>(mk, mv, a);
         else if (a.plan.packed)
             k_attn_partial_bf16<true, false><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16_PACKED, p->side>>>(mk, mv, a);
@@ -2161,8 +2165,8 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
         // launched above
     } else if (p->dtype == DENDRITE_TURBO) {
         DENDRITE_TRY(launch_turbo_partials(a, a.Q, n_out_rows, p->d_tq_signs, p->d_tq_S, p->d_tq_qs, s));
-    } else if (p->dtype == DENDRITE_FP8) {
-        DENDRITE_TRY(launch_attn_fp8(a, s));
+    } else if (f8) {
+        DENDRITE_TRY(launch_attn_fp8(a, false, s));
     } else if (a.plan.n_ctas > 0) {
         if (bf16) {
             if (a.plan.masks)
@@ -2301,11 +2305,12 @@ int attn_setup(dendrite_pool* p) {
         DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_draft, k_attn_partial_bf16<true, true>, THREADS,
                                                                     SMEM_BF16_PACKED));
         p->attn_ctas_per_sm = std::max(1, std::min({occ, occ_packed, occ_draft}));
-        p->tc_ready = attn_tc_setup() == DENDRITE_OK;
+        p->tc_ready = attn_tc_setup(false) == DENDRITE_OK;
         DENDRITE_CUDA(cudaFuncSetAttribute(k_plan_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kMaxExpandSegs * 16));
     } else if (p->dtype == DENDRITE_FP8) {
         DENDRITE_TRY(attn_fp8_setup(&p->attn_ctas_per_sm));
+        p->tc_ready = attn_tc_setup(true) == DENDRITE_OK;
     } else if (p->dtype == DENDRITE_TURBO) {
         p->attn_ctas_per_sm = turbo_ctas_per_sm();
     } else {

@@ -82,8 +82,9 @@ struct AttnArgs {
 
 // Tensor-core (tcgen05) partial kernel for units of many query rows; see
 // attn_tc.cu.  Units of the plan's tc class, CTAs [0, n_ctas).
-int attn_tc_setup();
-int launch_attn_tc(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, cudaStream_t s);
+// f8: the pool's blocks are 8-bit (the maps are then unused).
+int attn_tc_setup(bool f8);
+int launch_attn_tc(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, bool f8, cudaStream_t s);
 
 }  // namespace dendrite
 

@@ -25,13 +25,22 @@
 //   parts the even dimensions from the odd ones, and each of the two is an
 //   operand (their accumulators interleave to four consecutive columns).
 //
-// One producer warp streams tiles with cp.async.bulk into an mbarrier ring
-// (4 tiles a stage); four consumer warps share a unit: each row tile of 16
-// rows belongs to 4, 2 or 1 warps, which then take the stage's tiles in turn
-// and combine their states at the chunk's end.
+// Four warps share a unit: each row tile of 16 rows belongs to 4, 2 or 1 of
+// them, which take the unit's tiles two at a time in turn and combine their
+// states at the chunk's end.  Every warp copies its own tiles (cp.async.bulk
+// into a ring of two slots of two tiles): the next copy into a slot is issued
+// when the warp is done with it, no warp waits for another, and the registers
+// of a copying warp go to a third CTA on the SM.  What bounds the kernel is
+// the latency of a step's chain (products, maximum over four lanes,
+// exponentials, products), so warps side by side and two tiles per step pay:
+// with a producer warp, two CTAs and one tile per step, eight warps kept up
+// with 70 % of the HBM rate.  A row tile's warps beyond one copy of the tiles
+// read them from L2 (units of more than 16 rows).
 //
 // Every mbarrier wait is bounded, as in the bf16 kernel.
 #include <cuda_fp16.h>
+
+#include <climits>
 
 #include "attn_common.cuh"
 #include "attn_fp8.h"
@@ -41,35 +50,31 @@ using namespace dendrite;
 
 namespace {
 
-constexpr int F8_STAGES = 4;
-constexpr int F8_TILES = 4;                              // tiles per stage
-constexpr int F8_SLOT = 2 * kFp8TileBytes;               // K then V of one tile
-constexpr int F8_STAGE = F8_TILES * F8_SLOT;
+constexpr int F8_TILE = 2 * kFp8TileBytes;               // K then V of one tile
+constexpr int F8_SLOT = 2 * F8_TILE;                     // two tiles
+constexpr int F8_SLOTS = 2;                              // per warp
 constexpr int F8_WARPS = 4;
-constexpr int F8_THREADS = (F8_WARPS + 1) * 32;
-constexpr int F8_COMB = F8_STAGES * F8_STAGE;            // combine buffer: 4 warps x 16 rows x 128 fp32
-constexpr int F8_ML = F8_COMB + F8_WARPS * 16 * D * 4;   // per warp and row (m, l)
+constexpr int F8_THREADS = F8_WARPS * 32;
+constexpr int F8_ML = F8_WARPS * F8_SLOTS * F8_SLOT;     // per warp and row (m, l)
 constexpr int F8_BAR = F8_ML + F8_WARPS * 16 * 8;
-constexpr size_t F8_SMEM = F8_BAR + 2 * F8_STAGES * 8;
-static_assert(F8_STAGE % 16 == 0 && F8_BAR % 8 == 0, "alignment");
+constexpr size_t F8_SMEM = F8_BAR + F8_WARPS * F8_SLOTS * 8;
+// at a chunk's end a warp leaves its 16 rows of fp32 sums in the slot it read last
+static_assert(F8_SLOT >= 16 * D * 4 && F8_SLOT % 16 == 0 && F8_BAR % 8 == 0, "layout");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
-// Two e4m3 codes to fp16, exactly.
-__device__ __forceinline__ uint32_t unpack2(uint16_t c) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-    return h;
-}
+// Four e4m3 codes to fp16, exactly.
 __device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    lo = unpack2((uint16_t)w);
-    hi = unpack2((uint16_t)(w >> 16));
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
+// (not volatile: the compiler may interleave the chains of several accumulators)
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -79,8 +84,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// 2^(byte - 127); byte 0 is the denormal 2^-127.
-__device__ __forceinline__ float exp_of(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x400000u); }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -113,102 +116,102 @@ __device__ __forceinline__ float load_q(const __nv_bfloat16* row, bool valid, in
     return scale * __uint_as_float((uint32_t)e << 23);
 }
 
+// The pairs of tiles a warp reads, in order: of every chunk of the CTA's range
+// those of its turn.
+struct PairWalk {
+    int32_t t, u, cend = 0;              // next pair's first tile; its unit; the chunk's end
+    int64_t row = 0;                     // table offset of the unit's tile 0
+    int32_t head = 0, step = 1;
+    int32_t t_next;                      // where the next chunk begins
+    __device__ __forceinline__ PairWalk(int32_t t0, int32_t u0) : t(0), u(u0 - 1), t_next(t0) {}
+    // Moves on to the chunk of the next pair; false past the range's end.
+    __device__ __forceinline__ bool more(const AttnPlanDev& pl, int32_t t_end, int32_t bpb, int warp) {
+        while (t >= cend) {
+            if (t_next >= t_end) return false;
+            const AttnUnit& U = pl.units[++u];
+            if (t_next >= U.tile_off + U.n_blk) continue;
+            cend = min(t_end, U.tile_off + U.n_blk);
+            const int P = F8_WARPS / U.rt;
+            // a row tile past the unit's rows has no warps
+            t = (warp / P) * 16 >= U.n_rows ? cend : t_next + 2 * (warp % P);
+            t_next = cend;
+            step = 2 * P;
+            row = (int64_t)U.table_row * bpb + U.blk_start - U.tile_off;
+            head = U.kv_head;
+        }
+        return true;
+    }
+};
+
 template <bool DRAFT>
-__global__ void __launch_bounds__(F8_THREADS, 2) k_attn_partial_fp8(const AttnArgs a) {
+__global__ void __launch_bounds__(F8_THREADS, 3) k_attn_partial_fp8(const AttnArgs a) {
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ int abort_flag;
-    const uint32_t base = smem_u32(sm);
-    const uint32_t bar_full = base + F8_BAR, bar_empty = bar_full + F8_STAGES * 8;
+    __shared__ int last_slot[F8_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < F8_STAGES; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, F8_WARPS);
-        }
-    }
+    const uint32_t bars = smem_u32(sm) + F8_BAR + warp * F8_SLOTS * 8;
+    if (lane < F8_SLOTS) mbar_init(bars + 8 * lane, 1);
+    // The kernels after this one are let in at each CTA's end only: let in at
+    // the start, the merge and, behind it, the next call's partial kernel take
+    // SM slots as the first CTAs here end, and that call's CTAs crowd on few
+    // SMs (8 contexts of 32,768 tokens, calls back to back: 142 us, and 98 so).
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    pdl_trigger();
     const AttnPlanDev& pl = a.plan;
     const int c = blockIdx.x;
     const int32_t t_begin = pl.cta_begin[c], t_end = pl.cta_begin[c + 1];
     const int32_t u0 = pl.cta_unit[c];
-    if (threadIdx.x == 0) {
-        abort_flag = a.meta->status != 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
+    if (threadIdx.x == 0) abort_flag = a.meta->status != 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
     if (abort_flag) return;
     volatile int* abortp = &abort_flag;
-
-    if (warp == F8_WARPS) {
-        // ------------------------------------------------------ producer
-        const char* kp = reinterpret_cast<const char*>(a.pool_k);
-        const char* vp = reinterpret_cast<const char*>(a.pool_v);
-        uint32_t issued = 0, parity_bits = 0;
-        int32_t stage = 0, t = t_begin, u = u0;
-        while (t < t_end) {
-            const AttnUnit U = pl.units[u];
-            const int32_t uend = U.tile_off + U.n_blk;
-            if (t >= uend) { ++u; continue; }
-            const int32_t cend = min(t_end, uend);
-            const int32_t* trow = a.table + (int64_t)U.table_row * a.bpb + U.blk_start - U.tile_off;
-            int32_t next = lane < F8_TILES && t + lane < cend ? trow[t + lane] : 0;
-            for (int32_t st = t; st < cend; st += F8_TILES, ++stage) {
-                const int slot = stage % F8_STAGES;
-                const uint32_t ph = (uint32_t)(stage / F8_STAGES) & 1u;
-                const int ntiles = min(F8_TILES, cend - st);
-                int32_t blk = next;
-                if (lane < F8_TILES && st + F8_TILES + lane < cend) next = trow[st + F8_TILES + lane];
-                bool ok = true;
-                if (lane == 0 && !*abortp) {
-                    ok = mbar_wait(bar_empty + 8 * slot, ph ^ 1u, abortp);
-                    if (!ok) {
-                        *abortp = 1;
-                        atomicCAS(&a.meta->status, 0, DENDRITE_ETIMEOUT);
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) && !*abortp;
-                if (!__all_sync(0xffffffffu, ok)) continue;
-                if (lane == 0) mbar_expect_tx(bar_full + 8 * slot, (uint32_t)(ntiles * F8_SLOT));
-                __syncwarp();
-                if (lane < ntiles) {
-                    if ((uint32_t)blk >= (uint32_t)a.n_blocks) {   // broken table: poison, read a valid block
-                        atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
-                        blk = 0;
-                    }
-                    const int64_t off = ((int64_t)blk * a.n_kv + U.kv_head) * kFp8TileBytes;
-                    const uint32_t dst = base + slot * F8_STAGE + lane * F8_SLOT;
-                    bulk_load(dst, kp + off, kFp8TileBytes, bar_full + 8 * slot);
-                    bulk_load(dst + kFp8TileBytes, vp + off, kFp8TileBytes, bar_full + 8 * slot);
-                }
-                issued |= 1u << slot;
-                parity_bits = (parity_bits & ~(1u << slot)) | (ph << slot);
-            }
-            t = cend;
-            ++u;
-        }
-        if (lane == 0 && *abortp) {   // copies still in flight land before the CTA exits
-            for (int s = 0; s < F8_STAGES; ++s) {
-                if (!(issued >> s & 1u)) continue;
-                const uint64_t t0 = globaltimer();
-                while (!mbar_try_wait(bar_full + 8 * s, parity_bits >> s & 1u) && globaltimer() - t0 < WAIT_LIMIT_NS) {
-                }
-            }
-        }
-        return;
-    }
-
-    // ---------------------------------------------------------- consumers
     const float NEG_INF = -INFINITY;
     const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
     float2* ml = reinterpret_cast<float2*>(sm + F8_ML);
+    unsigned char* slots = sm + warp * F8_SLOTS * F8_SLOT;
     const int q = lane & 3, g = lane >> 2;
-    int32_t stage = 0, t = t_begin, u = u0;
+
+    // ---- copies: lane i < 2 copies tile i of a pair, its block id loaded a
+    // pair before
+    PairWalk ahead(t_begin, u0);
+    int32_t blk = 0, n_ahead = 0, head_ahead = 0, issued = 0;
+    auto look = [&]() {
+        n_ahead = ahead.more(pl, t_end, a.bpb, warp) ? min(2, ahead.cend - ahead.t) : 0;
+        if (lane < n_ahead) blk = a.table[ahead.row + ahead.t + lane];
+        head_ahead = ahead.head;
+    };
+    auto issue = [&]() {
+        if (!n_ahead) return;
+        const int slot = issued & 1;
+        if (lane == 0) mbar_expect_tx(bars + 8 * slot, (uint32_t)(n_ahead * F8_TILE));
+        __syncwarp();
+        if (lane < n_ahead) {
+            if ((uint32_t)blk >= (uint32_t)a.n_blocks) {   // broken table: poison, read a valid block
+                atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
+                blk = 0;
+            }
+            const int64_t off = ((int64_t)blk * a.n_kv + head_ahead) * kFp8TileBytes;
+            const uint32_t dst = smem_u32(slots) + slot * F8_SLOT + lane * F8_TILE;
+            bulk_load(dst, reinterpret_cast<const char*>(a.pool_k) + off, kFp8TileBytes, bars + 8 * slot);
+            bulk_load(dst + kFp8TileBytes, reinterpret_cast<const char*>(a.pool_v) + off, kFp8TileBytes, bars + 8 * slot);
+        }
+        ++issued;
+        ahead.t += ahead.step;
+        look();
+    };
+    static_assert(F8_SLOTS == 2, "slots alternate");
+    look();
+    for (int i = 0; i < F8_SLOTS; ++i) issue();
+
+    int32_t done = 0;           // pairs this warp has read
+    bool ok = true;
+    int32_t t = t_begin, u = u0;
     while (t < t_end) {
-        const AttnUnit U = pl.units[u];
+        const AttnUnit& U = pl.units[u];            // read again at the chunk's end: not held over the loop
         const int32_t uend = U.tile_off + U.n_blk;
         if (t >= uend) { ++u; continue; }
         const int32_t cend = min(t_end, uend);
+        const int32_t pos_of = (U.blk_start - U.tile_off) * BS;   // position of tile st: pos_of + 16 st
         const int P = F8_WARPS / U.rt;              // warps per row tile
         const int r = warp / P, part = warp % P;
         const int row0 = r * 16 + g, row1 = row0 + 8;
@@ -221,8 +224,9 @@ __global__ void __launch_bounds__(F8_THREADS, 2) k_attn_partial_fp8(const AttnAr
             const bool v0 = row0 < U.n_rows, v1 = row1 < U.n_rows;
             const AttnRow R0 = v0 ? unit_row(pl, U, row0) : AttnRow{0, 0};
             const AttnRow R1 = v1 ? unit_row(pl, U, row1) : AttnRow{0, 0};
-            lim0 = R0.limit;
-            lim1 = R1.limit;
+            // rows past the unit's (queries of zero, results unused) mask nothing
+            lim0 = v0 ? R0.limit : INT_MAX;
+            lim1 = v1 ? R1.limit : INT_MAX;
             if (DRAFT) {
                 mask0 = v0 ? draft_mask(pl, U, row0) : 0;
                 mask1 = v1 ? draft_mask(pl, U, row1) : 0;
@@ -245,74 +249,100 @@ __global__ void __launch_bounds__(F8_THREADS, 2) k_attn_partial_fp8(const AttnAr
 #pragma unroll
         for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         float m0 = NEG_INF, m1 = NEG_INF, w0 = NEG_INF, w1 = NEG_INF, l0 = 0.f, l1 = 0.f;
+        int slot = 0;     // of the chunk's last pair, once the loop is through
 
-        for (int32_t st = t; st < cend; st += F8_TILES, ++stage) {
-            const int slot = stage % F8_STAGES;
-            const uint32_t ph = (uint32_t)(stage / F8_STAGES) & 1u;
-            const int ntiles = min(F8_TILES, cend - st);
-            const bool last = st + F8_TILES >= cend;
-            bool ok = !*abortp;
-            if (ok) {
-                ok = mbar_wait(bar_full + 8 * slot, ph, abortp);
-                if (!ok) {
+        for (int32_t st = idle ? cend : t + 2 * part; st < cend; st += 2 * P) {
+            slot = done & 1;
+            if (ok) ok = mbar_wait(bars + 8 * slot, (uint32_t)(done >> 1) & 1u, abortp);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                if (lane == 0 && !*abortp) {
                     *abortp = 1;
                     atomicCAS(&a.meta->status, 0, DENDRITE_ETIMEOUT);
                 }
+                break;
             }
-            ok = __all_sync(0xffffffffu, ok) && !*abortp;
-            ok = __all_sync(0xffffffffu, ok);
-            for (int ti = part; ok && !idle && ti < ntiles; ti += P) {
-                const unsigned char* kt = sm + slot * F8_STAGE + ti * F8_SLOT;
-                const unsigned char* vt = kt + kFp8TileBytes;
-                // S = Q C^T: token group h (8 tokens), lane's token 8 h + g
-                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            ++done;
+            {
+                const unsigned char* kt = slots + slot * F8_SLOT;
+                const bool two = st + 1 < cend;   // else the second tile is not there
+                // S = Q C^T: token group h (8 tokens) of the pair, lane's token 8 h + g
+                float s[4][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const unsigned char* row = kt + (8 * h + g) * kFp8Dim;
+                for (int h = 0; h < 4; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
+                // the four groups' chains step by step beside one another: a
+                // product waits 24 cycles for the one before it in its chain
+                auto scores = [&](int h0) {
+                    uint4 v[2][2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(row + (((2 * q + k) ^ g) << 4));
-                        uint32_t b0, b1;
-                        unpack4(v.x, b0, b1);
-                        mma_f16(s[h], qa[4 * k], b0, b1);
-                        unpack4(v.y, b0, b1);
-                        mma_f16(s[h], qa[4 * k + 1], b0, b1);
-                        unpack4(v.z, b0, b1);
-                        mma_f16(s[h], qa[4 * k + 2], b0, b1);
-                        unpack4(v.w, b0, b1);
-                        mma_f16(s[h], qa[4 * k + 3], b0, b1);
+                    for (int h = 0; h < 2; ++h) {
+                        const unsigned char* row = kt + (h0 >> 1) * F8_TILE + (8 * h + g) * kFp8Dim;
+                        v[h][0] = *reinterpret_cast<const uint4*>(row + (((2 * q) ^ g) << 4));
+                        v[h][1] = *reinterpret_cast<const uint4*>(row + (((2 * q + 1) ^ g) << 4));
                     }
-                }
-                // scale by the tokens' and rows' powers of two, mask; the
-                // weights' logarithms beside the scores
-                const int32_t tile_pos = (U.blk_start + (st - U.tile_off) + ti) * BS;
-                uint32_t see0 = 0, see1 = 0;
-                if (DRAFT) {
-                    see0 = (uint32_t)draft_visible(mask0, lim0 - tile_pos);
-                    see1 = (uint32_t)draft_visible(mask1, lim1 - tile_pos);
-                }
-                float wl[2][4];
-                float mx0 = NEG_INF, mx1 = NEG_INF, wx0 = NEG_INF, wx1 = NEG_INF;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t ke = *reinterpret_cast<const uint16_t*>(kt + BS * kFp8Dim + 8 * h + 2 * q);
-                    const uint32_t ve = *reinterpret_cast<const uint16_t*>(vt + BS * kFp8Dim + 8 * h + 2 * q);
+                    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4& x = v[h][k >> 2];
+                            const uint32_t w = (k & 3) == 0 ? x.x : (k & 3) == 1 ? x.y : (k & 3) == 2 ? x.z : x.w;
+                            uint32_t b0, b1;
+                            unpack4(w, b0, b1);
+                            mma_f16(s[h0 + h], qa[k], b0, b1);
+                        }
+                    }
+                };
+                scores(0);
+                if (two) scores(2);
+                // scale by the tokens' and rows' powers of two; the weights'
+                // logarithms are the scores plus the tokens' exponents vl
+                uint32_t vb[4] = {0u, 0u, 0u, 0u};   // exponent bytes of the lane's tokens of group h, as they are
+                auto vl = [&](int h, int e) {   // byte - 127, by way of 2^23 + byte
+                    return __uint_as_float(0x4b000000u | ((vb[h] >> (8 * e)) & 255u)) - 8388735.f;
+                };
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const unsigned char* ex = kt + (h >> 1 && two ? F8_TILE : 0) + BS * kFp8Dim + 8 * (h & 1) + 2 * q;
+                    const uint32_t ke = *reinterpret_cast<const uint16_t*>(ex);
+                    vb[h] = *reinterpret_cast<const uint16_t*>(ex + kFp8TileBytes);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float kf = exp_of((ke >> (8 * e)) & 255u);
-                        const float vl = (float)((ve >> (8 * e)) & 255u) - 127.f;
-                        const int bit = 8 * h + 2 * q + e;
-                        const bool on0 = DRAFT ? (see0 >> bit) & 1u : tile_pos + bit < lim0;
-                        const bool on1 = DRAFT ? (see1 >> bit) & 1u : tile_pos + bit < lim1;
-                        // factors past fp32 are cut, so that a zero product stays zero
-                        s[h][e] = on0 ? s[h][e] * fminf(kf * f0, 3.4e38f) : NEG_INF;
-                        s[h][2 + e] = on1 ? s[h][2 + e] * fminf(kf * f1, 3.4e38f) : NEG_INF;
-                        wl[h][e] = s[h][e] + vl;
-                        wl[h][2 + e] = s[h][2 + e] + vl;
+                        const float kf = __uint_as_float(((ke >> (8 * e)) & 255u) << 23);
+                        s[h][e] *= kf * f0;
+                        s[h][2 + e] *= kf * f1;
+                    }
+                }
+                // mask: only where some row does not see the whole pair
+                const int32_t pos0 = pos_of + st * BS;
+                if (!two || __any_sync(0xffffffffu, pos0 + 2 * BS > min(lim0, lim1))) {
+                    const uint32_t have = two ? 0xffffffffu : 0xffffu;
+                    uint32_t see0, see1;
+                    if (DRAFT) {
+                        see0 = (uint32_t)draft_visible(mask0, lim0 - pos0) & have;
+                        see1 = (uint32_t)draft_visible(mask1, lim1 - pos0) & have;
+                    } else {
+                        see0 = lim0 - pos0 >= 32 ? have : lim0 > pos0 ? have & ((1u << (lim0 - pos0)) - 1u) : 0u;
+                        see1 = lim1 - pos0 >= 32 ? have : lim1 > pos0 ? have & ((1u << (lim1 - pos0)) - 1u) : 0u;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int bit = 8 * h + 2 * q + e;
+                            s[h][e] = (see0 >> bit) & 1u ? s[h][e] : NEG_INF;
+                            s[h][2 + e] = (see1 >> bit) & 1u ? s[h][2 + e] : NEG_INF;
+                        }
+                    }
+                }
+                float mx0 = NEG_INF, mx1 = NEG_INF, wx0 = NEG_INF, wx1 = NEG_INF;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
                         mx0 = fmaxf(mx0, s[h][e]);
                         mx1 = fmaxf(mx1, s[h][2 + e]);
-                        wx0 = fmaxf(wx0, wl[h][e]);
-                        wx1 = fmaxf(wx1, wl[h][2 + e]);
+                        wx0 = fmaxf(wx0, s[h][e] + vl(h, e));
+                        wx1 = fmaxf(wx1, s[h][2 + e] + vl(h, e));
                     }
                 }
 #pragma unroll
@@ -332,14 +362,14 @@ __global__ void __launch_bounds__(F8_THREADS, 2) k_attn_partial_fp8(const AttnAr
                 m1 = n1;
                 w0 = x0;
                 w1 = x1;
-                uint32_t pa[4];
+                uint32_t pa[2][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 4; ++h) {
                     l0 += ex2(s[h][0] - nu0) + ex2(s[h][1] - nu0);
                     l1 += ex2(s[h][2] - nu1) + ex2(s[h][3] - nu1);
-                    // weights in fp16: rounded by 2^-12, or 2^-25 of the row's largest weight
-                    pa[2 * h] = pack_f16(ex2(wl[h][0] - xu0), ex2(wl[h][1] - xu0));
-                    pa[2 * h + 1] = pack_f16(ex2(wl[h][2] - xu1), ex2(wl[h][3] - xu1));
+                    // weights in fp16: rounded by 2^-11, or 2^-25 of the row's largest weight
+                    pa[h >> 1][2 * (h & 1)] = pack_f16(ex2(s[h][0] + vl(h, 0) - xu0), ex2(s[h][1] + vl(h, 1) - xu0));
+                    pa[h >> 1][2 * (h & 1) + 1] = pack_f16(ex2(s[h][2] + vl(h, 0) - xu1), ex2(s[h][3] + vl(h, 1) - xu1));
                 }
                 if (!__all_sync(0xffffffffu, al0 == 1.f && al1 == 1.f)) {
 #pragma unroll
@@ -351,28 +381,36 @@ __global__ void __launch_bounds__(F8_THREADS, 2) k_attn_partial_fp8(const AttnAr
                     }
                 }
                 // O += W V
-                const uint32_t va = smem_u32(vt);
                 const int mi = lane >> 3, tok = (mi & 1) * 8 + (lane & 7);
+                const uint32_t va = smem_u32(kt + kFp8TileBytes) + tok * kFp8Dim;
+                // (a loop over the two tiles: unrolled, the step outgrows the instruction cache)
+#pragma unroll 1
+                for (int half = 0; half <= (two ? 1 : 0); ++half) {
+                    const uint32_t tile = va + half * F8_TILE;
+                    const uint32_t p[4] = {half ? pa[1][0] : pa[0][0], half ? pa[1][1] : pa[0][1], half ? pa[1][2] : pa[0][2],
+                                           half ? pa[1][3] : pa[0][3]};
 #pragma unroll
-                for (int cc = 0; cc < 8; cc += 2) {
-                    uint32_t v[4];
-                    ldsm_x4_t(va + tok * kFp8Dim + (((cc + (mi >> 1)) ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
+                    for (int cc = 0; cc < 8; cc += 2) {
+                        uint32_t v[4];
+                        ldsm_x4_t(tile + (((cc + (mi >> 1)) ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {   // chunk cc + k: tokens 0-7 in v[2 k], 8-15 in v[2 k + 1]
-                        uint32_t e0, d0, e1, d1;
-                        unpack4(__byte_perm(v[2 * k], 0u, 0x3120), e0, d0);
-                        unpack4(__byte_perm(v[2 * k + 1], 0u, 0x3120), e1, d1);
-                        mma_f16(o[2 * (cc + k)], pa, e0, e1);
-                        mma_f16(o[2 * (cc + k) + 1], pa, d0, d1);
+                        for (int k = 0; k < 2; ++k) {   // chunk cc + k: tokens 0-7 in v[2 k], 8-15 in v[2 k + 1]
+                            uint32_t e0, d0, e1, d1;
+                            unpack4(__byte_perm(v[2 * k], 0u, 0x3120), e0, d0);
+                            unpack4(__byte_perm(v[2 * k + 1], 0u, 0x3120), e1, d1);
+                            mma_f16(o[2 * (cc + k)], p, e0, e1);
+                            mma_f16(o[2 * (cc + k) + 1], p, d0, d1);
+                        }
                     }
                 }
             }
-            // the stage's tiles are read: back to the producer
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
-            if (!last) continue;
+            if (st + 2 * P < cend) issue();   // (the chunk's last slot is still needed)
+        }
 
+        {
             // ---------------------------------------- end of this unit's chunk
+            if (cend == t_end) pdl_trigger();   // the CTA's last
             l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
             l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -397,55 +435,73 @@ __global__ void __launch_bounds__(F8_THREADS, 2) k_attn_partial_fp8(const AttnAr
                         }
                     }
                 }
-                continue;
-            }
-            // the P warps of each row tile combine through shared memory
-            // (16-byte words XOR-ed with the row, so that a quarter warp's
-            // stores fall in distinct banks)
-            {
-                float* ob = reinterpret_cast<float*>(sm + F8_COMB) + warp * 16 * D;
+            } else {
+                // the P warps of each row tile combine through the slots they
+                // read last (16-byte words XOR-ed with the row, so that a
+                // quarter warp's stores fall in distinct banks); a warp that
+                // had no pair of this chunk takes no part, its slots hold
+                // copies for later ones
+                const bool took = t + 2 * part < cend;
+                if (took) {
+                    float* ob = reinterpret_cast<float*>(slots + slot * F8_SLOT);
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int row = g + 8 * hh;
-                    const float back = hh ? back1 : back0;
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int row = g + 8 * hh;
+                        const float back = hh ? back1 : back0;
 #pragma unroll
-                    for (int n = 0; n < 8; ++n)
-                        *reinterpret_cast<float4*>(ob + row * D + (((4 * n + q) ^ (row & 7)) << 2)) =
-                            make_float4(o[2 * n][2 * hh] * back, o[2 * n + 1][2 * hh] * back,
-                                        o[2 * n][2 * hh + 1] * back, o[2 * n + 1][2 * hh + 1] * back);
-                    if (q == 0) ml[warp * 16 + row] = hh ? make_float2(m1, l1) : make_float2(m0, l0);
-                }
-            }
-            consumer_sync();
-            if (ok) {
-                const float* obase = reinterpret_cast<const float*>(sm + F8_COMB);
-                for (int idx = threadIdx.x; idx < U.n_rows * (D / 4); idx += F8_WARPS * 32) {
-                    const int grow = idx / (D / 4), d4 = idx % (D / 4);
-                    const int row = grow & 15, wf = (grow >> 4) * P;
-                    float M = NEG_INF;
-                    for (int p2 = 0; p2 < P; ++p2) M = fmaxf(M, ml[(wf + p2) * 16 + row].x);
-                    const float Mu = M == NEG_INF ? 0.f : M;
-                    float L = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int p2 = 0; p2 < P; ++p2) {
-                        const float2 s2 = ml[(wf + p2) * 16 + row];
-                        const float wgt = exp2f(s2.x - Mu);
-                        L += s2.y * wgt;
-                        const float4 v = *reinterpret_cast<const float4*>(obase + ((wf + p2) * 16 + row) * D +
-                                                                          ((d4 ^ (row & 7)) << 2));
-                        acc.x += v.x * wgt;
-                        acc.y += v.y * wgt;
-                        acc.z += v.z * wgt;
-                        acc.w += v.w * wgt;
+                        for (int n = 0; n < 8; ++n)
+                            *reinterpret_cast<float4*>(ob + row * D + (((4 * n + q) ^ (row & 7)) << 2)) =
+                                make_float4(o[2 * n][2 * hh] * back, o[2 * n + 1][2 * hh] * back,
+                                            o[2 * n][2 * hh + 1] * back, o[2 * n + 1][2 * hh + 1] * back);
                     }
-                    *reinterpret_cast<float4*>(a.part_acc + (int64_t)(prow0 + grow) * D + 4 * d4) = acc;
-                    if (d4 == 0) a.part_ml[prow0 + grow] = make_float2(M, L);
                 }
+                if (q == 0) {
+                    ml[warp * 16 + g] = make_float2(m0, l0);
+                    ml[warp * 16 + g + 8] = make_float2(m1, l1);
+                }
+                if (lane == 0) last_slot[warp] = slot;
+                __syncthreads();
+                if (!*abortp) {
+                    const int took_of = (cend - t + 1) >> 1;   // warps of a row tile that had a pair: at most P
+                    for (int idx = threadIdx.x; idx < U.n_rows * (D / 4); idx += F8_THREADS) {
+                        const int grow = idx / (D / 4), d4 = idx % (D / 4);
+                        const int row = grow & 15, wf = (grow >> 4) * P, np = min(P, took_of);
+                        float M = NEG_INF;
+                        for (int p2 = 0; p2 < np; ++p2) M = fmaxf(M, ml[(wf + p2) * 16 + row].x);
+                        const float Mu = M == NEG_INF ? 0.f : M;
+                        float L = 0.f;
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int p2 = 0; p2 < np; ++p2) {
+                            const float2 s2 = ml[(wf + p2) * 16 + row];
+                            const float wgt = exp2f(s2.x - Mu);
+                            L += s2.y * wgt;
+                            const float* ob = reinterpret_cast<const float*>(
+                                sm + ((wf + p2) * F8_SLOTS + last_slot[wf + p2]) * F8_SLOT);
+                            const float4 v = *reinterpret_cast<const float4*>(ob + row * D + ((d4 ^ (row & 7)) << 2));
+                            acc.x += v.x * wgt;
+                            acc.y += v.y * wgt;
+                            acc.z += v.z * wgt;
+                            acc.w += v.w * wgt;
+                        }
+                        *reinterpret_cast<float4*>(a.part_acc + (int64_t)(prow0 + grow) * D + 4 * d4) = acc;
+                        if (d4 == 0) a.part_ml[prow0 + grow] = make_float2(M, L);
+                    }
+                }
+                fence_async_smem();
+                __syncthreads();   // the slots are free again before the next copy lands in them
             }
-            consumer_sync();   // the buffer is free again
+            if (ok && !idle && t + 2 * part < cend) issue();   // the chunk's last slot
         }
         t = cend;
         ++u;
+    }
+    // after a timeout, wait (bounded) for this warp's copies still in flight
+    if (lane == 0 && *abortp) {
+        for (int i = max(0, issued - F8_SLOTS); i < issued; ++i) {
+            const uint64_t t0 = globaltimer();
+            while (!mbar_try_wait(bars + 8 * (i & 1), (uint32_t)(i >> 1) & 1u) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+            }
+        }
     }
 }
 
@@ -468,9 +524,13 @@ int attn_fp8_setup(int* ctas_per_sm) {
     return DENDRITE_OK;
 }
 
-int launch_attn_fp8(const AttnArgs& a, cudaStream_t s) {
+int launch_attn_fp8(const AttnArgs& a, bool after_event, cudaStream_t s) {
     if (a.plan.n_ctas <= 0) return DENDRITE_OK;
-    if (a.plan.masks)
+    if (after_event) {
+        if (a.plan.masks) k_attn_partial_fp8<true><<<a.plan.n_ctas, F8_THREADS, F8_SMEM, s>>>(a);
+        else k_attn_partial_fp8<false><<<a.plan.n_ctas, F8_THREADS, F8_SMEM, s>>>(a);
+        DENDRITE_CUDA(cudaGetLastError());
+    } else if (a.plan.masks)
         DENDRITE_CUDA(launch_pdl(k_attn_partial_fp8<true>, dim3(a.plan.n_ctas), dim3(F8_THREADS), F8_SMEM, s, a));
     else
         DENDRITE_CUDA(launch_pdl(k_attn_partial_fp8<false>, dim3(a.plan.n_ctas), dim3(F8_THREADS), F8_SMEM, s, a));

@@ -6,6 +6,7 @@
 namespace dendrite {
 
 int attn_fp8_setup(int* ctas_per_sm);   // shared memory attributes; resident CTAs per SM
-int launch_attn_fp8(const AttnArgs& a, cudaStream_t s);
+// after_event: the stream's order comes from an event, not from the kernel before.
+int launch_attn_fp8(const AttnArgs& a, bool after_event, cudaStream_t s);
 
 }  // namespace dendrite

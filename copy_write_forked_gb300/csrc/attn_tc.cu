@@ -48,13 +48,15 @@
 // CTA records DENDRITE_ETIMEOUT, every role stops issuing work, the MMA warp
 // waits (bounded) for its issued MMAs and the producer for its copies in
 // flight, and the TMEM is freed before the CTA exits.
+#include <cuda_fp16.h>
+
 #include "attn_common.cuh"
+#include "rows.h"
 
 using namespace dendrite;
 
 namespace {
 
-constexpr int TC_NSTAGE = 4;
 constexpr int TC_TOK = 64;                                   // tokens per stage (4 blocks)
 constexpr int TC_HALF = TC_TOK * 128;                        // 64 tokens x 64 columns bf16 = 8 KiB
 constexpr int TC_RING_STAGE = 2 * TC_HALF;                   // K (or V) of a stage: half 0, half 1
@@ -64,32 +66,47 @@ constexpr int TC_SOFTMAX_WARP0 = 2;
 constexpr int TC_PV_WARP = TC_SOFTMAX_WARP0 + 4 * TC_ROWTILES;   // 10
 constexpr int TC_V_WARP = TC_PV_WARP + 1;                          // 11
 constexpr int TC_S1_WARP = TC_V_WARP + 1;                          // 12
-constexpr int TC_PV1_WARP = TC_S1_WARP + 1;                        // 13
-constexpr int TC_THREADS = (TC_PV1_WARP + 1) * 32;
-// K ring, then V ring: each TC_NSTAGE stages of 64 tokens
-constexpr int OFF_K = 0;
-constexpr int OFF_V = TC_NSTAGE * TC_RING_STAGE;
-constexpr int OFF_Q = 2 * TC_NSTAGE * TC_RING_STAGE;
-constexpr int OFF_BAR = OFF_Q + TC_ROWTILES * TC_QTILE;
-// mbarriers; S/P buffers are indexed 2 r + b (row tile r, buffer b):
-// S_FULL when S is in the buffer, P_FULL when P overwrote it, PV_DONE when
-// the P V product that read that P has completed (the buffer is free again)
-enum {
-    B_K_FULL = 0,
-    B_K_EMPTY = B_K_FULL + TC_NSTAGE,
-    B_V_FULL = B_K_EMPTY + TC_NSTAGE,
-    B_V_EMPTY = B_V_FULL + TC_NSTAGE,
-    B_S_FULL = B_V_EMPTY + TC_NSTAGE,
-    B_P_FULL = B_S_FULL + 4,
-    B_PV_DONE = B_P_FULL + 4,
-    B_Q_FULL = B_PV_DONE + 4,
-    B_FINAL = B_Q_FULL + 2,   // one per issuer: S0, PV0, S1, PV1
-    B_COUNT = B_FINAL + 4
+// Shared memory of a bf16 pool's kernel, and of an 8-bit pool's (F8), whose
+// rings are a stage shorter to make room for the tiles as they are stored:
+// F8_RAW slots of a stage's four tiles (K and V each).  Warp 12 copies them,
+// warps 0, 13, 14 and 11, one on each SM partition, convert a tile each, warp
+// 1 issues S for both row tiles and warp 15 is the second PV issuer.
+constexpr int F8_RAW = 3;
+constexpr int F8_RAW_TILE = 2 * kFp8TileBytes;
+constexpr int F8_RAW_SLOT = 4 * F8_RAW_TILE;
+template <bool F8>
+struct TcLayout {
+    static constexpr int NSTAGE = F8 ? 3 : 4;
+    static constexpr int PV1_WARP = F8 ? 15 : TC_S1_WARP + 1;
+    static constexpr int THREADS = (PV1_WARP + 1) * 32;
+    // K ring, then V ring: each NSTAGE stages of 64 tokens
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_V = NSTAGE * TC_RING_STAGE;
+    static constexpr int OFF_Q = 2 * NSTAGE * TC_RING_STAGE;
+    static constexpr int OFF_RAW = OFF_Q + TC_ROWTILES * TC_QTILE;
+    // draft trees: the mask of each row, written and read by the row's thread
+    static constexpr int OFF_MASK = OFF_RAW + (F8 ? F8_RAW * F8_RAW_SLOT : 0);
+    static constexpr int OFF_BAR = OFF_MASK + TC_ROWTILES * 128 * 8;
+    // mbarriers; S/P buffers are indexed 2 r + b (row tile r, buffer b):
+    // S_FULL when S is in the buffer, P_FULL when P overwrote it, PV_DONE when
+    // the P V product that read that P has completed (the buffer is free again)
+    static constexpr int B_K_FULL = 0;
+    static constexpr int B_K_EMPTY = B_K_FULL + NSTAGE;
+    static constexpr int B_V_FULL = B_K_EMPTY + NSTAGE;
+    static constexpr int B_V_EMPTY = B_V_FULL + NSTAGE;
+    static constexpr int B_S_FULL = B_V_EMPTY + NSTAGE;
+    static constexpr int B_P_FULL = B_S_FULL + 4;
+    static constexpr int B_PV_DONE = B_P_FULL + 4;
+    static constexpr int B_Q_FULL = B_PV_DONE + 4;
+    static constexpr int B_FINAL = B_Q_FULL + 2;   // one per issuer: S0, PV0, S1, PV1
+    static constexpr int B_RAW_FULL = B_FINAL + 4;      // F8: the copied tiles
+    static constexpr int B_RAW_EMPTY = B_RAW_FULL + (F8 ? F8_RAW : 0);
+    static constexpr int B_COUNT = B_RAW_EMPTY + (F8 ? F8_RAW : 0);
+    // a packed unit's extra tiles (logical block, member mask), per row tile
+    static constexpr int OFF_XINFO = OFF_BAR + B_COUNT * 8 + 16;
+    static constexpr int SMEM = 1024 + OFF_XINFO + TC_ROWTILES * kMaxTcExtraTiles * 8;
 };
-// a packed unit's extra tiles (logical block, member mask), per row tile
-constexpr int OFF_XINFO = OFF_BAR + B_COUNT * 8 + 16;
-constexpr int SMEM_TC = 1024 + OFF_XINFO + TC_ROWTILES * kMaxTcExtraTiles * 8;
-static_assert(SMEM_TC <= 227 * 1024, "shared memory budget");
+static_assert(TcLayout<false>::SMEM <= 227 * 1024 - 64 && TcLayout<true>::SMEM <= 227 * 1024 - 64, "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float RESCALE_THRESHOLD = 8.f;
 
@@ -201,6 +218,21 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     }
     return ok;
 }
+// The same by a call where the first look does not settle it, for the 8-bit
+// pools' kernel, whose six roles have to share the instruction cache.
+__device__ __noinline__ bool long_wait(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
+    return thread_wait(bar, parity, abortp, meta);
+}
+template <bool F8>
+__device__ __forceinline__ bool thread_wait_(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
+    if constexpr (!F8) return thread_wait(bar, parity, abortp, meta);
+    return mbar_test(bar, parity) || long_wait(bar, parity, abortp, meta);
+}
+template <bool F8>
+__device__ __forceinline__ bool warp_wait_(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
+    if constexpr (!F8) return warp_wait(bar, parity, abortp, meta);
+    return __all_sync(0xffffffffu, mbar_test(bar, parity) || long_wait(bar, parity, abortp, meta));
+}
 // Wait without an abort exit, used only to drain work already issued.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = globaltimer();
@@ -208,11 +240,217 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     }
 }
 
+// ------------------------------------------------ 8-bit pools: converting warps
+// Warp w brings tile w of each stage, K and V, to the bf16 stages the products
+// read.  A tile's values are code * 2^e, bf16 numbers exactly, so from here on
+// the kernel is the bf16 one.
+//   - The conversion is kept short in code: five roles run side by side, and
+//     where their loops together outgrow the instruction cache every step of
+//     every role waits for its instructions (the same loop unrolled, with a
+//     path of bf16 products beside this one by fp32, took 1,450 cycles a tile
+//     in place of 450).
+//   - A lane converts 16 codes at a time: one 16-byte load, two 16-byte stores
+//     into the two 16-byte chunks they fill in the 128-byte-swizzled stage.
+//     Eight neighbouring lanes take four chunks of one 64-column half of two
+//     tokens t and t ^ 5: their loads then differ in bit 2 of the swizzle and
+//     their stores in bit 0, and no two meet in a bank.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+// Two codes (the low 16 bits of c) times f as a pair of bf16.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t c, float f) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_bf16(x.x * f, x.y * f);
+}
+// The stages of a CTA's tile range, in order.
+struct StageWalk {
+    int32_t t, u, cend = 0;    // next stage's first tile; its unit; the end of the unit's tiles here
+    int64_t row = 0;           // table offset of tile 0 of the unit
+    int32_t head = 0;
+    __device__ __forceinline__ StageWalk(int32_t t0, int32_t u0) : t(t0), u(u0 - 1) {}
+    // Moves on to the unit of the next stage; false past the range's end.
+    __device__ __forceinline__ bool more(const AttnPlanDev& pl, int32_t t_end, int32_t bpb) {
+        if (t >= t_end) return false;
+        while (t >= cend) {
+            const AttnUnit& U = pl.units[++u];
+            cend = min(t_end, U.tile_off + U.n_blk);
+            row = (int64_t)U.table_row * bpb + U.blk_start - U.tile_off;
+            head = U.kv_head;
+        }
+        return true;
+    }
+    __device__ __forceinline__ int tiles() const { return min(4, cend - t); }
+    __device__ __forceinline__ void step() { t = min(t + 4, cend); }
+};
+
+// Copies the stages' tiles as they are stored, F8_RAW stages ahead; lane i < 4
+// copies tile i, whose block id it loaded a stage before.
+template <typename Y>
+__device__ __forceinline__ void copy_tiles(const AttnArgs& a, uint32_t base, uint32_t bars, volatile int* abortp,
+                                           int32_t t_begin, int32_t t_end, int32_t u0) {
+    const AttnPlanDev& pl = a.plan;
+    const int lane = threadIdx.x & 31;
+    auto bar = [bars](int i) { return bars + 8u * (uint32_t)i; };
+    const char* kp = reinterpret_cast<const char*>(a.pool_k);
+    const char* vp = reinterpret_cast<const char*>(a.pool_v);
+    StageWalk at(t_begin, u0);
+    int slot = 0, rounds = 0;          // rounds: stages copied so far
+    bool left = at.more(pl, t_end, a.bpb);
+    int n = left ? at.tiles() : 0;
+    int32_t blk = lane < n ? a.table[at.row + at.t + lane] : 0, head = at.head;
+    while (left) {
+        // the next stage's block ids while this one waits for its slot
+        at.step();
+        left = at.more(pl, t_end, a.bpb);
+        const int n_next = left ? at.tiles() : 0;
+        const int32_t blk_next = lane < n_next ? a.table[at.row + at.t + lane] : 0, head_next = at.head;
+        const uint32_t ph = (uint32_t)(rounds / F8_RAW) & 1u;
+        if (!warp_wait_<true>(bar(Y::B_RAW_EMPTY + slot), ph ^ 1u, abortp, a.meta)) break;
+        const uint32_t rb = bar(Y::B_RAW_FULL + slot);
+        if (lane == 0) mbar_expect_tx(rb, (uint32_t)(n * F8_RAW_TILE));
+        __syncwarp();
+        if (lane < n) {
+            if ((uint32_t)blk >= (uint32_t)a.n_blocks) {   // broken table: poison, read a valid block
+                atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
+                blk = 0;
+            }
+            const int64_t off = ((int64_t)blk * a.n_kv + head) * kFp8TileBytes;
+            const uint32_t dst = base + Y::OFF_RAW + slot * F8_RAW_SLOT + lane * F8_RAW_TILE;
+            bulk_load(dst, kp + off, kFp8TileBytes, rb);
+            bulk_load(dst + kFp8TileBytes, vp + off, kFp8TileBytes, rb);
+        }
+        ++rounds;
+        slot = slot == F8_RAW - 1 ? 0 : slot + 1;
+        n = n_next;
+        blk = blk_next;
+        head = head_next;
+    }
+    __syncwarp();
+    if (lane == 0 && *abortp) {   // copies still in flight land before the CTA exits
+        for (int i = max(0, rounds - F8_RAW); i < rounds; ++i)
+            drain_wait(bar(Y::B_RAW_FULL + i % F8_RAW), (uint32_t)(i / F8_RAW) & 1u);
+    }
+}
+
+template <typename Y>
+__device__ __forceinline__ void convert_tiles(const AttnArgs& a, unsigned char* sm, uint32_t base, uint32_t bars,
+                                              volatile int* abortp, int32_t t_begin, int32_t t_end, int32_t u0, int w) {
+    const AttnPlanDev& pl = a.plan;
+    const int lane = threadIdx.x & 31;
+    auto bar = [bars](int i) { return bars + 8u * (uint32_t)i; };
+    // this lane's share: chunk c (16 codes) of four tokens; the two chunks
+    // 2 c, 2 c + 1 of the stage row they fill
+    const int c = 4 * ((lane >> 3) & 1) + (lane & 3), up = c >> 2, k = (2 * c) & 7;
+    const int flip = (lane & 4) ? 5 : 0;
+    StageWalk now(t_begin, u0);
+    int slot = 0, stage = 0;
+    uint32_t raw_ph = 0, empty_ph = 1;
+    for (; now.more(pl, t_end, a.bpb); now.step()) {
+        const bool mine = w < now.tiles();
+        const unsigned char* raw = sm + Y::OFF_RAW + slot * F8_RAW_SLOT + w * F8_RAW_TILE;
+        if (!warp_wait_<true>(bar(Y::B_RAW_FULL + slot), raw_ph, abortp, a.meta)) break;
+        if (!warp_wait_<true>(bar(Y::B_K_EMPTY + stage), empty_ph, abortp, a.meta)) break;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+            if (kv && !warp_wait_<true>(bar(Y::B_V_EMPTY + stage), empty_ph, abortp, a.meta)) break;
+            if (mine) {
+                const unsigned char* src = raw + kv * kFp8TileBytes;
+                unsigned char* ring = sm + Y::OFF_K + kv * (Y::OFF_V - Y::OFF_K) + stage * TC_RING_STAGE + up * TC_HALF + w * 16 * 128;
+#pragma unroll 2
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = (((2 * i + (lane >> 4)) & 3) ^ flip) + 8 * (i >> 1), sw = tok & 7;
+                    const uint4 x = *reinterpret_cast<const uint4*>(src + tok * kFp8Dim + ((c ^ sw) << 4));
+                    const float f = __uint_as_float((uint32_t)src[kBlockSize * kFp8Dim + tok] << 23);   // 2^e
+                    *reinterpret_cast<uint4*>(ring + tok * 128 + ((k ^ sw) << 4)) =
+                        make_uint4(codes_bf16(x.x, f), codes_bf16(x.x >> 16, f), codes_bf16(x.y, f), codes_bf16(x.y >> 16, f));
+                    *reinterpret_cast<uint4*>(ring + tok * 128 + (((k + 1) ^ sw) << 4)) =
+                        make_uint4(codes_bf16(x.z, f), codes_bf16(x.z >> 16, f), codes_bf16(x.w, f), codes_bf16(x.w >> 16, f));
+                }
+            }
+            fence_async_smem();   // the stores, before the products read them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Y::B_K_FULL + kv * (Y::B_V_FULL - Y::B_K_FULL) + stage));
+        }
+        if (lane == 0) mbar_arrive(bar(Y::B_RAW_EMPTY + slot));
+        if (*abortp) break;
+        if (++slot == F8_RAW) { slot = 0; raw_ph ^= 1u; }
+        if (++stage == Y::NSTAGE) { stage = 0; empty_ph ^= 1u; }
+    }
+}
+
+// Issues S_r(k) = Q_r K^T of both row tiles, stage by stage, and gives the K
+// slot back once both are issued.
+template <typename Y>
+__device__ __forceinline__ void issue_scores(const AttnArgs& a, uint32_t base, uint32_t bars, uint32_t tmem,
+                                             volatile int* abortp, int32_t t_begin, int32_t t_end, int32_t u0) {
+    const AttnPlanDev& pl = a.plan;
+    auto bar = [bars](int i) { return bars + 8u * (uint32_t)i; };
+    if ((threadIdx.x & 31) == 0) {
+        int32_t js0 = 0, js1 = 0, qc0 = 0, qc1 = 0;   // stages and units of either row tile
+        bool ok = true, any = false;
+        int32_t t = t_begin, u = u0;
+        int stage = 0;
+        uint32_t ph = 0;
+        while (ok && t < t_end) {
+            const AttnUnit& U = pl.units[u];
+            const int32_t uend = U.tile_off + U.n_blk;
+            if (t >= uend) { ++u; continue; }
+            const int32_t cend = min(t_end, uend);
+            const int rt = U.rt;
+            for (int32_t first = t; ok && t < cend; t = min(t + 4, cend)) {
+                const int ntiles = min(4, cend - t);
+                ok = thread_wait_<true>(bar(Y::B_K_FULL + stage), ph, abortp, a.meta);
+#pragma unroll 1
+                for (int r = 0; ok && r < rt; ++r) {
+                    const int32_t js = r ? js1 : js0;
+                    if (t == first) {
+                        ok = thread_wait_<true>(bar(Y::B_Q_FULL + r), (uint32_t)(r ? qc1 : qc0) & 1u, abortp, a.meta);
+                        (r ? qc1 : qc0) += 1;
+                    }
+                    const int b = js & 1;
+                    ok = ok && thread_wait_<true>(bar(Y::B_PV_DONE + 2 * r + b), ((uint32_t)(js >> 1) & 1u) ^ 1u, abortp, a.meta);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sQ = base + Y::OFF_Q + r * TC_QTILE, sK = base + Y::OFF_K + stage * TC_RING_STAGE;
+                    const uint32_t id = idesc_bf16(128, 16 * ntiles, 0, 0);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16(tmem + r * 256 + 128 + b * 64,
+                                  sdesc(sQ + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
+                                  sdesc(sK + (kk >> 2) * TC_HALF + (kk & 3) * 32, 16, 1024), id, kk > 0);
+                    umma_commit(bar(Y::B_S_FULL + 2 * r + b));
+                    (r ? js1 : js0) += 1;
+                    any = true;
+                }
+                if (ok) umma_commit(bar(Y::B_K_EMPTY + stage));
+                if (++stage == Y::NSTAGE) { stage = 0; ph ^= 1u; }
+            }
+            t = cend;
+            ++u;
+        }
+        if (any) {   // every MMA this thread issued has finished before the TMEM is freed
+            umma_commit(bar(Y::B_FINAL));
+            drain_wait(bar(Y::B_FINAL), 0);
+        }
+    }
+    __syncwarp();
+}
+
 // DRAFT: the rows are nodes of draft trees (masked by their ancestors too).
-template <bool DRAFT>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+// F8: an 8-bit pool's blocks (tmK and tmV unused).
+template <bool DRAFT, bool F8>
+__global__ void __launch_bounds__(TcLayout<F8>::THREADS, 1)
 k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const AttnArgs a) {
+    using Y = TcLayout<F8>;
+    constexpr int TC_NSTAGE = Y::NSTAGE, OFF_K = Y::OFF_K, OFF_V = Y::OFF_V, OFF_Q = Y::OFF_Q, OFF_BAR = Y::OFF_BAR,
+                  OFF_XINFO = Y::OFF_XINFO, B_K_FULL = Y::B_K_FULL, B_K_EMPTY = Y::B_K_EMPTY, B_V_FULL = Y::B_V_FULL,
+                  B_V_EMPTY = Y::B_V_EMPTY, B_S_FULL = Y::B_S_FULL, B_P_FULL = Y::B_P_FULL, B_PV_DONE = Y::B_PV_DONE,
+                  B_Q_FULL = Y::B_Q_FULL, B_FINAL = Y::B_FINAL, B_COUNT = Y::B_COUNT, TC_PV1_WARP = Y::PV1_WARP;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int abort_flag;
     const uint32_t raw = smem_u32(smem_raw);
@@ -225,9 +463,9 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < TC_NSTAGE; ++s) {
-            mbar_init(bar(B_K_FULL + s), 1);
-            mbar_init(bar(B_K_EMPTY + s), 2);    // both S issuers (row tiles 0 and 1)
-            mbar_init(bar(B_V_FULL + s), 1);
+            mbar_init(bar(B_K_FULL + s), F8 ? 4 : 1);   // F8: every converting warp
+            mbar_init(bar(B_K_EMPTY + s), F8 ? 1 : 2);   // both S issuers (row tiles 0 and 1); F8: the one
+            mbar_init(bar(B_V_FULL + s), F8 ? 4 : 1);
             mbar_init(bar(B_V_EMPTY + s), 2);    // both PV issuers
         }
         for (int i = 0; i < 4; ++i) {
@@ -237,6 +475,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
         for (int r = 0; r < TC_ROWTILES; ++r) mbar_init(bar(B_Q_FULL + r), 4);
         for (int i = 0; i < 4; ++i) mbar_init(bar(B_FINAL + i), 1);
+        for (int i = Y::B_RAW_FULL; i < B_COUNT; ++i) mbar_init(bar(i), i < Y::B_RAW_EMPTY ? 1 : 4);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     pdl_trigger();
@@ -264,7 +503,13 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int32_t u0 = pl.tc_cta_unit[c];
     volatile int* abortp = &abort_flag;
 
-    if (warp == 0 || warp == TC_V_WARP) {
+    if (F8 && warp == TC_S1_WARP) {
+        copy_tiles<Y>(a, base, bars, abortp, t_begin, t_end, u0);
+    } else if (F8 && warp == 1) {
+        issue_scores<Y>(a, base, bars, tmem, abortp, t_begin, t_end, u0);
+    } else if (F8 && (warp == 0 || warp == TC_V_WARP || warp == 13 || warp == 14)) {
+        convert_tiles<Y>(a, sm, base, bars, abortp, t_begin, t_end, u0, warp == 0 ? 0 : warp == TC_V_WARP ? 3 : warp - 12);
+    } else if (!F8 && (warp == 0 || warp == TC_V_WARP)) {
         // ------------------------------------------------------ producers
         // Warp 0 streams K into the K ring, warp 11 V into the V ring, so a
         // K slot is refilled as soon as its S is done and a V slot as soon as
@@ -307,7 +552,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 const uint32_t ph = (uint32_t)(g / TC_NSTAGE) & 1u;
                 const int ntiles = min(4, cend - st);
                 int ok = 1;
-                if (lane == 0) ok = thread_wait(bar(b_empty + slot), ph ^ 1u, abortp, a.meta);
+                if (lane == 0) ok = thread_wait_<F8>(bar(b_empty + slot), ph ^ 1u, abortp, a.meta);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 if (lane == 0) mbar_expect_tx(bar(b_full + slot), (uint32_t)(ntiles * 2 * HALF_BYTES));
@@ -358,17 +603,17 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 const int32_t cend = min(t_end, uend);
                 const bool active = my_r < U.rt;
                 const int32_t nst = (cend - t + 3) >> 2;
-                if (s_role && active) ok = thread_wait(bar(B_Q_FULL + my_r), (uint32_t)qc++ & 1u, abortp, a.meta);
+                if (s_role && active) ok = thread_wait_<F8>(bar(B_Q_FULL + my_r), (uint32_t)qc++ & 1u, abortp, a.meta);
                 for (int32_t k = 0; k < nst && ok; ++k) {
                     const int32_t gg = g + k;
                     const int slot = gg % TC_NSTAGE;
                     const uint32_t ph = (uint32_t)(gg / TC_NSTAGE) & 1u;
                     const int ntiles = min(4, cend - (t + 4 * k));
                     if (s_role) {
-                        ok = thread_wait(bar(B_K_FULL + slot), ph, abortp, a.meta);
+                        ok = thread_wait_<F8>(bar(B_K_FULL + slot), ph, abortp, a.meta);
                         if (ok && active) {
                             const int b = js & 1;
-                            ok = thread_wait(bar(B_PV_DONE + 2 * my_r + b), ((uint32_t)(js >> 1) & 1u) ^ 1u, abortp,
+                            ok = thread_wait_<F8>(bar(B_PV_DONE + 2 * my_r + b), ((uint32_t)(js >> 1) & 1u) ^ 1u, abortp,
                                              a.meta);
                             if (!ok) break;
                             tc_fence_after();
@@ -389,10 +634,10 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                             mbar_arrive(bar(B_K_EMPTY + slot));
                         }
                     } else {
-                        ok = thread_wait(bar(B_V_FULL + slot), ph, abortp, a.meta);
+                        ok = thread_wait_<F8>(bar(B_V_FULL + slot), ph, abortp, a.meta);
                         if (ok && active) {
                             const int b = js & 1;
-                            ok = thread_wait(bar(B_P_FULL + 2 * my_r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
+                            ok = thread_wait_<F8>(bar(B_P_FULL + 2 * my_r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t vst = base + OFF_V + slot * TC_RING_STAGE;
@@ -431,6 +676,10 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
         const int row = r * 128 + trow;
         int2* xinfo = reinterpret_cast<int2*>(sm + OFF_XINFO) + r * kMaxTcExtraTiles;
+        // draft trees: the row's mask, in shared memory: in registers, or made
+        // again from the unit where it is needed, it cost spills in the loop
+        // (a third of its time)
+        uint64_t* mask_slot = reinterpret_cast<uint64_t*>(sm + Y::OFF_MASK) + r * 128 + trow;
         // This thread's row of a unit's Q into the K-major swizzled tile, and
         // the row's record.  A unit's Q is staged as soon as the previous
         // chunk's last S was read (no S MMA of it is pending then), before
@@ -444,6 +693,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 const uint4 v = v_ok ? __ldg(q + ch) : make_uint4(0u, 0u, 0u, 0u);
                 *reinterpret_cast<uint4*>(sQ + (ch >> 3) * 16384 + trow * 128 + (((ch & 7) ^ (trow & 7)) << 4)) = v;
             }
+            if constexpr (DRAFT) *mask_slot = v_ok ? draft_mask(pl, V, row) : 0;
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_Q_FULL + r));
@@ -466,7 +716,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
             const bool valid = row < U.n_rows;
             const AttnRow R = staged_u == u ? staged_R : stage_q(U);
-            if (U.n_blk > U.n_shared) {
+            if (!F8 && U.n_blk > U.n_shared) {
                 // a packed unit: its extra tiles' logical blocks and member
                 // masks into shared memory, once every warp of the row tile
                 // is done with the previous unit's (the plan keeps them to
@@ -484,9 +734,17 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 const int32_t st = t + 4 * k;
                 const int ntiles = min(4, cend - st);
                 const int b = js & 1;
-                ok = warp_wait(bar(B_S_FULL + 2 * r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
+                ok = warp_wait_<F8>(bar(B_S_FULL + 2 * r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
                 if (!ok) break;
                 tc_fence_after();
+                if ((DRAFT || F8) && row - lane >= U.n_rows) {
+                    // a warp without a row of the unit: its rows of Q are zero,
+                    // hence of S, which is zero as P too; it only passes the buffer on
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_P_FULL + 2 * r + b));
+                    continue;
+                }
                 float s[64];
                 {
                     uint32_t v0[32], v1[32];
@@ -503,12 +761,12 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 // mask stage columns past the chunk and positions the row does
                 // not see (only stages some row of the warp does not fully see)
                 const int32_t ti0 = st - U.tile_off;
-                if (ti0 + ntiles <= U.n_shared) {
+                if (F8 || ti0 + ntiles <= U.n_shared) {
                     const int32_t vis = min(ntiles * BS, R.limit - (U.blk_start + ti0) * BS);
                     if (!__all_sync(0xffffffffu, vis >= TC_TOK)) {
                         if constexpr (DRAFT) {
                             // draft trees: the stage's seen positions as bits
-                            uint64_t see = valid ? draft_visible(draft_mask(pl, U, row), R.limit - (U.blk_start + ti0) * BS) : 0;
+                            uint64_t see = draft_visible(*mask_slot, R.limit - (U.blk_start + ti0) * BS);
                             if (ntiles < 4) see &= (1ull << (ntiles * BS)) - 1ull;
 #pragma unroll
                             for (int i = 0; i < 64; ++i) s[i] = (see >> i) & 1ull ? s[i] : -INFINITY;
@@ -534,7 +792,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                         const int32_t v = seen ? min(BS, R.limit - lb * BS) : 0;
                         if constexpr (DRAFT) {
                             const uint32_t see =
-                                seen && valid ? (uint32_t)draft_visible(draft_mask(pl, U, row), R.limit - lb * BS) : 0u;
+                                seen ? (uint32_t)draft_visible(*mask_slot, R.limit - lb * BS) : 0u;
 #pragma unroll
                             for (int c = 0; c < BS; ++c) s[BS * j + c] = (see >> c) & 1u ? s[BS * j + c] : -INFINITY;
                         } else {
@@ -562,7 +820,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     const bool need = mx > m_ref + RESCALE_THRESHOLD;
                     if (__any_sync(0xffffffffu, need)) {
                         // O holds the PV of the previous stage once it completes
-                        ok = warp_wait(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u,
+                        ok = warp_wait_<F8>(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u,
                                        abortp, a.meta);
                         if (!ok) break;
                         tc_fence_after();
@@ -624,7 +882,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 }
             }
             // chunk done: O after the last PV -> partial row
-            ok = warp_wait(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u, abortp, a.meta);
+            ok = warp_wait_<F8>(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u, abortp, a.meta);
             if (!ok) break;
             tc_fence_after();
             const int32_t prow = U.prow_base + (c - U.cfirst) * U.n_rows + row;
@@ -658,29 +916,35 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
 namespace dendrite {
 
-template <bool DRAFT>
+template <bool DRAFT, bool F8>
 static int setup_one() {
-    if (cudaFuncSetAttribute(k_attn_partial_tc<DRAFT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TC) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(k_attn_partial_tc<DRAFT, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             TcLayout<F8>::SMEM) != cudaSuccess)
         return DENDRITE_ECUDA;
     int occ = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_tc<DRAFT>, TC_THREADS, SMEM_TC) !=
-            cudaSuccess ||
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_tc<DRAFT, F8>, TcLayout<F8>::THREADS,
+                                                      TcLayout<F8>::SMEM) != cudaSuccess ||
         occ != 1)
         return DENDRITE_ECUDA;   // the kernel's 512 TMEM columns need exactly one CTA per SM
     return DENDRITE_OK;
 }
 
-int attn_tc_setup() {
-    DENDRITE_TRY(setup_one<false>());
-    return setup_one<true>();
+int attn_tc_setup(bool f8) {
+    DENDRITE_TRY((f8 ? setup_one<false, true>() : setup_one<false, false>()));
+    return f8 ? setup_one<true, true>() : setup_one<true, false>();
 }
 
-int launch_attn_tc(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, cudaStream_t s) {
+template <bool F8>
+static void launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, cudaStream_t s) {
     if (a.plan.masks)
-        k_attn_partial_tc<true><<<n_ctas, TC_THREADS, SMEM_TC, s>>>(mk, mv, a);
+        k_attn_partial_tc<true, F8><<<n_ctas, TcLayout<F8>::THREADS, TcLayout<F8>::SMEM, s>>>(mk, mv, a);
     else
-        k_attn_partial_tc<false><<<n_ctas, TC_THREADS, SMEM_TC, s>>>(mk, mv, a);
+        k_attn_partial_tc<false, F8><<<n_ctas, TcLayout<F8>::THREADS, TcLayout<F8>::SMEM, s>>>(mk, mv, a);
+}
+
+int launch_attn_tc(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, bool f8, cudaStream_t s) {
+    if (f8) launch_one<true>(mk, mv, a, n_ctas, s);
+    else launch_one<false>(mk, mv, a, n_ctas, s);
     return cudaGetLastError() == cudaSuccess ? DENDRITE_OK : DENDRITE_ECUDA;
 }
 

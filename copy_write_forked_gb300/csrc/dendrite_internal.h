@@ -22,6 +22,7 @@ constexpr int kMaxUnitRowsF32 = 16;
 constexpr int kMaxUnitRowsTurbo = 64;  // rows per compressed-pool unit (4 warps x 16 rows)
 constexpr int kMaxUnitRowsFp8 = 64;    // rows per 8-bit-pool unit (4 warps x 16 rows)
 constexpr int kMaxUnitRowsTc = 256;   // rows per tcgen05 attention unit (2 row tiles of 128)
+constexpr int kTcMinRowsFp8 = 32;     // the same for 8-bit pools
 constexpr int kTcMinRowsDefault = 64; // segments with more rows per kv head use the tcgen05 kernel
 constexpr int32_t kFoldPctDefault = 100;  // fold a segment when that is estimated cheaper
 constexpr int32_t kPackPctDefault = 100;  // pack a segment's followers into it when that is estimated cheaper

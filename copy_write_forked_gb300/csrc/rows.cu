@@ -10,14 +10,14 @@
 // The angle is kept in turns, as a 64-bit fixed-point fraction: position *
 // fraction wraps at whole turns, so the range reduction is one integer
 // product and exact however far the position is (an fp32 angle at position
-// 10^6 would be off by 2^-4 rad).  The top 32 bits, a signed fraction of half
-// a turn, go to sincospif: an error of about 2^-24 of half a turn, below the
-// rounding of fp32 products.
+// 10^6 would be off by 2^-4 rad).  sine and cosine come from the fraction's
+// distance to the nearest quarter turn, as a sum of two floats, by Taylor
+// polynomials, and are rounded once (sincos_turns).
 //
-// 8-bit rows.  e is the least integer >= -127 with max|x| <= 448 * 2^e (over
-// the finite elements) and element k is stored as the e4m3 number nearest to
-// x_k * 2^-e, ties to even (with e = 120 at most 240, which is finite when read
-// back); a NaN or an infinity is stored as NaN.  The scale
+// 8-bit rows.  e is the least integer >= -126 with max|x| <= 448 * 2^e and
+// element k is stored as the e4m3 number nearest to x_k * 2^-e, ties to even
+// (with e = 120 at most 240, which is finite when read back); a row with a NaN
+// or an infinity is stored as NaN throughout.  The scale
 // is a power of two: x * 2^-e is exact in fp32, so a code depends on its
 // row's bits alone, and code * 2^e is again a bf16 number, exactly.
 //
@@ -59,7 +59,7 @@ struct GlobalWords {
     const int32_t* p;
     __device__ __forceinline__ int32_t operator[](int64_t i) const { return __ldg(p + i); }
 };
-constexpr int kRowsCap = 1536;
+constexpr int kRowsSmall = 256, kRowsCap = 1536;   // small calls copy fewer parameter bytes per launch
 
 template <typename A>
 __device__ __forceinline__ int32_t byte_of(const A& args, int64_t word0, int64_t i) {
@@ -103,63 +103,132 @@ struct RowsArgs {
     uint64_t freq[128];          // turns per position, as a fraction of 2^64
 };
 
-// Eight consecutive elements as fp32, and back.  Input rows are read once,
-// through L2 and not the read-only path: the queries may be rotated in place.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight consecutive elements as they are; input rows are read once, through L2
+// and not the read-only path: the queries may be rotated in place.
+template <typename T>
+struct Chunk {
+    uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void load(const T* p, Chunk<T>& x) {
+#pragma unroll
+    for (int k = 0; k < (int)(sizeof(T) / 2); ++k) x.w[k] = __ldcg(reinterpret_cast<const uint4*>(p) + k);
+}
+template <typename T>
+__device__ __forceinline__ void store(T* p, const Chunk<T>& x) {
+#pragma unroll
+    for (int k = 0; k < (int)(sizeof(T) / 2); ++k) reinterpret_cast<uint4*>(p)[k] = x.w[k];
+}
+__device__ __forceinline__ void to_float(const Chunk<__nv_bfloat16>& c, float (&x)[8]) {
+    const uint32_t w[4] = {c.w[0].x, c.w[0].y, c.w[0].z, c.w[0].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         x[2 * k] = __uint_as_float(w[k] << 16);
         x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void to_float(const Chunk<float>& c, float (&x)[8]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        x[4 * k] = __uint_as_float(c.w[k].x);
+        x[4 * k + 1] = __uint_as_float(c.w[k].y);
+        x[4 * k + 2] = __uint_as_float(c.w[k].z);
+        x[4 * k + 3] = __uint_as_float(c.w[k].w);
+    }
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+__device__ __forceinline__ void from_float(const float (&x)[8], Chunk<__nv_bfloat16>& c) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
         w[k] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    c.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-
-// max|x| over the finite elements.
-__device__ __forceinline__ float finite_max(const float (&x)[8]) {
-    float m = 0.f;
+__device__ __forceinline__ void from_float(const float (&x)[8], Chunk<float>& c) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float a = fabsf(x[k]);
-        m = fmaxf(m, a < INFINITY ? a : 0.f);
-    }
+    for (int k = 0; k < 2; ++k)
+        c.w[k] = make_uint4(__float_as_uint(x[4 * k]), __float_as_uint(x[4 * k + 1]), __float_as_uint(x[4 * k + 2]),
+                            __float_as_uint(x[4 * k + 3]));
+}
+// The bits of max|x| as fp32: magnitudes order as integers, with what is not
+// finite above all.
+__device__ __forceinline__ uint32_t top_bits(const float (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
     return m;
 }
-// The least e >= -127 with top <= 448 * 2^e: top = (1 + f) 2^(E - 127), and
-// 448 = 1.75 * 2^8.
-__device__ __forceinline__ int fp8_exponent(float top) {
-    const uint32_t b = __float_as_uint(top);
-    return max(-127, (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0));
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {   // of two 16-bit pairs
+    uint32_t y;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+__device__ __forceinline__ uint32_t top_bits(const Chunk<__nv_bfloat16>& c) {
+    const uint32_t m = max2(max2(c.w[0].x & 0x7fff7fffu, c.w[0].y & 0x7fff7fffu),
+                            max2(c.w[0].z & 0x7fff7fffu, c.w[0].w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+}
+
+// m cos and m sin of u / 2^64 turns, each rounded once (about half a step off;
+// through one fp32 angle it would be two).  With q the nearest quarter turn,
+// the rest x = 2 pi (u / 2^64 - q / 4), |x| <= pi/4, is p + e: p the rounded
+// product of its top 22 bits with 2 pi, e what that leaves out.
+//     sin x = p + (p^3 S(p^2) + e cos p),       S: Taylor to x^9
+//     cos x = (1 - p^2/2) + (p^4 C(p^2) - e sin p), C: Taylor to x^10
+// (first omitted terms 2^-29 and 2^-33 of the result), both sums with the
+// rounding of their first term and of p^2 carried in the second.
+__device__ __forceinline__ void sincos_turns(uint64_t u, float m, float& sn, float& cs) {
+    const uint32_t q = (uint32_t)((u + (1ull << 61)) >> 62);
+    const int64_t r = (int64_t)(u - ((uint64_t)q << 62));
+    const float hi = (float)(int32_t)(r >> 40);                    // 2^-24 turns
+    const float lo = (float)(uint32_t)((uint64_t)(r >> 16) & 0xffffffu);   // 2^-48 turns
+    constexpr float kTwoPi = 6.28318530717958647692f;
+    constexpr float kTwoPiRest = (float)(6.28318530717958647692 - (double)kTwoPi);
+    const float p = hi * (kTwoPi * 0x1p-24f);
+    float e = fmaf(hi, kTwoPi * 0x1p-24f, -p);
+    e = fmaf(hi, kTwoPiRest * 0x1p-24f, e);
+    e = fmaf(lo, kTwoPi * 0x1p-48f, e);
+    const float z = p * p;
+    const float zl = fmaf(p, p, -z);
+    float t = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+    t = fmaf(z, t, 1.f / 120.f);
+    t = fmaf(z, t, -1.f / 6.f);
+    const float st = fmaf(p * z, t, fmaf(-0.5f * z, e, e));
+    const float w = fmaf(-0.5f, z, 1.f);
+    float k = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+    k = fmaf(z, k, -1.f / 720.f);
+    k = fmaf(z, k, 1.f / 24.f);
+    float ct = fmaf(-0.5f, z, 1.f - w);            // what rounding 1 - z/2 left out
+    ct = fmaf(-0.5f, zl, ct);
+    ct = fmaf(z * z, k, ct);
+    ct = fmaf(-e, p + st, ct);
+    const float s = fmaf(p, m, st * m), c = fmaf(w, m, ct * m);
+    const float a = q & 1u ? c : s, b = q & 1u ? s : c;
+    sn = q & 2u ? -a : a;
+    cs = (q + 1u) & 2u ? -b : b;
+}
+
+// The exponent byte e + 127: e is the least >= -126 with top <= 448 * 2^e
+// (top = (1 + f) 2^(E - 127), and 448 = 1.75 * 2^8); 255 for a row that is not
+// finite.
+__device__ __forceinline__ uint32_t fp8_exponent(uint32_t top) {
+    if (top >= 0x7f800000u) return 255u;
+    return (uint32_t)max(1, (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
 }
 // Eight codes of x * 2^-e.
-__device__ __forceinline__ uint2 fp8_codes(const float (&x)[8], int e) {
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);   // e in [-127, 120]
-    const float top = e == 120 ? 240.f : 448.f;   // 256 * 2^120 would read back as an infinity
+__device__ __forceinline__ uint2 fp8_codes(const float (&x)[8], uint32_t byte) {
+    if (byte == 255u) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    const float inv = __uint_as_float((254u - byte) << 23);   // e in [-126, 120]
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        float a = x[2 * k], b = x[2 * k + 1];
-        a = fabsf(a) < INFINITY ? fminf(fmaxf(a * inv, -top), top) : __uint_as_float(0x7fffffffu);
-        b = fabsf(b) < INFINITY ? fminf(fmaxf(b * inv, -top), top) : __uint_as_float(0x7fffffffu);
-        w[k] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        float2 v = make_float2(x[2 * k] * inv, x[2 * k + 1] * inv);
+        if (byte == 247u) {   // 256 * 2^120 would read back as an infinity
+            v.x = fminf(fmaxf(v.x, -240.f), 240.f);
+            v.y = fminf(fmaxf(v.y, -240.f), 240.f);
+        }
+        w[k] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
     }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
@@ -170,11 +239,14 @@ __device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
 
 // args: branch[n], length[n], prefix of touched blocks[n], then the draft
 // tree depths as bytes.
-// T: the rows' type; FP8: the blocks hold 8-bit rows (else rows of T).
-template <typename T, bool FP8, typename A>
+// T: the rows' type; FP8: the blocks hold 8-bit rows (else rows of T); ROPE:
+// keys and queries turn (else every row is stored as it is).
+// Rows go through a thread four at a time (two of fp32), loads first.
+template <typename T, bool FP8, bool ROPE, typename A>
 __global__ void __launch_bounds__(128) k_append_rows(const __grid_constant__ A args, const __grid_constant__ RowsArgs a) {
     pdl_wait();
     constexpr int bs = kBlockSize;
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;
     const int32_t n = a.n, dim = a.dim;
     const int32_t items = dim >> 4;                     // threads per row
     const int32_t lanes = 128 / items;                  // rows in flight, cut to a power of two
@@ -182,7 +254,7 @@ __global__ void __launch_bounds__(128) k_append_rows(const __grid_constant__ A a
     const int32_t item = threadIdx.x % items, lane = threadIdx.x / items;
     // this thread's two chunks, whether they turn, and their first pair
     int32_t c0, c1;
-    if (a.interleaved || a.rot == 0) {
+    if (!ROPE || a.interleaved) {
         c0 = 8 * item;
         c1 = dim / 2 + 8 * item;
     } else if (16 * item < a.rot) {
@@ -192,7 +264,7 @@ __global__ void __launch_bounds__(128) k_append_rows(const __grid_constant__ A a
         c0 = a.rot + 8 * (item - a.rot / 16);
         c1 = c0 + (dim - a.rot) / 2;
     }
-    const bool turn0 = c0 < a.rot, turn1 = c1 < a.rot;
+    const bool turn0 = ROPE && c0 < a.rot, turn1 = ROPE && c1 < a.rot;
     const int32_t n_rows = 2 * a.n_kv + a.nq;           // rows per token: K heads, V heads, Q heads
     const int32_t status = a.meta->status;
     const T* K = static_cast<const T*>(a.K) + blockIdx.y * a.kv_layer;
@@ -220,96 +292,109 @@ __global__ void __launch_bounds__(128) k_append_rows(const __grid_constant__ A a
         const int32_t nt = s1 - s0;
         const int32_t tp = min(lp2, nt <= 1 ? 1 : 1 << (32 - __clz(nt - 1)));
         const int32_t r0 = lane / tp, rstep = lp2 / tp;
-        const bool worker = lane < lp2;
         for (int32_t k0 = 0; k0 < nt; k0 += tp) {
             const int32_t k = k0 + lane % tp;
-            const bool live = worker && k < nt;
+            const bool live = lane < lp2 && k < nt;
             const int32_t slot = s0 + (live ? k : 0);
             const int32_t tok = lblk * bs + slot - L;       // 0 .. n_new - 1
-            float cs[8], sn[8];
-            if (a.rot) {
-                const int32_t pos = L + (a.has_depth ? byte_of(args, 3 * (int64_t)n, (int64_t)(a.one_tree ? 0 : i) * a.n_new + tok) : tok);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int32_t pair = a.interleaved ? (q < 4 ? c0 / 2 + q : c1 / 2 + q - 4) : c0 + q;
-                    const bool on = a.interleaved ? (q < 4 ? turn0 : turn1) : turn0;
-                    cs[q] = 1.f;
-                    sn[q] = 0.f;
-                    if (on) {
-                        const uint64_t f = a.freq[pair & 127] * (uint64_t)(uint32_t)pos;
-                        const float half_turns = (float)(int32_t)(uint32_t)(f >> 32) * 4.656612873077393e-10f;   // 2^-31
-                        sincospif(half_turns, &sn[q], &cs[q]);
-                        cs[q] *= a.m;
-                        sn[q] *= a.m;
-                    }
-                }
-            }
             const int64_t in_row = (int64_t)i * a.n_new + tok;
+            const int64_t kv_at = in_row * a.n_kv * dim, q_at = in_row * a.nq * dim;
             const int32_t n_iter = (n_rows + rstep * (int)gridDim.z - 1) / (rstep * (int)gridDim.z);
-#pragma unroll 2
-            for (int32_t it = 0; it < n_iter; ++it) {
-                const int32_t rr = (it * (int)gridDim.z + (int)blockIdx.z) * rstep + r0;
-                const bool act = live && rr < n_rows;
-                const int32_t kind = rr < a.n_kv ? 0 : rr < 2 * a.n_kv ? 1 : 2;   // K, V, Q
-                const int32_t h = rr - (kind == 0 ? 0 : kind == 1 ? a.n_kv : 2 * a.n_kv);
-                const T* src = kind == 0 ? K : kind == 1 ? V : Q;
-                src += (in_row * (kind == 2 ? a.nq : a.n_kv) + h) * dim;
-                float x[8], y[8];
-                if (act) {
-                    load8(src + c0, x);
-                    load8(src + c1, y);
-                } else {
+            float cs[8], sn[8];
+            for (int32_t it0 = 0; it0 < n_iter; it0 += U) {
+                Chunk<T> x[U], y[U];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) x[q] = y[q] = 0.f;
+                for (int u = 0; u < U; ++u) {
+                    const int32_t rr = ((it0 + u) * (int)gridDim.z + (int)blockIdx.z) * rstep + r0;
+                    if (!live || rr >= n_rows) continue;
+                    const T* src = rr < a.n_kv       ? K + kv_at + rr * dim
+                                   : rr < 2 * a.n_kv ? V + kv_at + (rr - a.n_kv) * dim
+                                                     : Q + q_at + (rr - 2 * a.n_kv) * dim;
+                    load(src + c0, x[u]);
+                    load(src + c1, y[u]);
                 }
-                if (a.rot && kind != 1) {
-                    if (a.interleaved) {
-                        if (turn0) {
+                if (ROPE && it0 == 0) {   // the angles, while the first rows are on their way
+                    const int32_t pos = L + (a.has_depth ? byte_of(args, 3 * (int64_t)n, (int64_t)(a.one_tree ? 0 : i) * a.n_new + tok) : tok);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float u = x[2 * q], v = x[2 * q + 1];
-                                x[2 * q] = u * cs[q] - v * sn[q];
-                                x[2 * q + 1] = v * cs[q] + u * sn[q];
-                            }
-                        }
-                        if (turn1) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float u = y[2 * q], v = y[2 * q + 1];
-                                y[2 * q] = u * cs[4 + q] - v * sn[4 + q];
-                                y[2 * q + 1] = v * cs[4 + q] + u * sn[4 + q];
-                            }
-                        }
-                    } else if (turn0) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float u = x[q], v = y[q];
-                            x[q] = u * cs[q] - v * sn[q];
-                            y[q] = v * cs[q] + u * sn[q];
-                        }
+                    for (int q = 0; q < 8; ++q) {
+                        const int32_t pair = a.interleaved ? (q < 4 ? c0 / 2 + q : c1 / 2 + q - 4) : c0 + q;
+                        const bool on = a.interleaved ? (q < 4 ? turn0 : turn1) : turn0;
+                        cs[q] = 1.f;
+                        sn[q] = 0.f;
+                        if (on) sincos_turns(a.freq[pair & 127] * (uint64_t)(uint32_t)pos, a.m, sn[q], cs[q]);
                     }
                 }
-                char* tile = (kind == 0 ? kp : vp) + ((int64_t)dst * a.n_kv + (kind == 2 ? 0 : h)) * tile_bytes;
-                if constexpr (FP8) {
-                    // the row's largest element: its eight threads are eight neighbouring lanes
-                    float top = fmaxf(finite_max(x), finite_max(y));
 #pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    if (act && kind != 2) {
-                        const int e = fp8_exponent(top);
-                        *reinterpret_cast<uint2*>(tile + fp8_at(slot, c0)) = fp8_codes(x, e);
-                        *reinterpret_cast<uint2*>(tile + fp8_at(slot, c1)) = fp8_codes(y, e);
-                        if (item == 0) tile[bs * kFp8Dim + slot] = (char)(e + 127);
+                for (int u = 0; u < U; ++u) {
+                    const int32_t rr = ((it0 + u) * (int)gridDim.z + (int)blockIdx.z) * rstep + r0;
+                    const bool act = live && rr < n_rows;
+                    const int32_t kind = rr < a.n_kv ? 0 : rr < 2 * a.n_kv ? 1 : 2;   // K, V, Q
+                    const int32_t h = rr - (kind == 0 ? 0 : kind == 1 ? a.n_kv : 2 * a.n_kv);
+                    float f[8], g[8];
+                    uint32_t top = 0;
+                    const bool turns = ROPE && act && kind != 1;
+                    if (turns) {
+                        to_float(x[u], f);
+                        to_float(y[u], g);
+                        if (a.interleaved) {
+                            if (turn0) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const float c = f[2 * q], d = f[2 * q + 1];
+                                    f[2 * q] = c * cs[q] - d * sn[q];
+                                    f[2 * q + 1] = d * cs[q] + c * sn[q];
+                                }
+                            }
+                            if (turn1) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const float c = g[2 * q], d = g[2 * q + 1];
+                                    g[2 * q] = c * cs[4 + q] - d * sn[4 + q];
+                                    g[2 * q + 1] = d * cs[4 + q] + c * sn[4 + q];
+                                }
+                            }
+                        } else if (turn0) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float c = f[q], d = g[q];
+                                f[q] = c * cs[q] - d * sn[q];
+                                g[q] = d * cs[q] + c * sn[q];
+                            }
+                        }
+                        if (!FP8 || kind == 2) {
+                            from_float(f, x[u]);
+                            from_float(g, y[u]);
+                        }
                     }
-                } else if (act && kind != 2) {
-                    T* out = reinterpret_cast<T*>(tile) + slot * dim;
-                    store8(out + c0, x);
-                    store8(out + c1, y);
-                }
-                if (act && kind == 2) {
-                    T* out = q_out + (in_row * a.nq + h) * dim;
-                    store8(out + c0, x);
-                    store8(out + c1, y);
+                    if constexpr (FP8) {
+                        if (act && kind != 2) {
+                            if (turns) top = max(top_bits(f), top_bits(g));
+                            else top = max(top_bits(x[u]), top_bits(y[u]));
+                        }
+                        // the row's largest element: its eight threads are eight neighbouring lanes
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    }
+                    if (!act) continue;
+                    char* tile = (kind == 0 ? kp : vp) + ((int64_t)dst * a.n_kv + (kind == 2 ? 0 : h)) * tile_bytes;
+                    if (kind == 2) {
+                        T* out = q_out + q_at + h * dim;
+                        store(out + c0, x[u]);
+                        store(out + c1, y[u]);
+                    } else if constexpr (FP8) {
+                        if (!turns) {
+                            to_float(x[u], f);
+                            to_float(y[u], g);
+                        }
+                        const uint32_t e = fp8_exponent(top);
+                        *reinterpret_cast<uint2*>(tile + fp8_at(slot, c0)) = fp8_codes(f, e);
+                        *reinterpret_cast<uint2*>(tile + fp8_at(slot, c1)) = fp8_codes(g, e);
+                        if (item == 0) tile[bs * kFp8Dim + slot] = (char)e;
+                    } else {
+                        T* out = reinterpret_cast<T*>(tile) + slot * dim;
+                        store(out + c0, x[u]);
+                        store(out + c1, y[u]);
+                    }
                 }
             }
         }
@@ -331,8 +416,10 @@ __global__ void __launch_bounds__(128) k_append_rows(const __grid_constant__ A a
 
 // ------------------------------------------------------------------ gather
 // args: branch[n], first position[n], output row[n], prefix of touched blocks[n],
-// row count[n].  One CTA per (branch, block) and share of the heads; a thread
-// moves 8 elements, so that a warp's stores cover whole 128-byte lines.
+// row count[n].  One CTA per (branch, block) and share of the heads.  A thread
+// owns 8 elements of the row of one slot and walks the heads with them, four
+// rows' loads in flight, so that nothing is divided in the loop; a warp's
+// stores cover whole 128-byte lines.
 struct ReadArgs {
     int32_t n, bpb, n_kv, dim, n_blocks, uniform, n_tiles;
     const int32_t* table;
@@ -344,10 +431,14 @@ struct ReadArgs {
 };
 
 template <typename T, bool FP8, typename A>
-__global__ void __launch_bounds__(128) k_read_rows(const __grid_constant__ A args, const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(256) k_read_rows(const __grid_constant__ A args, const __grid_constant__ ReadArgs a) {
     pdl_wait();
     constexpr int bs = kBlockSize;
-    const int32_t n = a.n, dim = a.dim, chunks = dim >> 3;
+    constexpr int U = 4;
+    const int32_t n = a.n, dim = a.dim;
+    const int32_t chunks = dim >> 3;                    // threads per row
+    const int32_t lp2 = 1 << (31 - __clz(256 / chunks));
+    const int32_t d = 8 * (threadIdx.x % chunks), lane = threadIdx.x / chunks;
     if (a.meta->status) return;
     const int64_t tile_bytes = FP8 ? kFp8TileBytes : (int64_t)bs * dim * (int)sizeof(T);
     for (int32_t t = blockIdx.x; t < a.n_tiles; t += gridDim.x) {
@@ -361,38 +452,51 @@ __global__ void __launch_bounds__(128) k_read_rows(const __grid_constant__ A arg
             if (threadIdx.x == 0) atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
             return;
         }
+        if (lane >= lp2) continue;
         const int64_t row0 = (int64_t)args[2 * (int64_t)n + i] + lblk * bs - p0;   // output row of slot 0
-        const int32_t per_slot = 2 * a.n_kv * chunks;       // K then V, head, chunk
-        const int32_t total = (s1 - s0) * per_slot;
-#pragma unroll 4
-        for (int32_t e = blockIdx.z * 128 + threadIdx.x; e < total; e += 128 * gridDim.z) {
-            const int32_t slot = s0 + e / per_slot;
-            int32_t r = e % per_slot;
-            const bool v = r >= a.n_kv * chunks;
-            r -= v ? a.n_kv * chunks : 0;
-            const int32_t h = r / chunks, d = 8 * (r % chunks);
-            const char* tile = (v ? a.vp : a.kp) + ((int64_t)src * a.n_kv + h) * tile_bytes;
-            T* out = static_cast<T*>(v ? a.V : a.K) + ((row0 + slot) * a.n_kv + h) * dim + d;
-            if constexpr (FP8) {
-                const uint2 w = *reinterpret_cast<const uint2*>(tile + fp8_at(slot, d));
-                // 2^(byte - 127), a denormal for byte 0
-                const uint32_t b = (unsigned char)tile[bs * kFp8Dim + slot];
-                const float s = __uint_as_float(b ? b << 23 : 0x400000u);
-                const uint32_t q[2] = {w.x, w.y};
-                float x[8];
+        const int32_t nt = s1 - s0;
+        const int32_t tp = min(lp2, nt <= 1 ? 1 : 1 << (32 - __clz(nt - 1)));
+        const int32_t rstep = lp2 / tp * (int)gridDim.z;
+        for (int32_t slot = s0 + lane % tp; slot < s1; slot += tp) {
+            for (int32_t r0 = (int)blockIdx.z * (lp2 / tp) + lane / tp; r0 < 2 * a.n_kv; r0 += U * rstep) {
+                Chunk<T> x[U];
+                uint2 w[U];
+                uint32_t e[U];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-                    const float2 f = __half22float2(__half2(hr));
-                    x[2 * k] = f.x * s;
-                    x[2 * k + 1] = f.y * s;
+                for (int u = 0; u < U; ++u) {
+                    const int32_t r = r0 + u * rstep;
+                    if (r >= 2 * a.n_kv) continue;
+                    const char* tile = (r < a.n_kv ? a.kp : a.vp) +
+                                       ((int64_t)src * a.n_kv + (r < a.n_kv ? r : r - a.n_kv)) * tile_bytes;
+                    if constexpr (FP8) {
+                        w[u] = *reinterpret_cast<const uint2*>(tile + fp8_at(slot, d));
+                        e[u] = (unsigned char)tile[bs * kFp8Dim + slot];
+                    } else {
+                        load(reinterpret_cast<const T*>(tile) + slot * dim + d, x[u]);
+                    }
                 }
-                store8(out, x);
-            } else {
-                constexpr int W = 8 * sizeof(T) / 16;
-                const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(tile) + slot * dim + d);
 #pragma unroll
-                for (int k = 0; k < W; ++k) reinterpret_cast<uint4*>(out)[k] = from[k];
+                for (int u = 0; u < U; ++u) {
+                    const int32_t r = r0 + u * rstep;
+                    if (r >= 2 * a.n_kv) continue;
+                    T* out = static_cast<T*>(r < a.n_kv ? a.K : a.V) +
+                             ((row0 + slot) * a.n_kv + (r < a.n_kv ? r : r - a.n_kv)) * dim + d;
+                    if constexpr (FP8) {
+                        const float s = __uint_as_float(e[u] << 23);   // 2^e
+                        const uint32_t q[2] = {w[u].x, w[u].y};
+                        float f[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                                (__nv_fp8x2_storage_t)(q[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+                            const float2 v = __half22float2(__half2(hr));
+                            f[2 * k] = v.x * s;
+                            f[2 * k + 1] = v.y * s;
+                        }
+                        from_float(f, x[u]);
+                    }
+                    store(out, x[u]);
+                }
             }
         }
     }
@@ -472,6 +576,11 @@ __global__ void __launch_bounds__(128) k_keep_rows(const __grid_constant__ A arg
 // Calls `go` with the argument words: as kernel parameters, or staged.
 template <typename Fill, typename Go>
 int with_words(dendrite_pool* p, size_t words, cudaStream_t s, Fill fill, Go go) {
+    if (words <= (size_t)kRowsSmall) {
+        ParamWords<kRowsSmall> a;
+        fill(a.v);
+        return go(a);
+    }
     if (words <= (size_t)kRowsCap) {
         ParamWords<kRowsCap> a;
         fill(a.v);
@@ -571,7 +680,7 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s) {
             // turns per position modulo one: whole turns change nothing at whole positions
             const double turns = c.rope->inv_freq[k] * 0.15915494309189533577;   // 1 / (2 pi)
             const double frac = turns - std::floor(turns);
-            a.freq[k] = frac >= 1.0 ? 0 : (uint64_t)std::ldexp(frac, 64);
+            a.freq[k] = frac >= 1.0 ? 0 : (uint64_t)(frac * 18446744073709551616.0);
         }
         a.has_depth = c.depth != nullptr;
         a.one_tree = c.n_trees == 1;
@@ -606,12 +715,14 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s) {
     const dim3 grid((unsigned)std::min<int64_t>(c.touched, (int64_t)p->sm_count * 64), (unsigned)c.n_layers_in, z);
     return with_words(p, words, s, fill, [&](auto args) -> int {
         using A = decltype(args);
-        if (p->dtype == DENDRITE_FP8)
-            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, A>, grid, dim3(128), 0, s, args, a));
+        if (p->dtype == DENDRITE_FP8 && !c.rope)
+            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, false, A>, grid, dim3(128), 0, s, args, a));
+        else if (p->dtype == DENDRITE_FP8)
+            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, true, A>, grid, dim3(128), 0, s, args, a));
         else if (p->dtype == DENDRITE_BF16)
-            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, false, A>, grid, dim3(128), 0, s, args, a));
+            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, false, true, A>, grid, dim3(128), 0, s, args, a));
         else
-            DENDRITE_CUDA(launch_pdl(k_append_rows<float, false, A>, grid, dim3(128), 0, s, args, a));
+            DENDRITE_CUDA(launch_pdl(k_append_rows<float, false, true, A>, grid, dim3(128), 0, s, args, a));
         return DENDRITE_OK;
     });
 }
@@ -712,17 +823,21 @@ int dendrite_read_kv(dendrite_pool* p, int32_t layer, const int32_t* branches, c
             tile += counts[i] ? (starts[i] + counts[i] - 1) / bs - starts[i] / bs + 1 : 0;
         }
     };
-    const int64_t per_tile = (int64_t)bs * 2 * p->n_kv * p->head_dim / 8;   // 8-element moves
+    // rows side by side in a CTA, as in the append: over a tile's tokens first, the rest over heads
+    int32_t lanes = 256 / (p->head_dim / 8), tp = 1, longest = 0;
+    while (lanes & (lanes - 1)) lanes &= lanes - 1;
+    for (int32_t i = 0; i < n; ++i) longest = std::max(longest, counts[i]);
+    while (tp < lanes && tp < std::min(longest, bs)) tp *= 2;
     const dim3 grid((unsigned)std::min<int64_t>(tiles, (int64_t)p->sm_count * 64), 1,
-                    head_splits(p, tiles, std::max<int64_t>(1, per_tile / 256)));
+                    head_splits(p, tiles, (2 * p->n_kv + lanes / tp - 1) / (lanes / tp)));
     return with_words(p, 5 * (size_t)n, s, fill, [&](auto args) -> int {
         using A = decltype(args);
         if (p->dtype == DENDRITE_FP8)
-            DENDRITE_CUDA(launch_pdl(k_read_rows<__nv_bfloat16, true, A>, grid, dim3(128), 0, s, args, a));
+            DENDRITE_CUDA(launch_pdl(k_read_rows<__nv_bfloat16, true, A>, grid, dim3(256), 0, s, args, a));
         else if (p->dtype == DENDRITE_BF16)
-            DENDRITE_CUDA(launch_pdl(k_read_rows<__nv_bfloat16, false, A>, grid, dim3(128), 0, s, args, a));
+            DENDRITE_CUDA(launch_pdl(k_read_rows<__nv_bfloat16, false, A>, grid, dim3(256), 0, s, args, a));
         else
-            DENDRITE_CUDA(launch_pdl(k_read_rows<float, false, A>, grid, dim3(128), 0, s, args, a));
+            DENDRITE_CUDA(launch_pdl(k_read_rows<float, false, A>, grid, dim3(256), 0, s, args, a));
         return DENDRITE_OK;
     });
 }

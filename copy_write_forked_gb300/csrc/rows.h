@@ -10,7 +10,8 @@ namespace dendrite {
 // 8-bit pools: a (block, kv head) tile is 16 rows of 128 e4m3 codes, the
 // 16-byte chunk c of slot s at chunk c ^ (s & 7) (so that the attention
 // kernel's loads of eight slots fall in distinct banks), then one exponent
-// byte per slot: value = code * 2^(byte - 127).
+// byte per slot: value = code * 2^(byte - 127), byte 1..247; 255: a row of NaN.
+// A slot never written holds byte 0 and codes 0.
 constexpr int kFp8Dim = 128;
 constexpr int kFp8TileBytes = kBlockSize * kFp8Dim + kBlockSize;
 constexpr int kMaxDraft = 64;   // drafted tokens per branch: one mask bit each

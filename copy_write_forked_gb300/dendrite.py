@@ -372,20 +372,23 @@ class Pool:
         self._check_tensor(V, "V")
         if not isinstance(rope, Rope):
             raise DendriteError(-1, "rope must be a Rope")
-        want = lead + (n, n_new, self.n_kv_heads, self.head_dim)
-        if tuple(K.shape) != want or K.shape != V.shape:
-            raise DendriteError(-1, f"K/V shape {tuple(K.shape)}")
+        ks = K.shape
+        if ks != lead + (n, n_new, self.n_kv_heads, self.head_dim) or V.shape != ks:
+            raise DendriteError(-1, f"K/V shape {tuple(ks)}")
         if Q is None:
             return None, 0, None
         self._check_tensor(Q, "Q")
-        if Q.dim() != len(want) or Q.shape[:-2] != K.shape[:-2] or Q.shape[-1] != self.head_dim:
-            raise DendriteError(-1, f"Q shape {tuple(Q.shape)}")
+        qs = Q.shape
+        nq = qs[-2] if len(qs) > 1 else 0
+        if qs != lead + (n, n_new, nq, self.head_dim):
+            raise DendriteError(-1, f"Q shape {tuple(qs)}")
         if out is None:
             out = torch.empty_like(Q)
-        self._check_tensor(out, "out")
-        if out.shape != Q.shape:
-            raise DendriteError(-1, "out shape")
-        return Q.data_ptr(), Q.shape[-2], out
+        else:
+            self._check_tensor(out, "out")
+            if out.shape != qs:
+                raise DendriteError(-1, "out shape")
+        return Q.data_ptr(), nq, out
 
     def append_rope(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, rope: Rope,
                     Q: Optional[torch.Tensor] = None, parents=None, out: Optional[torch.Tensor] = None,
@@ -395,7 +398,8 @@ class Pool:
         several) is turned too and returned (``out`` may be Q).  ``parents``:
         the new tokens are draft trees (int32 ``[n_new]`` for every branch or
         ``[n_branches][n_new]``, -1 or an earlier index), token j at its depth."""
-        nb, n_new = len(branches), K.shape[-3] if K.dim() >= 4 else 0
+        ks = K.shape
+        nb, n_new = len(branches), ks[-3] if len(ks) >= 4 else 0
         lead = () if self.n_layers == 1 else (self.n_layers,)
         qp, nq, out = self._rotated(K, V, rope, Q, out, lead, nb, n_new)
         keep, pp, nt = _trees(parents, nb, n_new)
@@ -457,9 +461,8 @@ class Pool:
         total = sum(counts)
         if total > len(branches) * self._max_len:   # past any branch: refused before the rows are allocated
             raise DendriteError(-1, "read_kv counts")
-        shape = (max(0, total), self.n_kv_heads, self.head_dim)
-        k = torch.empty(shape, dtype=self.dtype, device=self.device)
-        v = torch.empty(shape, dtype=self.dtype, device=self.device)
+        k = torch.empty((max(0, total), self.n_kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
+        v = torch.empty_like(k)
         _check(lib().dendrite_read_kv(self._h, int(layer), _ptr(ba), _ptr(sa), _ptr(ca), len(branches), k.data_ptr(),
                                       v.data_ptr(), _stream_ptr(stream, self._dev)), "read_kv")
         return k, v

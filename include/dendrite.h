@@ -128,14 +128,14 @@ typedef struct dendrite_pool_opts {
  * stack int32[num_blocks] starts as [num_blocks-1, ..., 0] so block 0 is handed
  * out first; block tables int32[max_branches][max_blocks_per_branch] (-1 = empty).
  * 8-bit pools (DENDRITE_FP8) quantise every row of 128 as it is appended: e is
- * the least integer >= -127 with max|x| <= 448 * 2^e over the row's finite
- * elements, and x is stored as the e4m3 number nearest to x * 2^-e (ties to
- * even; at most 240 where e = 120, so that it reads back finite; a NaN or an
- * infinity as NaN).  A (block, head) tile is 2,064 bytes: 16
- * slots of 128 codes, the 16-byte chunk c of slot s at chunk c ^ (s & 7), then
- * the 16 slots' exponent bytes e + 127.  129 bytes per row instead of bf16's
- * 256; a row reads back as code * 2^e, which bf16 holds exactly, and attention
- * reads those values.
+ * the least integer >= -126 with max|x| <= 448 * 2^e, and x is stored as the
+ * e4m3 number nearest to x * 2^-e (ties to even; at most 240 where e = 120, so
+ * that it reads back finite).  A row with a NaN or an infinity is stored as NaN
+ * throughout.  A (block, head) tile is 2,064 bytes: 16 slots of 128 codes, the
+ * 16-byte chunk c of slot s at chunk c ^ (s & 7), then the 16 slots' exponent
+ * bytes e + 127 (255: a row of NaN).  129 bytes per row instead of bf16's 256;
+ * a row reads back as code * 2^e, which bf16 holds exactly, and attention reads
+ * those values.
  * Synchronous.  Uses the current CUDA device.
  */
 int dendrite_pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads,

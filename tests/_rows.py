@@ -25,22 +25,24 @@ E4M3 = e4m3_values()
 
 
 def quantise(x):
-    """x [..., 128] -> (codes uint8, exponents int): nearest code, ties to even, of x * 2^-e."""
+    """x [..., 128] -> (codes uint8, exponents int): nearest code, ties to even, of x * 2^-e; a row
+    that is not finite is NaN throughout, with exponent 128."""
     x = np.asarray(x, np.float64)
-    fine = np.isfinite(x)
-    top = np.where(fine, np.abs(x), 0).max(-1)
-    e = np.full(top.shape, -127)
-    for k in range(-126, 121):     # the least e with top <= 448 * 2^e
+    fine = np.isfinite(x).all(-1)
+    x = np.where(fine[..., None], x, 0)
+    top = np.abs(x).max(-1)
+    e = np.full(top.shape, -126)
+    for k in range(-125, 121):     # the least e with top <= 448 * 2^e
         e = np.where(top > 448 * 2.0 ** (k - 1), k, e)
-    y = np.where(fine, np.abs(x), 0) * 2.0 ** -e[..., None].astype(float)
+    y = np.abs(x) * 2.0 ** -e[..., None].astype(float)
     y = np.where(e[..., None] == 120, np.minimum(y, 240.0), y)   # 256 * 2^120 is past bf16
     pos = E4M3[:127]
     hi = np.clip(np.searchsorted(pos, y), 0, 126)
     lo = np.clip(hi - 1, 0, 126)
     up = (pos[hi] - y < y - pos[lo]) | ((pos[hi] - y == y - pos[lo]) & (hi % 2 == 0))
     code = np.where(up | (pos[hi] == y), hi, lo).astype(np.uint8)
-    code |= (np.signbit(x) & fine).astype(np.uint8) << 7
-    return np.where(fine, code, 0x7f).astype(np.uint8), e
+    code |= np.signbit(x).astype(np.uint8) << 7
+    return np.where(fine[..., None], code, 0x7f).astype(np.uint8), np.where(fine, e, 128)
 
 
 def dequantise(codes, e):
@@ -186,13 +188,17 @@ def attention_bound(kind, out, dev, mag, size, top):
     numerator's to fp16, 2^-11 mag, or, where a weight times its token's scale is under
     2^-14 of the largest of them, by 2^-25 of that largest: a scale is under
     max|v| / 224 and a code at most 448, so 2 * 2^-25 `top` over all tokens; queries as
-    fp16 lose 2^-25 of the row's largest element each, inside the scores' 2^-16.  The exponentials, the running rescales
+    fp16 lose 2^-25 of the row's largest element each, inside the scores' 2^-16.
+    Segments of many rows of an fp8 pool run the bf16 kernel's products on the exact
+    bf16 values of the codes, its weights rounded to bf16 too: the larger of the two.  The exponentials, the running rescales
     and the merge: a few 2^-22 of mag each, below 2^-18 together.
     The stored output: half a step, 2^-8 of it in bf16, 2^-24 in fp32."""
     scores = 2 * 2.0 ** -16 * size * dev + 2.0 ** -18 * mag
     if kind == "fp32":
         return scores + 2.0 ** -24 * np.abs(out) + 1e-30
-    weights = 2.0 ** -11 * mag + 2.0 ** -24 * top if kind == "fp8" else 1.01 * 2.0 ** -8 * dev
+    weights = 1.01 * 2.0 ** -8 * dev
+    if kind == "fp8":
+        weights = np.maximum(weights, 2.0 ** -11 * mag + 2.0 ** -24 * top)
     return scores + weights + 2.0 ** -8 * (np.abs(out) + scores + weights) + 1e-30
 
 

@@ -216,7 +216,7 @@ def test_rows_that_are_not_finite_stay_in_their_row():
         assert np.isfinite(k[[0, 3]]).all()
         for row, col in ((1, 5), (2, 9)):
             bad = np.flatnonzero(~np.isfinite(k[row])).tolist()
-            assert set(bad) <= {col, col + 64} and bad
+            assert bad == list(range(128)) if kind == "fp8" else set(bad) <= {col, col + 64} and bad
         pool.close()
 
 
