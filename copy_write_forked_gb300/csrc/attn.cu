@@ -1515,6 +1515,7 @@ struct HostPlan {
     std::vector<int64_t> cuts;
     int64_t tiles = 0, unique_tiles = 0;
     int32_t n_tc_units = 0;
+    int32_t tc_rows = 0;             // segments with more rows per kv head go to the tcgen05 kernel (set per call)
     size_t partial_rows = 0;
     std::vector<int32_t> parent, fork_len, len, queried, seg_members, cursor;
     std::vector<Segment> psegs;
@@ -1657,10 +1658,10 @@ int build_plan(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_l
     static thread_local std::vector<int32_t> prev;
     prev.clear();
     if (bf16 && p->pack_pct >= 0)
-        pack_segments(FoldParams{RM, tc_on ? p->tc_min_rows : -1, small_rows, p->fold_pct}, p->pack_pct, n_nodes,
+        pack_segments(FoldParams{RM, tc_on ? hp.tc_rows : -1, small_rows, p->fold_pct}, p->pack_pct, n_nodes,
                       hp.parent.data(), hp.fork_len.data(), p->block_size, hp.psegs, hp.seg_members, hp.pxt, &prev);
     if (p->fold_pct >= 0)
-        fold_segments(FoldParams{RM, tc_on ? p->tc_min_rows : -1, small_rows, p->fold_pct}, n_nodes,
+        fold_segments(FoldParams{RM, tc_on ? hp.tc_rows : -1, small_rows, p->fold_pct}, n_nodes,
                       hp.parent.data(), hp.fork_len.data(), hp.len.data(), p->block_size, hp.queried.data(), n,
                       hp.psegs, hp.seg_members, &prev);
     return build_units(p, branches, n, q_len, nq, max_ctas, max_tc_ctas, hp, allow_device);
@@ -1744,12 +1745,12 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
     const bool tc_on = max_tc_ctas > 0 && p->tc_min_rows >= 0;
     // Segments, their members and their units (kv head major, then row
     // group), tensor-core segments first: pass 0 takes the segments read by
-    // more than tc_min_rows rows per kv head, pass 1 the rest.
+    // more than tc_rows rows per kv head, pass 1 the rest.
     size_t n_units_total = 0, n_members_total = 0, n_tiles_total = 0;
     for (const Segment& sg : hp.psegs) {
         if ((int64_t)sg.n_members * RM >= (int64_t)1 << 24) return DENDRITE_ELIMIT;   // rows as exact fp32
         const int32_t rows_per_head = sg.n_members * RM;
-        const int32_t group_rows = (tc_on && rows_per_head > p->tc_min_rows) ? kMaxUnitRowsTc : small_rows;
+        const int32_t group_rows = (tc_on && rows_per_head > hp.tc_rows) ? kMaxUnitRowsTc : small_rows;
         const size_t units = (size_t)nkv * ((rows_per_head + group_rows - 1) / group_rows);
         if (sg.n_x && units != (size_t)nkv) return DENDRITE_EINVAL;   // packed: one row group per kv head
         if (sg.n_x > kMaxTcExtraTiles && group_rows == kMaxUnitRowsTc) return DENDRITE_ELIMIT;
@@ -1786,7 +1787,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
         int64_t tile_off = 0, weight = 0;
         for (const Segment& sg : hp.psegs) {
             const int32_t rows_per_head = sg.n_members * RM;
-            const bool tc = tc_on && rows_per_head > p->tc_min_rows;
+            const bool tc = tc_on && rows_per_head > hp.tc_rows;
             if (tc != (pass == 0)) continue;
             const int32_t group_rows = tc ? kMaxUnitRowsTc : small_rows;
             AttnSeg S;
@@ -2442,6 +2443,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
         const auto t0 = std::chrono::steady_clock::now();
         static thread_local HostPlan hp;
         hp.clear();
+        hp.tc_rows = parents ? p->tc_min_rows_draft : p->tc_min_rows;
         if (grow) {
             hp.psegs = pc.segs;
             hp.seg_members = pc.seg_members;
@@ -2488,7 +2490,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
             const int32_t rpm = q_len * (n_q_heads / p->n_kv);
             const bool tc_on = p->dtype == DENDRITE_BF16 && tc_ctas(p) > 0;
             for (const Segment& sg : hp.psegs)
-                if (tc_on && sg.n_x > kMaxTcExtraTiles && (int64_t)sg.n_members * rpm > p->tc_min_rows) grow = false;
+                if (tc_on && sg.n_x > kMaxTcExtraTiles && (int64_t)sg.n_members * rpm > hp.tc_rows) grow = false;
             if (!grow) hp.clear();
         }
         if (grow) {
@@ -2688,6 +2690,7 @@ extern "C" int dendrite_tree_attn_decode_noalloc(dendrite_pool* p, const void* Q
     DENDRITE_TRY(noalloc_scratch(p->device, &scratch));
     static thread_local HostPlan hp;
     hp.clear();
+    hp.tc_rows = p->tc_min_rows;
     DENDRITE_TRY(build_plan(p, branches, n, q_len, n_q_heads, p->sm_count * p->attn_ctas_per_sm, tc_ctas(p), hp,
                             false));
     // scratch layout: plan sections, then partial acc rows, then partial (m, l)

@@ -22,8 +22,13 @@ constexpr int kMaxUnitRowsF32 = 16;
 constexpr int kMaxUnitRowsTurbo = 64;  // rows per compressed-pool unit (4 warps x 16 rows)
 constexpr int kMaxUnitRowsFp8 = 64;    // rows per 8-bit-pool unit (4 warps x 16 rows)
 constexpr int kMaxUnitRowsTc = 256;   // rows per tcgen05 attention unit (2 row tiles of 128)
-constexpr int kTcMinRowsFp8 = 32;     // the same for 8-bit pools
 constexpr int kTcMinRowsDefault = 64; // segments with more rows per kv head use the tcgen05 kernel
+// The same for 8-bit pools and for draft trees over bf16 pools.  32 branches
+// of about 7,500 tokens, 8 kv heads, draft trees, small kernel / tcgen05
+// kernel: 8-bit 145 / 199 us at 32 rows and 238 / 211 at 36; bf16 121 / 145
+// at 16 rows, 188 / 150 at 20 and 260 / 137 at 64.
+constexpr int kTcMinRowsFp8 = 32;
+constexpr int kTcMinRowsDraft = 16;
 constexpr int32_t kFoldPctDefault = 100;  // fold a segment when that is estimated cheaper
 constexpr int32_t kPackPctDefault = 100;  // pack a segment's followers into it when that is estimated cheaper
 constexpr int kAppendMetaThreads = 1024;
@@ -270,6 +275,7 @@ struct dendrite_pool {
     int sm_count = 0;
     int attn_ctas_per_sm = 1;
     int32_t tc_min_rows = dendrite::kTcMinRowsDefault;   // < 0: tensor-core attention kernel off
+    int32_t tc_min_rows_draft = dendrite::kTcMinRowsDraft;   // the same, for draft trees
     int32_t tc_sms = 0;   // SMs of the tcgen05 kernel beside the mma.sync one (0: estimated, -1: no split)
     int32_t fold_pct = dendrite::kFoldPctDefault;        // < 0: segments are never folded
     int32_t pack_pct = dendrite::kPackPctDefault;        // < 0: segments are never packed

@@ -1161,8 +1161,8 @@ int pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads, int3
     p->elt = dtype == DENDRITE_FP32 ? 4 : 2;   // compressed and 8-bit pools take bf16 rows
     p->max_branches = max_branches;
     p->bpb = bpb;
-    if (dtype == DENDRITE_FP8) p->tc_min_rows = kTcMinRowsFp8;
-    if (opts && opts->tc_min_rows) p->tc_min_rows = opts->tc_min_rows;
+    if (dtype == DENDRITE_FP8) p->tc_min_rows = p->tc_min_rows_draft = kTcMinRowsFp8;
+    if (opts && opts->tc_min_rows) p->tc_min_rows = p->tc_min_rows_draft = opts->tc_min_rows;
     if (opts) p->tc_sms = opts->tc_sms;
     if (opts && opts->pack_segments) p->pack_pct = opts->pack_segments;
     if (opts && opts->n_layers) p->n_layers = opts->n_layers;

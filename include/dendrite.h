@@ -76,10 +76,11 @@ typedef struct dendrite_pool dendrite_pool;
 typedef struct dendrite_pool_opts {
     int32_t max_branches;          /* live handles at once (default 4096)                 */
     int32_t max_blocks_per_branch; /* block-table row length (default 4096 = 64K tokens)  */
-    int32_t tc_min_rows;           /* bf16 attention: sharing segments read by more than  *
-                                    * this many query rows per KV head run on the tcgen05 *
-                                    * (tensor memory) kernel, the others on the mma.sync  *
-                                    * kernel.  0 = default (64); -1 = never.               */
+    int32_t tc_min_rows;           /* bf16 and 8-bit attention: sharing segments read by  *
+                                    * more than this many query rows per KV head run on   *
+                                    * the tcgen05 (tensor memory) kernel, the others on   *
+                                    * the mma.sync kernel.  0 = default (bf16 64, draft   *
+                                    * trees over bf16 16, 8-bit 32); -1 = never.           */
     int32_t n_layers;              /* model layers held (0 = 1): every layer has its own  *
                                     * K and V pools; block ids, tables, refcounts and the *
                                     * free stack are shared by all layers.                */

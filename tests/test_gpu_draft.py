@@ -377,3 +377,19 @@ def test_refusals():
     assert [c.pool.branch_len(b) for b in c.br] == [85, 85]
     c.pool.sync()
     c.pool.close()
+
+
+@pytest.mark.parametrize("kind,new,decode_tc,draft_tc", [("bf16", 4, False, False), ("bf16", 5, False, True), ("bf16", 16, False, True),
+                                                         ("bf16", 17, True, True), ("fp8", 8, False, False), ("fp8", 9, True, True)])
+def test_rows_per_head_choose_the_kernel(kind, new, decode_tc, draft_tc):
+    """4 rows per drafted token: the tcgen05 kernel from the documented rows on, for each kind of call, and for each its own."""
+    rng = random.Random(11)
+    c = Case(kind, [100, 33, 7], new, 2, 4)
+    c.append(c.br, new)
+    q = torch.randn(len(c.br), new, 8, 128, dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):      # a draft call after a decode call of the same rows, and the other way round
+        c.pool.tree_attn_decode(q, c.br)
+        assert (c.pool.last_plan_stats()["n_tc_units"] > 0) == decode_tc
+        c.attend(c.br, [R.tree(rng, new) for _ in c.br])
+        assert (c.pool.last_plan_stats()["n_tc_units"] > 0) == draft_tc
+    c.pool.close()
