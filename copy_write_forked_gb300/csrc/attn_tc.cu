@@ -22,9 +22,9 @@
 //   warps 0, 11 TMA producers: stream 64-token stages (4 blocks of 16 tokens)
 //               of K and of V into two 4-stage rings, block ids fetched 32
 //               tiles at a time.
-//   warps 1, 12 TMEM owner (warp 1); lane 0 issues the S MMAs of row tile
-//               0 (warp 1) or 1 (warp 12) and their commits.
-//   warps 10, 13 lane 0 issues the P V MMAs of row tile 0 or 1.
+//   warps 1, 12 TMEM owner (warp 1); an elected lane issues the S MMAs of row
+//               tile 0 (warp 1) or 1 (warp 12) and their commits.
+//   warps 10, 13 an elected lane issues the P V MMAs of row tile 0 or 1.
 //   warps 2-9   softmax, one query row per thread (warps 2-5 row tile 0,
 //               warps 6-9 row tile 1): read the row of S from TMEM, mask,
 //               exponentiate (base 2), write P (bf16) back into the first 32
@@ -66,23 +66,40 @@ constexpr int TC_SOFTMAX_WARP0 = 2;
 constexpr int TC_PV_WARP = TC_SOFTMAX_WARP0 + 4 * TC_ROWTILES;   // 10
 constexpr int TC_V_WARP = TC_PV_WARP + 1;                          // 11
 constexpr int TC_S1_WARP = TC_V_WARP + 1;                          // 12
-// Shared memory of a bf16 pool's kernel, and of an 8-bit pool's (F8), whose
-// rings are a stage shorter to make room for the tiles as they are stored:
-// F8_RAW slots of a stage's four tiles (K and V each).  Warp 12 copies them,
-// warps 0, 13, 14 and 11, one on each SM partition, convert a tile each, warp
-// 1 issues S for both row tiles and warp 15 is the second PV issuer.
+// Shared memory and roles of a bf16 pool's kernel, and of an 8-bit pool's (F8).
+// The K ring of that one is two stages (a slot is free again once S is issued;
+// V's is held until P V is done) to make room for the tiles as they are stored:
+// F8_RAW slots of a stage's four tiles (K and V each).  Its 21 warps, of 80
+// registers a thread: 0-7 softmax, 8-11 the issuers (S and PV of row tile 0, then
+// of 1), 12 copies the stored tiles, 13-20 convert one half tile (K or V) each.
+//
+// What bounds it is the issue of instructions: 4,096 scores and 16,384 codes a
+// stage of 64 rows take some 2,000 cycles, half of them issuing.  The attention of
+// 32 draft trees of 16 nodes (64 rows a kv head) over 7,000 tokens each, 360 MB of
+// codes, takes 140 us (2.6 TB/s); of 12 trees of 32 nodes (256 rows) over 16,000
+// tokens 124 us.  On the way there, the first case / the second:
+//   - one branch-selected issuer thread a row tile, one unit on one row tile: 191 / 148 us
+//   - an elected lane of a converged warp as issuer, units of up to 128 rows
+//     split along their tokens (below): 154 / 134
+//   - packed fp32 arithmetic, scores read twice instead of held, an issuer each
+//     for S and PV of both row tiles, K ring of 2 and V ring of 4 stages: 140 / 124
+// Waits and the rescaling of O are out of line and the issuers share their code:
+// with everything in line a tenth of the instruction fetches missed the SM's cache.
 constexpr int F8_RAW = 3;
 constexpr int F8_RAW_TILE = 2 * kFp8TileBytes;
 constexpr int F8_RAW_SLOT = 4 * F8_RAW_TILE;
+constexpr int F8_ISSUE_WARP = 8, F8_COPY_WARP = 12, F8_CONV_WARP = 13;
 template <bool F8>
 struct TcLayout {
-    static constexpr int NSTAGE = F8 ? 3 : 4;
-    static constexpr int PV1_WARP = F8 ? 15 : TC_S1_WARP + 1;
-    static constexpr int THREADS = (PV1_WARP + 1) * 32;
-    // K ring, then V ring: each NSTAGE stages of 64 tokens
+    static constexpr int NK = F8 ? 2 : 4, NV = 4;   // stages of the K and V rings
+    static constexpr int S0_WARP = F8 ? F8_ISSUE_WARP : 1;   // owns the TMEM too
+    static constexpr int PV1_WARP = TC_S1_WARP + 1;
+    static constexpr int SOFTMAX_WARP0 = F8 ? 0 : TC_SOFTMAX_WARP0;
+    static constexpr int THREADS = F8 ? 672 : (PV1_WARP + 1) * 32;
+    // K ring, then V ring, in stages of 64 tokens
     static constexpr int OFF_K = 0;
-    static constexpr int OFF_V = NSTAGE * TC_RING_STAGE;
-    static constexpr int OFF_Q = 2 * NSTAGE * TC_RING_STAGE;
+    static constexpr int OFF_V = NK * TC_RING_STAGE;
+    static constexpr int OFF_Q = (NK + NV) * TC_RING_STAGE;
     static constexpr int OFF_RAW = OFF_Q + TC_ROWTILES * TC_QTILE;
     // draft trees: the mask of each row, written and read by the row's thread
     static constexpr int OFF_MASK = OFF_RAW + (F8 ? F8_RAW * F8_RAW_SLOT : 0);
@@ -91,22 +108,28 @@ struct TcLayout {
     // S_FULL when S is in the buffer, P_FULL when P overwrote it, PV_DONE when
     // the P V product that read that P has completed (the buffer is free again)
     static constexpr int B_K_FULL = 0;
-    static constexpr int B_K_EMPTY = B_K_FULL + NSTAGE;
-    static constexpr int B_V_FULL = B_K_EMPTY + NSTAGE;
-    static constexpr int B_V_EMPTY = B_V_FULL + NSTAGE;
-    static constexpr int B_S_FULL = B_V_EMPTY + NSTAGE;
+    static constexpr int B_K_EMPTY = B_K_FULL + NK;
+    static constexpr int B_V_FULL = B_K_EMPTY + NK;
+    static constexpr int B_V_EMPTY = B_V_FULL + NV;
+    static constexpr int B_S_FULL = B_V_EMPTY + NV;
     static constexpr int B_P_FULL = B_S_FULL + 4;
     static constexpr int B_PV_DONE = B_P_FULL + 4;
     static constexpr int B_Q_FULL = B_PV_DONE + 4;
     static constexpr int B_FINAL = B_Q_FULL + 2;   // one per issuer: S0, PV0, S1, PV1
     static constexpr int B_RAW_FULL = B_FINAL + 4;      // F8: the copied tiles
     static constexpr int B_RAW_EMPTY = B_RAW_FULL + (F8 ? F8_RAW : 0);
-    static constexpr int B_COUNT = B_RAW_EMPTY + (F8 ? F8_RAW : 0);
+    // F8, split units: (m, l) of both groups written; both accumulators read
+    static constexpr int B_ML_FULL = B_RAW_EMPTY + (F8 ? F8_RAW : 0);
+    static constexpr int B_ML_DONE = B_ML_FULL + (F8 ? 1 : 0);
+    static constexpr int B_COUNT = B_ML_DONE + (F8 ? 1 : 0);
     // a packed unit's extra tiles (logical block, member mask), per row tile
     static constexpr int OFF_XINFO = OFF_BAR + B_COUNT * 8 + 16;
-    static constexpr int SMEM = 1024 + OFF_XINFO + TC_ROWTILES * kMaxTcExtraTiles * 8;
+    // F8: (m, l) of the rows of a split unit, per group
+    static constexpr int OFF_ML = OFF_XINFO + TC_ROWTILES * kMaxTcExtraTiles * 8;
+    static constexpr int SMEM = 1024 + OFF_ML + (F8 ? TC_ROWTILES * 128 * 8 : 0);
 };
-static_assert(TcLayout<false>::SMEM <= 227 * 1024 - 64 && TcLayout<true>::SMEM <= 227 * 1024 - 64, "shared memory budget");
+static_assert(TcLayout<false>::SMEM <= 227 * 1024 - 64 && TcLayout<true>::SMEM <= 227 * 1024 - 64,
+              "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float RESCALE_THRESHOLD = 8.f;
 
@@ -118,6 +141,9 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
     return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
            (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
+// A descriptor `bytes` further (the start address does not leave its field:
+// shared memory ends below 2^18).
+__device__ __forceinline__ uint64_t sdesc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 // Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B,
 // A/B major-ness (0 = K-major, 1 = MN-major), N >> 3, M >> 4.
 __device__ __forceinline__ uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
@@ -144,12 +170,49 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                  : "memory");
 }
+// One lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
 // 2^x by the SFU (PTX ex2.approx.ftz.f32: relative error about 2^-22,
 // results below 2^-126 flushed to zero; 2^-inf = +0).
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Two fp32 in one register pair and their packed arithmetic (each rounded as
+// the scalar instruction rounds).
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float low(f32x2 x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float high(f32x2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// The largest of three (a NaN counts for nothing, as in fmaxf).
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return d;
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -174,12 +237,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         TC_W8(0), TC_W8(8), TC_W8(16), TC_W8(24)
         : "memory");
 }
+// 16 columns.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        TC_W8(0), TC_W8(8)
+        : "memory");
+}
 #define TC_RW8(i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), \
                   "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7])
 // Wait for this thread's tcgen05.ld results.  The registers pass through the
 // statement so that no use of them is scheduled before the wait.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : TC_RW8(0), TC_RW8(8), TC_RW8(16), TC_RW8(24)::"memory");
+}
+// Half a stage's scores: what the row does not see becomes -inf.
+__device__ __forceinline__ void mask_half(uint32_t (&v)[32], uint32_t see) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = (see >> i) & 1u ? v[i] : 0xff800000u;
 }
 // Orders later uses of v after the preceding statement (a wait issued for
 // several loads at once).
@@ -219,14 +295,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return ok;
 }
 // The same by a call where the first look does not settle it, for the 8-bit
-// pools' kernel, whose six roles have to share the instruction cache.
+// pools' kernel, whose roles have to share the instruction cache.
 __device__ __noinline__ bool long_wait(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
     return thread_wait(bar, parity, abortp, meta);
-}
-template <bool F8>
-__device__ __forceinline__ bool thread_wait_(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
-    if constexpr (!F8) return thread_wait(bar, parity, abortp, meta);
-    return mbar_test(bar, parity) || long_wait(bar, parity, abortp, meta);
 }
 template <bool F8>
 __device__ __forceinline__ bool warp_wait_(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
@@ -241,14 +312,12 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
 }
 
 // ------------------------------------------------ 8-bit pools: converting warps
-// Warp w brings tile w of each stage, K and V, to the bf16 stages the products
-// read.  A tile's values are code * 2^e, bf16 numbers exactly, so from here on
+// Two warps bring tile w of each stage, one K and one V, to the bf16 stages the
+// products read.  A tile's values are code * 2^e, bf16 numbers exactly, so from here on
 // the kernel is the bf16 one.
-//   - The conversion is kept short in code: five roles run side by side, and
-//     where their loops together outgrow the instruction cache every step of
-//     every role waits for its instructions (the same loop unrolled, with a
-//     path of bf16 products beside this one by fp32, took 1,450 cycles a tile
-//     in place of 450).
+//   - By fp32 products, two codes at a time: a path of bf16 products beside it for
+//     small exponents made the roles' loops outgrow the instruction cache (1,450
+//     cycles a tile in place of 450).
 //   - A lane converts 16 codes at a time: one 16-byte load, two 16-byte stores
 //     into the two 16-byte chunks they fill in the 128-byte-swizzled stage.
 //     Eight neighbouring lanes take four chunks of one 64-column half of two
@@ -264,7 +333,8 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t c, float f) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
     const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack_bf16(x.x * f, x.y * f);
+    const f32x2 y = mul2(pair(x.x, x.y), pair(f, f));
+    return pack_bf16(low(y), high(y));
 }
 // The stages of a CTA's tile range, in order.
 struct StageWalk {
@@ -337,107 +407,163 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, uint32_t base, uin
 }
 
 template <typename Y>
-__device__ __forceinline__ void convert_tiles(const AttnArgs& a, unsigned char* sm, uint32_t base, uint32_t bars,
-                                              volatile int* abortp, int32_t t_begin, int32_t t_end, int32_t u0, int w) {
+__device__ __forceinline__ void convert_tiles(const AttnArgs& a, unsigned char* sm, uint32_t bars, volatile int* abortp,
+                                              int32_t t_begin, int32_t t_end, int32_t u0, int w, int kv) {
     const AttnPlanDev& pl = a.plan;
     const int lane = threadIdx.x & 31;
     auto bar = [bars](int i) { return bars + 8u * (uint32_t)i; };
+    const int b_full = kv ? Y::B_V_FULL : Y::B_K_FULL, b_empty = kv ? Y::B_V_EMPTY : Y::B_K_EMPTY;
     // this lane's share: chunk c (16 codes) of four tokens; the two chunks
     // 2 c, 2 c + 1 of the stage row they fill
     const int c = 4 * ((lane >> 3) & 1) + (lane & 3), up = c >> 2, k = (2 * c) & 7;
     const int flip = (lane & 4) ? 5 : 0;
+    unsigned char* ring = sm + (kv ? Y::OFF_V : Y::OFF_K) + up * TC_HALF + w * 16 * 128;
+    const unsigned char* raws = sm + Y::OFF_RAW + w * F8_RAW_TILE + kv * kFp8TileBytes;
     StageWalk now(t_begin, u0);
     int slot = 0, stage = 0;
     uint32_t raw_ph = 0, empty_ph = 1;
     for (; now.more(pl, t_end, a.bpb); now.step()) {
-        const bool mine = w < now.tiles();
-        const unsigned char* raw = sm + Y::OFF_RAW + slot * F8_RAW_SLOT + w * F8_RAW_TILE;
         if (!warp_wait_<true>(bar(Y::B_RAW_FULL + slot), raw_ph, abortp, a.meta)) break;
-        if (!warp_wait_<true>(bar(Y::B_K_EMPTY + stage), empty_ph, abortp, a.meta)) break;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-            if (kv && !warp_wait_<true>(bar(Y::B_V_EMPTY + stage), empty_ph, abortp, a.meta)) break;
-            if (mine) {
-                const unsigned char* src = raw + kv * kFp8TileBytes;
-                unsigned char* ring = sm + Y::OFF_K + kv * (Y::OFF_V - Y::OFF_K) + stage * TC_RING_STAGE + up * TC_HALF + w * 16 * 128;
-#pragma unroll 2
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = (((2 * i + (lane >> 4)) & 3) ^ flip) + 8 * (i >> 1), sw = tok & 7;
-                    const uint4 x = *reinterpret_cast<const uint4*>(src + tok * kFp8Dim + ((c ^ sw) << 4));
-                    const float f = __uint_as_float((uint32_t)src[kBlockSize * kFp8Dim + tok] << 23);   // 2^e
-                    *reinterpret_cast<uint4*>(ring + tok * 128 + ((k ^ sw) << 4)) =
-                        make_uint4(codes_bf16(x.x, f), codes_bf16(x.x >> 16, f), codes_bf16(x.y, f), codes_bf16(x.y >> 16, f));
-                    *reinterpret_cast<uint4*>(ring + tok * 128 + (((k + 1) ^ sw) << 4)) =
-                        make_uint4(codes_bf16(x.z, f), codes_bf16(x.z >> 16, f), codes_bf16(x.w, f), codes_bf16(x.w >> 16, f));
-                }
+        if (!warp_wait_<true>(bar(b_empty + stage), empty_ph, abortp, a.meta)) break;
+        if (w < now.tiles()) {
+            const unsigned char* src = raws + slot * F8_RAW_SLOT;
+            unsigned char* dst = ring + stage * TC_RING_STAGE;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = (((2 * i + (lane >> 4)) & 3) ^ flip) + 8 * (i >> 1), sw = tok & 7;
+                const uint4 x = *reinterpret_cast<const uint4*>(src + tok * kFp8Dim + ((c ^ sw) << 4));
+                const float f = __uint_as_float((uint32_t)src[kBlockSize * kFp8Dim + tok] << 23);   // 2^e
+                *reinterpret_cast<uint4*>(dst + tok * 128 + ((k ^ sw) << 4)) =
+                    make_uint4(codes_bf16(x.x, f), codes_bf16(x.x >> 16, f), codes_bf16(x.y, f),
+                               codes_bf16(x.y >> 16, f));
+                *reinterpret_cast<uint4*>(dst + tok * 128 + (((k + 1) ^ sw) << 4)) =
+                    make_uint4(codes_bf16(x.z, f), codes_bf16(x.z >> 16, f), codes_bf16(x.w, f),
+                               codes_bf16(x.w >> 16, f));
             }
-            fence_async_smem();   // the stores, before the products read them
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(Y::B_K_FULL + kv * (Y::B_V_FULL - Y::B_K_FULL) + stage));
         }
-        if (lane == 0) mbar_arrive(bar(Y::B_RAW_EMPTY + slot));
-        if (*abortp) break;
+        fence_async_smem();   // the stores, before the products read them
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bar(b_full + stage));
+            mbar_arrive(bar(Y::B_RAW_EMPTY + slot));
+        }
         if (++slot == F8_RAW) { slot = 0; raw_ph ^= 1u; }
-        if (++stage == Y::NSTAGE) { stage = 0; empty_ph ^= 1u; }
+        if (++stage == (kv ? Y::NV : Y::NK)) { stage = 0; empty_ph ^= 1u; }
     }
 }
 
-// Issues S_r(k) = Q_r K^T of both row tiles, stage by stage, and gives the K
-// slot back once both are issued.
+// The row tiles of a unit's chunk of nst stages, 8-bit pools.  A unit of up to
+// 128 rows is split along its tokens instead: both groups of softmax warps hold
+// its rows, group r takes the stages k with k % 2 = r, and the two (m, l, O) are
+// joined when the chunk ends.
+struct RowTiles {
+    bool split;
+    int n;
+    __device__ __forceinline__ RowTiles(const AttnUnit& U, int32_t nst)
+        : split(U.rt == 1), n(split ? min(nst, 2) : U.rt) {}
+    __device__ __forceinline__ bool mine(int r, int32_t k) const { return r < n && (!split || (k & 1) == r); }
+};
+
+// One issuer of row tile r, stage by stage: of S_r(k) = Q_r K^T once stage k's K
+// landed and the P V that read its buffer completed, or of O_r += P_r V once
+// stage k's V landed and P_r(k) is in tensor memory.  Where the row tile does not
+// take part it simply gives the ring slot back.
+//   - All lanes run the loop and one is elected for the products: their operands
+//     then are the warp's, not one thread's (from a branch on the lane a stage's
+//     products took about 2,000 cycles to issue, 250 this way).
+//   - Both kinds share the code, which has to stay in the instruction cache.
 template <typename Y>
-__device__ __forceinline__ void issue_scores(const AttnArgs& a, uint32_t base, uint32_t bars, uint32_t tmem,
-                                             volatile int* abortp, int32_t t_begin, int32_t t_end, int32_t u0) {
+__device__ __forceinline__ void issue_products(const AttnArgs& a, uint32_t base, uint32_t bars, uint32_t tmem,
+                                               volatile int* abortp, int32_t t_begin, int32_t t_end, int32_t u0,
+                                               bool scores, int r) {
     const AttnPlanDev& pl = a.plan;
-    auto bar = [bars](int i) { return bars + 8u * (uint32_t)i; };
-    if ((threadIdx.x & 31) == 0) {
-        int32_t js0 = 0, js1 = 0, qc0 = 0, qc1 = 0;   // stages and units of either row tile
-        bool ok = true, any = false;
-        int32_t t = t_begin, u = u0;
-        int stage = 0;
-        uint32_t ph = 0;
-        while (ok && t < t_end) {
-            const AttnUnit& U = pl.units[u];
-            const int32_t uend = U.tile_off + U.n_blk;
-            if (t >= uend) { ++u; continue; }
-            const int32_t cend = min(t_end, uend);
-            const int rt = U.rt;
-            for (int32_t first = t; ok && t < cend; t = min(t + 4, cend)) {
-                const int ntiles = min(4, cend - t);
-                ok = thread_wait_<true>(bar(Y::B_K_FULL + stage), ph, abortp, a.meta);
+    const uint64_t dq = sdesc(base + Y::OFF_Q + r * TC_QTILE, 16, 1024), dk = sdesc(base + Y::OFF_K, 16, 1024),
+                   dv = sdesc(base + Y::OFF_V, TC_HALF, 1024);
+    const uint32_t ring_full = bars + 8 * (scores ? Y::B_K_FULL : Y::B_V_FULL);
+    const uint32_t ring_empty = bars + 8 * (scores ? Y::B_K_EMPTY : Y::B_V_EMPTY);
+    const uint32_t ready = bars + 8 * ((scores ? Y::B_PV_DONE : Y::B_P_FULL) + 2 * r);   // + 8 b
+    const uint32_t done = bars + 8 * ((scores ? Y::B_S_FULL : Y::B_PV_DONE) + 2 * r);
+    const uint32_t q_full = bars + 8 * (Y::B_Q_FULL + r), fin = bars + 8 * (Y::B_FINAL + 2 * r + (scores ? 0 : 1));
+    int32_t t = t_begin, u = u0, js = 0;   // js: stages of this row tile
+    int stage = 0;
+    uint32_t ph = 0, qph = 0;
+    bool ok = true;
+    while (ok && t < t_end) {
+        const AttnUnit& U = pl.units[u];
+        const int32_t uend = U.tile_off + U.n_blk;
+        if (t >= uend) { ++u; continue; }
+        const int32_t cend = min(t_end, uend);
+        const RowTiles tiles(U, (cend - t + 3) >> 2);
+        const int32_t first = tiles.split ? r : 0;
+        if (scores && r < tiles.n) {
+            ok = warp_wait_<true>(q_full, qph, abortp, a.meta);
+            qph ^= 1u;
+        }
 #pragma unroll 1
-                for (int r = 0; ok && r < rt; ++r) {
-                    const int32_t js = r ? js1 : js0;
-                    if (t == first) {
-                        ok = thread_wait_<true>(bar(Y::B_Q_FULL + r), (uint32_t)(r ? qc1 : qc0) & 1u, abortp, a.meta);
-                        (r ? qc1 : qc0) += 1;
-                    }
-                    const int b = js & 1;
-                    ok = ok && thread_wait_<true>(bar(Y::B_PV_DONE + 2 * r + b), ((uint32_t)(js >> 1) & 1u) ^ 1u, abortp, a.meta);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t sQ = base + Y::OFF_Q + r * TC_QTILE, sK = base + Y::OFF_K + stage * TC_RING_STAGE;
-                    const uint32_t id = idesc_bf16(128, 16 * ntiles, 0, 0);
+        for (int32_t k = 0; ok && t < cend; ++k, t += 4) {
+            const int ntiles = min(4, cend - t);
+            ok = warp_wait_<true>(ring_full + 8 * stage, ph, abortp, a.meta);
+            if (!ok) break;
+            if (tiles.mine(r, k)) {
+                const int b = js & 1;
+                ok = warp_wait_<true>(ready + 8 * b, ((uint32_t)(js >> 1) & 1u) ^ (scores ? 1u : 0u), abortp, a.meta);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t tS = tmem + r * 256 + 128 + b * 64;   // S, then P: 16 tokens per 8 columns
+                if (elect_one()) {
+                    if (scores) {
+                        const uint64_t dK = sdesc_at(dk, stage * TC_RING_STAGE);
+                        const uint32_t id = idesc_bf16(128, 16 * ntiles, 0, 0);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16(tmem + r * 256 + 128 + b * 64,
-                                  sdesc(sQ + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
-                                  sdesc(sK + (kk >> 2) * TC_HALF + (kk & 3) * 32, 16, 1024), id, kk > 0);
-                    umma_commit(bar(Y::B_S_FULL + 2 * r + b));
-                    (r ? js1 : js0) += 1;
-                    any = true;
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_bf16(tS, sdesc_at(dq, (kk >> 2) * 16384 + (kk & 3) * 32),
+                                      sdesc_at(dK, (kk >> 2) * TC_HALF + (kk & 3) * 32), id, kk > 0);
+                    } else {
+                        const uint64_t dV = sdesc_at(dv, stage * TC_RING_STAGE);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (kk < ntiles)
+                                umma_bf16_ta(tmem + r * 256, tS + kk * 8, sdesc_at(dV, kk * 2048),
+                                             idesc_bf16(128, 128, 0, 1), kk > 0 || k > first);
+                    }
+                    umma_commit(done + 8 * b);
+                    umma_commit(ring_empty + 8 * stage);
                 }
-                if (ok) umma_commit(bar(Y::B_K_EMPTY + stage));
-                if (++stage == Y::NSTAGE) { stage = 0; ph ^= 1u; }
+                ++js;
+            } else if (elect_one()) {
+                mbar_arrive(ring_empty + 8 * stage);
             }
-            t = cend;
-            ++u;
+            __syncwarp();
+            if (++stage == (scores ? Y::NK : Y::NV)) { stage = 0; ph ^= 1u; }
         }
-        if (any) {   // every MMA this thread issued has finished before the TMEM is freed
-            umma_commit(bar(Y::B_FINAL));
-            drain_wait(bar(Y::B_FINAL), 0);
-        }
+        t = cend;
+        ++u;
+    }
+    if (js && elect_one()) {   // every MMA issued here has finished before the TMEM is freed
+        umma_commit(fin);
+        drain_wait(fin, 0);
     }
     __syncwarp();
+}
+
+// 8-bit pools: O of the warp's rows times 2^d where need, once the PV before
+// this stage (bar_pv, phase) has completed.
+__device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint32_t bar_pv, uint32_t phase,
+                                          volatile int* abortp, DevMeta* meta) {
+    if (!warp_wait_<true>(bar_pv, phase, abortp, meta)) return false;
+    tc_fence_after();
+    const float alpha = need ? ex2_approx(d) : 1.f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(tl + c0, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+        tmem_st32(tl + c0, v);
+    }
+    tmem_wait_st();
+    return true;
 }
 
 // DRAFT: the rows are nodes of draft trees (masked by their ancestors too).
@@ -447,10 +573,11 @@ __global__ void __launch_bounds__(TcLayout<F8>::THREADS, 1)
 k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const AttnArgs a) {
     using Y = TcLayout<F8>;
-    constexpr int TC_NSTAGE = Y::NSTAGE, OFF_K = Y::OFF_K, OFF_V = Y::OFF_V, OFF_Q = Y::OFF_Q, OFF_BAR = Y::OFF_BAR,
+    constexpr int TC_NSTAGE = Y::NV, OFF_K = Y::OFF_K, OFF_V = Y::OFF_V, OFF_Q = Y::OFF_Q, OFF_BAR = Y::OFF_BAR,
                   OFF_XINFO = Y::OFF_XINFO, B_K_FULL = Y::B_K_FULL, B_K_EMPTY = Y::B_K_EMPTY, B_V_FULL = Y::B_V_FULL,
                   B_V_EMPTY = Y::B_V_EMPTY, B_S_FULL = Y::B_S_FULL, B_P_FULL = Y::B_P_FULL, B_PV_DONE = Y::B_PV_DONE,
-                  B_Q_FULL = Y::B_Q_FULL, B_FINAL = Y::B_FINAL, B_COUNT = Y::B_COUNT, TC_PV1_WARP = Y::PV1_WARP;
+                  B_Q_FULL = Y::B_Q_FULL, B_FINAL = Y::B_FINAL, B_COUNT = Y::B_COUNT, TC_PV1_WARP = Y::PV1_WARP,
+                  TC_S0_WARP = Y::S0_WARP;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int abort_flag;
     const uint32_t raw = smem_u32(smem_raw);
@@ -462,9 +589,11 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     auto bar = [bars](int i) { return bars + 8u * (uint32_t)i; };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < TC_NSTAGE; ++s) {
+        for (int s = 0; s < Y::NK; ++s) {
             mbar_init(bar(B_K_FULL + s), F8 ? 4 : 1);   // F8: every converting warp
-            mbar_init(bar(B_K_EMPTY + s), F8 ? 1 : 2);   // both S issuers (row tiles 0 and 1); F8: the one
+            mbar_init(bar(B_K_EMPTY + s), 2);    // both S issuers (row tiles 0 and 1)
+        }
+        for (int s = 0; s < Y::NV; ++s) {
             mbar_init(bar(B_V_FULL + s), F8 ? 4 : 1);
             mbar_init(bar(B_V_EMPTY + s), 2);    // both PV issuers
         }
@@ -475,7 +604,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
         for (int r = 0; r < TC_ROWTILES; ++r) mbar_init(bar(B_Q_FULL + r), 4);
         for (int i = 0; i < 4; ++i) mbar_init(bar(B_FINAL + i), 1);
-        for (int i = Y::B_RAW_FULL; i < B_COUNT; ++i) mbar_init(bar(i), i < Y::B_RAW_EMPTY ? 1 : 4);
+        for (int i = Y::B_RAW_FULL; i < B_COUNT; ++i) mbar_init(bar(i), i < Y::B_RAW_EMPTY ? 1 : 8);   // 8 warps
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     pdl_trigger();
@@ -486,7 +615,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
     __syncthreads();
     if (abort_flag) return;
-    if (warp == 1) {
+    if (warp == TC_S0_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(TMEM_COLS)
                      : "memory");
@@ -503,12 +632,14 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int32_t u0 = pl.tc_cta_unit[c];
     volatile int* abortp = &abort_flag;
 
-    if (F8 && warp == TC_S1_WARP) {
-        copy_tiles<Y>(a, base, bars, abortp, t_begin, t_end, u0);
-    } else if (F8 && warp == 1) {
-        issue_scores<Y>(a, base, bars, tmem, abortp, t_begin, t_end, u0);
-    } else if (F8 && (warp == 0 || warp == TC_V_WARP || warp == 13 || warp == 14)) {
-        convert_tiles<Y>(a, sm, base, bars, abortp, t_begin, t_end, u0, warp == 0 ? 0 : warp == TC_V_WARP ? 3 : warp - 12);
+    if (F8 && warp >= 8) {
+        if (warp < F8_COPY_WARP)
+            issue_products<Y>(a, base, bars, tmem, abortp, t_begin, t_end, u0, !(warp & 1),
+                              (warp - F8_ISSUE_WARP) >> 1);
+        else if (warp == F8_COPY_WARP) copy_tiles<Y>(a, base, bars, abortp, t_begin, t_end, u0);
+        else
+            convert_tiles<Y>(a, sm, bars, abortp, t_begin, t_end, u0, (warp - F8_CONV_WARP) >> 1,
+                             (warp - F8_CONV_WARP) & 1);
     } else if (!F8 && (warp == 0 || warp == TC_V_WARP)) {
         // ------------------------------------------------------ producers
         // Warp 0 streams K into the K ring, warp 11 V into the V ring, so a
@@ -552,7 +683,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 const uint32_t ph = (uint32_t)(g / TC_NSTAGE) & 1u;
                 const int ntiles = min(4, cend - st);
                 int ok = 1;
-                if (lane == 0) ok = thread_wait_<F8>(bar(b_empty + slot), ph ^ 1u, abortp, a.meta);
+                if (lane == 0) ok = thread_wait(bar(b_empty + slot), ph ^ 1u, abortp, a.meta);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 if (lane == 0) mbar_expect_tx(bar(b_full + slot), (uint32_t)(ntiles * 2 * HALF_BYTES));
@@ -578,7 +709,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             for (int s = 0; s < TC_NSTAGE; ++s)
                 if (issued >> s & 1u) drain_wait(bar(b_full + s), parity_bits >> s & 1u);
         }
-    } else if (warp == 1 || warp == TC_PV_WARP || warp == TC_S1_WARP || warp == TC_PV1_WARP) {
+    } else if (!F8 && (warp == 1 || warp == TC_PV_WARP || warp == TC_S1_WARP || warp == TC_PV1_WARP)) {
         // ------------------------------------------------------ MMA issuers
         // Four single-thread issuers, one chain of waits each: for row tile
         // r, an S issuer (warp 1 for r = 0, warp 12 for r = 1) issues
@@ -591,7 +722,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // arrives.
         const bool s_role = warp == 1 || warp == TC_S1_WARP;
         const int my_r = (warp == 1 || warp == TC_PV_WARP) ? 0 : 1;
-        if (lane == 0) {
+        {
             const uint32_t sQ = base + OFF_Q + my_r * TC_QTILE;
             int32_t g = 0, js = 0, qc = 0;
             bool ok = true, any = false;
@@ -603,63 +734,68 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 const int32_t cend = min(t_end, uend);
                 const bool active = my_r < U.rt;
                 const int32_t nst = (cend - t + 3) >> 2;
-                if (s_role && active) ok = thread_wait_<F8>(bar(B_Q_FULL + my_r), (uint32_t)qc++ & 1u, abortp, a.meta);
+                if (s_role && active) ok = warp_wait(bar(B_Q_FULL + my_r), (uint32_t)qc++ & 1u, abortp, a.meta);
                 for (int32_t k = 0; k < nst && ok; ++k) {
                     const int32_t gg = g + k;
                     const int slot = gg % TC_NSTAGE;
                     const uint32_t ph = (uint32_t)(gg / TC_NSTAGE) & 1u;
                     const int ntiles = min(4, cend - (t + 4 * k));
                     if (s_role) {
-                        ok = thread_wait_<F8>(bar(B_K_FULL + slot), ph, abortp, a.meta);
+                        ok = warp_wait(bar(B_K_FULL + slot), ph, abortp, a.meta);
                         if (ok && active) {
                             const int b = js & 1;
-                            ok = thread_wait_<F8>(bar(B_PV_DONE + 2 * my_r + b), ((uint32_t)(js >> 1) & 1u) ^ 1u, abortp,
+                            ok = warp_wait(bar(B_PV_DONE + 2 * my_r + b), ((uint32_t)(js >> 1) & 1u) ^ 1u, abortp,
                                              a.meta);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t stage = base + OFF_K + slot * TC_RING_STAGE;
                             const uint32_t id = idesc_bf16(128, 16 * ntiles, 0, 0);
                             const uint32_t dS = tmem + my_r * 256 + 128 + b * 64;
+                            if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const uint32_t qoff = (kk >> 2) * 16384 + (kk & 3) * 32;
-                                const uint32_t koff = (kk >> 2) * TC_HALF + (kk & 3) * 32;
-                                umma_bf16(dS, sdesc(sQ + qoff, 16, 1024), sdesc(stage + koff, 16, 1024), id, kk > 0);
+                                for (int kk = 0; kk < 8; ++kk) {
+                                    const uint32_t qoff = (kk >> 2) * 16384 + (kk & 3) * 32;
+                                    const uint32_t koff = (kk >> 2) * TC_HALF + (kk & 3) * 32;
+                                    umma_bf16(dS, sdesc(sQ + qoff, 16, 1024), sdesc(stage + koff, 16, 1024), id, kk > 0);
+                                }
+                                umma_commit(bar(B_S_FULL + 2 * my_r + b));
+                                umma_commit(bar(B_K_EMPTY + slot));
                             }
-                            umma_commit(bar(B_S_FULL + 2 * my_r + b));
-                            umma_commit(bar(B_K_EMPTY + slot));
                             ++js;
                             any = true;
-                        } else if (ok) {
+                        } else if (ok && elect_one()) {
                             mbar_arrive(bar(B_K_EMPTY + slot));
                         }
                     } else {
-                        ok = thread_wait_<F8>(bar(B_V_FULL + slot), ph, abortp, a.meta);
+                        ok = warp_wait(bar(B_V_FULL + slot), ph, abortp, a.meta);
                         if (ok && active) {
                             const int b = js & 1;
-                            ok = thread_wait_<F8>(bar(B_P_FULL + 2 * my_r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
+                            ok = warp_wait(bar(B_P_FULL + 2 * my_r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t vst = base + OFF_V + slot * TC_RING_STAGE;
                             const uint32_t id = idesc_bf16(128, 128, 0, 1);
                             const uint32_t tP = tmem + my_r * 256 + 128 + b * 64;   // 16 tokens per 8 columns
-                            for (int kk = 0; kk < ntiles; ++kk)
-                                umma_bf16_ta(tmem + my_r * 256, tP + kk * 8, sdesc(vst + kk * 2048, TC_HALF, 1024), id,
-                                             kk > 0 || k > 0);
-                            umma_commit(bar(B_PV_DONE + 2 * my_r + b));
-                            umma_commit(bar(B_V_EMPTY + slot));
+                            if (elect_one()) {
+                                for (int kk = 0; kk < ntiles; ++kk)
+                                    umma_bf16_ta(tmem + my_r * 256, tP + kk * 8, sdesc(vst + kk * 2048, TC_HALF, 1024),
+                                                 id, kk > 0 || k > 0);
+                                umma_commit(bar(B_PV_DONE + 2 * my_r + b));
+                                umma_commit(bar(B_V_EMPTY + slot));
+                            }
                             ++js;
                             any = true;
-                        } else if (ok) {
+                        } else if (ok && elect_one()) {
                             mbar_arrive(bar(B_V_EMPTY + slot));
                         }
                     }
+                    __syncwarp();
                 }
                 g += nst;
                 t = cend;
                 ++u;
             }
-            if (any) {   // every MMA this thread issued has finished before the TMEM is freed
+            if (any && elect_one()) {   // every MMA issued here has finished before the TMEM is freed
                 const uint32_t fb = bar(B_FINAL + (s_role ? 0 : 1) + 2 * my_r);
                 umma_commit(fb);
                 drain_wait(fb, 0);
@@ -668,13 +804,14 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         __syncwarp();
     } else {
         // ------------------------------------------------------ softmax
-        const int r = (warp - TC_SOFTMAX_WARP0) >> 2;
+        const int r = (warp - Y::SOFTMAX_WARP0) >> 2;
         const int sub = warp & 3;                 // TMEM lanes 32 sub .. 32 sub + 31
         const int trow = sub * 32 + lane;         // row within the row tile
         const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + r * 256;
         unsigned char* sQ = sm + OFF_Q + r * TC_QTILE;
         const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
-        const int row = r * 128 + trow;
+        // row of the unit (F8: both groups hold the rows of a split unit)
+        auto row_of = [&](const AttnUnit& V) { return F8 && V.rt == 1 ? trow : r * 128 + trow; };
         int2* xinfo = reinterpret_cast<int2*>(sm + OFF_XINFO) + r * kMaxTcExtraTiles;
         // draft trees: the row's mask, in shared memory: in registers, or made
         // again from the unit where it is needed, it cost spills in the loop
@@ -685,6 +822,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // chunk's last S was read (no S MMA of it is pending then), before
         // that chunk's epilogue, so the next chunk's S overlaps the epilogue.
         auto stage_q = [&](const AttnUnit& V) -> AttnRow {
+            const int row = row_of(V);
             const bool v_ok = row < V.n_rows;
             const AttnRow RR = v_ok ? unit_row(pl, V, row) : AttnRow{0, 0};
             const uint4* q = reinterpret_cast<const uint4*>(Q + (int64_t)RR.q_row * D);
@@ -704,16 +842,20 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         int32_t t = t_begin, u = u0;
         int32_t staged_u = -1;      // unit whose Q is already in the tile
         AttnRow staged_R{0, 0};
+        uint32_t joined = 0;        // phase of the joins of split units
         while (ok && t < t_end) {
             const AttnUnit U = pl.units[u];
             const int32_t uend = U.tile_off + U.n_blk;
             if (t >= uend) { ++u; continue; }
             const int32_t cend = min(t_end, uend);
-            if (r >= U.rt) {
+            const int32_t nst = (cend - t + 3) >> 2;
+            const RowTiles tiles(U, nst);
+            if (r >= (F8 ? tiles.n : U.rt)) {
                 t = cend;
                 ++u;
                 continue;
             }
+            const int row = row_of(U);
             const bool valid = row < U.n_rows;
             const AttnRow R = staged_u == u ? staged_R : stage_q(U);
             if (!F8 && U.n_blk > U.n_shared) {
@@ -728,9 +870,9 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     xinfo[i] = *reinterpret_cast<const int2*>(pl.xtiles + U.x_off + i);
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + r) : "memory");
             }
-            const int32_t nst = (cend - t + 3) >> 2;
+            const int32_t k0 = F8 && tiles.split ? r : 0, k_step = F8 && tiles.split ? 2 : 1;
             float m_ref = -INFINITY, l = 0.f;
-            for (int32_t k = 0; k < nst && ok; ++k, ++js) {
+            for (int32_t k = k0; k < nst && ok; k += k_step, ++js) {
                 const int32_t st = t + 4 * k;
                 const int ntiles = min(4, cend - st);
                 const int b = js & 1;
@@ -745,6 +887,70 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     if (lane == 0) mbar_arrive(bar(B_P_FULL + 2 * r + b));
                     continue;
                 }
+                if constexpr (F8) {
+                    // the scores are read twice from tensor memory, half a stage at
+                    // a time: 32 of them fit the 80 registers a thread has
+                    const int32_t off = R.limit - (U.blk_start + st - U.tile_off) * BS;
+                    const bool plain = __all_sync(0xffffffffu, off >= TC_TOK) && ntiles == 4;
+                    const uint32_t tS = tl + 128 + b * 64;
+                    uint64_t see = ~0ull;
+                    if (!plain) {
+                        see = DRAFT       ? draft_visible(*mask_slot, off)
+                              : off >= 64 ? ~0ull
+                              : off > 0   ? (1ull << off) - 1ull
+                                          : 0ull;
+                        if (ntiles < 4) see &= (1ull << (ntiles * BS)) - 1ull;
+                    }
+                    float mx;
+                    {
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t v[32];
+                            tmem_ld32(tS + 32 * half, v);
+                            tmem_wait_ld(v);
+                            if (!plain) mask_half(v, (uint32_t)(see >> (32 * half)));
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
+                        }
+                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+                    }
+                    if (k == k0) {
+                        m_ref = mx;   // this stage's PV overwrites O
+                    } else {
+                        const bool need = mx > m_ref + RESCALE_THRESHOLD;
+                        if (__any_sync(0xffffffffu, need)) {
+                            ok = rescale_rows(need, m_ref - mx, tl, bar(B_PV_DONE + 2 * r + ((js - 1) & 1)),
+                                              (uint32_t)((js - 1) >> 1) & 1u, abortp, a.meta);
+                            if (!ok) break;
+                            if (need) {
+                                l *= ex2_approx(m_ref - mx);
+                                m_ref = mx;
+                            }
+                        }
+                    }
+                    const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const f32x2 scale2 = pair(a.scale_log2, a.scale_log2), nref2 = pair(nref, nref);
+                    f32x2 l2[2] = {0, 0};
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[32], pk[16];
+                        tmem_ld32(tS + 32 * half, v);
+                        tmem_wait_ld(v);
+                        if (!plain) mask_half(v, (uint32_t)(see >> (32 * half)));
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const f32x2 x = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale2,
+                                                 nref2);
+                            pk[i] = pack_bf16(ex2_approx(low(x)), ex2_approx(high(x)));
+                            l2[i & 1] = add2(l2[i & 1], pair(__uint_as_float(pk[i] << 16),
+                                                             __uint_as_float(pk[i] & 0xffff0000u)));
+                        }
+                        tmem_st16(tS + 16 * half, pk);   // over columns already read
+                    }
+                    const f32x2 ls = add2(l2[0], l2[1]);
+                    l += low(ls) + high(ls);
+                } else {
                 float s[64];
                 {
                     uint32_t v0[32], v1[32];
@@ -761,7 +967,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 // mask stage columns past the chunk and positions the row does
                 // not see (only stages some row of the warp does not fully see)
                 const int32_t ti0 = st - U.tile_off;
-                if (F8 || ti0 + ntiles <= U.n_shared) {
+                if (ti0 + ntiles <= U.n_shared) {
                     const int32_t vis = min(ntiles * BS, R.limit - (U.blk_start + ti0) * BS);
                     if (!__all_sync(0xffffffffu, vis >= TC_TOK)) {
                         if constexpr (DRAFT) {
@@ -820,7 +1026,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     const bool need = mx > m_ref + RESCALE_THRESHOLD;
                     if (__any_sync(0xffffffffu, need)) {
                         // O holds the PV of the previous stage once it completes
-                        ok = warp_wait_<F8>(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u,
+                        ok = warp_wait(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u,
                                        abortp, a.meta);
                         if (!ok) break;
                         tc_fence_after();
@@ -841,9 +1047,9 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                         }
                     }
                 }
+                const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
                 // P = 2^(s * scale - m_ref) in bf16; the row sum is taken over
                 // the rounded values (eight independent chains)
-                const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
                 uint32_t pk[32];
                 {
                     float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -859,6 +1065,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 // P over the S it came from (token 2 i in the low half of
                 // column i); unused columns past the chunk hold P = 0
                 tmem_st32(tl + 128 + b * 64, pk);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -872,7 +1079,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     const AttnUnit& V = pl.units[u2];
                     const int32_t e2 = V.tile_off + V.n_blk;
                     if (t2 >= e2) { ++u2; continue; }
-                    if (r < V.rt) break;
+                    if (r < (F8 ? RowTiles(V, (min(t_end, e2) - t2 + 3) >> 2).n : V.rt)) break;
                     t2 = min(t_end, e2);
                     ++u2;
                 }
@@ -887,6 +1094,53 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             tc_fence_after();
             const int32_t prow = U.prow_base + (c - U.cfirst) * U.n_rows + row;
             float* dst = a.part_acc + (int64_t)(valid ? prow : 0) * D;
+            if (F8 && tiles.split && tiles.n == 2) {
+                // join: each group stores half of the columns of both
+                float2* ml = reinterpret_cast<float2*>(sm + Y::OFF_ML);
+                ml[r * 128 + trow] = make_float2(m_ref, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Y::B_ML_FULL));
+                ok = warp_wait_<F8>(bar(Y::B_ML_FULL), joined, abortp, a.meta);
+                if (!ok) break;
+                tc_fence_after();
+                const float2 o = ml[(r ^ 1) * 128 + trow];
+                const float m = fmaxf(m_ref, o.x);
+                const float mine = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+                const float other = o.x == -INFINITY ? 0.f : ex2_approx(o.x - m);
+                const uint32_t tl_o = tmem + ((uint32_t)(sub * 32) << 16) + (r ^ 1) * 256;
+#pragma unroll 1
+                for (int c0 = r * (D / 2); c0 < (r + 1) * (D / 2); c0 += 32) {
+                    uint32_t v[32], w[32];
+                    tmem_ld32(tl + c0, v);
+                    tmem_ld32(tl_o + c0, w);
+                    tmem_wait_ld(v);
+                    reg_tie(w);
+                    if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            float4 x;
+                            x.x = __uint_as_float(v[i]) * mine + __uint_as_float(w[i]) * other;
+                            x.y = __uint_as_float(v[i + 1]) * mine + __uint_as_float(w[i + 1]) * other;
+                            x.z = __uint_as_float(v[i + 2]) * mine + __uint_as_float(w[i + 2]) * other;
+                            x.w = __uint_as_float(v[i + 3]) * mine + __uint_as_float(w[i + 3]) * other;
+                            *reinterpret_cast<float4*>(dst + c0 + i) = x;
+                        }
+                    }
+                }
+                if (valid && r == 0) a.part_ml[prow] = make_float2(m, l * mine + o.y * other);
+                // neither accumulator is written again, nor its (m, l), before both groups are done
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Y::B_ML_DONE));
+                ok = warp_wait_<F8>(bar(Y::B_ML_DONE), joined, abortp, a.meta);
+                if (!ok) break;
+                tc_fence_after();
+                joined ^= 1u;
+                t = cend;
+                ++u;
+                continue;
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t v[32];
@@ -908,7 +1162,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1)
+    if (warp == TC_S0_WARP)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
 }
 
