@@ -22,9 +22,9 @@
 //   warps 0, 11 TMA producers: stream 64-token stages (4 blocks of 16 tokens)
 //               of K and of V into two 4-stage rings, block ids fetched 32
 //               tiles at a time.
-//   warps 1, 12 TMEM owner (warp 1); an elected lane issues the S MMAs of row
-//               tile 0 (warp 1) or 1 (warp 12) and their commits.
-//   warps 10, 13 an elected lane issues the P V MMAs of row tile 0 or 1.
+//   warps 1, 12 TMEM owner (warp 1); one lane issues the S MMAs of row tile
+//               0 (warp 1) or 1 (warp 12) and their commits.
+//   warps 10, 13 one lane issues the P V MMAs of row tile 0 or 1.
 //   warps 2-9   softmax, one query row per thread (warps 2-5 row tile 0,
 //               warps 6-9 row tile 1): read the row of S from TMEM, mask,
 //               exponentiate (base 2), write P (bf16) back into the first 32
@@ -722,7 +722,20 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // arrives.
         const bool s_role = warp == 1 || warp == TC_S1_WARP;
         const int my_r = (warp == 1 || warp == TC_PV_WARP) ? 0 : 1;
-        {
+        // Draft trees: all lanes run the loop and one is elected for the
+        // products, as in the 8-bit pools' issuers (96 rows, 8,192 tokens:
+        // 173 -> 166 us).  Without them it is one lane's loop: electing gained
+        // 0.5 % of a verification call and lost 1.2 % of the stress step, where
+        // memory is the bound.
+        auto one = [] {
+            if constexpr (DRAFT) return elect_one();
+            return true;
+        };
+        auto wait = [&](uint32_t wb, uint32_t parity) {
+            if constexpr (DRAFT) return warp_wait(wb, parity, abortp, a.meta);
+            return thread_wait(wb, parity, abortp, a.meta);
+        };
+        if (DRAFT || lane == 0) {
             const uint32_t sQ = base + OFF_Q + my_r * TC_QTILE;
             int32_t g = 0, js = 0, qc = 0;
             bool ok = true, any = false;
@@ -734,24 +747,23 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 const int32_t cend = min(t_end, uend);
                 const bool active = my_r < U.rt;
                 const int32_t nst = (cend - t + 3) >> 2;
-                if (s_role && active) ok = warp_wait(bar(B_Q_FULL + my_r), (uint32_t)qc++ & 1u, abortp, a.meta);
+                if (s_role && active) ok = wait(bar(B_Q_FULL + my_r), (uint32_t)qc++ & 1u);
                 for (int32_t k = 0; k < nst && ok; ++k) {
                     const int32_t gg = g + k;
                     const int slot = gg % TC_NSTAGE;
                     const uint32_t ph = (uint32_t)(gg / TC_NSTAGE) & 1u;
                     const int ntiles = min(4, cend - (t + 4 * k));
                     if (s_role) {
-                        ok = warp_wait(bar(B_K_FULL + slot), ph, abortp, a.meta);
+                        ok = wait(bar(B_K_FULL + slot), ph);
                         if (ok && active) {
                             const int b = js & 1;
-                            ok = warp_wait(bar(B_PV_DONE + 2 * my_r + b), ((uint32_t)(js >> 1) & 1u) ^ 1u, abortp,
-                                             a.meta);
+                            ok = wait(bar(B_PV_DONE + 2 * my_r + b), ((uint32_t)(js >> 1) & 1u) ^ 1u);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t stage = base + OFF_K + slot * TC_RING_STAGE;
                             const uint32_t id = idesc_bf16(128, 16 * ntiles, 0, 0);
                             const uint32_t dS = tmem + my_r * 256 + 128 + b * 64;
-                            if (elect_one()) {
+                            if (one()) {
 #pragma unroll
                                 for (int kk = 0; kk < 8; ++kk) {
                                     const uint32_t qoff = (kk >> 2) * 16384 + (kk & 3) * 32;
@@ -763,20 +775,20 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                             }
                             ++js;
                             any = true;
-                        } else if (ok && elect_one()) {
+                        } else if (ok && one()) {
                             mbar_arrive(bar(B_K_EMPTY + slot));
                         }
                     } else {
-                        ok = warp_wait(bar(B_V_FULL + slot), ph, abortp, a.meta);
+                        ok = wait(bar(B_V_FULL + slot), ph);
                         if (ok && active) {
                             const int b = js & 1;
-                            ok = warp_wait(bar(B_P_FULL + 2 * my_r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
+                            ok = wait(bar(B_P_FULL + 2 * my_r + b), (uint32_t)(js >> 1) & 1u);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t vst = base + OFF_V + slot * TC_RING_STAGE;
                             const uint32_t id = idesc_bf16(128, 128, 0, 1);
                             const uint32_t tP = tmem + my_r * 256 + 128 + b * 64;   // 16 tokens per 8 columns
-                            if (elect_one()) {
+                            if (one()) {
                                 for (int kk = 0; kk < ntiles; ++kk)
                                     umma_bf16_ta(tmem + my_r * 256, tP + kk * 8, sdesc(vst + kk * 2048, TC_HALF, 1024),
                                                  id, kk > 0 || k > 0);
@@ -785,17 +797,17 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                             }
                             ++js;
                             any = true;
-                        } else if (ok && elect_one()) {
+                        } else if (ok && one()) {
                             mbar_arrive(bar(B_V_EMPTY + slot));
                         }
                     }
-                    __syncwarp();
+                    if constexpr (DRAFT) __syncwarp();
                 }
                 g += nst;
                 t = cend;
                 ++u;
             }
-            if (any && elect_one()) {   // every MMA issued here has finished before the TMEM is freed
+            if (any && one()) {   // every MMA issued here has finished before the TMEM is freed
                 const uint32_t fb = bar(B_FINAL + (s_role ? 0 : 1) + 2 * my_r);
                 umma_commit(fb);
                 drain_wait(fb, 0);
