@@ -216,21 +216,35 @@ __device__ __forceinline__ uint32_t fp8_exponent(uint32_t top) {
     if (top >= 0x7f800000u) return 255u;
     return (uint32_t)max(1, (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
 }
-// Eight codes of x * 2^-e.
-__device__ __forceinline__ uint2 fp8_codes(const float (&x)[8], uint32_t byte) {
+// Two codes of (x, y) * 2^-e (inv: that power of two, twice).
+__device__ __forceinline__ uint32_t two_codes(float x, float y, uint64_t inv) {
+    uint64_t v;
+    float2 f;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(inv));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+}
+// Eight codes of x * 2^-e.  At e = 120 they end at 240 (256 * 2^120 would read
+// back as an infinity); out of line, for it hardly ever happens.
+__device__ __noinline__ uint2 fp8_codes_top(float4 x, float4 y, uint32_t byte) {
     if (byte == 255u) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-    const float inv = __uint_as_float((254u - byte) << 23);   // e in [-126, 120]
+    const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
     uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        float2 v = make_float2(x[2 * k] * inv, x[2 * k + 1] * inv);
-        if (byte == 247u) {   // 256 * 2^120 would read back as an infinity
-            v.x = fminf(fmaxf(v.x, -240.f), 240.f);
-            v.y = fminf(fmaxf(v.y, -240.f), 240.f);
-        }
-        w[k] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-    }
+    for (int k = 0; k < 4; ++k)
+        w[k] = __nv_cvt_float2_to_fp8x2(make_float2(fminf(fmaxf(f[2 * k] * 0x1p-120f, -240.f), 240.f),
+                                                    fminf(fmaxf(f[2 * k + 1] * 0x1p-120f, -240.f), 240.f)),
+                                        __NV_SATFINITE, __NV_E4M3);
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+__device__ __forceinline__ uint2 fp8_codes(const float (&x)[8], uint32_t byte) {
+    if (byte >= 247u)
+        return fp8_codes_top(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), byte);
+    const uint32_t b = (254u - byte) << 23;   // e in [-126, 119]
+    const uint64_t inv = (uint64_t)b << 32 | b;
+    return make_uint2(two_codes(x[0], x[1], inv) | two_codes(x[2], x[3], inv) << 16,
+                      two_codes(x[4], x[5], inv) | two_codes(x[6], x[7], inv) << 16);
 }
 // Byte offset of element d (a multiple of 8) of slot s in an 8-bit tile.
 __device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
@@ -241,12 +255,16 @@ __device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
 // tree depths as bytes.
 // T: the rows' type; FP8: the blocks hold 8-bit rows (else rows of T); ROPE:
 // keys and queries turn (else every row is stored as it is).
-// Rows go through a thread four at a time (two of fp32), loads first.
+// Rows go through a thread U at a time, loads first.  Rotating rows of 16 bits:
+// four, at four CTAs an SM (three-a-time and six-a-time lost 2 to 5 %, two at six
+// CTAs 17 %).  Rows that are only quantised: two, at eight CTAs (32,768 tokens of 8
+// heads appended and read back 94.9 us, against 98.7 with four at five CTAs and
+// 104 with one at twelve).
 template <typename T, bool FP8, bool ROPE, typename A>
-__global__ void __launch_bounds__(128) k_append_rows(const __grid_constant__ A args, const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_constant__ A args, const __grid_constant__ RowsArgs a) {
     pdl_wait();
     constexpr int bs = kBlockSize;
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    constexpr int U = ROPE && sizeof(T) == 2 ? 4 : 2;
     const int32_t n = a.n, dim = a.dim;
     const int32_t items = dim >> 4;                     // threads per row
     const int32_t lanes = 128 / items;                  // rows in flight, cut to a power of two
@@ -417,8 +435,9 @@ __global__ void __launch_bounds__(128) k_append_rows(const __grid_constant__ A a
 // ------------------------------------------------------------------ gather
 // args: branch[n], first position[n], output row[n], prefix of touched blocks[n],
 // row count[n].  One CTA per (branch, block) and share of the heads.  A thread
-// owns 8 elements of the row of one slot and walks the heads with them, four
-// rows' loads in flight, so that nothing is divided in the loop; a warp's
+// owns 8 elements of the row of one slot and walks the heads with them, U rows'
+// loads in flight, so that nothing is divided in the loop (8-bit rows: eight
+// rather than four, 92.4 against 94.9 us for the case above, sixteen 97.8); a warp's
 // stores cover whole 128-byte lines.
 struct ReadArgs {
     int32_t n, bpb, n_kv, dim, n_blocks, uniform, n_tiles;
@@ -434,7 +453,7 @@ template <typename T, bool FP8, typename A>
 __global__ void __launch_bounds__(256) k_read_rows(const __grid_constant__ A args, const __grid_constant__ ReadArgs a) {
     pdl_wait();
     constexpr int bs = kBlockSize;
-    constexpr int U = 4;
+    constexpr int U = FP8 ? 8 : 4;
     const int32_t n = a.n, dim = a.dim;
     const int32_t chunks = dim >> 3;                    // threads per row
     const int32_t lp2 = 1 << (31 - __clz(256 / chunks));
