@@ -333,6 +333,24 @@ __global__ void __launch_bounds__(F8_THREADS, 3) k_attn_partial_fp8(const AttnAr
                             s[h][2 + e] = (see1 >> bit) & 1u ? s[h][2 + e] : NEG_INF;
                         }
                     }
+                    // A V row of NaN that no row sees (left behind a branch's
+                    // end by a roll-back, or by the block's last owner) would
+                    // spread through its weight of zero: it becomes zero here.
+                    bool nan_row = false;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) nan_row |= (vb[h] & 255u) == 255u || vb[h] >> 8 == 255u;
+                    if (__any_sync(0xffffffffu, nan_row)) {
+                        const uint32_t seen = __reduce_or_sync(0xffffffffu, (row0 < U.n_rows ? see0 : 0u) |
+                                                                                (row1 < U.n_rows ? see1 : 0u));
+                        for (int tk = 0; tk < (two ? 32 : 16); ++tk) {
+                            if ((seen >> tk) & 1u) continue;
+                            unsigned char* row = slots + slot * F8_SLOT + (tk >> 4) * F8_TILE + kFp8TileBytes +
+                                                 (tk & 15) * kFp8Dim;
+                            reinterpret_cast<uint32_t*>(row)[lane] = 0u;
+                        }
+                        fence_async_smem();   // before the slot's next copy
+                        __syncwarp();
+                    }
                 }
                 float mx0 = NEG_INF, mx1 = NEG_INF, wx0 = NEG_INF, wx1 = NEG_INF;
 #pragma unroll

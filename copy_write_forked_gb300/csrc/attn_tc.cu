@@ -339,6 +339,7 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t c, float f) {
 // The stages of a CTA's tile range, in order.
 struct StageWalk {
     int32_t t, u, cend = 0;    // next stage's first tile; its unit; the end of the unit's tiles here
+    int32_t unit_end = 0;      // the end of the unit's tiles
     int64_t row = 0;           // table offset of tile 0 of the unit
     int32_t head = 0;
     __device__ __forceinline__ StageWalk(int32_t t0, int32_t u0) : t(t0), u(u0 - 1) {}
@@ -347,7 +348,8 @@ struct StageWalk {
         if (t >= t_end) return false;
         while (t >= cend) {
             const AttnUnit& U = pl.units[++u];
-            cend = min(t_end, U.tile_off + U.n_blk);
+            unit_end = U.tile_off + U.n_blk;
+            cend = min(t_end, unit_end);
             row = (int64_t)U.table_row * bpb + U.blk_start - U.tile_off;
             head = U.kv_head;
         }
@@ -356,6 +358,16 @@ struct StageWalk {
     __device__ __forceinline__ int tiles() const { return min(4, cend - t); }
     __device__ __forceinline__ void step() { t = min(t + 4, cend); }
 };
+
+// Tokens of the unit's last tile that one of its branches holds.
+__device__ __noinline__ int32_t held_tokens(const AttnPlanDev& pl, const AttnUnit& U) {
+    const int32_t rm = pl.q_len * pl.group;
+    int32_t len = 0;
+    for (int32_t i = U.row_lo / rm + (threadIdx.x & 31); i <= (U.row_lo + U.n_rows - 1) / rm; i += 32)
+        len = max(len, pl.members[U.mem_off + i].len);
+    len = __reduce_max_sync(0xffffffffu, len);
+    return min(kBlockSize, len - (U.blk_start + U.n_blk - 1) * kBlockSize);
+}
 
 // Copies the stages' tiles as they are stored, F8_RAW stages ahead; lane i < 4
 // copies tile i, whose block id it loaded a stage before.
@@ -440,6 +452,16 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, unsigned char* 
                     make_uint4(codes_bf16(x.z, f), codes_bf16(x.z >> 16, f), codes_bf16(x.w, f),
                                codes_bf16(x.w >> 16, f));
             }
+        }
+        if (kv && w < now.tiles() && now.t + w == now.unit_end - 1) {
+            // What V holds behind the longest branch's end (left by a roll-back,
+            // or by the block's last owner) may be NaN and would spread through
+            // its weight of zero: those rows become zero.
+            __syncwarp();
+            unsigned char* tile = sm + Y::OFF_V + stage * TC_RING_STAGE + w * 16 * 128;
+            for (int i = held_tokens(pl, pl.units[now.u]) * 16 + lane; i < kBlockSize * 16; i += 32)
+                *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * TC_HALF + (i >> 4) * 128 + (i & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async_smem();   // the stores, before the products read them
         __syncwarp();

@@ -268,6 +268,40 @@ def test_keys_that_are_not_finite_touch_only_the_rows_that_see_them():
     pool.close()
 
 
+@pytest.mark.parametrize("rows", [-1, 1])
+@pytest.mark.parametrize("group,q_len", [(1, 1), (8, 3), (8, 40)])
+def test_rows_behind_a_branch_touch_nothing(rows, group, q_len):
+    """Rows of NaN that a roll-back, an acceptance or a block's last owner left behind a branch's end."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    pool = Pool(8, 16, 2, 128, F8, max_branches=8, tc_min_rows=rows)
+    nan = torch.full((1, 128, 2, 128), float("nan"), device="cuda", dtype=torch.bfloat16)
+
+    def rows_of(n):
+        return torch.randn(1, n, 2, 128, generator=g, device="cuda").bfloat16()
+
+    def attend(b, k, v, q_len):
+        q = rows_of(q_len * group).reshape(1, q_len, 2 * group, 128)
+        _attend("fp8", [(R.held(R.f64(k[0]), "fp8"), R.held(R.f64(v[0]), "fp8"))], q, pool.tree_attn_decode(q, [b]), q_len)
+
+    b = pool.new_branch()
+    pool.append_kv([b], nan, nan)          # every block of the pool holds NaN
+    pool.free([b])
+    b = pool.new_branch()
+    for n, more in ((41, 5), (57, 18)):    # ends inside a block, three blocks in; more rows come and go
+        k, v = rows_of(n), rows_of(n)
+        pool.append_kv([b], k, v)
+        attend(b, k, v, q_len)
+        pool.append_kv([b], nan[:, :more].contiguous(), nan[:, :more].contiguous())
+        pool.accept_draft([b], more, [[]])
+        attend(b, k, v, q_len)
+        child = pool.fork(b, 1)            # a copied tail block
+        pool.append_kv(child, k[:, :1].contiguous(), v[:, :1].contiguous())
+        attend(child[0], torch.cat((k, k[:, :1]), 1), torch.cat((v, v[:, :1]), 1), q_len)
+        pool.free(child)
+        pool.truncate([b], [0])
+    pool.close()
+
+
 def test_layers_and_the_split_append():
     g = torch.Generator(device="cuda").manual_seed(6)
     L, kv, nq = 3, 2, 8
