@@ -2357,7 +2357,7 @@ extern "C" int dendrite_tree_attn_draft(dendrite_pool* p, int32_t layer, const v
     if (!p) return DENDRITE_EINVAL;
     if (p->poisoned) return p->poisoned;
     if (p->dtype == DENDRITE_TURBO) return DENDRITE_EDTYPE;
-    if (n <= 0) return DENDRITE_EINVAL;
+    if (n <= 0 || n > p->max_branches) return DENDRITE_EINVAL;
     DENDRITE_TRY(check_trees(parents, n_trees, n, n_draft));
     DENDRITE_CUDA(cudaSetDevice(p->device));
     DENDRITE_TRY(check_not_capturing((cudaStream_t)stream));

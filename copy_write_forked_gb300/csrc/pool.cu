@@ -1068,9 +1068,10 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
 // Host checks of a rotating append of n x n_new tokens in n_layers layers;
 // fills the rotation fields of `c` (depth holds the draft tree depths it
 // points to).
-int check_rotation(dendrite_pool* p, int32_t n, int32_t n_new, const int32_t* parents, int32_t n_trees, const void* Q,
-                   int32_t n_q_heads, void* q_out, const dendrite_rope* rope, int32_t n_layers, RowsCall& c,
-                   std::vector<uint8_t>& depth) {
+int check_rotation(dendrite_pool* p, int32_t n, int32_t n_new, const int32_t* parents, int32_t n_trees, const void* K,
+                   const void* V, const void* Q, int32_t n_q_heads, void* q_out, const dendrite_rope* rope,
+                   int32_t n_layers, RowsCall& c, std::vector<uint8_t>& depth) {
+    if (n > p->max_branches) return DENDRITE_EINVAL;   // some would be named twice
     if (!rope || rope->rot_dim < 16 || rope->rot_dim > p->head_dim || rope->rot_dim % 16) return DENDRITE_EINVAL;
     if (rope->interleaved != 0 && rope->interleaved != 1) return DENDRITE_EINVAL;
     if (!std::isfinite(rope->scale)) return DENDRITE_EINVAL;
@@ -1082,9 +1083,12 @@ int check_rotation(dendrite_pool* p, int32_t n, int32_t n_new, const int32_t* pa
         if (n_q_heads < 1 || !q_out || (((uintptr_t)Q | (uintptr_t)q_out) & 15)) return DENDRITE_EINVAL;
         const int64_t rows = (int64_t)n * n_new * n_q_heads;
         if (rows * n_layers >= INT32_MAX / 2) return DENDRITE_ELIMIT;
-        // in place, or apart
-        const uintptr_t x = (uintptr_t)Q, y = (uintptr_t)q_out, bytes = (uintptr_t)(rows * n_layers * p->head_dim * p->elt);
-        if (x != y && x < y + bytes && y < x + bytes) return DENDRITE_EINVAL;
+        // in place, or apart from everything that is read
+        const uintptr_t y = (uintptr_t)q_out, token = (uintptr_t)n * n_new * n_layers * p->head_dim * p->elt;
+        auto meets = [&](const void* from, uintptr_t heads) {
+            return (uintptr_t)from < y + token * n_q_heads && y < (uintptr_t)from + token * heads;
+        };
+        if ((Q != q_out && meets(Q, n_q_heads)) || meets(K, p->n_kv) || meets(V, p->n_kv)) return DENDRITE_EINVAL;
         c.Q = Q;
         c.q_out = q_out;
         c.n_q_heads = n_q_heads;
@@ -1429,7 +1433,7 @@ int dendrite_append_rope(dendrite_pool* p, const int32_t* branches, int32_t n, i
     if (!K || !V || (((uintptr_t)K | (uintptr_t)V) & 15)) return DENDRITE_EINVAL;
     RowsCall c{};
     std::vector<uint8_t> depth;
-    DENDRITE_TRY(check_rotation(p, n, n_new, parents, n_trees, Q, n_q_heads, q_out, rope, p->n_layers, c, depth));
+    DENDRITE_TRY(check_rotation(p, n, n_new, parents, n_trees, K, V, Q, n_q_heads, q_out, rope, p->n_layers, c, depth));
     int64_t touched = 0;
     DENDRITE_TRY(append_check(p, branches, n, n_new, &touched));
     cudaStream_t s = (cudaStream_t)stream;
@@ -1454,7 +1458,7 @@ int dendrite_append_layer_rope(dendrite_pool* p, int32_t layer, const int32_t* p
     const int32_t n = (int32_t)pa.branches.size();
     RowsCall c{};
     std::vector<uint8_t> depth;
-    DENDRITE_TRY(check_rotation(p, n, pa.n_new, parents, n_trees, Q, n_q_heads, q_out, rope, 1, c, depth));
+    DENDRITE_TRY(check_rotation(p, n, pa.n_new, parents, n_trees, K, V, Q, n_q_heads, q_out, rope, 1, c, depth));
     DENDRITE_TRY(check_not_capturing((cudaStream_t)stream));
     DENDRITE_TRY(append_launch(p, pa.branches.data(), pa.lens.data(), n, pa.n_new, pa.touched, true, K, V, layer, 1, 0,
                                (cudaStream_t)stream, /*meta=*/false, &c));

@@ -294,7 +294,8 @@ int dendrite_rope_init(dendrite_rope* rope, int32_t rot_dim, int32_t interleaved
  *             differ in size is padded with nodes that nothing hangs on.
  *   Q, q_out: device, [n_layers][n_branches][n_new][n_q_heads][head_dim] in the
  *             dtype of K (no layer dimension in a one-layer pool); q_out may be
- *             Q itself, but may not overlap it otherwise.  Q NULL: keys alone.
+ *             Q itself, but may not overlap it otherwise, nor K or V.  Q NULL:
+ *             keys alone.
  *   rope:     host; read during the call.
  * Products are taken in fp32 and rounded once, to the row's stored type.
  * DENDRITE_TURBO pools return DENDRITE_EDTYPE.  Otherwise as dendrite_append_kv.

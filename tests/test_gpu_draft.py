@@ -393,3 +393,43 @@ def test_rows_per_head_choose_the_kernel(kind, new, decode_tc, draft_tc):
         c.attend(c.br, [R.tree(rng, new) for _ in c.br])
         assert (c.pool.last_plan_stats()["n_tc_units"] > 0) == draft_tc
     c.pool.close()
+
+
+@pytest.mark.parametrize("kind,blocks", [("fp8", 270_000), ("bf16", 136_000)])
+def test_offsets_past_32_bits(kind, blocks):
+    """A step on blocks more than 4 GiB into the pools gives what it gives on the first ones."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    kv, nq, new = 8, 32, 20
+    x = torch.randn(1, 65536, kv, 128, generator=g, device="cuda").bfloat16()
+    q = torch.randn(1, new, nq, 128, generator=g, device="cuda").bfloat16()
+    parents = R.tree(random.Random(5), new)
+    path, j = [], new - 1
+    while j >= 0:
+        path, j = [j] + path, parents[j]
+    results = []
+    for filled in (0, blocks):
+        pool = Pool(filled + 64, 16, kv, 128, R.POOL_DTYPE[kind], max_branches=256)
+        for lo in range(0, filled, 4096):
+            pool.append_kv([pool.new_branch()], *[x[:, :16 * min(4096, filled - lo)].contiguous()] * 2)
+        b = pool.new_branch()
+        pool.append_kv([b], x[:, :333].contiguous(), x[:, 333:666].contiguous())
+        turned = pool.append_rope([b], x[:, :new].contiguous(), x[:, new:2 * new].contiguous(), Rope(128), Q=q, parents=parents)
+        out = pool.tree_attn_draft(turned, [b], parents)
+        pool.accept_draft([b], new, [path])
+        one = pool.tree_attn_decode(q[:, :1].contiguous(), [b])
+        if filled:
+            assert min(pool.read_table(b)[:20]) >= filled
+        results.append([turned, out, one, *pool.read_kv([b], [0], [333 + len(path)])])
+        pool.sync()
+        pool.close()
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_the_most_rows_of_a_tree(kind):
+    """64 drafted tokens of 64 query heads a kv head: 4,096 rows, many units of every kernel."""
+    rng = random.Random(4)
+    c = Case(kind, [50, 3], 64, 1, 64)
+    c.append(c.br, 64)
+    c.attend(c.br, [R.tree(rng, 64) for _ in c.br])
+    c.pool.close()

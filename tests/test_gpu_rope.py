@@ -249,6 +249,11 @@ def test_refusals():
     broken._c.inv_freq[3] = float("nan")
     with pytest.raises(DendriteError):
         pool.append_rope([b], x, x, broken)
+    mixed = torch.zeros(x.numel() + q.numel(), device="cuda", dtype=torch.bfloat16)   # the rotated queries over K's last rows
+    over = mixed[x.numel() - 128:][:q.numel()].view_as(q)
+    for a in (dict(K=mixed[:x.numel()].view_as(x), V=x), dict(K=x, V=mixed[:x.numel()].view_as(x))):
+        with pytest.raises(DendriteError):
+            pool.append_rope([b], a["K"], a["V"], r, Q=q, out=over)
     pool.append_rope([], x[:0].contiguous(), x[:0].contiguous(), r)   # nothing to do
     assert pool.branch_len(b) == 65
     with pytest.raises(DendriteError):
