@@ -209,14 +209,14 @@ __device__ __forceinline__ int32_t block_exclusive_scan(int32_t v, int32_t* warp
 // The kernel is a chain of dependent memory round trips, so it keeps them
 // few: with at most one branch per thread the tail id, the decision and the
 // stack offset stay in registers, and the table rows are written by one warp
-// per branch with its lanes over the new blocks (one stack read per lane
-// rather than one per block in turn).
+// per branch, or several where the branches are few (prompts), with its lanes
+// over the new blocks and four stack reads per lane at a time.
 template <typename A>
 __global__ void __launch_bounds__(kAppendMetaThreads)
 k_append_meta(const __grid_constant__ A args, int32_t n, int32_t n_new, int32_t bs, int32_t bpb,
               int32_t n_blocks, int32_t* table, int32_t* refcount, const int32_t* stack, int32_t* holders,
               int32_t* last, int32_t* call, DevMeta* meta) {
-    constexpr int NT = kAppendMetaThreads, NW = NT / 32;
+    constexpr int NT = kAppendMetaThreads, NW = NT / 32, U = 4;
     __shared__ int32_t warp_sums[NW];
     __shared__ int32_t chunk_total;
     __shared__ int32_t status0, top0, bad;
@@ -322,13 +322,15 @@ k_append_meta(const __grid_constant__ A args, int32_t n, int32_t n_new, int32_t 
             }
             __syncthreads();
             const int32_t cnt = min(NT, n - base);
-            for (int32_t k = warp; k < cnt; k += NW) {
+            const int32_t per = max(1, NW / cnt);   // warps side by side on a branch
+            for (int32_t w = warp; w < cnt * per; w += NW) {
+                const int32_t k = w / per, part = w % per;
                 const int32_t b = args[base + k], L = args[n + base + k];
                 int32_t o = s_off[k];
                 const int32_t src = s_src[k];
                 int32_t* row = table + (int64_t)b * bpb;
                 if (src >= 0) {
-                    if (lane == 0) {
+                    if (lane == 0 && part == 0) {
                         const int32_t blk = stack[top0 - 1 - o];
                         atomicSub(refcount + src, 1);
                         refcount[blk] = 1;
@@ -337,10 +339,19 @@ k_append_meta(const __grid_constant__ A args, int32_t n, int32_t n_new, int32_t 
                     ++o;
                 }
                 const int32_t nb0 = (L + bs - 1) / bs, nb1 = (L + n_new + bs - 1) / bs;
-                for (int32_t j = nb0 + lane; j < nb1; j += 32) {
-                    const int32_t blk = stack[top0 - 1 - (o + j - nb0)];
-                    refcount[blk] = 1;
-                    row[j] = blk;
+                for (int32_t j0 = nb0 + 32 * part + lane; j0 < nb1; j0 += 32 * per * U) {
+                    int32_t blk[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (j0 + 32 * per * u < nb1) blk[u] = stack[top0 - 1 - (o + j0 + 32 * per * u - nb0)];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int32_t j = j0 + 32 * per * u;
+                        if (j < nb1) {
+                            refcount[blk[u]] = 1;
+                            row[j] = blk[u];
+                        }
+                    }
                 }
             }
             __syncthreads();
