@@ -25,7 +25,7 @@
 // the row of one token and walks the heads with them: the 8 angles are
 // computed once per thread, not once per head.  All of a tile's tokens and
 // heads are spread over 128 threads; tiles are (branch, block) pairs, and few
-// tiles are split over their heads (grid.z) until about 8 CTAs per SM exist.
+// tiles are split over their heads (grid.z) until the SMs are full.
 // The kernel is bound by HBM at large sizes and by its chain of dependent
 // reads (table, row) at small ones.  4 x 4,099 tokens of 8 + 8 + 32 heads,
 // rotated: 67 us for 402 MB in and out (6.0 TB/s); 8 x 4,096 tokens of 8 + 8
@@ -260,8 +260,8 @@ __device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
 // T: the rows' type; FP8: the blocks hold 8-bit rows (else rows of T); ROPE:
 // keys and queries turn (else every row is stored as it is).
 // Rows go through a thread U at a time, loads first.  Rotating rows of 16 bits:
-// four, at four CTAs an SM (three-a-time and six-a-time lost 2 to 5 %, two at six
-// CTAs 17 %).  Rows that are only quantised: two, at eight CTAs (32,768 tokens of 8
+// four, at four CTAs an SM (three or six at a time lost 1 to 5 %, two at six CTAs
+// 17 %).  Rows that are only quantised: two, at eight CTAs (32,768 tokens of 8
 // heads appended and read back 94.9 us, against 98.7 with four at five CTAs and
 // 104 with one at twelve).
 template <typename T, bool FP8, bool ROPE, typename A>
@@ -617,9 +617,9 @@ int with_words(dendrite_pool* p, size_t words, cudaStream_t s, Fill fill, Go go)
     return p->staging.release(s);
 }
 
-// CTAs along the heads so that `tiles` tiles make about 8 per SM, at most `most`.
-unsigned head_splits(const dendrite_pool* p, int64_t tiles, int64_t most) {
-    const int64_t want = (8 * (int64_t)p->sm_count + tiles - 1) / std::max<int64_t>(tiles, 1);
+// CTAs along the heads so that `tiles` tiles make about per_sm per SM, at most `most`.
+unsigned head_splits(const dendrite_pool* p, int64_t tiles, int64_t most, int per_sm) {
+    const int64_t want = (per_sm * (int64_t)p->sm_count + tiles - 1) / std::max<int64_t>(tiles, 1);
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), 64));
 }
 
@@ -734,7 +734,9 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s) {
     int32_t lanes = 128 / (a.dim / 16), tp = 1;
     while (lanes & (lanes - 1)) lanes &= lanes - 1;
     while (tp < lanes && tp < std::min(n_new, bs)) tp *= 2;
-    const unsigned z = head_splits(p, c.touched * c.n_layers_in, (n_rows + lanes / tp - 1) / (lanes / tp));
+    // (rotating rows: as many as run at once, for each CTA makes the angles anew:
+    // 32 x 16 tokens of 48 heads 8 us, and 10 with 8 an SM)
+    const unsigned z = head_splits(p, c.touched * c.n_layers_in, (n_rows + lanes / tp - 1) / (lanes / tp), c.rope ? 4 : 8);
     const dim3 grid((unsigned)std::min<int64_t>(c.touched, (int64_t)p->sm_count * 64), (unsigned)c.n_layers_in, z);
     return with_words(p, words, s, fill, [&](auto args) -> int {
         using A = decltype(args);
@@ -852,7 +854,7 @@ int dendrite_read_kv(dendrite_pool* p, int32_t layer, const int32_t* branches, c
     for (int32_t i = 0; i < n; ++i) longest = std::max(longest, counts[i]);
     while (tp < lanes && tp < std::min(longest, bs)) tp *= 2;
     const dim3 grid((unsigned)std::min<int64_t>(tiles, (int64_t)p->sm_count * 64), 1,
-                    head_splits(p, tiles, (2 * p->n_kv + lanes / tp - 1) / (lanes / tp)));
+                    head_splits(p, tiles, (2 * p->n_kv + lanes / tp - 1) / (lanes / tp), 8));
     return with_words(p, 5 * (size_t)n, s, fill, [&](auto args) -> int {
         using A = decltype(args);
         if (p->dtype == DENDRITE_FP8)
