@@ -146,6 +146,7 @@ struct Branch {
     int32_t live = 0;
     int32_t len = 0;
     int32_t node = -1;
+    int32_t cut = 0;   // rolled back into a block (or forked from a branch that was), and not appended to since
 };
 
 struct Node {

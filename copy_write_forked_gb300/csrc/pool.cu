@@ -377,6 +377,49 @@ k_append_meta(const __grid_constant__ A args, int32_t n, int32_t n_new, int32_t 
     }
 }
 
+// --------------------------------------------- append, tails copied first
+// Where a row written in place would race with the copies of its block
+// (tails_first): CTA i copies the slots branch i holds of its copied-on-write
+// tail, in every layer, before the rows are written, and clears the source so
+// that the kernels of phase 2 copy nothing.
+struct TailLayout {
+    unsigned char *k, *v;
+    int64_t k_layer, v_layer, k_tile, v_tile;   // bytes
+    int32_t k_slot, v_slot, extra;   // bytes of a slot; extra: one more byte per slot behind a tile's slots
+    int32_t bs, bpb, n_kv, n_layers, n_blocks;
+};
+
+template <typename A>
+__global__ void __launch_bounds__(256)
+k_copy_tails(const __grid_constant__ A args, const TailLayout a, const int32_t* table, int32_t* call, DevMeta* meta) {
+    pdl_wait();
+    if (meta->status) return;
+    const int32_t i = blockIdx.x, n = gridDim.x, L = args[n + i], held = L % a.bs;
+    const int32_t src = call[n + i];
+    if (src < 0) return;
+    const int32_t dst = table[(int64_t)args[i] * a.bpb + L / a.bs];
+    if ((uint32_t)dst >= (uint32_t)a.n_blocks || src >= a.n_blocks) {
+        if (threadIdx.x == 0) atomicCAS(&meta->status, 0, DENDRITE_ECORRUPT);
+        return;
+    }
+    for (int32_t y = 0; y < a.n_layers; ++y) {
+        for (int32_t h = 0; h < a.n_kv; ++h) {
+            for (int v = 0; v < 2; ++v) {
+                unsigned char* pool = v ? a.v + y * a.v_layer : a.k + y * a.k_layer;
+                const int64_t tile = v ? a.v_tile : a.k_tile;
+                const int32_t slot = v ? a.v_slot : a.k_slot;
+                const unsigned char* from = pool + ((int64_t)src * a.n_kv + h) * tile;
+                unsigned char* to = pool + ((int64_t)dst * a.n_kv + h) * tile;
+                for (int32_t w = threadIdx.x; w < held * slot / 16; w += 256)
+                    reinterpret_cast<uint4*>(to)[w] = reinterpret_cast<const uint4*>(from)[w];
+                if (a.extra && (int32_t)threadIdx.x < held) to[a.bs * slot + threadIdx.x] = from[a.bs * slot + threadIdx.x];
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) call[n + i] = -1;
+}
+
 // ------------------------------------------------------- append, phase 2
 // One CTA at a time per (branch, touched block, kv head) tile: copies the
 // valid slots of a copied-on-write tail (if any) and scatters the new rows
@@ -963,6 +1006,57 @@ int append_check(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n
     return DENDRITE_OK;
 }
 
+// Whether an append has to copy its shared tails before it writes a row.  The
+// last holder of a tail in a call writes in place while the others copy what
+// they hold of it: a race where it holds less of the block than they do.  Such
+// branches differ in length within a block that one of them got from the other,
+// which only a roll-back makes: the node that owns the block's first position
+// is then on both their paths.
+bool tails_first(dendrite_pool* p, const int32_t* branches, const int32_t* lens, int32_t n) {
+    bool cut = false;
+    for (int32_t i = 0; i < n; ++i) cut |= p->br[branches[i]].cut != 0;
+    if (!cut) return false;
+    struct Tail {
+        int32_t owner, block, len;
+    };
+    static thread_local std::vector<Tail> tails;
+    tails.clear();
+    for (int32_t i = 0; i < n; ++i) {
+        const int32_t first = lens[i] / p->block_size * p->block_size;
+        int32_t id = p->br[branches[i]].node;
+        if (first == lens[i] || (p->nodes[id].fork_len <= first && p->nodes[id].first_child < 0)) continue;
+        while (p->nodes[id].fork_len > first) id = p->nodes[id].parent;
+        tails.push_back(Tail{id, first, lens[i]});
+    }
+    std::sort(tails.begin(), tails.end(), [](const Tail& a, const Tail& b) {
+        return a.owner != b.owner ? a.owner < b.owner : a.block != b.block ? a.block < b.block : a.len < b.len;
+    });
+    for (size_t k = 1; k < tails.size(); ++k)
+        if (tails[k].owner == tails[k - 1].owner && tails[k].block == tails[k - 1].block && tails[k].len != tails[k - 1].len)
+            return true;
+    return false;
+}
+
+TailLayout tail_layout(const dendrite_pool* p) {
+    TailLayout t{};
+    const int64_t tiles = p->num_blocks * p->n_kv;
+    t.k = static_cast<unsigned char*>(p->d_k);
+    t.v = static_cast<unsigned char*>(p->d_v);
+    t.k_layer = (int64_t)p->layer_bytes;
+    t.v_layer = (int64_t)p->layer_bytes_v;
+    t.k_tile = (int64_t)p->layer_bytes / tiles;
+    t.v_tile = (int64_t)p->layer_bytes_v / tiles;
+    t.extra = p->dtype == DENDRITE_FP8;
+    t.k_slot = (int32_t)((t.k_tile - (t.extra ? p->block_size : 0)) / p->block_size);
+    t.v_slot = (int32_t)((t.v_tile - (t.extra ? p->block_size : 0)) / p->block_size);
+    t.bs = p->block_size;
+    t.bpb = p->bpb;
+    t.n_kv = p->n_kv;
+    t.n_layers = p->n_layers;
+    t.n_blocks = (int32_t)p->num_blocks;
+    return t;
+}
+
 // Launches the metadata kernel (meta) and/or the copy kernel (copy) of an
 // append whose branches had lengths lens[] before it.  The copy writes layers
 // [layer0, layer0 + n_layers_in) from K/V (layer y's rows in_layer 16-byte
@@ -1001,6 +1095,9 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
             DENDRITE_CUDA(launch_pdl(k_append_meta<decltype(args)>, dim3(1), dim3(kAppendMetaThreads), 0, s, args,
                                      n, n_new, bs, p->bpb, (int32_t)p->num_blocks, p->d_table, p->d_refcount,
                                      p->d_stack, p->d_holders, p->d_last, p->d_call_i32, p->d_meta));
+            if (tails_first(p, branches, lens, n))
+                DENDRITE_CUDA(launch_pdl(k_copy_tails<decltype(args)>, dim3((unsigned)n), dim3(256), 0, s, args,
+                                         tail_layout(p), (const int32_t*)p->d_table, p->d_call_i32, p->d_meta));
             prof_end(p, T_APPEND_META, s);
         }
         if (copy && (rotate || p->dtype == DENDRITE_FP8)) {
@@ -1121,6 +1218,7 @@ void append_commit_lengths(dendrite_pool* p, const int32_t* branches, int32_t n,
     for (int32_t i = 0; i < n; ++i) {
         Branch& b = p->br[branches[i]];
         b.len += n_new;
+        b.cut = 0;
         p->nodes[b.node].len = b.len;
     }
     p->version++;
@@ -1301,6 +1399,7 @@ int dendrite_branch_new(dendrite_pool* p, int32_t* out) {
     const int32_t h = alloc_handle(p);
     p->br[h].live = 1;
     p->br[h].len = 0;
+    p->br[h].cut = 0;
     p->br[h].node = new_node(p, -1, 0, h);
     p->version++;
     p->shape_version++;   // the tree's shape changed, not only lengths
@@ -1335,6 +1434,7 @@ int dendrite_fork_batch(dendrite_pool* p, const int32_t* parents, const int32_t*
             const int32_t h = alloc_handle(p);
             p->br[h].live = 1;
             p->br[h].len = L;
+            p->br[h].cut = p->br[pa].cut;
             p->br[h].node = new_node(p, p->br[pa].node, L, h);
             out_children[k++] = h;
             child.push_back(h);
@@ -1607,6 +1707,7 @@ int dendrite_truncate(dendrite_pool* p, const int32_t* branches, const int32_t* 
         const int32_t old = b.node;
         b.node = new_node(p, old, new_lens[i], branches[i]);
         b.len = new_lens[i];
+        b.cut = b.len % bs != 0;
         p->nodes[old].handle = -1;
         drop_node_ref(p, old);
     }

@@ -181,6 +181,49 @@ def test_copy_on_write_keeps_the_older_rows(kind):
         p.close()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+@pytest.mark.parametrize("how", ["append", "rope", "split"])
+def test_branches_of_different_lengths_in_one_shared_tail(kind, how):
+    """Siblings of a half-full tail, one of them rolled back inside it, appended to in one call: the one served last
+    writes in place and must not overwrite what the others still have to copy.  Tables are those of one call each."""
+    rows = R.ROW_DTYPE[kind]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    layers, kv = (2, 8) if how == "split" else (1, 8)
+    x = torch.randn(layers, 1, 44, kv, 128, generator=g, device="cuda").to(rows)
+    y = torch.randn(layers, 9, 20, kv, 128, generator=g, device="cuda").to(rows)
+    for cut in (33, 40, 43):
+        state = []
+        for one_call in (True, False):
+            pool = Pool(128, 16, kv, 128, R.POOL_DTYPE[kind], max_branches=16, n_layers=layers)
+            root = pool.new_branch()
+            pool.append_kv([root], *[x if layers > 1 else x[0]] * 2)
+            kids = pool.fork(root, 8)
+            pool.free([root])
+            pool.truncate([kids[3]], [cut])
+            order = kids[:3] + kids[4:] + pool.fork(kids[3], 1) + [kids[3]]   # the shortest hold the block last
+            for br in ([order] if one_call else [[b] for b in order]):
+                at = [order.index(b) for b in br]
+                new = y[:, at].contiguous()
+                if how == "split":
+                    pool.append_begin(br, 20)
+                    for layer in range(layers):
+                        pool.append_layer(layer, new[layer], new[layer])
+                elif how == "rope":
+                    pool.append_rope(br, new[0], new[0], Rope(128))
+                else:
+                    pool.append_kv(br, new[0], new[0])
+            state.append(([pool.read_table(b) for b in order], pool.read_refcounts(), pool.read_free_stack()))
+            for layer in range(layers):
+                lens = [pool.branch_len(b) for b in order]
+                k, v = (R.f64(z) for z in pool.read_kv(order, [0] * 9, lens, layer=layer))
+                for i, n in enumerate(lens):
+                    old, start = R.held(R.f64(x[layer, 0]), kind)[:n - 20], sum(lens[:i])
+                    assert np.array_equal(k[start:start + n - 20], old) and np.array_equal(v[start:start + n - 20], old), (cut, i)
+                    assert np.array_equal(v[start + n - 20:start + n], R.held(R.f64(y[layer, i]), kind))
+            pool.close()
+        assert state[0] == state[1]
+
+
 def test_another_stream_and_two_calls_at_once():
     pools = [Pool(64, 16, 4, 128, torch.bfloat16, max_branches=8) for _ in range(2)]
     rope = Rope(128)
