@@ -73,8 +73,11 @@ constexpr int TC_S1_WARP = TC_V_WARP + 1;                          // 12
 // registers a thread: 0-7 softmax, 8-11 the issuers (S and PV of row tile 0, then
 // of 1), 12 copies the stored tiles, 13-20 convert one half tile (K or V) each.
 //
-// What bounds it is the issue of instructions: 4,096 scores and 16,384 codes a
-// stage of 64 rows take some 2,000 cycles, half of them issuing.  The attention of
+// What bounds it are the chains of the roles side by side: 4,096 scores and
+// 16,384 codes a stage of 64 rows take some 2,000 cycles, in which every role works
+// most of the time, the SM issues in 56 of 100 cycles and shared memory moves about
+// half of what it can (fewer instructions alone do not help: with fp16 operands a
+// pair of codes takes two instructions less, and the first case 150 us).  The attention of
 // 32 draft trees of 16 nodes (64 rows a kv head) over 7,000 tokens each, 360 MB of
 // codes, takes 140 us (2.6 TB/s); of 12 trees of 32 nodes (256 rows) over 16,000
 // tokens 124 us.  On the way there, the first case / the second:
