@@ -248,12 +248,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         TC_W8(0), TC_W8(8)
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : TC_R8(0), TC_R8(8)
+        : "r"(taddr));
+}
 #define TC_RW8(i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), \
                   "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7])
 // Wait for this thread's tcgen05.ld results.  The registers pass through the
 // statement so that no use of them is scheduled before the wait.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : TC_RW8(0), TC_RW8(8), TC_RW8(16), TC_RW8(24)::"memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : TC_RW8(0), TC_RW8(8)::"memory");
 }
 // Half a stage's scores: what the row does not see becomes -inf.
 __device__ __forceinline__ void mask_half(uint32_t (&v)[32], uint32_t see) {
@@ -571,21 +580,35 @@ __device__ __forceinline__ void issue_products(const AttnArgs& a, uint32_t base,
     __syncwarp();
 }
 
-// 8-bit pools: O of the warp's rows times 2^d where need, once the PV before
-// this stage (bar_pv, phase) has completed.
-__device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint32_t bar_pv, uint32_t phase,
-                                          volatile int* abortp, DevMeta* meta) {
-    if (!warp_wait_<true>(bar_pv, phase, abortp, meta)) return false;
-    tc_fence_after();
+// 8-bit pools: brings what a row has so far to a reference 2^-d higher, where
+// need: O, once the PV before this stage (bar_pv, phase) has completed (with_o),
+// and the stage's first 32 weights (with_p).  d is whole, so the weights stay
+// the rounded ones they were.
+__device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint32_t tP, bool with_o, bool with_p,
+                                          uint32_t bar_pv, uint32_t phase, volatile int* abortp, DevMeta* meta) {
     const float alpha = need ? ex2_approx(d) : 1.f;
-#pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t v[32];
-        tmem_ld32(tl + c0, v);
-        tmem_wait_ld(v);
+    if (with_p) {
+        uint32_t v[16];
+        tmem_wait_st();
+        tmem_ld16(tP, v);
+        tmem_wait_ld16(v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-        tmem_st32(tl + c0, v);
+        for (int i = 0; i < 16; ++i)
+            v[i] = pack_bf16(__uint_as_float(v[i] << 16) * alpha, __uint_as_float(v[i] & 0xffff0000u) * alpha);
+        tmem_st16(tP, v);
+    }
+    if (with_o) {
+        if (!warp_wait_<true>(bar_pv, phase, abortp, meta)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(tl + c0, v);
+            tmem_wait_ld(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+            tmem_st32(tl + c0, v);
+        }
     }
     tmem_wait_st();
     return true;
@@ -925,8 +948,9 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     continue;
                 }
                 if constexpr (F8) {
-                    // the scores are read twice from tensor memory, half a stage at
-                    // a time: 32 of them fit the 80 registers a thread has
+                    // half a stage at a time: 32 scores fit the 80 registers a thread
+                    // has, and a reference that the second half outgrows is raised
+                    // for the first half's weights too
                     const int32_t off = R.limit - (U.blk_start + st - U.tile_off) * BS;
                     const bool plain = __all_sync(0xffffffffu, off >= TC_TOK) && ntiles == 4;
                     const uint32_t tS = tl + 128 + b * 64;
@@ -938,43 +962,42 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                                           : 0ull;
                         if (ntiles < 4) see &= (1ull << (ntiles * BS)) - 1ull;
                     }
-                    float mx;
-                    {
-                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t v[32];
-                            tmem_ld32(tS + 32 * half, v);
-                            tmem_wait_ld(v);
-                            if (!plain) mask_half(v, (uint32_t)(see >> (32 * half)));
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
-                        }
-                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
-                    }
-                    if (k == k0) {
-                        m_ref = mx;   // this stage's PV overwrites O
-                    } else {
-                        const bool need = mx > m_ref + RESCALE_THRESHOLD;
-                        if (__any_sync(0xffffffffu, need)) {
-                            ok = rescale_rows(need, m_ref - mx, tl, bar(B_PV_DONE + 2 * r + ((js - 1) & 1)),
-                                              (uint32_t)((js - 1) >> 1) & 1u, abortp, a.meta);
-                            if (!ok) break;
-                            if (need) {
-                                l *= ex2_approx(m_ref - mx);
-                                m_ref = mx;
-                            }
-                        }
-                    }
-                    const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
-                    const f32x2 scale2 = pair(a.scale_log2, a.scale_log2), nref2 = pair(nref, nref);
                     f32x2 l2[2] = {0, 0};
+                    const f32x2 scale2 = pair(a.scale_log2, a.scale_log2);
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t v[32], pk[16];
+                    for (int half = 0; half < 2;) {
+                        uint32_t v[32];
                         tmem_ld32(tS + 32 * half, v);
                         tmem_wait_ld(v);
                         if (!plain) mask_half(v, (uint32_t)(see >> (32 * half)));
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
+                        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+                        // whole references: what is rescaled keeps its bits
+                        if (k == k0 && half == 0) {
+                            m_ref = ceilf(mx);
+                        } else {
+                            const bool need = mx > m_ref + RESCALE_THRESHOLD;
+                            if (__any_sync(0xffffffffu, need)) {
+                                const float m_new = ceilf(mx);
+                                ok = rescale_rows(need, m_ref - m_new, tl, tS, k != k0, half != 0,
+                                                  bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u,
+                                                  abortp, a.meta);
+                                if (!ok) break;
+                                if (need) {
+                                    const float alpha = ex2_approx(m_ref - m_new);
+                                    l *= alpha;
+                                    l2[0] = mul2(l2[0], pair(alpha, alpha));
+                                    l2[1] = mul2(l2[1], pair(alpha, alpha));
+                                    m_ref = m_new;
+                                }
+                                continue;   // this half again: its scores need not outlive the call
+                            }
+                        }
+                        const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+                        const f32x2 nref2 = pair(nref, nref);
+                        uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const f32x2 x = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale2,
@@ -984,7 +1007,9 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                                                              __uint_as_float(pk[i] & 0xffff0000u)));
                         }
                         tmem_st16(tS + 16 * half, pk);   // over columns already read
+                        ++half;
                     }
+                    if (!ok) break;
                     const f32x2 ls = add2(l2[0], l2[1]);
                     l += low(ls) + high(ls);
                 } else {

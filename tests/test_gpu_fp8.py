@@ -255,6 +255,27 @@ def test_attention_over_rows_of_very_different_size(case):
     pool.close()
 
 
+@pytest.mark.parametrize("q_len", [1, 12, 70])
+@pytest.mark.parametrize("step", [0.05, 0.4, 1.5, -0.4])
+def test_running_maximum(step, q_len):
+    """Scores that climb (or fall) with the position: the reference moves in every stage, in the middle of stages and not at all."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    kv, group, n = 2, 4, 400
+    q = torch.randn(1, q_len, kv * group, 128, generator=g, device="cuda")
+    q[..., 0] = 8.0
+    K = torch.randn(1, n, kv, 128, generator=g, device="cuda") * 0.3
+    K[..., 0] = step * torch.arange(n, device="cuda")[None, :, None]
+    V = torch.randn(1, n, kv, 128, generator=g, device="cuda")
+    K, V, q = K.bfloat16(), V.bfloat16(), q.bfloat16()
+    pool = Pool(64, 16, kv, 128, F8, max_branches=4)
+    b = pool.new_branch()
+    pool.append_kv([b], K, V)
+    out = pool.tree_attn_decode(q, [b])
+    pool.sync()
+    _attend("fp8", [(R.held(R.f64(K[0]), "fp8"), R.held(R.f64(V[0]), "fp8"))], q, out, q_len)
+    pool.close()
+
+
 def test_keys_that_are_not_finite_touch_only_the_rows_that_see_them():
     g = torch.Generator(device="cuda").manual_seed(4)
     pool = Pool(64, 16, 1, 128, F8, max_branches=4)
