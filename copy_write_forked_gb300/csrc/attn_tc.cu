@@ -79,13 +79,14 @@ constexpr int TC_S1_WARP = TC_V_WARP + 1;                          // 12
 // half of what it can (fewer instructions alone do not help: with fp16 operands a
 // pair of codes takes two instructions less, and the first case 150 us).  The attention of
 // 32 draft trees of 16 nodes (64 rows a kv head) over 7,000 tokens each, 360 MB of
-// codes, takes 140 us (2.6 TB/s); of 12 trees of 32 nodes (256 rows) over 16,000
-// tokens 124 us.  On the way there, the first case / the second:
-//   - one branch-selected issuer thread a row tile, one unit on one row tile: 191 / 148 us
+// codes, takes 143 us (2.5 TB/s); of 12 trees of 32 nodes (256 rows) over 16,000
+// tokens 128 us, of 61 nodes (488 rows) 230.  On the way there, in these cases:
+//   - one branch-selected issuer thread a row tile, one unit on one row tile: 191 / 148 / 277 us
 //   - an elected lane of a converged warp as issuer, units of up to 128 rows
-//     split along their tokens (below): 154 / 134
-//   - packed fp32 arithmetic, scores read twice instead of held, an issuer each
-//     for S and PV of both row tiles, K ring of 2 and V ring of 4 stages: 140 / 124
+//     split along their tokens (below): 154 / 134 / 244
+//   - packed fp32 arithmetic, scores not held over a stage, an issuer each
+//     for S and PV of both row tiles, K ring of 2 and V ring of 4 stages: 142 / 124 / 243
+//   - scores read once, maximum and weights half a stage at a time: 143 / 128 / 230
 // Waits and the rescaling of O are out of line and the issuers share their code:
 // with everything in line a tenth of the instruction fetches missed the SM's cache.
 constexpr int F8_RAW = 3;
