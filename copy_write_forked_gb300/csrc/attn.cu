@@ -2382,11 +2382,6 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
         DENDRITE_TRY(check_live(p, branches[i]));
         if (p->br[branches[i]].len < q_len) return DENDRITE_EINVAL;
     }
-    {
-        std::vector<int32_t> s(branches, branches + n);
-        std::sort(s.begin(), s.end());
-        if (std::adjacent_find(s.begin(), s.end()) != s.end()) return DENDRITE_EINVAL;
-    }
     cudaStream_t s = (cudaStream_t)stream;
     // the whole call's device work, plan upload and expansion included (its
     // events start after the host has built the plan)
@@ -2396,6 +2391,11 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
     const bool same_query = pc.valid && pc.q_len == q_len && pc.n_q_heads == n_q_heads && pc.n_trees == n_trees &&
                             (int32_t)pc.branches.size() == n && std::equal(branches, branches + n, pc.branches.begin()) &&
                             (!parents || std::equal(pc.parents.begin(), pc.parents.end(), parents));
+    if (!same_query) {   // (the branches of the cached plan are distinct)
+        std::vector<int32_t> o(branches, branches + n);
+        std::sort(o.begin(), o.end());
+        if (std::adjacent_find(o.begin(), o.end()) != o.end()) return DENDRITE_EINVAL;
+    }
     const bool hit = same_query && pc.version == p->version;
     // Only appends since the plan was built, and no queried branch reached a
     // new block: the segments, units and partition are unchanged, and only

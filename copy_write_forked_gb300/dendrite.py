@@ -421,22 +421,28 @@ class Pool:
                                                 _stream_ptr(stream, self._dev)), "append_layer_rope")
         return out
 
+    def _query(self, Q, n, out):
+        """Checks of an attention call over n branches; returns (Q's shape, the output)."""
+        self._check_tensor(Q, "Q")
+        qs = Q.shape
+        if len(qs) != 4 or qs[0] != n or qs[3] != self.head_dim:
+            raise DendriteError(-1, f"Q shape {tuple(qs)}")
+        if out is None:
+            return qs, torch.empty_like(Q)
+        self._check_tensor(out, "out")
+        if out.shape != qs:
+            raise DendriteError(-1, "out shape")
+        return qs, out
+
     def tree_attn_draft(self, Q: torch.Tensor, branches: Sequence[int], parents, out: Optional[torch.Tensor] = None,
                         stream=None, layer: int = 0) -> torch.Tensor:
         """Attention of draft trees: Q ``[n_branches][n_draft][n_q_heads][head_dim]``
         are each branch's last n_draft tokens; token j sees what stands before
         the drafts, its ancestors and itself (``parents`` as in :meth:`append_rope`)."""
-        self._check_tensor(Q, "Q")
-        if Q.dim() != 4 or Q.shape[0] != len(branches) or Q.shape[3] != self.head_dim:
-            raise DendriteError(-1, f"Q shape {tuple(Q.shape)}")
-        if out is None:
-            out = torch.empty_like(Q)
-        self._check_tensor(out, "out")
-        if out.shape != Q.shape:
-            raise DendriteError(-1, "out shape")
-        keep, pp, nt = _trees(parents, len(branches), Q.shape[1])
+        qs, out = self._query(Q, len(branches), out)
+        keep, pp, nt = _trees(parents, len(branches), qs[1])
         ba = _arr(branches)
-        _check(lib().dendrite_tree_attn_draft(self._h, int(layer), Q.data_ptr(), Q.shape[2], Q.shape[1], _ptr(ba),
+        _check(lib().dendrite_tree_attn_draft(self._h, int(layer), Q.data_ptr(), qs[2], qs[1], _ptr(ba),
                                               len(branches), pp, nt, out.data_ptr(), _stream_ptr(stream, self._dev)),
                "tree_attn_draft")
         return out
@@ -470,16 +476,9 @@ class Pool:
     def tree_attn_decode(self, Q: torch.Tensor, branches: Sequence[int], out: Optional[torch.Tensor] = None,
                          stream=None, layer: int = 0) -> torch.Tensor:
         """Q: ``[n_branches][q_len][n_q_heads][head_dim]``; returns out of the same shape."""
-        self._check_tensor(Q, "Q")
-        if Q.dim() != 4 or Q.shape[0] != len(branches) or Q.shape[3] != self.head_dim:
-            raise DendriteError(-1, f"Q shape {tuple(Q.shape)}")
-        if out is None:
-            out = torch.empty_like(Q)
-        self._check_tensor(out, "out")
-        if out.shape != Q.shape:
-            raise DendriteError(-1, "out shape")
+        qs, out = self._query(Q, len(branches), out)
         ba = _arr(branches)
-        _check(lib().dendrite_tree_attn_decode_layer(self._h, int(layer), Q.data_ptr(), Q.shape[2], Q.shape[1],
+        _check(lib().dendrite_tree_attn_decode_layer(self._h, int(layer), Q.data_ptr(), qs[2], qs[1],
                                                      _ptr(ba), len(branches), out.data_ptr(),
                                                      _stream_ptr(stream, self._dev)),
                "tree_attn_decode")
