@@ -2383,6 +2383,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
         if (p->br[branches[i]].len < q_len) return DENDRITE_EINVAL;
     }
     cudaStream_t s = (cudaStream_t)stream;
+    if (p->dtype == DENDRITE_FP8) DENDRITE_TRY(check_not_capturing(s));
     // the whole call's device work, plan upload and expansion included (its
     // events start after the host has built the plan)
     bool began = false;

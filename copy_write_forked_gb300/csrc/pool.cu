@@ -1065,6 +1065,7 @@ TailLayout tail_layout(const dendrite_pool* p) {
 int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens, int32_t n, int32_t n_new,
                   int64_t touched, bool copy, const void* K, const void* V, int32_t layer0, int32_t n_layers_in,
                   int64_t in_layer, cudaStream_t s, bool meta = true, const RowsCall* rotate = nullptr) {
+    if (p->dtype == DENDRITE_FP8 && !rotate) DENDRITE_TRY(check_not_capturing(s));
     const int32_t bs = p->block_size;
     // args: branch[n], len[n], tile prefix[n]
     constexpr int CAP = 768;

@@ -301,9 +301,9 @@ int dendrite_rope_init(dendrite_rope* rope, int32_t rot_dim, int32_t interleaved
  * DENDRITE_TURBO pools return DENDRITE_EDTYPE.  Otherwise as dendrite_append_kv.
  * dendrite_append_layer_rope is dendrite_append_layer's turn of the same: layer
  * `layer` of the pending append (Q without a layer dimension).
- * These two and the draft and read calls below return DENDRITE_EINVAL on a
- * stream that is being captured into a graph (a replay would use the lengths
- * and tables of the capture).
+ * These two, the draft and read calls below, and the append and attention calls
+ * of 8-bit pools return DENDRITE_EINVAL on a stream that is being captured into a
+ * graph (a replay would use the lengths, tables and plan of the capture).
  */
 #define DENDRITE_MAX_DRAFT 64
 int dendrite_append_rope(dendrite_pool* pool, const int32_t* branches, int32_t n_branches, int32_t n_new,

@@ -383,3 +383,33 @@ def test_refusals():
     pool.sync()
     pool.close()
     tq.close()
+
+
+def test_captured_calls_are_refused():
+    """Appends and attention of an 8-bit pool on a capturing stream: refused, and nothing of the pool changed."""
+    from copy_write_forked_gb300.dendrite import _arr, _ptr, lib
+    pool = Pool(16, 16, 2, 128, F8, max_branches=4)
+    b = pool.new_branch()
+    x = torch.randn(1, 20, 2, 128, device="cuda").bfloat16()
+    q = torch.randn(1, 1, 8, 128, device="cuda").bfloat16()
+    pool.append_kv([b], x, x)
+    want = pool.tree_attn_decode(q, [b])
+    out = torch.zeros_like(q)
+    ba = _arr([b])
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    L = lib()
+    with torch.cuda.stream(s):
+        graph.capture_begin()
+        rcs = [L.dendrite_append_kv(pool._h, _ptr(ba), 1, 20, x.data_ptr(), x.data_ptr(), s.cuda_stream),
+               L.dendrite_append_begin(pool._h, _ptr(ba), 1, 20, s.cuda_stream),
+               L.dendrite_tree_attn_decode_layer(pool._h, 0, q.data_ptr(), 8, 1, _ptr(ba), 1, out.data_ptr(), s.cuda_stream)]
+        graph.capture_end()
+    assert rcs == [-1, -1, -1]
+    assert pool.branch_len(b) == 20 and torch.equal(pool.tree_attn_decode(q, [b]), want)
+    pool.append_kv([b], x, x)
+    k, _ = pool.read_kv([b], [20], [20])
+    assert np.array_equal(R.f64(k), R.held(R.f64(x[0]), "fp8"))
+    pool.sync()
+    pool.close()
