@@ -6,12 +6,12 @@
 #include <stdint.h>
 
 #include <chrono>
-#include <deque>
 #include <string>
 #include <utility>
 #include <vector>
 
 #include "dendrite.h"
+#include "span_ring.h"
 
 namespace dendrite {
 
@@ -158,7 +158,8 @@ struct Node {
     int32_t first_child = -1, next_sib = -1, prev_sib = -1;   // the child nodes, as a list
 };
 
-// Pinned host -> device staging ring for per-call argument arrays.
+// Pinned host -> device staging ring for per-call argument arrays: one region
+// a call, from reserve to release.
 class Staging {
 public:
     int init(size_t cap);
@@ -167,22 +168,16 @@ public:
     int reserve(size_t bytes, char** h, char** d);
     // Copy the reserved region to the device on `stream`.
     int upload(cudaStream_t stream, char* h, size_t bytes);
-    // Mark every region reserved since the last release as reusable once
-    // the work queued on `stream` so far has completed.
+    // Mark the region as reusable once the work queued on `stream` so far has
+    // completed.
     int release(cudaStream_t stream);
 
 private:
     int grow(size_t need);
-    int wait_overlap(size_t off, size_t n);
     char* h_ = nullptr;
     char* d_ = nullptr;
-    size_t cap_ = 0;
-    size_t head_ = 0;
-    size_t pending_begin_ = 0, pending_end_ = 0;
-    bool pending_ = false;
-    bool pending_wrapped_ = false;
-    struct Region { size_t off, end; cudaEvent_t ev; };
-    std::deque<Region> inflight_;
+    SpanRing<cudaEvent_t> ring_;
+    size_t off_ = 0, bytes_ = 0;   // the region reserved and not yet released (bytes_ 0: none)
     std::vector<cudaEvent_t> spare_;
 };
 

@@ -753,81 +753,53 @@ int check_live(const dendrite_pool* p, int32_t h) {
 
 // ----------------------------------------------------------------- staging
 int Staging::init(size_t cap) {
-    cap_ = cap;
-    if (cudaMallocHost(&h_, cap) != cudaSuccess) return cuda_err(cudaErrorMemoryAllocation);
-    if (cudaMalloc(&d_, cap) != cudaSuccess) return cuda_err(cudaErrorMemoryAllocation);
+    if (cudaMallocHost(&h_, cap) != cudaSuccess || cudaMalloc(&d_, cap) != cudaSuccess) {
+        destroy();
+        return cuda_err(cudaErrorMemoryAllocation);
+    }
+    ring_.reset(cap);
     return DENDRITE_OK;
 }
 
 void Staging::destroy() {
-    for (auto& r : inflight_) cudaEventDestroy(r.ev);
+    ring_.drain([](cudaEvent_t e) { cudaEventDestroy(e); });
     for (auto e : spare_) cudaEventDestroy(e);
-    inflight_.clear();
     spare_.clear();
     if (h_) cudaFreeHost(h_);
     if (d_) cudaFree(d_);
     h_ = d_ = nullptr;
-}
-
-int Staging::wait_overlap(size_t off, size_t n) {
-    while (!inflight_.empty()) {
-        const Region& r = inflight_.front();
-        const bool overlap = r.off < off + n && off < r.end;
-        if (!overlap) {
-            // regions are handed out in ring order; stop at the first one that
-            // does not overlap unless it lies behind the new range
-            bool later = false;
-            for (const Region& q : inflight_)
-                if (q.off < off + n && off < q.end) later = true;
-            if (!later) break;
-        }
-        DENDRITE_CUDA(cudaEventSynchronize(r.ev));
-        spare_.push_back(r.ev);
-        inflight_.pop_front();
-    }
-    return DENDRITE_OK;
+    ring_.reset(0);
 }
 
 int Staging::grow(size_t need) {
     // wait for everything in flight, then reallocate
-    for (auto& r : inflight_) {
-        cudaEventSynchronize(r.ev);
-        spare_.push_back(r.ev);
-    }
-    inflight_.clear();
-    size_t cap = cap_;
+    ring_.drain([&](cudaEvent_t e) {
+        cudaEventSynchronize(e);
+        spare_.push_back(e);
+    });
+    size_t cap = std::max<size_t>(ring_.cap(), 4096);
     while (cap < need) cap *= 2;
-    cudaFreeHost(h_);
-    cudaFree(d_);
-    h_ = d_ = nullptr;
-    cap_ = 0;
-    head_ = 0;
-    pending_ = false;
+    destroy();
     return init(cap);
 }
 
 int Staging::reserve(size_t bytes, char** h, char** d) {
-    bytes = (bytes + 255) & ~size_t(255);
-    if (bytes == 0) bytes = 256;
-    if (bytes > cap_ / 2) {
-        if (pending_) return DENDRITE_EINVAL;   // one oversized region per call only
-        DENDRITE_TRY(grow(bytes * 2));
+    if (bytes_) {   // a call failed before its release: its copy may be in flight
+        DENDRITE_CUDA(cudaDeviceSynchronize());
+        bytes_ = 0;
     }
-    size_t off = head_;
-    if (off + bytes > cap_) {
-        off = 0;
-        if (pending_) pending_wrapped_ = true;
-    }
-    DENDRITE_TRY(wait_overlap(off, bytes));
-    if (!pending_) {
-        pending_ = true;
-        pending_wrapped_ = false;
-        pending_begin_ = off;
-    }
-    pending_end_ = off + bytes;
-    head_ = off + bytes;
-    *h = h_ + off;
-    *d = d_ + off;
+    bytes = std::max<size_t>((bytes + 255) & ~size_t(255), 256);
+    if (bytes > ring_.cap() / 2) DENDRITE_TRY(grow(bytes * 2));
+    cudaError_t err = cudaSuccess;
+    if (!ring_.place(bytes, &off_, [&](cudaEvent_t e) {
+            err = cudaEventSynchronize(e);
+            spare_.push_back(e);
+            return err == cudaSuccess;
+        }))
+        return cuda_err(err);
+    bytes_ = bytes;
+    *h = h_ + off_;
+    *d = d_ + off_;
     return DENDRITE_OK;
 }
 
@@ -837,7 +809,6 @@ int Staging::upload(cudaStream_t stream, char* h, size_t bytes) {
 }
 
 int Staging::release(cudaStream_t stream) {
-    if (!pending_) return DENDRITE_OK;
     cudaEvent_t ev;
     if (!spare_.empty()) {
         ev = spare_.back();
@@ -846,16 +817,8 @@ int Staging::release(cudaStream_t stream) {
         DENDRITE_CUDA(cudaEventCreateWithFlags(&ev, cudaEventDisableTiming));
     }
     DENDRITE_CUDA(cudaEventRecord(ev, stream));
-    if (pending_wrapped_) {
-        inflight_.push_back({pending_begin_, cap_, ev});
-        cudaEvent_t ev2;
-        DENDRITE_CUDA(cudaEventCreateWithFlags(&ev2, cudaEventDisableTiming));
-        DENDRITE_CUDA(cudaEventRecord(ev2, stream));
-        inflight_.push_back({0, pending_end_, ev2});
-    } else {
-        inflight_.push_back({pending_begin_, pending_end_, ev});
-    }
-    pending_ = false;
+    ring_.use(off_, bytes_, ev);
+    bytes_ = 0;
     return DENDRITE_OK;
 }
 
@@ -1090,6 +1053,22 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
             acc += (L + n_new - 1) / bs - L / bs + 1;
         }
     };
+    const bool by_rows = copy && (rotate || p->dtype == DENDRITE_FP8);
+    RowsCall rows{};
+    if (by_rows) {
+        if (rotate) rows = *rotate;
+        rows.branches = branches;
+        rows.lens = lens;
+        rows.n = n;
+        rows.n_new = n_new;
+        rows.touched = touched;
+        rows.K = K;
+        rows.V = V;
+        rows.layer0 = layer0;
+        rows.n_layers_in = n_layers_in;
+        rows.kv_layer = in_layer * (16 / p->elt);
+    }
+    const int32_t* rows_staged = nullptr;   // its argument words on the device, where they are not kernel parameters
     auto launch = [&](auto args) -> int {
         if (meta) {
             prof_begin(p, T_APPEND_META, s);
@@ -1101,20 +1080,9 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
                                          tail_layout(p), (const int32_t*)p->d_table, p->d_call_i32, p->d_meta));
             prof_end(p, T_APPEND_META, s);
         }
-        if (copy && (rotate || p->dtype == DENDRITE_FP8)) {
-            RowsCall c = rotate ? *rotate : RowsCall{};
-            c.branches = branches;
-            c.lens = lens;
-            c.n = n;
-            c.n_new = n_new;
-            c.touched = touched;
-            c.K = K;
-            c.V = V;
-            c.layer0 = layer0;
-            c.n_layers_in = n_layers_in;
-            c.kv_layer = in_layer * (16 / p->elt);
+        if (by_rows) {
             prof_begin(p, T_APPEND_COPY, s);
-            DENDRITE_TRY(launch_append_rows(p, c, s));
+            DENDRITE_TRY(launch_append_rows(p, rows, rows_staged, s));
             prof_end(p, T_APPEND_COPY, s);
         } else if (copy && p->dtype == DENDRITE_TURBO) {
             prof_begin(p, T_APPEND_COPY, s);
@@ -1160,18 +1128,30 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
     // (k_append_meta reads the arguments of a different branch in every
     // lane: from kernel parameters such reads are serialised, so larger
     // calls keep them in device memory)
-    if (3 * n <= CAP && !(copy && p->dtype == DENDRITE_TURBO)) {
+    // What is staged, of this call's arguments and of the rows', is one region,
+    // reserved and uploaded before the first launch: a call that cannot have it
+    // has changed nothing.
+    const bool param = 3 * n <= CAP && !(copy && p->dtype == DENDRITE_TURBO);
+    const size_t bytes = param ? 0 : ((size_t)n * 12 + 15) & ~size_t(15);
+    const size_t rows_bytes = by_rows ? staged_rows_words(rows) * 4 : 0;
+    char *h, *d;
+    if (bytes + rows_bytes) {
+        DENDRITE_TRY(p->staging.reserve(bytes + rows_bytes, &h, &d));
+        if (bytes) fill((int32_t*)h);
+        if (rows_bytes) {
+            fill_rows_words(rows, bs, (int32_t*)(h + bytes));
+            rows_staged = (const int32_t*)(d + bytes);
+        }
+        DENDRITE_TRY(p->staging.upload(s, h, bytes + rows_bytes));
+    }
+    if (param) {
         ParamArgs<CAP> a;
         fill(a.v);
-        return launch(a);
+        DENDRITE_TRY(launch(a));
+    } else {
+        DENDRITE_TRY(launch(GlobalArgs{(const int32_t*)d}));
     }
-    char *h, *d;
-    const size_t bytes = (size_t)n * 12;
-    DENDRITE_TRY(p->staging.reserve(bytes, &h, &d));
-    fill((int32_t*)h);
-    DENDRITE_TRY(p->staging.upload(s, h, bytes));
-    DENDRITE_TRY(launch(GlobalArgs{(const int32_t*)d}));
-    return p->staging.release(s);
+    return bytes + rows_bytes ? p->staging.release(s) : DENDRITE_OK;
 }
 
 // Host checks of a rotating append of n x n_new tokens in n_layers layers;

@@ -671,7 +671,33 @@ void tree_depths(const int32_t* parents, int32_t n_trees, int32_t t, std::vector
         }
 }
 
-int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s) {
+// branch[n], length[n], prefix of touched blocks[n], then the draft tree depths as bytes.
+static size_t rows_words(const RowsCall& c) {
+    const size_t n_depth = c.depth ? (size_t)c.n_trees * c.n_new : 0;
+    return 3 * (size_t)c.n + (n_depth + 3) / 4;
+}
+
+size_t staged_rows_words(const RowsCall& c) {
+    const size_t words = rows_words(c);
+    return words > (size_t)kRowsCap ? words : 0;
+}
+
+void fill_rows_words(const RowsCall& c, int32_t bs, int32_t* w) {
+    const size_t n = c.n;
+    int32_t acc = 0;
+    for (size_t i = 0; i < n; ++i) {
+        w[i] = c.branches[i];
+        w[n + i] = c.lens[i];
+        w[2 * n + i] = acc;
+        acc += (c.lens[i] + c.n_new - 1) / bs - c.lens[i] / bs + 1;
+    }
+    if (c.depth) {
+        w[rows_words(c) - 1] = 0;   // the bytes after the last depth
+        std::memcpy(w + 3 * n, c.depth, (size_t)c.n_trees * c.n_new);
+    }
+}
+
+int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* staged, cudaStream_t s) {
     const int32_t bs = p->block_size, n = c.n, n_new = c.n_new;
     RowsArgs a{};
     a.n = n;
@@ -714,21 +740,6 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s) {
         uniform = uniform < 0 ? k : (uniform == k ? k : 0);
     }
     a.uniform = std::max(uniform, 0);
-    const size_t n_depth = a.has_depth ? (size_t)c.n_trees * n_new : 0;
-    const size_t words = 3 * (size_t)n + (n_depth + 3) / 4;
-    auto fill = [&](int32_t* w) {
-        int32_t acc = 0;
-        for (int32_t i = 0; i < n; ++i) {
-            w[i] = c.branches[i];
-            w[n + i] = c.lens[i];
-            w[2 * (size_t)n + i] = acc;
-            acc += (c.lens[i] + n_new - 1) / bs - c.lens[i] / bs + 1;
-        }
-        if (n_depth) {
-            w[words - 1] = 0;   // the bytes after the last depth
-            std::memcpy(w + 3 * (size_t)n, c.depth, n_depth);
-        }
-    };
     // rows side by side in a CTA: 128 / (dim / 16) threads over a tile's tokens, the rest over heads
     const int32_t n_rows = 2 * a.n_kv + a.nq;
     int32_t lanes = 128 / (a.dim / 16), tp = 1;
@@ -738,7 +749,7 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s) {
     // 32 x 16 tokens of 48 heads 8 us, and 10 with 8 an SM)
     const unsigned z = head_splits(p, c.touched * c.n_layers_in, (n_rows + lanes / tp - 1) / (lanes / tp), c.rope ? 4 : 8);
     const dim3 grid((unsigned)std::min<int64_t>(c.touched, (int64_t)p->sm_count * 64), (unsigned)c.n_layers_in, z);
-    return with_words(p, words, s, fill, [&](auto args) -> int {
+    auto go = [&](auto args) -> int {
         using A = decltype(args);
         if (p->dtype == DENDRITE_FP8 && !c.rope)
             DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, false, A>, grid, dim3(128), 0, s, args, a));
@@ -749,7 +760,16 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s) {
         else
             DENDRITE_CUDA(launch_pdl(k_append_rows<float, false, true, A>, grid, dim3(128), 0, s, args, a));
         return DENDRITE_OK;
-    });
+    };
+    if (staged) return go(GlobalWords{staged});
+    if (rows_words(c) <= (size_t)kRowsSmall) {
+        ParamWords<kRowsSmall> w;
+        fill_rows_words(c, bs, w.v);
+        return go(w);
+    }
+    ParamWords<kRowsCap> w;
+    fill_rows_words(c, bs, w.v);
+    return go(w);
 }
 
 }  // namespace dendrite

@@ -35,7 +35,12 @@ struct RowsCall {
     int32_t n_trees;
 };
 
-int launch_append_rows(dendrite_pool* p, const RowsCall& c, cudaStream_t s);
+// The kernel's argument words: how many the caller has to stage (0: they go as
+// kernel parameters), the words themselves, and the launch (staged: their device
+// copy, or null where none are staged).
+size_t staged_rows_words(const RowsCall& c);
+void fill_rows_words(const RowsCall& c, int32_t block_size, int32_t* words);
+int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* staged, cudaStream_t s);
 
 // Checks n_trees (1 or n) trees of t drafted tokens (parents[j] in [-1, j)).
 int check_trees(const int32_t* parents, int32_t n_trees, int32_t n, int32_t t);
