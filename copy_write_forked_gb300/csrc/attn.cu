@@ -220,9 +220,32 @@ struct ConsumerCtx {
     volatile int* abortp;
     const int4* info;   // [NSTAGE][4]: each tile's logical block and row mask, written by the producer
     int warp, lane, c;
+    bool unclean;       // CUT: V may hold rows that are not finite
 };
 
-template <int P, bool PACKED, bool DRAFT>
+// Whether the tile holds tokens that none of the warp's rows sees, and then which
+// halves of its V fragments to keep: keep0 for the lane's tokens 2 (lane % 4) and
+// the next, keep1 for those 8 on.  A row of V that nothing sees may be what a
+// roll-back or the block's last owner left; were it not finite, it would spread
+// through its weight of zero, so it is multiplied as zero.  pos0: position of the
+// lane's first token; vl, see: the lane's rows' limits, and draft trees' bits.
+template <bool DRAFT>
+__device__ __forceinline__ bool unseen_tokens(int lane, int32_t pos0, int32_t vl0, int32_t vl1, uint32_t see0,
+                                              uint32_t see1, uint32_t& keep0, uint32_t& keep1) {
+    const int32_t top = max(vl0, vl1);
+    if (__any_sync(0xffffffffu, top >= pos0 - (lane & 3) * 2 + BS)) return false;   // some row sees all of it
+    uint32_t seen = see0 | see1;
+    if (!DRAFT)
+        seen = (pos0 < top ? 1u : 0u) | (pos0 + 1 < top ? 2u : 0u) | (pos0 + 8 < top ? 0x100u : 0u) |
+               (pos0 + 9 < top ? 0x200u : 0u);
+#pragma unroll
+    for (int x = 4; x <= 16; x <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, x);
+    keep0 = (seen & 1u ? 0xffffu : 0u) | (seen & 2u ? 0xffff0000u : 0u);
+    keep1 = (seen & 0x100u ? 0xffffu : 0u) | (seen & 0x200u ? 0xffff0000u : 0u);
+    return true;
+}
+
+template <int P, bool PACKED, bool DRAFT, bool CUT>
 __device__ __forceinline__ void consume_chunk(const ConsumerCtx& x, const AttnUnit& U, int32_t t, int32_t cend,
                                               int32_t& stage) {
     constexpr int NCOL = D / P, NT = NCOL / 8;   // columns and 8-column n-tiles of this warp
@@ -364,13 +387,28 @@ __device__ __forceinline__ void consume_chunk(const ConsumerCtx& x, const AttnUn
             {
                 const int mi = lane >> 3;
                 const int tok = (mi & 1) * 8 + (lane & 7);
+                uint32_t keep0, keep1;
+                auto add = [&](auto some_unseen) {
 #pragma unroll
-                for (int np = 0; np < NT / 2; ++np) {
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4_t(vt + swz(tok, col0 + np * 16 + (mi >> 1) * 8), b0, b1, b2, b3);
-                    mma16816(o[2 * np], pa, b0, b1);
-                    mma16816(o[2 * np + 1], pa, b2, b3);
-                }
+                    for (int np = 0; np < NT / 2; ++np) {
+                        uint32_t b0, b1, b2, b3;
+                        ldsm_x4_t(vt + swz(tok, col0 + np * 16 + (mi >> 1) * 8), b0, b1, b2, b3);
+                        if constexpr (decltype(some_unseen)::value) {
+                            b0 &= keep0;
+                            b1 &= keep1;
+                            b2 &= keep0;
+                            b3 &= keep1;
+                        }
+                        mma16816(o[2 * np], pa, b0, b1);
+                        mma16816(o[2 * np + 1], pa, b2, b3);
+                    }
+                };
+                // only a tile of its unit's end, or a packed unit's extra one, may end behind its branches
+                if (CUT && x.unclean && st + ti >= U.tile_off + U.n_shared - 1 &&
+                    unseen_tokens<DRAFT>(lane, pos0, vl0, vl1, see0, see1, keep0, keep1))
+                    add(std::true_type{});
+                else
+                    add(std::false_type{});
             }
         }
 
@@ -407,12 +445,14 @@ __device__ __forceinline__ void consume_chunk(const ConsumerCtx& x, const AttnUn
 // logical block and row mask into shared memory and the consumers mask by
 // them (plans without packed units run without that step or its memory).
 // DRAFT: the rows are nodes of draft trees (masked by their ancestors too).
-template <bool PACKED, bool DRAFT>
+// CUT: some branch was rolled back into a block, where V rows may stand behind its
+// end (AttnArgs::cut).
+template <bool PACKED, bool DRAFT, bool CUT>
 __global__ void __launch_bounds__(THREADS, 2)
 k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const AttnArgs a) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, unclean_flag;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* sm = smem_raw + (base - raw);
@@ -438,6 +478,7 @@ k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const int32_t u0 = pl.cta_unit[c];
     if (threadIdx.x == 0) {
         abort_flag = a.meta->status != 0;
+        if (CUT) unclean_flag = a.meta->unclean;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -559,7 +600,8 @@ k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
     int32_t stage = 0;
     int32_t t = t_begin, u = u0;
-    const ConsumerCtx ctx{&a, base, bar_full, bar_empty, abortp, info, warp, lane, c};
+    const bool unclean = CUT && unclean_flag;
+    const ConsumerCtx ctx{&a, base, bar_full, bar_empty, abortp, info, warp, lane, c, unclean};
     while (t < t_end) {
         const AttnUnit U = pl.units[u];
         const int32_t uend = U.tile_off + U.n_blk;
@@ -567,8 +609,8 @@ k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const int32_t cend = min(t_end, uend);
         if (U.rt != 1) {
             // 32 or 64 rows: the warps of a row tile split head_dim (no exchange)
-            if (U.rt == 2) consume_chunk<2, PACKED, DRAFT>(ctx, U, t, cend, stage);
-            else consume_chunk<1, PACKED, DRAFT>(ctx, U, t, cend, stage);
+            if (U.rt == 2) consume_chunk<2, PACKED, DRAFT, CUT>(ctx, U, t, cend, stage);
+            else consume_chunk<1, PACKED, DRAFT, CUT>(ctx, U, t, cend, stage);
             t = cend;
             ++u;
             continue;
@@ -708,13 +750,28 @@ k_attn_partial_bf16(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 {
                     const int mi = lane >> 3;
                     const int tok = (mi & 1) * 8 + (lane & 7);
+                    uint32_t keep0, keep1;
+                    auto add = [&](auto some_unseen) {
 #pragma unroll
-                    for (int np = 0; np < 8; ++np) {
-                        uint32_t b0, b1, b2, b3;
-                        ldsm_x4_t(vt + swz(tok, np * 16 + (mi >> 1) * 8), b0, b1, b2, b3);
-                        mma16816(o[2 * np], pa, b0, b1);
-                        mma16816(o[2 * np + 1], pa, b2, b3);
-                    }
+                        for (int np = 0; np < 8; ++np) {
+                            uint32_t b0, b1, b2, b3;
+                            ldsm_x4_t(vt + swz(tok, np * 16 + (mi >> 1) * 8), b0, b1, b2, b3);
+                            if constexpr (decltype(some_unseen)::value) {
+                                b0 &= keep0;
+                                b1 &= keep1;
+                                b2 &= keep0;
+                                b3 &= keep1;
+                            }
+                            mma16816(o[2 * np], pa, b0, b1);
+                            mma16816(o[2 * np + 1], pa, b2, b3);
+                        }
+                    };
+                    // only a tile of its unit's end, or a packed unit's extra one, may end behind its branches
+                    if (CUT && unclean && st + ti >= U.tile_off + U.n_shared - 1 &&
+                        unseen_tokens<DRAFT>(lane, pos0, vl0, vl1, see0, see1, keep0, keep1))
+                        add(std::true_type{});
+                    else
+                        add(std::false_type{});
                 }
             }
 
@@ -2109,6 +2166,19 @@ int tc_ctas(const dendrite_pool* p) {
     return (p->tc_ready && p->tc_min_rows >= 0) ? p->sm_count : 0;
 }
 
+// The mma.sync kernel of a bf16 call: without tile info and its memory where no
+// unit is packed, unless drafts or roll-backs make it rare.
+struct MmaKernel {
+    void (*fn)(CUtensorMap, CUtensorMap, AttnArgs);
+    size_t smem;
+};
+MmaKernel mma_kernel(const AttnArgs& a) {
+    if (a.plan.masks) return {a.cut ? k_attn_partial_bf16<true, true, true> : k_attn_partial_bf16<true, true, false>, SMEM_BF16_PACKED};
+    if (a.cut) return {k_attn_partial_bf16<true, false, true>, SMEM_BF16_PACKED};
+    if (a.plan.packed) return {k_attn_partial_bf16<true, false, false>, SMEM_BF16_PACKED};
+    return {k_attn_partial_bf16<false, false, false>, SMEM_BF16};
+}
+
 // The partial kernels of one attention call (tensor-core class, then the
 // mma.sync or fp32 class), then the merge.  The mma.sync, fp32 and merge
 // kernels are launched with programmatic stream serialisation: their
@@ -2146,14 +2216,12 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
     if (beside) {
         DENDRITE_CUDA(cudaStreamWaitEvent(p->side, p->ev_fork, 0));
         prof_begin(p, T_ATTN_MMA_SIDE, p->side);
-        if (f8)
+        if (f8) {
             DENDRITE_TRY(launch_attn_fp8(a, true, p->side));
-        else if (a.plan.masks)
-            k_attn_partial_bf16<true, true><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16_PACKED, p->side>>>(mk, mv, a);
-        else if (a.plan.packed)
-            k_attn_partial_bf16<true, false><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16_PACKED, p->side>>>(mk, mv, a);
-        else
-            k_attn_partial_bf16<false, false><<<dim3(a.plan.n_ctas), dim3(THREADS), SMEM_BF16, p->side>>>(mk, mv, a);
+        } else {
+            const MmaKernel k = mma_kernel(a);
+            k.fn<<<dim3(a.plan.n_ctas), dim3(THREADS), k.smem, p->side>>>(mk, mv, a);
+        }
         DENDRITE_CUDA(cudaGetLastError());
         prof_end(p, T_ATTN_MMA_SIDE, p->side);
         DENDRITE_CUDA(cudaEventRecord(p->ev_join, p->side));
@@ -2170,15 +2238,8 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
         DENDRITE_TRY(launch_attn_fp8(a, false, s));
     } else if (a.plan.n_ctas > 0) {
         if (bf16) {
-            if (a.plan.masks)
-                DENDRITE_CUDA(launch_pdl(k_attn_partial_bf16<true, true>, dim3(a.plan.n_ctas), dim3(THREADS),
-                                         SMEM_BF16_PACKED, s, mk, mv, a));
-            else if (a.plan.packed)
-                DENDRITE_CUDA(launch_pdl(k_attn_partial_bf16<true, false>, dim3(a.plan.n_ctas), dim3(THREADS),
-                                         SMEM_BF16_PACKED, s, mk, mv, a));
-            else
-                DENDRITE_CUDA(launch_pdl(k_attn_partial_bf16<false, false>, dim3(a.plan.n_ctas), dim3(THREADS),
-                                         SMEM_BF16, s, mk, mv, a));
+            const MmaKernel k = mma_kernel(a);
+            DENDRITE_CUDA(launch_pdl(k.fn, dim3(a.plan.n_ctas), dim3(THREADS), k.smem, s, mk, mv, a));
         } else {
             DENDRITE_CUDA(launch_pdl(k_attn_partial_f32, dim3(a.plan.n_ctas), dim3(128),
                                      2 * BS * p->head_dim * sizeof(float), s, a));
@@ -2242,6 +2303,12 @@ AttnArgs attn_args(const dendrite_pool* p, int32_t layer, const void* Q, void* o
     return a;
 }
 
+bool any_cut(const dendrite_pool* p, const int32_t* branches, int32_t n) {
+    for (int32_t i = 0; i < n; ++i)
+        if (p->br[branches[i]].cut) return true;
+    return false;
+}
+
 int ensure_capacity(dendrite_pool* p, size_t plan_bytes, size_t partial_rows) {
     if (plan_bytes > p->plan_cap) {
         size_t cap = std::max<size_t>(plan_bytes * 2, 1 << 20);
@@ -2292,20 +2359,20 @@ int attn_setup(dendrite_pool* p) {
             DENDRITE_TRY(encode_pool_map(p, static_cast<char*>(p->d_v) + off, p->tmap_v[l].bytes));
         }
         p->tmaps_ok = true;
-        DENDRITE_CUDA(cudaFuncSetAttribute(k_attn_partial_bf16<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)SMEM_BF16));
-        DENDRITE_CUDA(cudaFuncSetAttribute(k_attn_partial_bf16<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)SMEM_BF16_PACKED));
-        DENDRITE_CUDA(cudaFuncSetAttribute(k_attn_partial_bf16<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)SMEM_BF16_PACKED));
-        int occ = 0, occ_packed = 0, occ_draft = 0;
-        DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_bf16<false, false>, THREADS,
-                                                                    SMEM_BF16));
-        DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_packed, k_attn_partial_bf16<true, false>, THREADS,
-                                                                    SMEM_BF16_PACKED));
-        DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_draft, k_attn_partial_bf16<true, true>, THREADS,
-                                                                    SMEM_BF16_PACKED));
-        p->attn_ctas_per_sm = std::max(1, std::min({occ, occ_packed, occ_draft}));
+        int ctas = 0;
+        auto one = [&](auto* fn, size_t smem) -> int {
+            DENDRITE_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+            int occ = 0;
+            DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, THREADS, smem));
+            ctas = ctas ? std::min(ctas, occ) : occ;
+            return DENDRITE_OK;
+        };
+        DENDRITE_TRY(one(k_attn_partial_bf16<false, false, false>, SMEM_BF16));
+        DENDRITE_TRY(one(k_attn_partial_bf16<true, false, false>, SMEM_BF16_PACKED));
+        DENDRITE_TRY(one(k_attn_partial_bf16<true, false, true>, SMEM_BF16_PACKED));
+        DENDRITE_TRY(one(k_attn_partial_bf16<true, true, false>, SMEM_BF16_PACKED));
+        DENDRITE_TRY(one(k_attn_partial_bf16<true, true, true>, SMEM_BF16_PACKED));
+        p->attn_ctas_per_sm = std::max(1, ctas);
         p->tc_ready = attn_tc_setup(false) == DENDRITE_OK;
         DENDRITE_CUDA(cudaFuncSetAttribute(k_plan_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kMaxExpandSegs * 16));
@@ -2591,6 +2658,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
     }
     AttnArgs a = attn_args(p, layer, Q, out);
     a.plan = pc.dev;
+    a.cut = any_cut(p, branches, n);
     a.part_acc = p->d_partial;
     a.part_ml = reinterpret_cast<float2*>(p->d_partial + p->partial_rows_cap * p->head_dim);
     if (!began) prof_begin(p, T_ATTN_TOTAL, s);
@@ -2709,6 +2777,7 @@ extern "C" int dendrite_tree_attn_decode_noalloc(dendrite_pool* p, const void* Q
     }
     AttnArgs a = attn_args(p, 0, Q, out);
     a.plan = plan_view(hp, off, reinterpret_cast<const char*>(scratch), n, q_len, n_q_heads, n_q_heads / p->n_kv);
+    a.cut = any_cut(p, branches, n);
     a.part_acc = reinterpret_cast<float*>(scratch + plan_bytes);
     a.part_ml = reinterpret_cast<float2*>(scratch + plan_bytes + acc_bytes);
     return launch_attention(p, 0, a, s);

@@ -78,6 +78,10 @@ struct AttnArgs {
     int32_t n_blocks;
     float scale_log2;      // log2(e) / sqrt(head_dim)
     const float* tq_signs; // compressed pools: rotation signs [128] (the merge rotates rows back); else null
+    // A queried branch was rolled back into a block and not appended to since (see
+    // Branch::cut): rows may stand behind its end.  Elsewhere appends keep the V rows
+    // behind a branch's end finite (bf16 pools).
+    bool cut;
 };
 
 // Tensor-core (tcgen05) partial kernel for units of many query rows; see

@@ -128,8 +128,10 @@ struct TcLayout {
     static constexpr int B_COUNT = B_ML_DONE + (F8 ? 1 : 0);
     // a packed unit's extra tiles (logical block, member mask), per row tile
     static constexpr int OFF_XINFO = OFF_BAR + B_COUNT * 8 + 16;
+    // and how many of their tokens a branch of the mask holds
+    static constexpr int OFF_XHELD = OFF_XINFO + TC_ROWTILES * kMaxTcExtraTiles * 8;
     // F8: (m, l) of the rows of a split unit, per group
-    static constexpr int OFF_ML = OFF_XINFO + TC_ROWTILES * kMaxTcExtraTiles * 8;
+    static constexpr int OFF_ML = OFF_XHELD + TC_ROWTILES * kMaxTcExtraTiles;
     static constexpr int SMEM = 1024 + OFF_ML + (F8 ? TC_ROWTILES * 128 * 8 : 0);
 };
 static_assert(TcLayout<false>::SMEM <= 227 * 1024 - 64 && TcLayout<true>::SMEM <= 227 * 1024 - 64,
@@ -372,14 +374,49 @@ struct StageWalk {
     __device__ __forceinline__ void step() { t = min(t + 4, cend); }
 };
 
-// Tokens of the unit's last tile that one of its branches holds.
-__device__ __noinline__ int32_t held_tokens(const AttnPlanDev& pl, const AttnUnit& U) {
+// Tokens of the last of the unit's n_tiles own tiles that one of its branches holds.
+__device__ __noinline__ int32_t held_tokens(const AttnPlanDev& pl, const AttnUnit& U, int32_t n_tiles) {
     const int32_t rm = pl.q_len * pl.group;
     int32_t len = 0;
     for (int32_t i = U.row_lo / rm + (threadIdx.x & 31); i <= (U.row_lo + U.n_rows - 1) / rm; i += 32)
         len = max(len, pl.members[U.mem_off + i].len);
     len = __reduce_max_sync(0xffffffffu, len);
-    return min(kBlockSize, len - (U.blk_start + U.n_blk - 1) * kBlockSize);
+    return min(kBlockSize, len - (U.blk_start + n_tiles - 1) * kBlockSize);
+}
+// Makes the rows of V behind the first `held` of a tile's 16 zero (tile: its 64-
+// column half 0 in the V ring; a warp's work): left there by a roll-back or the
+// block's last owner they may be NaN, and would spread through their weight of zero.
+__device__ __forceinline__ void clear_unheld(unsigned char* tile, int32_t held) {
+    for (int i = held * 16 + (threadIdx.x & 31); i < kBlockSize * 16; i += 32)
+        *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * TC_HALF + (i >> 4) * 128 + (i & 7) * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+}
+
+// bf16 pools, a softmax warp: of a stage's tiles those that may end behind their
+// branches (the last of the unit's own range, extra ones), once V has landed.  All
+// warps of a unit make the same zeros, each before it passes on the P that is
+// multiplied with them.  first: the stage's first tile in the unit; limit: of the
+// lane's row; g: stage of the CTA; xheld: held tokens of the extra tiles.
+__device__ __noinline__ bool clear_tails(const AttnArgs& a, unsigned char* sm, uint32_t bars, volatile int* abortp,
+                                         const AttnUnit& U, int32_t first, int ntiles, int32_t limit, int32_t g,
+                                         const unsigned char* xheld) {
+    using Y = TcLayout<false>;
+    const int slot = g % Y::NV;
+    bool landed = false;
+    for (int j = max(0, U.n_shared - 1 - first); j < ntiles; ++j) {
+        const int32_t x = first + j - U.n_shared;   // of the extra tiles
+        // a row that sees the tile to its end spares the look at the branches
+        if (x < 0 && __any_sync(0xffffffffu, limit >= (U.blk_start + U.n_shared) * kBlockSize)) continue;
+        const int32_t held =
+            x < 0 ? held_tokens(a.plan, U, U.n_shared) : (int32_t)xheld[min(x, kMaxTcExtraTiles - 1)];
+        if (held >= kBlockSize) continue;
+        if (!landed && !warp_wait(bars + 8 * (Y::B_V_FULL + slot), (uint32_t)(g / Y::NV) & 1u, abortp, a.meta))
+            return false;
+        landed = true;
+        clear_unheld(sm + Y::OFF_V + slot * TC_RING_STAGE + j * 16 * 128, held);
+    }
+    if (landed) fence_async_smem();
+    return true;
 }
 
 // Copies the stages' tiles as they are stored, F8_RAW stages ahead; lane i < 4
@@ -467,14 +504,9 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, unsigned char* 
             }
         }
         if (kv && w < now.tiles() && now.t + w == now.unit_end - 1) {
-            // What V holds behind the longest branch's end (left by a roll-back,
-            // or by the block's last owner) may be NaN and would spread through
-            // its weight of zero: those rows become zero.
             __syncwarp();
-            unsigned char* tile = sm + Y::OFF_V + stage * TC_RING_STAGE + w * 16 * 128;
-            for (int i = held_tokens(pl, pl.units[now.u]) * 16 + lane; i < kBlockSize * 16; i += 32)
-                *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * TC_HALF + (i >> 4) * 128 + (i & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+            const AttnUnit& U = pl.units[now.u];
+            clear_unheld(sm + Y::OFF_V + stage * TC_RING_STAGE + w * 16 * 128, held_tokens(pl, U, U.n_blk));
         }
         fence_async_smem();   // the stores, before the products read them
         __syncwarp();
@@ -617,7 +649,9 @@ __device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint3
 
 // DRAFT: the rows are nodes of draft trees (masked by their ancestors too).
 // F8: an 8-bit pool's blocks (tmK and tmV unused).
-template <bool DRAFT, bool F8>
+// CUT: bf16, some branch was rolled back into a block, where V rows may stand behind
+// its end (8-bit pools' V is cleared there as it is converted, in every call).
+template <bool DRAFT, bool F8, bool CUT>
 __global__ void __launch_bounds__(TcLayout<F8>::THREADS, 1)
 k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const AttnArgs a) {
@@ -628,7 +662,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                   B_Q_FULL = Y::B_Q_FULL, B_FINAL = Y::B_FINAL, B_COUNT = Y::B_COUNT, TC_PV1_WARP = Y::PV1_WARP,
                   TC_S0_WARP = Y::S0_WARP;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, unclean_flag;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* sm = smem_raw + (base - raw);
@@ -660,6 +694,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     if (a.plan.counts && (int32_t)blockIdx.x >= a.plan.counts[1]) return;   // past the device-expanded split
     if (threadIdx.x == 0) {
         abort_flag = a.meta->status != 0;
+        if (CUT) unclean_flag = a.meta->unclean;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -874,6 +909,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // row of the unit (F8: both groups hold the rows of a split unit)
         auto row_of = [&](const AttnUnit& V) { return F8 && V.rt == 1 ? trow : r * 128 + trow; };
         int2* xinfo = reinterpret_cast<int2*>(sm + OFF_XINFO) + r * kMaxTcExtraTiles;
+        unsigned char* xheld = sm + Y::OFF_XHELD + r * kMaxTcExtraTiles;
         // draft trees: the row's mask, in shared memory: in registers, or made
         // again from the unit where it is needed, it cost spills in the loop
         // (a third of its time)
@@ -904,6 +940,8 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         int32_t staged_u = -1;      // unit whose Q is already in the tile
         AttnRow staged_R{0, 0};
         uint32_t joined = 0;        // phase of the joins of split units
+        int32_t g = 0;              // CUT: stages before this chunk
+        const bool unclean = CUT && unclean_flag;   // V may hold rows that are not finite
         while (ok && t < t_end) {
             const AttnUnit U = pl.units[u];
             const int32_t uend = U.tile_off + U.n_blk;
@@ -912,6 +950,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             const int32_t nst = (cend - t + 3) >> 2;
             const RowTiles tiles(U, nst);
             if (r >= (F8 ? tiles.n : U.rt)) {
+                g += nst;
                 t = cend;
                 ++u;
                 continue;
@@ -920,15 +959,23 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             const bool valid = row < U.n_rows;
             const AttnRow R = staged_u == u ? staged_R : stage_q(U);
             if (!F8 && U.n_blk > U.n_shared) {
-                // a packed unit: its extra tiles' logical blocks and member
-                // masks into shared memory, once every warp of the row tile
+                // a packed unit: its extra tiles' logical blocks, member masks
+                // and held tokens into shared memory, once every warp of the row tile
                 // is done with the previous unit's (the plan keeps them to
                 // kMaxTcExtraTiles; a unit past that reads none and is flagged)
                 const int32_t nx = U.n_blk - U.n_shared;
                 if (nx > kMaxTcExtraTiles && trow == 0) atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + r) : "memory");
-                for (int32_t i = trow; i < min(nx, kMaxTcExtraTiles); i += 128)
-                    xinfo[i] = *reinterpret_cast<const int2*>(pl.xtiles + U.x_off + i);
+                for (int32_t i = trow; i < min(nx, kMaxTcExtraTiles); i += 128) {
+                    const int2 e = *reinterpret_cast<const int2*>(pl.xtiles + U.x_off + i);
+                    xinfo[i] = e;
+                    if constexpr (CUT) {
+                        int32_t len = 0;
+                        for (uint32_t mm = (uint32_t)e.y; mm; mm &= mm - 1u)
+                            len = max(len, pl.members[U.mem_off + __ffs(mm) - 1].len);
+                        xheld[i] = (unsigned char)min(BS, len - e.x * BS);
+                    }
+                }
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + r) : "memory");
             }
             const int32_t k0 = F8 && tiles.split ? r : 0, k_step = F8 && tiles.split ? 2 : 1;
@@ -1128,6 +1175,10 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 // P over the S it came from (token 2 i in the low half of
                 // column i); unused columns past the chunk hold P = 0
                 tmem_st32(tl + 128 + b * 64, pk);
+                if (CUT && unclean && ti0 + ntiles >= U.n_shared) {
+                    ok = clear_tails(a, sm, bars, abortp, pl.units[u], ti0, ntiles, R.limit, g + k, xheld);
+                    if (!ok) break;
+                }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1151,6 +1202,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     staged_u = u2;
                 }
             }
+            g += nst;
             // chunk done: O after the last PV -> partial row
             ok = warp_wait_<F8>(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u, abortp, a.meta);
             if (!ok) break;
@@ -1233,35 +1285,41 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
 namespace dendrite {
 
-template <bool DRAFT, bool F8>
+template <bool DRAFT, bool F8, bool CUT>
 static int setup_one() {
-    if (cudaFuncSetAttribute(k_attn_partial_tc<DRAFT, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             TcLayout<F8>::SMEM) != cudaSuccess)
+    constexpr auto fn = k_attn_partial_tc<DRAFT, F8, CUT>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLayout<F8>::SMEM) != cudaSuccess)
         return DENDRITE_ECUDA;
     int occ = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_tc<DRAFT, F8>, TcLayout<F8>::THREADS,
-                                                      TcLayout<F8>::SMEM) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, TcLayout<F8>::THREADS, TcLayout<F8>::SMEM) !=
+            cudaSuccess ||
         occ != 1)
         return DENDRITE_ECUDA;   // the kernel's 512 TMEM columns need exactly one CTA per SM
     return DENDRITE_OK;
 }
 
 int attn_tc_setup(bool f8) {
-    DENDRITE_TRY((f8 ? setup_one<false, true>() : setup_one<false, false>()));
-    return f8 ? setup_one<true, true>() : setup_one<true, false>();
+    if (f8) {
+        DENDRITE_TRY((setup_one<false, true, false>()));
+        return setup_one<true, true, false>();
+    }
+    DENDRITE_TRY((setup_one<false, false, false>()));
+    DENDRITE_TRY((setup_one<true, false, false>()));
+    DENDRITE_TRY((setup_one<false, false, true>()));
+    return setup_one<true, false, true>();
 }
 
-template <bool F8>
+template <bool F8, bool CUT>
 static void launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, cudaStream_t s) {
-    if (a.plan.masks)
-        k_attn_partial_tc<true, F8><<<n_ctas, TcLayout<F8>::THREADS, TcLayout<F8>::SMEM, s>>>(mk, mv, a);
-    else
-        k_attn_partial_tc<false, F8><<<n_ctas, TcLayout<F8>::THREADS, TcLayout<F8>::SMEM, s>>>(mk, mv, a);
+    using Y = TcLayout<F8>;
+    if (a.plan.masks) k_attn_partial_tc<true, F8, CUT><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
+    else k_attn_partial_tc<false, F8, CUT><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
 }
 
 int launch_attn_tc(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, bool f8, cudaStream_t s) {
-    if (f8) launch_one<true>(mk, mv, a, n_ctas, s);
-    else launch_one<false>(mk, mv, a, n_ctas, s);
+    if (f8) launch_one<true, false>(mk, mv, a, n_ctas, s);
+    else if (a.cut) launch_one<false, true>(mk, mv, a, n_ctas, s);
+    else launch_one<false, false>(mk, mv, a, n_ctas, s);
     return cudaGetLastError() == cudaSuccess ? DENDRITE_OK : DENDRITE_ECUDA;
 }
 

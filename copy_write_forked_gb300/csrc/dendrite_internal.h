@@ -42,7 +42,11 @@ struct DevMeta {
     int32_t rel_hi;     // largest block id released by the current free call
     int32_t rel_count;  // blocks released by the current free call
     int32_t rel_done;   // CTAs of the current free call that finished releasing
-    int32_t pad[2];
+    // bf16 pools: a V row that is not finite was appended since the pool was made.
+    // From then on appends clear V behind their branches' ends, and attention over a
+    // branch that was rolled back masks it (a weight of zero times NaN is NaN).
+    int32_t unclean;
+    int32_t pad;
 };
 
 // One sharing segment: blocks [blk_start, blk_start + n_blk) of the table row

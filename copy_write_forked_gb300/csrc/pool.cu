@@ -83,6 +83,7 @@ __global__ void k_init(int32_t* stack, int32_t* refcount, int32_t* holders, int3
         meta->rel_hi = -1;
         meta->rel_count = 0;
         meta->rel_done = 0;
+        meta->unclean = 0;
     }
 }
 
@@ -427,12 +428,23 @@ k_copy_tails(const __grid_constant__ A args, const TailLayout a, const int32_t* 
 // touched blocks per branch (host computed; depends only on lengths).
 // blockIdx.y selects the layer: the input rows of layer y start y * in_layer
 // 16-byte words after Kin / Vin, its pool y * pool_layer words after Kp / Vp.
+// Eight bf16 numbers' largest magnitude, as bits; what is not finite is above all.
+__device__ __forceinline__ uint32_t max_bf16(const uint4& x) {
+    auto max2 = [](uint32_t a, uint32_t b) {
+        uint32_t y;
+        asm("max.u16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    };
+    const uint32_t m = max2(max2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), max2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    return max(m & 0xffffu, m >> 16);
+}
+
 template <typename A>
 __global__ void __launch_bounds__(128, 16) k_append_copy(const __grid_constant__ A args, int32_t n, int32_t n_new, int32_t bs, int32_t bpb, int32_t n_kv,
                               int32_t row_vec, int32_t n_blocks, const int32_t* __restrict__ table,
                               const int32_t* __restrict__ call, const uint4* __restrict__ Kin0,
                               const uint4* __restrict__ Vin0, uint4* __restrict__ Kp0, uint4* __restrict__ Vp0,
-                              int64_t in_layer, int64_t pool_layer, const DevMeta* meta, int64_t n_tiles,
+                              int64_t in_layer, int64_t pool_layer, DevMeta* meta, int64_t n_tiles,
                               int32_t uniform) {
     pdl_wait();
     // one tile per CTA up to 64 CTAs per SM (the scheduler starts the next
@@ -492,12 +504,13 @@ __global__ void __launch_bounds__(128, 16) k_append_copy(const __grid_constant__
         }
     };
     const int32_t status = meta->status;
+    const bool unclean = meta->unclean;
     const int32_t dst = table[(int64_t)args[i] * bpb + lblk];
     const int32_t csrc = lblk == L / bs ? cow_src[i] : -1;
     gather(threadIdx.x);
     if (status) return;
     if ((uint32_t)dst >= (uint32_t)n_blocks || csrc >= n_blocks) {
-        if (threadIdx.x == 0) atomicCAS(const_cast<int32_t*>(&meta->status), 0, DENDRITE_ECORRUPT);
+        if (threadIdx.x == 0) atomicCAS(&meta->status, 0, DENDRITE_ECORRUPT);
         return;
     }
     uint4* kd = Kp + ((int64_t)dst * n_kv + h) * tile_vec;
@@ -522,8 +535,12 @@ __global__ void __launch_bounds__(128, 16) k_append_copy(const __grid_constant__
             if (idx[u] < 0) continue;
             kd[idx[u]] = kv[u];
             vd[idx[u]] = vv[u];
+            if (max_bf16(vv[u]) >= 0x7f80u) meta->unclean = 1;   // (fp32 rows may set it too: nothing reads it there)
         }
     }
+    // the block is this branch's alone now: V behind its new end becomes finite
+    if (unclean)
+        for (int32_t e = total + threadIdx.x; e < tile_vec; e += blockDim.x) vd[e] = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -1118,7 +1135,7 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
             DENDRITE_CUDA(launch_pdl(k_append_copy<decltype(args)>, dim3(grid, (unsigned)n_layers_in), dim3(128), 0,
                                      s, args, n, n_new, bs, p->bpb, p->n_kv, row_vec, (int32_t)p->num_blocks,
                                      (const int32_t*)p->d_table, (const int32_t*)p->d_call_i32, (const uint4*)K,
-                                     (const uint4*)V, kp, vp, in_layer, pool_layer, (const DevMeta*)p->d_meta, n_tiles,
+                                     (const uint4*)V, kp, vp, in_layer, pool_layer, p->d_meta, n_tiles,
                                      uniform));
             prof_end(p, T_APPEND_COPY, s);
         }
@@ -1284,7 +1301,7 @@ int pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads, int3
     // Slots past a branch's length are read by the attention tiles and given
     // weight zero; they must hold finite values (0 x NaN is NaN; a zero record
     // decodes to a zero row).  Zero them once here; afterwards they only ever
-    // hold appended rows.
+    // hold appended rows (for those that are not finite see DevMeta::unclean).
     if (cudaMemset(p->d_k, 0, k_bytes) != cudaSuccess || cudaMemset(p->d_v, 0, v_bytes) != cudaSuccess)
         return fail(cuda_err(cudaErrorUnknown));
     if (dtype == DENDRITE_TURBO) {

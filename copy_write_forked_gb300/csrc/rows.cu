@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
     }
     const bool turn0 = ROPE && c0 < a.rot, turn1 = ROPE && c1 < a.rot;
     const int32_t n_rows = 2 * a.n_kv + a.nq;           // rows per token: K heads, V heads, Q heads
-    const int32_t status = a.meta->status;
+    const int32_t status = a.meta->status, unclean = a.meta->unclean;
     const T* K = static_cast<const T*>(a.K) + blockIdx.y * a.kv_layer;
     const T* V = static_cast<const T*>(a.V) + blockIdx.y * a.kv_layer;
     const T* Q = static_cast<const T*>(a.Q) + blockIdx.y * a.q_layer;
@@ -416,10 +416,18 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                         T* out = reinterpret_cast<T*>(tile) + slot * dim;
                         store(out + c0, x[u]);
                         store(out + c1, y[u]);
+                        if constexpr (sizeof(T) == 2)   // (fp32 attention reads no row that nothing sees)
+                            if (kind == 1 && max(top_bits(x[u]), top_bits(y[u])) >= 0x7f800000u) a.meta->unclean = 1;
                     }
                 }
             }
         }
+        // bf16: V behind the branch's new end becomes finite
+        if (!FP8 && sizeof(T) == 2 && unclean)
+            for (int32_t h = blockIdx.z; h < a.n_kv; h += gridDim.z) {
+                uint4* to = reinterpret_cast<uint4*>(vp + ((int64_t)dst * a.n_kv + h) * tile_bytes);
+                for (int32_t w = s1 * (dim / 8) + threadIdx.x; w < bs * (dim / 8); w += 128) to[w] = make_uint4(0u, 0u, 0u, 0u);
+            }
         // the valid slots of a copied-on-write tail, stored rows as they are
         if (csrc >= 0 && s0 > 0) {
             const int32_t words = FP8 ? kFp8Dim / 16 : dim * (int)sizeof(T) / 16;

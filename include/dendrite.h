@@ -367,10 +367,9 @@ int dendrite_tree_attn_decode_layer(dendrite_pool* pool, int32_t layer, const vo
  *   Q, out: device, [n_branches][n_draft][n_q_heads][head_dim].
  * Otherwise as dendrite_tree_attn_decode_layer with q_len = n_draft; the trees
  * are part of the cached plan.  A parents array of a chain (parents[j] = j - 1)
- * gives that call's result.  As there, K and V rows have to be finite in every
- * position a branch holds: a row a query does not see is weighed with zero (in
- * bf16 pools also a row behind a branch's end that a roll-back or a freed
- * branch left in the block).
+ * gives that call's result.  As there, V rows have to be finite in every position
+ * a branch holds (a row a query does not see is weighed with zero); what stands in
+ * a block behind a branch's end touches nothing.
  * DENDRITE_TURBO pools return DENDRITE_EDTYPE.
  */
 int dendrite_tree_attn_draft(dendrite_pool* pool, int32_t layer, const void* Q, int32_t n_q_heads, int32_t n_draft,
