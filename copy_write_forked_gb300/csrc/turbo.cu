@@ -460,7 +460,9 @@ __device__ __forceinline__ void tq_decode16(const uint32_t* rec, int j, const fl
 // One warp's rows against one tile: 16 query rows (fp16 at qrows, row stride
 // 512 bytes, chunks XOR-ed with row & 7) against the tile's 16 tokens (key and
 // value records at rk / rv, decoded unit rows at kt / vt).  pos0: position of
-// the lane's first column; a0/a1, b0/b1: the rows' score scales.
+// the lane's first column; a0/a1, b0/b1: the rows' score scales.  last: the
+// unit's last tile, where values that no row sees count as zero: what a roll-back
+// or the block's last owner left there may be NaN, or of another size altogether.
 struct TqRows {
     float o[16][4];
     float m0, m1, l0, l1, vs;
@@ -469,7 +471,7 @@ struct TqRows {
 __device__ __forceinline__ void tq_tile(TqRows& st, uint32_t qrows, const unsigned char* rk,
                                         const unsigned char* rv, uint32_t kt, uint32_t vt, int32_t pos0,
                                         int32_t lim0, int32_t lim1, float a0, float a1, float b0, float b1,
-                                        int lane) {
+                                        int lane, bool last) {
     const float NEG_INF = -INFINITY;
     // per-token scalars of this lane's columns: tokens 2 (lane % 4) + e + 8 nt
     float kn[2][2], en[2][2], vn[2][2];
@@ -482,6 +484,14 @@ __device__ __forceinline__ void tq_tile(TqRows& st, uint32_t qrows, const unsign
             kn[nt][e] = __uint_as_float(kr[0]);
             en[nt][e] = __uint_as_float(kr[20]);
             vn[nt][e] = __uint_as_float(reinterpret_cast<const uint32_t*>(rv + tok * TQ_REC_ROW)[0]);
+        }
+    }
+    if (last) {
+        const int32_t end = __reduce_max_sync(FULL, max(lim0, lim1));
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) vn[nt][e] = pos0 + 8 * nt + e < end ? vn[nt][e] : 0.f;
         }
     }
     // the QJL bits of tokens lane / 4 and 8 + lane / 4
@@ -725,7 +735,7 @@ __global__ void __launch_bounds__(128, 3) k_attn_partial_turbo(const AttnArgs a,
                 for (int pss = 0; pss < 8; ++pss) tq_decode_pass(pss, rk, rv, dk, dv, tab, lane);
                 __syncwarp();
                 tq_tile(st, sbase + TQ_Q_OFF, rk, rv, wbase + 2 * TQ_STAGE, wbase + 2 * TQ_STAGE + TQ_DEC_TILE,
-                        (lpos + tt) * BS + 2 * (lane & 3), lim0, lim1, a0, a1, b0, b1, lane);
+                        (lpos + tt) * BS + 2 * (lane & 3), lim0, lim1, a0, a1, b0, b1, lane, tt == uend - 1);
                 __syncwarp();   // records and decoded tiles are reused by the next tile
             }
             cp_async_wait0();
@@ -814,7 +824,7 @@ __global__ void __launch_bounds__(128, 3) k_attn_partial_turbo(const AttnArgs a,
                 if (has_rows)
                     tq_tile(st, sbase + TQB_Q_OFF + rbase * 512, rk, rv, sbase + TQB_DEC_OFF,
                             sbase + TQB_DEC_OFF + TQ_DEC_TILE, (lpos + tt) * BS + 2 * (lane & 3), lim0, lim1, a0,
-                            a1, b0, b1, lane);
+                            a1, b0, b1, lane, tt == uend - 1);
                 __syncthreads();   // records and decoded tile are reused by the next tile
             }
             cp_async_wait0();

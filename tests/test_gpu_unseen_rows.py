@@ -9,10 +9,21 @@ import torch
 
 import _rows as R
 from copy_write_forked_gb300.dendrite import Pool, Rope
+from copy_write_forked_gb300.workloads import turbo_codec
 
 pytestmark = pytest.mark.gpu
 KINDS = ["bf16", "fp8", "fp32"]
 KV, D = 2, 128
+
+
+def new_pool(kind, blocks, **kw):
+    if kind == "turbo":
+        return Pool(blocks, 16, KV, D, torch.bfloat16, turbo=turbo_codec(), **kw)
+    return Pool(blocks, 16, KV, D, R.POOL_DTYPE[kind], **kw)
+
+
+def row_dtype(kind):
+    return torch.bfloat16 if kind == "turbo" else R.ROW_DTYPE[kind]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -26,9 +37,10 @@ class Pools:
     """The same calls on a pool of untouched blocks and on one whose every block holds `fill`."""
 
     def __init__(self, kind, blocks, fill, **kw):
-        self.dtype = R.ROW_DTYPE[kind]
+        self.dtype = row_dtype(kind)
+        self.turbo = kind == "turbo"
         self.fill = fill
-        self.pools = [Pool(blocks, 16, KV, D, R.POOL_DTYPE[kind], max_branches=64, **kw) for _ in range(2)]
+        self.pools = [new_pool(kind, blocks, max_branches=64, **kw) for _ in range(2)]
         self.g = torch.Generator(device="cuda").manual_seed(3)
         p = self.pools[1]
         b = p.new_branch()
@@ -58,7 +70,10 @@ class Pools:
         """n rows appended and rolled back: in the used pool they are junk."""
         for p, x in zip(self.pools, (torch.zeros_like(self.junk(n, len(br))), self.junk(n, len(br)))):
             p.append_kv(br, x, x)
-            p.accept_draft(br, n, [[] for _ in br])
+            if self.turbo:
+                p.truncate(br, [p.branch_len(b) - n for b in br])
+            else:
+                p.accept_draft(br, n, [[] for _ in br])
 
     def same(self, name, *args, **kw):
         a, b = (getattr(p, name)(*args, **kw) for p in self.pools)
@@ -77,7 +92,7 @@ class Pools:
 @pytest.mark.parametrize("fill", [float("nan"), float("inf")])
 @pytest.mark.parametrize("rows", [-1, 1])
 @pytest.mark.parametrize("group,q_len", [(1, 1), (4, 5), (8, 3), (16, 4), (8, 30), (16, 17)])
-@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kind", KINDS + ["turbo"])
 def test_last_owners_and_roll_backs(kind, group, q_len, rows, fill):
     """Row groups of 1 to 272 rows: every row tile of both kernels; ends at each place in a stage of four tiles."""
     p = Pools(kind, 40, fill, tc_min_rows=rows)
@@ -97,7 +112,7 @@ def test_last_owners_and_roll_backs(kind, group, q_len, rows, fill):
 @pytest.mark.parametrize("opts", [dict(), dict(pack_segments=1_000_000, tc_min_rows=8), dict(pack_segments=1_000_000, tc_min_rows=-1),
                                   dict(pack_segments=-1), dict(fold_segments=1_000_000), dict(device_planning=1)])
 @pytest.mark.parametrize("width,q_len", [(3, 1), (7, 2), (5, 9)])
-@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "turbo"])
 def test_forks_of_one_prefix(kind, width, q_len, opts):
     """Leaves of 1 to 40 tokens behind a prefix: extra tiles of a packed segment end in them."""
     p = Pools(kind, 60 + 8 * width, float("nan"), **opts)
@@ -148,11 +163,11 @@ def test_the_allocation_free_call(kind):
     p.close()
 
 
-@pytest.mark.parametrize("how", ["kv", "rope", "layers", "layers_rope"])
-@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kind,how", [(k, h) for k in KINDS + ["turbo"] for h in ("kv", "rope", "layers", "layers_rope")
+                                      if k != "turbo" or "rope" not in h])   # compressed pools do not rotate
 def test_every_way_of_appending(kind, how):
     """Junk brought in by, and written over by, each kind of append, in every layer."""
-    layers, dt, rope = 2, R.ROW_DTYPE[kind], Rope(D)
+    layers, dt, rope = 2, row_dtype(kind), Rope(D)
     g = torch.Generator(device="cuda").manual_seed(5)
     rows = lambda *s: torch.randn(*s, D, generator=g, device="cuda").to(dt)  # noqa: E731
 
@@ -173,7 +188,7 @@ def test_every_way_of_appending(kind, how):
     q = rows(1, 2, KV * 4)
     outs = []
     for junk in (False, True):
-        p = Pool(8, 16, KV, D, R.POOL_DTYPE[kind], max_branches=8, n_layers=layers)
+        p = new_pool(kind, 8, max_branches=8, n_layers=layers)
         if junk:
             b = p.new_branch()
             k = rows(layers, 1, 128, KV) * 0
@@ -199,3 +214,14 @@ def test_every_way_of_appending(kind, how):
         outs.append(torch.stack(out))
         p.close()
     assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
+
+
+def test_large_values_behind_a_branch_of_a_compressed_pool():
+    """Its weights are kept in units of the largest value's size: one that nothing sees has no say in them."""
+    p = Pools("turbo", 8, 1e30)
+    b = p.new()
+    p.append([b], 37)
+    p.attend([b], 4, 1)
+    p.leave([b], 4)
+    p.attend([b], 4, 3)
+    p.close()
