@@ -11,7 +11,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
-from typing import List, Optional, Sequence
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 
@@ -335,6 +335,28 @@ class Pool:
         if t.get_device() != self._dev:
             raise DendriteError(-1, f"{name} is on another device than the pool")
 
+    def _other(self, stream, *tensors: torch.Tensor) -> Optional[torch.cuda.Stream]:
+        """``stream`` where it is another than the current one (else None).  The tensors' memory
+        is then kept until that stream's work is done, however early they are freed."""
+        if stream is None or stream.cuda_stream == torch.cuda.current_stream(self._dev).cuda_stream:
+            return None
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=self.device)
+        for t in tensors:
+            t.record_stream(stream)
+        return stream
+
+    def _output(self, shape, stream) -> torch.Tensor:
+        """A new output of a call on ``stream``: that stream's memory (work queued on the current
+        one may still use what is free there), kept for the current one too."""
+        other = self._other(stream)
+        if other is None:
+            return torch.empty(shape, dtype=self.dtype, device=self.device)
+        with torch.cuda.stream(other):
+            out = torch.empty(shape, dtype=self.dtype, device=self.device)
+        out.record_stream(torch.cuda.current_stream(self._dev))
+        return out
+
     def append_kv(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, stream=None) -> None:
         """K, V: ``[n_branches][n_new][n_kv_heads][head_dim]``; for a pool of
         several layers ``[n_layers][n_branches][n_new][n_kv_heads][head_dim]``."""
@@ -347,6 +369,7 @@ class Pool:
         k4 = K.shape[-4:]
         if k4[0] != nb or k4[2] != self.n_kv_heads or k4[3] != self.head_dim:
             raise DendriteError(-1, f"K/V shape {tuple(K.shape)}")
+        self._other(stream, K, V)
         ba = _arr(branches)
         _check(lib().dendrite_append_kv(self._h, _ptr(ba), nb, k4[1], K.data_ptr(), V.data_ptr(),
                                         _stream_ptr(stream, self._dev)), "append_kv")
@@ -363,10 +386,11 @@ class Pool:
         self._check_tensor(V, "V")
         if K.shape != V.shape or K.dim() != 4 or K.shape[2] != self.n_kv_heads or K.shape[3] != self.head_dim:
             raise DendriteError(-1, f"K/V shape {tuple(K.shape)}")
+        self._other(stream, K, V)
         _check(lib().dendrite_append_layer(self._h, int(layer), K.data_ptr(), V.data_ptr(),
                                            _stream_ptr(stream, self._dev)), "append_layer")
 
-    def _rotated(self, K, V, rope, Q, out, lead, n, n_new):
+    def _rotated(self, K, V, rope, Q, out, lead, n, n_new, stream):
         """Shapes of a rotating append; returns (Q address, query heads, output)."""
         self._check_tensor(K, "K")
         self._check_tensor(V, "V")
@@ -375,6 +399,7 @@ class Pool:
         ks = K.shape
         if ks != lead + (n, n_new, self.n_kv_heads, self.head_dim) or V.shape != ks:
             raise DendriteError(-1, f"K/V shape {tuple(ks)}")
+        self._other(stream, K, V)
         if Q is None:
             return None, 0, None
         self._check_tensor(Q, "Q")
@@ -383,11 +408,12 @@ class Pool:
         if qs != lead + (n, n_new, nq, self.head_dim):
             raise DendriteError(-1, f"Q shape {tuple(qs)}")
         if out is None:
-            out = torch.empty_like(Q)
+            out = self._output(qs, stream)
         else:
             self._check_tensor(out, "out")
             if out.shape != qs:
                 raise DendriteError(-1, "out shape")
+        self._other(stream, Q, out)
         return Q.data_ptr(), nq, out
 
     def append_rope(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, rope: Rope,
@@ -401,7 +427,7 @@ class Pool:
         ks = K.shape
         nb, n_new = len(branches), ks[-3] if len(ks) >= 4 else 0
         lead = () if self.n_layers == 1 else (self.n_layers,)
-        qp, nq, out = self._rotated(K, V, rope, Q, out, lead, nb, n_new)
+        qp, nq, out = self._rotated(K, V, rope, Q, out, lead, nb, n_new, stream)
         keep, pp, nt = _trees(parents, nb, n_new)
         ba = _arr(branches)
         _check(lib().dendrite_append_rope(self._h, _ptr(ba), nb, n_new, pp, nt, K.data_ptr(), V.data_ptr(), qp, nq,
@@ -414,24 +440,28 @@ class Pool:
                           stream=None) -> Optional[torch.Tensor]:
         """:meth:`append_layer` with the rotation of :meth:`append_rope`."""
         nb, n_new = (K.shape[0], K.shape[1]) if K.dim() == 4 else (0, 0)
-        qp, nq, out = self._rotated(K, V, rope, Q, out, (), nb, n_new)
+        qp, nq, out = self._rotated(K, V, rope, Q, out, (), nb, n_new, stream)
         keep, pp, nt = _trees(parents, nb, n_new)
         _check(lib().dendrite_append_layer_rope(self._h, int(layer), pp, nt, K.data_ptr(), V.data_ptr(), qp, nq,
                                                 out.data_ptr() if qp is not None else None, rope._ptr,
                                                 _stream_ptr(stream, self._dev)), "append_layer_rope")
         return out
 
-    def _query(self, Q, n, out):
+    def _query(self, Q, n, out, stream):
         """Checks of an attention call over n branches; returns (Q's shape, the output)."""
         self._check_tensor(Q, "Q")
         qs = Q.shape
         if len(qs) != 4 or qs[0] != n or qs[3] != self.head_dim:
             raise DendriteError(-1, f"Q shape {tuple(qs)}")
         if out is None:
-            return qs, torch.empty_like(Q)
-        self._check_tensor(out, "out")
-        if out.shape != qs:
-            raise DendriteError(-1, "out shape")
+            if stream is None:
+                return qs, torch.empty_like(Q)
+            out = self._output(qs, stream)
+        else:
+            self._check_tensor(out, "out")
+            if out.shape != qs:
+                raise DendriteError(-1, "out shape")
+        self._other(stream, Q, out)
         return qs, out
 
     def tree_attn_draft(self, Q: torch.Tensor, branches: Sequence[int], parents, out: Optional[torch.Tensor] = None,
@@ -439,7 +469,7 @@ class Pool:
         """Attention of draft trees: Q ``[n_branches][n_draft][n_q_heads][head_dim]``
         are each branch's last n_draft tokens; token j sees what stands before
         the drafts, its ancestors and itself (``parents`` as in :meth:`append_rope`)."""
-        qs, out = self._query(Q, len(branches), out)
+        qs, out = self._query(Q, len(branches), out, stream)
         keep, pp, nt = _trees(parents, len(branches), qs[1])
         ba = _arr(branches)
         _check(lib().dendrite_tree_attn_draft(self._h, int(layer), Q.data_ptr(), qs[2], qs[1], _ptr(ba),
@@ -458,17 +488,26 @@ class Pool:
                                            _stream_ptr(stream, self._dev)), "accept_draft")
 
     def read_kv(self, branches: Sequence[int], starts: Sequence[int], counts: Sequence[int], stream=None,
-                layer: int = 0):
+                layer: int = 0, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
         """K and V of positions ``starts[i] .. starts[i] + counts[i] - 1`` of each
-        branch, one branch after the other: two ``[sum counts][n_kv_heads][head_dim]``."""
+        branch, one branch after the other: two ``[sum counts][n_kv_heads][head_dim]``
+        (``out``: the tensors to write)."""
         if len(branches) != len(starts) or len(branches) != len(counts):
             raise DendriteError(-1, "branches / starts / counts length")
         ba, sa, ca = _arr(branches), _arr(starts), _arr(counts)
         total = sum(counts)
         if total > len(branches) * self._max_len:   # past any branch: refused before the rows are allocated
             raise DendriteError(-1, "read_kv counts")
-        k = torch.empty((max(0, total), self.n_kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
-        v = torch.empty_like(k)
+        shape = (max(0, total), self.n_kv_heads, self.head_dim)
+        if out is None:
+            k, v = self._output(shape, stream), self._output(shape, stream)
+        else:
+            k, v = out
+            for t in (k, v):
+                self._check_tensor(t, "out")
+                if t.shape != shape:
+                    raise DendriteError(-1, f"out shape {tuple(t.shape)}")
+            self._other(stream, k, v)
         _check(lib().dendrite_read_kv(self._h, int(layer), _ptr(ba), _ptr(sa), _ptr(ca), len(branches), k.data_ptr(),
                                       v.data_ptr(), _stream_ptr(stream, self._dev)), "read_kv")
         return k, v
@@ -476,7 +515,7 @@ class Pool:
     def tree_attn_decode(self, Q: torch.Tensor, branches: Sequence[int], out: Optional[torch.Tensor] = None,
                          stream=None, layer: int = 0) -> torch.Tensor:
         """Q: ``[n_branches][q_len][n_q_heads][head_dim]``; returns out of the same shape."""
-        qs, out = self._query(Q, len(branches), out)
+        qs, out = self._query(Q, len(branches), out, stream)
         ba = _arr(branches)
         _check(lib().dendrite_tree_attn_decode_layer(self._h, int(layer), Q.data_ptr(), qs[2], qs[1],
                                                      _ptr(ba), len(branches), out.data_ptr(),
@@ -493,6 +532,7 @@ class Pool:
         self._check_tensor(out, "out")
         if Q.dim() != 4 or Q.shape[0] != len(branches) or Q.shape[3] != self.head_dim or out.shape != Q.shape:
             raise DendriteError(-1, f"Q/out shape {tuple(Q.shape)}")
+        self._other(stream, Q, out)
         ba = _arr(branches)
         _check(lib().dendrite_tree_attn_decode_noalloc(self._h, Q.data_ptr(), Q.shape[2], Q.shape[1], _ptr(ba),
                                                        len(branches), out.data_ptr(),
