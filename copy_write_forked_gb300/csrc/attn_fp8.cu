@@ -13,11 +13,14 @@
 //   A row of Q is brought to (-4, 4) by a power of two (returned with the
 //   score), which loses nothing that fp16 keeps of a bf16 row: elements under
 //   2^-14 of the row's largest lose bits below 2^-25 of it.
-//   The weights w_rt = p_rt 2^f_t get a running reference of their own, as
-//   log2 w is score + f_t: w is stored as 2^(score + f_t - m2) in [0, 1] in
-//   fp16, whatever the spread of the tokens' scales, while the row sum l takes
-//   p = 2^(score - m) in fp32.  acc is in units of 2^m2 and is brought to
-//   2^m when the chunk's partial row is written.
+//   The weights w_rt = p_rt 2^f_t get a running reference W of their own, as
+//   log2 w is score + f_t: w is stored as 2^(score + f_t - W) in fp16, whatever the
+//   spread of the tokens' scales, while the row sum l takes p = 2^(score - m) in
+//   fp32.  W is whole and 15 below the largest (weights reach 2^15: fp16 keeps 11
+//   bits of those down to 2^-29 of the largest, where a reference at the largest
+//   would end at 2^-14, and the many small weights beside one large would be off by
+//   the same side of a step).  acc is in units of 2^W and is brought to 2^m when the
+//   chunk's partial row is written.
 //
 //   K needs no ldmatrix: the mma's k order is free as long as Q and K agree,
 //   so a lane takes 32 consecutive codes of its token (two 16-byte loads).
@@ -95,6 +98,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// The least reference under which weights of up to 2^x stay in fp16: whole, so that
+// sums rescaled from one to another keep their bits.  (From 2^23 on x is whole itself,
+// and x - 15 might round to a reference more than 15 below: there it is x.)
+constexpr float kWeightTop = 15.f;
+__device__ __forceinline__ float weight_ref(float x) { return ceilf(x) - (fabsf(x) < 0x1p23f ? kWeightTop : 0.f); }
 
 // A row's 32 elements 32 q .. 32 q + 31 (q = lane % 4) as fp16 pairs w[0..15],
 // scaled by a power of two common to the row; returns that power's inverse
@@ -376,7 +385,8 @@ __global__ void __launch_bounds__(F8_THREADS, 3) k_attn_partial_fp8(const AttnAr
                     wx0 = fmaxf(wx0, __shfl_xor_sync(0xffffffffu, wx0, x));
                     wx1 = fmaxf(wx1, __shfl_xor_sync(0xffffffffu, wx1, x));
                 }
-                const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1), x0 = fmaxf(w0, wx0), x1 = fmaxf(w1, wx1);
+                const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+                const float x0 = fmaxf(w0, weight_ref(wx0)), x1 = fmaxf(w1, weight_ref(wx1));
                 const float nu0 = n0 == NEG_INF ? 0.f : n0, nu1 = n1 == NEG_INF ? 0.f : n1;
                 const float xu0 = x0 == NEG_INF ? 0.f : x0, xu1 = x1 == NEG_INF ? 0.f : x1;
                 l0 *= ex2(m0 - nu0);
@@ -391,7 +401,7 @@ __global__ void __launch_bounds__(F8_THREADS, 3) k_attn_partial_fp8(const AttnAr
                 for (int h = 0; h < 4; ++h) {
                     l0 += ex2(s[h][0] - nu0) + ex2(s[h][1] - nu0);
                     l1 += ex2(s[h][2] - nu1) + ex2(s[h][3] - nu1);
-                    // weights in fp16: rounded by 2^-11, or 2^-25 of the row's largest weight
+                    // weights in fp16: rounded by 2^-11, or 2^-40 of the row's largest weight
                     pa[h >> 1][2 * (h & 1)] = pack_f16(ex2(s[h][0] + vl(h, 0) - xu0), ex2(s[h][1] + vl(h, 1) - xu0));
                     pa[h >> 1][2 * (h & 1) + 1] = pack_f16(ex2(s[h][2] + vl(h, 0) - xu1), ex2(s[h][3] + vl(h, 1) - xu1));
                 }
@@ -439,8 +449,17 @@ __global__ void __launch_bounds__(F8_THREADS, 3) k_attn_partial_fp8(const AttnAr
             l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-            // acc from units of 2^w to units of 2^m
-            const float back0 = w0 == NEG_INF ? 0.f : ex2(w0 - m0), back1 = w1 == NEG_INF ? 0.f : ex2(w1 - m1);
+            // acc from units of 2^w to units of 2^m (in two steps: w - m may be 15 below
+            // the least exponent, with values of that size)
+            const float back0 = w0 == NEG_INF ? 0.f : ex2(w0 - m0 + kWeightTop);
+            const float back1 = w1 == NEG_INF ? 0.f : ex2(w1 - m1 + kWeightTop);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+                o[n][0] *= 0x1p-15f;
+                o[n][1] *= 0x1p-15f;
+                o[n][2] *= 0x1p-15f;
+                o[n][3] *= 0x1p-15f;
+            }
             const int32_t prow0 = U.prow_base + (c - U.cfirst) * U.n_rows;
             if (P == 1) {
                 if (ok && !idle) {

@@ -136,7 +136,8 @@ typedef struct dendrite_pool_opts {
  * 16-byte chunk c of slot s at chunk c ^ (s & 7), then the 16 slots' exponent
  * bytes e + 127 (255: a row of NaN).  129 bytes per row instead of bf16's 256;
  * a row reads back as code * 2^e, which bf16 holds exactly, and attention reads
- * those values.
+ * those values.  Scores times log2(e) / sqrt(head_dim) have to stay under 2^23 in
+ * magnitude (they share fp32's digits with the exponents of V).
  * Synchronous.  Uses the current CUDA device.
  */
 int dendrite_pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads,
