@@ -323,8 +323,10 @@ __global__ void __launch_bounds__(F8_THREADS, 3) k_attn_partial_fp8(const AttnAr
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float kf = __uint_as_float(((ke >> (8 * e)) & 255u) << 23);
-                        s[h][e] *= kf * f0;
-                        s[h][2 + e] *= kf * f1;
+                        // (one after the other: the two together may pass fp32's range
+                        // where the score, of rows that hardly meet, does not)
+                        s[h][e] = s[h][e] * kf * f0;
+                        s[h][2 + e] = s[h][2 + e] * kf * f1;
                     }
                 }
                 // mask: only where some row does not see the whole pair

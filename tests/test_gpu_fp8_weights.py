@@ -115,3 +115,25 @@ def test_scores_of_extreme_size(size):
     v = R.dequantise(*R.quantise(R.f64(V[0, 41])))[0]
     assert np.array_equal(out, np.broadcast_to(v, out.shape))   # a bf16 number, exactly
     pool.close()
+
+
+@pytest.mark.parametrize("rows", [-1, 1])
+@pytest.mark.parametrize("key,query", [(2.0 ** 95, 2.0 ** 50), (2.0 ** 100, 2.0 ** 100), (2.0 ** -100, 2.0 ** -100), (2.0 ** 110, 2.0 ** -110)])
+def test_keys_and_queries_of_extreme_size_that_hardly_meet(key, query, rows):
+    """Their sizes multiplied may be past fp32's range; the scores, 0 or near it, are not."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    K = torch.zeros(1, 75, 2, D, device="cuda")
+    K[..., 1] = key
+    V = torch.randn(1, 75, 2, D, generator=g, device="cuda")
+    q = torch.zeros(1, 1, 8, D, device="cuda")
+    q[..., 0] = query
+    K, V, q = K.bfloat16(), V.bfloat16(), q.bfloat16()
+    pool = Pool(8, 16, 2, D, torch.float8_e4m3fn, max_branches=4, tc_min_rows=rows)
+    b = pool.new_branch()
+    pool.append_kv([b], K, V)
+    out = pool.tree_attn_decode(q, [b])
+    pool.sync()
+    k, v = (R.dequantise(*R.quantise(R.f64(x[0]))) for x in (K, V))
+    ref = R.attention(R.f64(q[0]), k, v, np.ones((1, 75), bool))
+    assert (np.abs(R.f64(out[0]) - ref[0]) <= R.attention_bound("fp8", *ref)).all()
+    pool.close()
