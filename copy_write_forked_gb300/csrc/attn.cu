@@ -1767,16 +1767,34 @@ constexpr int32_t kDevicePlanMaxTilesPerUnit = 32;
 // (tile_weight per tile plus the unit starts); the ns per weight are fitted
 // to the kernels on GB300 (tcgen05: 255 ns per 16-token tile of a 256-row
 // unit per SM; mma.sync: 60 ns per 4-row tile per CTA, two CTAs per SM).
-int split_tc_sms(const dendrite_pool* p, int64_t w_tc, int64_t w_small, int64_t tiles_tc, int64_t tiles_small) {
+//
+// 8-bit pools' kernels have rates of their own: 318 ns per tile of a 256-row unit
+// (222 of 64 rows), and on an SM's three CTAs 88 ns per 4-row tile and 1,430 ns per
+// unit (fitted to calls split at 30 to 130 SMs: 4 to 32 prefixes of 4,096 to 32,768
+// tokens, 64 to 1,024 rows, leaves of 64 to 1,024 tokens, each within 3 %).  Neither
+// is bound by HBM there, so a split gains next to nothing: 16 prefixes of 32,768
+// tokens, each with 64 leaves of 1,024, take 986 us without one and 978 with the best;
+// with the bf16 kernels' rates one was taken that made it 1,194 (32 prefixes of 4,096
+// with 16 leaves of 512: 249, best 242, was 289).
+struct SplitRates {
+    double tc_ns, small_ns;          // SM ns per weight
+    double small_start_ns;           // SM ns per unit, beside its start weight
+    double small_bytes;              // bytes per ns one SM's small-kernel CTAs read at most
+};
+constexpr SplitRates kSplitBf16{85.0, 30.0, 0.0, 70.0};
+constexpr SplitRates kSplitFp8{106.0, 44.0, 950.0, 47.0};
+
+int split_tc_sms(const dendrite_pool* p, int64_t w_tc, int64_t w_small, int64_t tiles_tc, int64_t tiles_small,
+                 int64_t units_small) {
     const int sms = p->sm_count;
     if (p->tc_sms < 0 || sms < 2) return 0;
     if (p->tc_sms > 0) return p->tc_sms < sms ? p->tc_sms : 0;
-    constexpr double kTcNsPerWeight = 85.0, kSmallNsPerWeight = 30.0;   // SM ns
+    const bool f8 = p->dtype == DENDRITE_FP8;
+    const SplitRates& r = f8 ? kSplitFp8 : kSplitBf16;
     constexpr double kHbmBytesPerNs = 6700.0;                           // measured copy bandwidth
-    constexpr double kSmallBytesPerNsPerSm = 70.0;                      // one SM's two mma.sync CTAs
     const double tile_bytes =   // K and V of one kv head
-        p->dtype == DENDRITE_FP8 ? 2.0 * kFp8TileBytes : 2.0 * p->block_size * p->head_dim * 2;
-    const double A = (double)w_tc * kTcNsPerWeight, S = (double)w_small * kSmallNsPerWeight;
+        f8 ? 2.0 * kFp8TileBytes : 2.0 * p->block_size * p->head_dim * 2;
+    const double A = (double)w_tc * r.tc_ns, S = (double)w_small * r.small_ns + (double)units_small * r.small_start_ns;
     const double Bt = (double)tiles_tc * tile_bytes, Bs = (double)tiles_small * tile_bytes;
     const double serial = std::max(A / sms, Bt / kHbmBytesPerNs) + std::max(S / sms, Bs / kHbmBytesPerNs);
     const double floor_ns = (Bt + Bs) / kHbmBytesPerNs;
@@ -1784,7 +1802,7 @@ int split_tc_sms(const dendrite_pool* p, int64_t w_tc, int64_t w_small, int64_t 
     int best_n = 0;
     for (int n = 1; n < sms; ++n) {
         const int m = sms - n;
-        const double t = std::max(std::max(A / n, S / m), std::max(floor_ns, Bs / (m * kSmallBytesPerNsPerSm)));
+        const double t = std::max(std::max(A / n, S / m), std::max(floor_ns, Bs / (m * r.small_bytes)));
         if (t < best) {
             best = t;
             best_n = n;
@@ -1904,7 +1922,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
         PlanClass& ct = hp.hdr.cls[0];
         PlanClass& cs = hp.hdr.cls[1];
         if (ct.u_hi > ct.u_lo && cs.u_hi > cs.u_lo) {
-            const int n = split_tc_sms(p, ct.weight, cs.weight, ct.tiles, cs.tiles);
+            const int n = split_tc_sms(p, ct.weight, cs.weight, ct.tiles, cs.tiles, cs.u_hi - cs.u_lo);
             if (n > 0) {
                 max_tc_ctas = std::min(max_tc_ctas, n);
                 max_ctas = std::min(max_ctas, (p->sm_count - n) * p->attn_ctas_per_sm);
