@@ -1614,6 +1614,17 @@ struct ClassWeights {
     int64_t min_per_cta;       // smallest total weight worth a CTA of its own
 };
 constexpr ClassWeights kSmallWeights{10, 2, 8};
+// 8-bit pools' small kernel reads a tile in half the time (88 SM ns) and starts a
+// unit in no less (1,430), so a start weighs three times as much: with the weights
+// above, CTAs of many short leaves ended long after those of a prefix.  8 prefixes of
+// 16,384 tokens with 4 leaves of 20 tokens each 112 -> 66 us (6 leaves 156 -> 100, 8
+// 160 -> 103; on the tcgen05 kernel 109, 111 and 113), the beam 30.3 -> 28.1, MCTS 368
+// -> 346; single contexts of any length unchanged.  20 gives 80 us, 40 to 60 62 to 65
+// but more elsewhere.
+constexpr ClassWeights kSmallWeightsFp8{30, 2, 8};
+inline const ClassWeights& small_weights(const dendrite_pool* p) {
+    return p->dtype == DENDRITE_FP8 ? kSmallWeightsFp8 : kSmallWeights;
+}
 constexpr ClassWeights kTcWeights{24, -1, 32};
 inline int64_t tile_weight(int rt) { return 1 + rt; }
 inline int64_t start_weight(const ClassWeights& cw, int32_t n_rows) {
@@ -1778,14 +1789,12 @@ constexpr int32_t kDevicePlanMaxTilesPerUnit = 32;
 // with 16 leaves of 512: 249, best 242, was 289).
 struct SplitRates {
     double tc_ns, small_ns;          // SM ns per weight
-    double small_start_ns;           // SM ns per unit, beside its start weight
     double small_bytes;              // bytes per ns one SM's small-kernel CTAs read at most
 };
-constexpr SplitRates kSplitBf16{85.0, 30.0, 0.0, 70.0};
-constexpr SplitRates kSplitFp8{106.0, 44.0, 950.0, 47.0};
+constexpr SplitRates kSplitBf16{85.0, 30.0, 70.0};
+constexpr SplitRates kSplitFp8{106.0, 44.0, 47.0};
 
-int split_tc_sms(const dendrite_pool* p, int64_t w_tc, int64_t w_small, int64_t tiles_tc, int64_t tiles_small,
-                 int64_t units_small) {
+int split_tc_sms(const dendrite_pool* p, int64_t w_tc, int64_t w_small, int64_t tiles_tc, int64_t tiles_small) {
     const int sms = p->sm_count;
     if (p->tc_sms < 0 || sms < 2) return 0;
     if (p->tc_sms > 0) return p->tc_sms < sms ? p->tc_sms : 0;
@@ -1794,7 +1803,7 @@ int split_tc_sms(const dendrite_pool* p, int64_t w_tc, int64_t w_small, int64_t 
     constexpr double kHbmBytesPerNs = 6700.0;                           // measured copy bandwidth
     const double tile_bytes =   // K and V of one kv head
         f8 ? 2.0 * kFp8TileBytes : 2.0 * p->block_size * p->head_dim * 2;
-    const double A = (double)w_tc * r.tc_ns, S = (double)w_small * r.small_ns + (double)units_small * r.small_start_ns;
+    const double A = (double)w_tc * r.tc_ns, S = (double)w_small * r.small_ns;
     const double Bt = (double)tiles_tc * tile_bytes, Bs = (double)tiles_small * tile_bytes;
     const double serial = std::max(A / sms, Bt / kHbmBytesPerNs) + std::max(S / sms, Bs / kHbmBytesPerNs);
     const double floor_ns = (Bt + Bs) / kHbmBytesPerNs;
@@ -1853,7 +1862,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
     int64_t n_rows = 0;
     for (int pass = 0; pass < 2; ++pass) {
         PlanClass& pc = hp.hdr.cls[pass];
-        const ClassWeights& cwt = pass == 0 ? kTcWeights : kSmallWeights;
+        const ClassWeights& cwt = pass == 0 ? kTcWeights : small_weights(p);
         pc = PlanClass{};
         pc.u_lo = n_unit;
         pc.s_lo = (int32_t)hp.segplan.size();
@@ -1922,14 +1931,14 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
         PlanClass& ct = hp.hdr.cls[0];
         PlanClass& cs = hp.hdr.cls[1];
         if (ct.u_hi > ct.u_lo && cs.u_hi > cs.u_lo) {
-            const int n = split_tc_sms(p, ct.weight, cs.weight, ct.tiles, cs.tiles, cs.u_hi - cs.u_lo);
+            const int n = split_tc_sms(p, ct.weight, cs.weight, ct.tiles, cs.tiles);
             if (n > 0) {
                 max_tc_ctas = std::min(max_tc_ctas, n);
                 max_ctas = std::min(max_ctas, (p->sm_count - n) * p->attn_ctas_per_sm);
             }
         }
         ct.c0 = ct.u_hi > ct.u_lo ? class_ctas(ct.weight, max_tc_ctas, kTcWeights) : 0;
-        cs.c0 = cs.u_hi > cs.u_lo ? class_ctas(cs.weight, max_ctas, kSmallWeights) : 0;
+        cs.c0 = cs.u_hi > cs.u_lo ? class_ctas(cs.weight, max_ctas, small_weights(p)) : 0;
     }
     if (n_rows >= INT32_MAX / 2) return DENDRITE_ELIMIT;
     hp.hdr.n_units = n_unit;
@@ -1973,7 +1982,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
         partition_class(hp, 0, hp.n_tc_units, hp.hdr.cls[0].tiles, hp.hdr.cls[0].weight, max_tc_ctas, kTcWeights,
                         hp.tc_cta_begin, hp.tc_cta_unit);
         partition_class(hp, hp.n_tc_units, (int32_t)hp.units.size(), hp.hdr.cls[1].tiles, hp.hdr.cls[1].weight,
-                        max_ctas, kSmallWeights, hp.cta_begin, hp.cta_unit);
+                        max_ctas, small_weights(p), hp.cta_begin, hp.cta_unit);
         // partial rows per unit
         size_t prow = 0;
         for (AttnUnit& U : hp.units) {

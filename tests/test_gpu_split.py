@@ -1,5 +1,6 @@
 """How a call with wide prefixes and private leaves shares the SMs between the two
 attention kernels: by what each pool type's own kernels take."""
+import numpy as np
 import pytest
 import torch
 
@@ -46,3 +47,26 @@ def test_bf16_calls_split_as_before():
     # end there from 2105 / 50.08 = 42.04 SMs on: 43.
     n_tc, n = _ctas("bf16", 2, 16384, 64, 1024)
     assert n_tc == 43 and n == 2 * (torch.cuda.get_device_properties(0).multi_processor_count - n_tc)
+
+
+@pytest.mark.parametrize("width,leaf", [(4, 20), (7, 3)])
+def test_8_bit_prefixes_beside_many_short_leaves(width, leaf):
+    """A plan whose small kernel has long units of up to 28 rows and many short ones of 4: right, whatever CTA has which."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n, prefix, kv = 4, 1500, 2
+    pool = Pool(n * (prefix // 16 + 4 * width), 16, kv, 128, torch.float8_e4m3fn, max_branches=64)
+    rows = lambda *s: torch.randn(*s, kv, 128, generator=g, device="cuda").bfloat16()  # noqa: E731
+    roots = [pool.new_branch() for _ in range(n)]
+    K, V = rows(n, prefix), rows(n, prefix)
+    pool.append_kv(roots, K, V)
+    kids = [c for k in pool.fork_batch(roots, [width] * n) for c in k]
+    k, v = rows(n * width, leaf), rows(n * width, leaf)
+    pool.append_kv(kids, k, v)
+    q = torch.randn(n * width, 1, 4 * kv, 128, generator=g, device="cuda").bfloat16()
+    out = pool.tree_attn_decode(q, kids)
+    pool.sync()
+    for i in range(n * width):
+        kk, vv = (R.held(R.f64(torch.cat((a[i // width], b[i]))), "fp8") for a, b in ((K, k), (V, v)))
+        ref = R.attention(R.f64(q[i]), kk, vv, np.ones((1, len(kk)), bool))
+        assert (np.abs(R.f64(out[i]) - ref[0]) <= R.attention_bound("fp8", *ref)).all()
+    pool.close()
