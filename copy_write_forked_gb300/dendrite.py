@@ -336,9 +336,9 @@ class Pool:
             raise DendriteError(-1, f"{name} is on another device than the pool")
 
     def _other(self, stream, *tensors: torch.Tensor) -> Optional[torch.cuda.Stream]:
-        """``stream`` where it is another than the current one (else None).  The tensors' memory
-        is then kept until that stream's work is done, however early they are freed."""
-        if stream is None or stream.cuda_stream == torch.cuda.current_stream(self._dev).cuda_stream:
+        """``stream`` (not None) where it is another than the current one, else None.  The tensors'
+        memory is then kept until that stream's work is done, however early they are freed."""
+        if stream.cuda_stream == torch.cuda.current_stream(self._dev).cuda_stream:
             return None
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(stream.cuda_stream, device=self.device)
@@ -357,6 +357,20 @@ class Pool:
         out.record_stream(torch.cuda.current_stream(self._dev))
         return out
 
+    def _out(self, Q: torch.Tensor, out: Optional[torch.Tensor], stream) -> torch.Tensor:
+        """The output beside queries Q: the given one, checked, or a new one."""
+        if out is None:
+            if stream is None:
+                return torch.empty_like(Q)
+            out = self._output(Q.shape, stream)
+        else:
+            self._check_tensor(out, "out")
+            if out.shape != Q.shape:
+                raise DendriteError(-1, "out shape")
+        if stream is not None:
+            self._other(stream, Q, out)
+        return out
+
     def append_kv(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, stream=None) -> None:
         """K, V: ``[n_branches][n_new][n_kv_heads][head_dim]``; for a pool of
         several layers ``[n_layers][n_branches][n_new][n_kv_heads][head_dim]``."""
@@ -369,7 +383,8 @@ class Pool:
         k4 = K.shape[-4:]
         if k4[0] != nb or k4[2] != self.n_kv_heads or k4[3] != self.head_dim:
             raise DendriteError(-1, f"K/V shape {tuple(K.shape)}")
-        self._other(stream, K, V)
+        if stream is not None:
+            self._other(stream, K, V)
         ba = _arr(branches)
         _check(lib().dendrite_append_kv(self._h, _ptr(ba), nb, k4[1], K.data_ptr(), V.data_ptr(),
                                         _stream_ptr(stream, self._dev)), "append_kv")
@@ -386,7 +401,8 @@ class Pool:
         self._check_tensor(V, "V")
         if K.shape != V.shape or K.dim() != 4 or K.shape[2] != self.n_kv_heads or K.shape[3] != self.head_dim:
             raise DendriteError(-1, f"K/V shape {tuple(K.shape)}")
-        self._other(stream, K, V)
+        if stream is not None:
+            self._other(stream, K, V)
         _check(lib().dendrite_append_layer(self._h, int(layer), K.data_ptr(), V.data_ptr(),
                                            _stream_ptr(stream, self._dev)), "append_layer")
 
@@ -399,7 +415,8 @@ class Pool:
         ks = K.shape
         if ks != lead + (n, n_new, self.n_kv_heads, self.head_dim) or V.shape != ks:
             raise DendriteError(-1, f"K/V shape {tuple(ks)}")
-        self._other(stream, K, V)
+        if stream is not None:
+            self._other(stream, K, V)
         if Q is None:
             return None, 0, None
         self._check_tensor(Q, "Q")
@@ -407,13 +424,7 @@ class Pool:
         nq = qs[-2] if len(qs) > 1 else 0
         if qs != lead + (n, n_new, nq, self.head_dim):
             raise DendriteError(-1, f"Q shape {tuple(qs)}")
-        if out is None:
-            out = self._output(qs, stream)
-        else:
-            self._check_tensor(out, "out")
-            if out.shape != qs:
-                raise DendriteError(-1, "out shape")
-        self._other(stream, Q, out)
+        out = self._out(Q, out, stream)
         return Q.data_ptr(), nq, out
 
     def append_rope(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, rope: Rope,
@@ -453,16 +464,7 @@ class Pool:
         qs = Q.shape
         if len(qs) != 4 or qs[0] != n or qs[3] != self.head_dim:
             raise DendriteError(-1, f"Q shape {tuple(qs)}")
-        if out is None:
-            if stream is None:
-                return qs, torch.empty_like(Q)
-            out = self._output(qs, stream)
-        else:
-            self._check_tensor(out, "out")
-            if out.shape != qs:
-                raise DendriteError(-1, "out shape")
-        self._other(stream, Q, out)
-        return qs, out
+        return qs, self._out(Q, out, stream)
 
     def tree_attn_draft(self, Q: torch.Tensor, branches: Sequence[int], parents, out: Optional[torch.Tensor] = None,
                         stream=None, layer: int = 0) -> torch.Tensor:
@@ -499,7 +501,10 @@ class Pool:
         if total > len(branches) * self._max_len:   # past any branch: refused before the rows are allocated
             raise DendriteError(-1, "read_kv counts")
         shape = (max(0, total), self.n_kv_heads, self.head_dim)
-        if out is None:
+        if out is None and stream is None:
+            k = torch.empty(shape, dtype=self.dtype, device=self.device)
+            v = torch.empty_like(k)
+        elif out is None:
             k, v = self._output(shape, stream), self._output(shape, stream)
         else:
             k, v = out
@@ -507,7 +512,8 @@ class Pool:
                 self._check_tensor(t, "out")
                 if t.shape != shape:
                     raise DendriteError(-1, f"out shape {tuple(t.shape)}")
-            self._other(stream, k, v)
+            if stream is not None:
+                self._other(stream, k, v)
         _check(lib().dendrite_read_kv(self._h, int(layer), _ptr(ba), _ptr(sa), _ptr(ca), len(branches), k.data_ptr(),
                                       v.data_ptr(), _stream_ptr(stream, self._dev)), "read_kv")
         return k, v
@@ -532,7 +538,8 @@ class Pool:
         self._check_tensor(out, "out")
         if Q.dim() != 4 or Q.shape[0] != len(branches) or Q.shape[3] != self.head_dim or out.shape != Q.shape:
             raise DendriteError(-1, f"Q/out shape {tuple(Q.shape)}")
-        self._other(stream, Q, out)
+        if stream is not None:
+            self._other(stream, Q, out)
         ba = _arr(branches)
         _check(lib().dendrite_tree_attn_decode_noalloc(self._h, Q.data_ptr(), Q.shape[2], Q.shape[1], _ptr(ba),
                                                        len(branches), out.data_ptr(),
