@@ -41,10 +41,10 @@
 // read them from L2 (units of more than 16 rows).
 //
 // 8 contexts of 32,768 tokens, 4 rows a kv head: 96 us for 549 MB (5.7 TB/s; at
-// 18 % of the warps and 49 % of the issue slots it is the chain's latency that
+// 18 % of the warps and 50 % of the issue slots it is the chain's latency that
 // keeps it from 6.8); 8 prefixes of 4,096 tokens read by 16 rows each, with 256
-// tokens behind them for each of 4 branches: 33 us a call for 85 MB, where a call
-// on one short context takes 14.
+// tokens behind them for each of 4 branches: 31.6 us a call for 85 MB, where a call
+// on one short context takes 12 to 17 (the host's pace).
 //
 // Every mbarrier wait is bounded, as in the bf16 kernel.
 #include <cuda_fp16.h>

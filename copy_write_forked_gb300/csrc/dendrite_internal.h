@@ -24,14 +24,14 @@ constexpr int kMaxUnitRowsFp8 = 64;    // rows per 8-bit-pool unit (4 warps x 16
 constexpr int kMaxUnitRowsTc = 256;   // rows per tcgen05 attention unit (2 row tiles of 128)
 constexpr int kTcMinRowsDefault = 64; // segments with more rows per kv head use the tcgen05 kernel
 // The same for 8-bit pools and for draft trees over bf16 pools.  Small kernel /
-// tcgen05 kernel, 8 kv heads:
-//   8-bit, draft trees, 32 branches of about 7,500 tokens: 32 rows 145 / 199 us, 36
-//     rows 238 / 211
-//   8-bit, causal, the same contexts: 16 rows 100 / 181, 32 rows 167 / 186, 36 rows
-//     295 / 187; 8 prefixes of 16,384 tokens shared by short leaves: 16 rows 67 / 109,
-//     32 rows 102 / 113, 36 rows 174 / 115
-//   bf16, draft trees: 16 rows 121 / 145, 20 rows 188 / 150, 64 rows 260 / 137
-// (bf16, causal, at its 64: the contexts 255 / 175 with 64 rows, the prefixes 155 / 108.)
+// tcgen05 kernel in us a call, 8 kv heads; 32 branches of about 7,350 tokens each:
+//   8-bit, draft trees: 16 rows 106 / 186, 32 rows 179 / 186, 36 rows 311 / 187
+//   8-bit, causal: 16 rows 99 / 182, 32 rows 168 / 186, 36 rows 296 / 187
+//   bf16, draft trees: 16 rows 155 / 176, 24 rows 236 / 180, 64 rows 338 / 167
+//   bf16, causal: 32 rows 193 / 185, 36 rows 259 / 185, 64 rows 256 / 175
+// 8 prefixes of 16,384 tokens shared by short leaves, causal:
+//   8-bit: 16 rows 67 / 109, 32 rows 102 / 113, 36 rows 174 / 115
+//   bf16: 32 rows 115 / 105, 64 rows 155 / 108
 constexpr int kTcMinRowsFp8 = 32;
 constexpr int kTcMinRowsDraft = 16;
 constexpr int32_t kFoldPctDefault = 100;  // fold a segment when that is estimated cheaper
