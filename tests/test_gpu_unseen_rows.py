@@ -149,11 +149,15 @@ def test_draft_trees(kind, new, rows):
     p.close()
 
 
+@pytest.mark.parametrize("rolled_back", [False, True])
+@pytest.mark.parametrize("rows", [-1, 1])
 @pytest.mark.parametrize("kind", KINDS)
-def test_the_allocation_free_call(kind):
-    p = Pools(kind, 20, float("nan"))
+def test_the_allocation_free_call(kind, rows, rolled_back):
+    p = Pools(kind, 20, float("nan"), tc_min_rows=rows)
     b = p.new()
     p.append([b], 37)
+    if rolled_back:
+        p.leave([b], 9)
     q = p.rows(1, 1, KV * 4)
     outs = [torch.zeros_like(q) for _ in range(2)]
     for pool, o in zip(p.pools, outs):
