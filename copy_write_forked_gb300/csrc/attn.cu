@@ -183,7 +183,7 @@ __device__ __forceinline__ void merge_row_wide(const AttnArgs& a, int32_t o, int
     }
     wait_partials(waited);
     if (*reinterpret_cast<volatile const int32_t*>(&a.meta->status)) return;
-    const float inv = 1.f / L;
+    const float inv = pbeg == pend ? 0.f : 1.f / L;   // (cross attention to a branch of no rows: zeros)
     float y[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
     if (a.tq_signs) {
         // compressed pools: the partials live in the rotated space; rotate
@@ -1087,7 +1087,7 @@ __global__ void __launch_bounds__(256, WIDE ? 2 : 1) k_attn_merge(const AttnArgs
     }
     wait_partials(waited);
     if (*reinterpret_cast<volatile const int32_t*>(&a.meta->status)) return;
-    const float inv = 1.f / L;
+    const float inv = pbeg == pend ? 0.f : 1.f / L;
     if constexpr (WIDE) {
         T* dst = static_cast<T*>(a.out) + (int64_t)o * D + 4 * lane;
         if constexpr (sizeof(T) == 2) {
@@ -1239,7 +1239,7 @@ __global__ void __launch_bounds__(256, 3) k_attn_merge_grouped(const AttnArgs a)
     if (*reinterpret_cast<volatile const int32_t*>(&a.meta->status)) return;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
-        const float inv = 1.f / L[i];
+        const float inv = pbeg == pend ? 0.f : 1.f / L[i];
         const int64_t o = ((int64_t)qi * pl.q_len + j) * pl.n_q_heads + h * G + g0 + i;
         T* dst = static_cast<T*>(a.out) + o * D + 4 * lane;
         if constexpr (sizeof(T) == 2) {
@@ -2010,8 +2010,8 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
             hp.path[4 * e + 3] = S.group_rows;
         }
     }
-    for (int32_t i = 0; i < n; ++i)
-        if (hp.path_off[i + 1] == hp.path_off[i]) return DENDRITE_EINVAL;   // a branch with no visible key
+    for (int32_t i = 0; i < n; ++i)   // a branch with no visible key
+        if (hp.path_off[i + 1] == hp.path_off[i] && p->br[branches[i]].len > 0) return DENDRITE_EINVAL;
     return DENDRITE_OK;
 }
 
@@ -2105,7 +2105,7 @@ void plan_pack(const HostPlan& hp, const size_t (&off)[kPlanSections + 1], char*
 }
 
 AttnPlanDev plan_view(const HostPlan& hp, const size_t (&off)[kPlanSections + 1], const char* d, int32_t n,
-                      int32_t q_len, int32_t nq, int32_t group) {
+                      int32_t q_len, int32_t nq, int32_t group, bool cross) {
     AttnPlanDev v{};
     v.segs = reinterpret_cast<const AttnSeg*>(d + off[SEC_SEGS]);
     v.members = reinterpret_cast<const AttnMember*>(d + off[SEC_MEMBERS]);
@@ -2119,6 +2119,8 @@ AttnPlanDev plan_view(const HostPlan& hp, const size_t (&off)[kPlanSections + 1]
     v.tc_cta_unit = reinterpret_cast<const int32_t*>(d + off[SEC_TC_UNIT]);
     v.counts = hp.device ? reinterpret_cast<const int32_t*>(d + off[SEC_COUNTS]) : nullptr;
     v.masks = hp.masks.empty() ? nullptr : reinterpret_cast<const uint64_t*>(d + off[SEC_MASKS]);
+    v.back = cross ? 0 : q_len;
+    v.step = cross || v.masks ? 0 : 1;
     v.packed = hp.small_packed ? 1 : 0;
     v.n_units = (int32_t)hp.units.size();
     v.n_ctas = (int32_t)hp.cta_unit.size();
@@ -2186,7 +2188,7 @@ void draft_masks(const int32_t* parents, int32_t n_trees, int32_t n, int32_t t, 
 }
 
 int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads, int32_t q_len, const int32_t* branches,
-              int32_t n, const int32_t* parents, int32_t n_trees, void* out, void* stream);
+              int32_t n, const int32_t* parents, int32_t n_trees, bool cross, void* out, void* stream);
 
 // CTAs the tensor-core kernel may use on this pool (0: not used).
 int tc_ctas(const dendrite_pool* p) {
@@ -2442,7 +2444,7 @@ extern "C" int dendrite_tree_attn_decode(dendrite_pool* p, const void* Q, int32_
 extern "C" int dendrite_tree_attn_decode_layer(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
                                                int32_t q_len, const int32_t* branches, int32_t n, void* out,
                                                void* stream) {
-    return attn_call(p, layer, Q, n_q_heads, q_len, branches, n, nullptr, 0, out, stream);
+    return attn_call(p, layer, Q, n_q_heads, q_len, branches, n, nullptr, 0, false, out, stream);
 }
 
 extern "C" int dendrite_tree_attn_draft(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
@@ -2455,14 +2457,24 @@ extern "C" int dendrite_tree_attn_draft(dendrite_pool* p, int32_t layer, const v
     DENDRITE_TRY(check_trees(parents, n_trees, n, n_draft));
     DENDRITE_CUDA(cudaSetDevice(p->device));
     DENDRITE_TRY(check_not_capturing((cudaStream_t)stream));
-    return attn_call(p, layer, Q, n_q_heads, n_draft, branches, n, parents, n_trees, out, stream);
+    return attn_call(p, layer, Q, n_q_heads, n_draft, branches, n, parents, n_trees, false, out, stream);
+}
+
+extern "C" int dendrite_tree_attn_cross(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
+                                        int32_t q_len, const int32_t* branches, int32_t n, void* out, void* stream) {
+    if (!p) return DENDRITE_EINVAL;
+    if (p->poisoned) return p->poisoned;
+    DENDRITE_CUDA(cudaSetDevice(p->device));
+    DENDRITE_TRY(check_not_capturing((cudaStream_t)stream));
+    return attn_call(p, layer, Q, n_q_heads, q_len, branches, n, nullptr, 0, true, out, stream);
 }
 
 namespace {
 
-// One attention call; parents: n_trees draft trees of q_len nodes, or null.
+// One attention call; parents: n_trees draft trees of q_len nodes, or null;
+// cross: every query sees every position of its branch.
 int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads, int32_t q_len, const int32_t* branches,
-              int32_t n, const int32_t* parents, int32_t n_trees, void* out, void* stream) {
+              int32_t n, const int32_t* parents, int32_t n_trees, bool cross, void* out, void* stream) {
     if (!p) return DENDRITE_EINVAL;
     if (p->poisoned) return p->poisoned;
     if (layer < 0 || layer >= p->n_layers) return DENDRITE_EINVAL;
@@ -2474,7 +2486,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
     if ((int64_t)n * q_len * n_q_heads >= INT32_MAX / 2) return DENDRITE_ELIMIT;
     for (int32_t i = 0; i < n; ++i) {
         DENDRITE_TRY(check_live(p, branches[i]));
-        if (p->br[branches[i]].len < q_len) return DENDRITE_EINVAL;
+        if (p->br[branches[i]].len < (cross ? 0 : q_len)) return DENDRITE_EINVAL;
     }
     cudaStream_t s = (cudaStream_t)stream;
     if (p->dtype == DENDRITE_FP8) DENDRITE_TRY(check_not_capturing(s));
@@ -2483,13 +2495,17 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
     bool began = false;
     const int max_ctas = p->sm_count * p->attn_ctas_per_sm;
     PlanCache& pc = p->plan;
-    const bool same_query = pc.valid && pc.q_len == q_len && pc.n_q_heads == n_q_heads && pc.n_trees == n_trees &&
+    const bool same_query = pc.valid && pc.q_len == q_len && pc.n_q_heads == n_q_heads && pc.n_trees == n_trees && pc.cross == cross &&
                             (int32_t)pc.branches.size() == n && std::equal(branches, branches + n, pc.branches.begin()) &&
                             (!parents || std::equal(pc.parents.begin(), pc.parents.end(), parents));
     if (!same_query) {   // (the branches of the cached plan are distinct)
         std::vector<int32_t> o(branches, branches + n);
         std::sort(o.begin(), o.end());
         if (std::adjacent_find(o.begin(), o.end()) != o.end()) return DENDRITE_EINVAL;
+    }
+    if (cross && std::all_of(branches, branches + n, [&](int32_t b) { return p->br[b].len == 0; })) {   // no plan: zeros
+        DENDRITE_CUDA(cudaMemsetAsync(out, 0, (size_t)n * q_len * n_q_heads * p->head_dim * p->elt, s));
+        return DENDRITE_OK;
     }
     const bool hit = same_query && pc.version == p->version;
     // Only appends since the plan was built, and no queried branch reached a
@@ -2615,7 +2631,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
         }
         DENDRITE_CUDA(cudaEventRecord(p->plan_copied[ib], s));
         if (hp.device) DENDRITE_TRY(launch_plan_expand(p, p->d_plan[ib], off, hp.hdr.n_units, hp.hdr.n_segs, s));
-        pc.dev = plan_view(hp, off, p->d_plan[ib], n, q_len, n_q_heads, n_q_heads / p->n_kv);
+        pc.dev = plan_view(hp, off, p->d_plan[ib], n, q_len, n_q_heads, n_q_heads / p->n_kv, cross);
         pc.n_partial_rows = hp.partial_rows;
         pc.valid = true;
         pc.device = hp.device;
@@ -2656,6 +2672,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
         pc.n_q_heads = n_q_heads;
         pc.branches.assign(branches, branches + n);
         pc.n_trees = n_trees;
+        pc.cross = cross;
         pc.parents.assign(parents, parents ? parents + (size_t)n_trees * q_len : nullptr);
         pc.stats.n_segments = (int32_t)hp.segs.size();
         pc.stats.n_units = (int32_t)hp.units.size();
@@ -2803,7 +2820,7 @@ extern "C" int dendrite_tree_attn_decode_noalloc(dendrite_pool* p, const void* Q
         DENDRITE_CUDA(cudaMemcpyAsync(scratch, g_noalloc_host, off[kPlanSections], cudaMemcpyHostToDevice, s));
     }
     AttnArgs a = attn_args(p, 0, Q, out);
-    a.plan = plan_view(hp, off, reinterpret_cast<const char*>(scratch), n, q_len, n_q_heads, n_q_heads / p->n_kv);
+    a.plan = plan_view(hp, off, reinterpret_cast<const char*>(scratch), n, q_len, n_q_heads, n_q_heads / p->n_kv, false);
     a.cut = any_cut(p, branches, n);
     a.part_acc = reinterpret_cast<float*>(scratch + plan_bytes);
     a.part_ml = reinterpret_cast<float2*>(scratch + plan_bytes + acc_bytes);

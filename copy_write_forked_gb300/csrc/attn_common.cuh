@@ -22,7 +22,7 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 // query token j = (sr % (q_len G)) / G and head group g = sr % G; it reads the
 // Q/out row (member, token, kv head, group) and sees positions
 // < len - q_len + j + 1 (a row of a draft tree: < len - q_len, and what its
-// mask adds).
+// mask adds; cross attention: < len).
 // The two divisions use the divisors' fp32 reciprocals (the host limits
 // segment rows to 2^24, so sr converts exactly and the estimate is off by at
 // most one, which one remainder test corrects): integer division by a
@@ -41,7 +41,7 @@ __device__ __forceinline__ AttnRow unit_row(const AttnPlanDev& pl, const AttnUni
     const int32_t mi = div_rcp(sr, RM, pl.rcp_rows_per_member), rem = sr - mi * RM;
     const int32_t j = div_rcp(rem, G, pl.rcp_group), g = rem - j * G;
     const AttnMember M = pl.members[U.mem_off + mi];
-    const int32_t limit = M.len - pl.q_len + (pl.masks ? 0 : j + 1);
+    const int32_t limit = M.len - pl.back + (j + 1) * pl.step;
     return AttnRow{(M.qi * pl.q_len + j) * pl.n_q_heads + U.kv_head * G + g, limit, mi};
 }
 

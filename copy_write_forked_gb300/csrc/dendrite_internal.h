@@ -51,7 +51,7 @@ struct DevMeta {
     // From then on appends clear V behind their branches' ends, and attention over a
     // branch that was rolled back masks it (a weight of zero times NaN is NaN).
     int32_t unclean;
-    int32_t pad;
+    int32_t rows_done;  // CTAs of the current fork onto selected rows that finished
 };
 
 // One sharing segment: blocks [blk_start, blk_start + n_blk) of the table row
@@ -147,6 +147,8 @@ struct AttnPlanDev {
     float rcp_rows_per_member;     // 1 / (q_len G)
     float rcp_group;               // 1 / G
     const uint64_t* masks;         // [n_queried][q_len] drafted tokens each query sees (draft trees), or null
+    int32_t back, step;            // query j of a branch of len rows sees positions < len - back + (j + 1) step:
+                                   // causal q_len, 1; draft trees q_len, 0 (and their masks); cross attention 0, 0
     int32_t packed;                // some unit reads extra tiles (the mma.sync kernel then needs its tile info)
 };
 
@@ -243,6 +245,7 @@ struct PlanCache {
     size_t sec_off[16] = {};         // section offsets of the packed plan
     std::vector<int32_t> parents;    // draft trees the plan's masks were made from (empty: none)
     int32_t n_trees = 0;
+    bool cross = false;              // every query sees every position
     uint64_t version = 0, shape_version = 0;
     int32_t q_len = 0, n_q_heads = 0;
     std::vector<int32_t> branches;

@@ -84,6 +84,7 @@ __global__ void k_init(int32_t* stack, int32_t* refcount, int32_t* holders, int3
         meta->rel_count = 0;
         meta->rel_done = 0;
         meta->unclean = 0;
+        meta->rows_done = 0;
     }
 }
 
@@ -1176,7 +1177,7 @@ int append_launch(dendrite_pool* p, const int32_t* branches, const int32_t* lens
 // points to).
 int check_rotation(dendrite_pool* p, int32_t n, int32_t n_new, const int32_t* parents, int32_t n_trees, const void* K,
                    const void* V, const void* Q, int32_t n_q_heads, void* q_out, const dendrite_rope* rope,
-                   int32_t n_layers, RowsCall& c, std::vector<uint8_t>& depth) {
+                   int32_t n_layers, RowsCall& c, std::vector<uint8_t>& depth, const dendrite_positions* at = nullptr) {
     if (n > p->max_branches) return DENDRITE_EINVAL;   // some would be named twice
     if (!rope || rope->rot_dim < 16 || rope->rot_dim > p->head_dim || rope->rot_dim % 16) return DENDRITE_EINVAL;
     if (rope->interleaved != 0 && rope->interleaved != 1) return DENDRITE_EINVAL;
@@ -1207,6 +1208,25 @@ int check_rotation(dendrite_pool* p, int32_t n, int32_t n_new, const int32_t* pa
         c.n_trees = n_trees;
     } else if (n_trees != 0) {
         return DENDRITE_EINVAL;
+    }
+    if (at) {
+        if (!at->at || ((uintptr_t)at->at & 3) || at->n_axes < 1 || at->n_axes > DENDRITE_MAX_AXES || at->reserved)
+            return DENDRITE_EINVAL;
+        // (strides below 2^47: n, n_new and the axes are below 2^31, and all fits in 64 bits of bytes)
+        int64_t last = 0;
+        const int64_t strides[3] = {at->branch_stride, at->token_stride, at->axis_stride}, counts[3] = {n, n_new, at->n_axes};
+        for (int k = 0; k < 3; ++k) {
+            if (strides[k] < 0 || strides[k] >= (int64_t)1 << 47) return DENDRITE_EINVAL;
+            if (strides[k] && counts[k] - 1 > ((int64_t)1 << 60) / strides[k]) return DENDRITE_ELIMIT;
+            last += strides[k] * (counts[k] - 1);
+        }
+        for (int32_t i = 0; i < rope->rot_dim / 2; ++i)
+            if (at->axis[i] >= at->n_axes) return DENDRITE_EINVAL;
+        if (c.Q) {   // read by every block of rows, while others' queries are written
+            const uintptr_t y = (uintptr_t)q_out, size = (uintptr_t)c.q_layer * n_layers * p->elt;
+            if ((uintptr_t)at->at < y + size && y < (uintptr_t)(at->at + last + 1)) return DENDRITE_EINVAL;
+        }
+        c.at = at;
     }
     c.rope = rope;
     return DENDRITE_OK;
@@ -1476,6 +1496,57 @@ int dendrite_fork(dendrite_pool* p, int32_t parent, int32_t n_children, int32_t*
     return dendrite_fork_batch(p, &parent, &n_children, 1, out_children, stream);
 }
 
+int dendrite_fork_rows(dendrite_pool* p, const int32_t* parents, const int32_t* starts, const int32_t* counts,
+                       int32_t n, const int32_t* rows, int32_t per_head, int32_t* out_children, void* stream) {
+    DENDRITE_TRY(prelude(p));
+    if (p->pending.active) return DENDRITE_EINVAL;
+    if (n < 0 || (n > 0 && (!parents || !starts || !counts || !out_children))) return DENDRITE_EINVAL;
+    if (per_head != 0 && per_head != 1) return DENDRITE_EINVAL;
+    if (n == 0) return DENDRITE_OK;
+    const int32_t bs = p->block_size;
+    ForkRows c{};
+    for (int32_t i = 0; i < n; ++i) {
+        DENDRITE_TRY(check_live(p, parents[i]));
+        const int32_t L = p->br[parents[i]].len;
+        if (starts[i] < 0 || starts[i] > L || counts[i] < 0 || (L == 0 && counts[i] > 0)) return DENDRITE_EINVAL;
+        const int64_t len = (int64_t)starts[i] + counts[i], shared = starts[i] / bs;
+        if ((len + bs - 1) / bs > p->bpb) return DENDRITE_ELIMIT;
+        c.total += counts[i];
+        c.blocks += (len + bs - 1) / bs - shared;
+        c.items += (shared + kShareChunk - 1) / kShareChunk + (len + bs - 1) / bs - shared;
+    }
+    if (n > (int64_t)p->free_handles.size()) return DENDRITE_ELIMIT;
+    if (c.items > INT32_MAX / 2 || c.total > INT32_MAX / 2) return DENDRITE_ELIMIT;
+    if (c.total > 0 && (!rows || ((uintptr_t)rows & 3))) return DENDRITE_EINVAL;
+    cudaStream_t s = (cudaStream_t)stream;
+    DENDRITE_TRY(check_not_capturing(s));
+    std::vector<int32_t> children(n);   // the handles that alloc_handle will hand out
+    for (int32_t i = 0; i < n; ++i) children[i] = p->free_handles[p->free_handles.size() - 1 - i];
+    c.parents = parents;
+    c.starts = starts;
+    c.counts = counts;
+    c.children = children.data();
+    c.n = n;
+    c.rows = rows;
+    c.per_head = per_head != 0;
+    prof_begin(p, T_FORK, s);
+    if (c.items > 0) DENDRITE_TRY(launch_fork_rows(p, c, s));
+    prof_end(p, T_FORK, s);
+    for (int32_t i = 0; i < n; ++i) {
+        // cut from the parent at its last whole shared block, then its own
+        const int32_t h = alloc_handle(p);
+        p->br[h].live = 1;
+        p->br[h].len = starts[i] + counts[i];
+        p->br[h].cut = 0;
+        p->br[h].node = new_node(p, p->br[parents[i]].node, starts[i] / bs * bs, h);
+        p->nodes[p->br[h].node].len = p->br[h].len;
+        out_children[i] = h;
+    }
+    p->version++;
+    p->shape_version++;   // the tree's shape changed, not only lengths
+    return DENDRITE_OK;
+}
+
 int dendrite_append_kv(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n_new, const void* K,
                        const void* V, void* stream) {
     DENDRITE_TRY(prelude(p));
@@ -1531,9 +1602,14 @@ int dendrite_append_layer(dendrite_pool* p, int32_t layer, const void* K, const 
     return DENDRITE_OK;
 }
 
-int dendrite_append_rope(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n_new, const int32_t* parents,
-                         int32_t n_trees, const void* K, const void* V, const void* Q, int32_t n_q_heads, void* q_out,
-                         const dendrite_rope* rope, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// An append whose rows turn: by length, by the depths of draft trees, or by given positions.
+int append_turned(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n_new, const int32_t* parents,
+                  int32_t n_trees, const dendrite_positions* at, const void* K, const void* V, const void* Q,
+                  int32_t n_q_heads, void* q_out, const dendrite_rope* rope, void* stream) {
     DENDRITE_TRY(prelude(p));
     if (p->dtype == DENDRITE_TURBO) return DENDRITE_EDTYPE;
     if (p->pending.active) return DENDRITE_EINVAL;
@@ -1542,7 +1618,7 @@ int dendrite_append_rope(dendrite_pool* p, const int32_t* branches, int32_t n, i
     if (!K || !V || (((uintptr_t)K | (uintptr_t)V) & 15)) return DENDRITE_EINVAL;
     RowsCall c{};
     std::vector<uint8_t> depth;
-    DENDRITE_TRY(check_rotation(p, n, n_new, parents, n_trees, K, V, Q, n_q_heads, q_out, rope, p->n_layers, c, depth));
+    DENDRITE_TRY(check_rotation(p, n, n_new, parents, n_trees, K, V, Q, n_q_heads, q_out, rope, p->n_layers, c, depth, at));
     int64_t touched = 0;
     DENDRITE_TRY(append_check(p, branches, n, n_new, &touched));
     cudaStream_t s = (cudaStream_t)stream;
@@ -1556,9 +1632,10 @@ int dendrite_append_rope(dendrite_pool* p, const int32_t* branches, int32_t n, i
     return DENDRITE_OK;
 }
 
-int dendrite_append_layer_rope(dendrite_pool* p, int32_t layer, const int32_t* parents, int32_t n_trees,
-                               const void* K, const void* V, const void* Q, int32_t n_q_heads, void* q_out,
-                               const dendrite_rope* rope, void* stream) {
+// The same for one layer of the pending append.
+int append_layer_turned(dendrite_pool* p, int32_t layer, const int32_t* parents, int32_t n_trees,
+                        const dendrite_positions* at, const void* K, const void* V, const void* Q, int32_t n_q_heads,
+                        void* q_out, const dendrite_rope* rope, void* stream) {
     DENDRITE_TRY(prelude(p));
     if (p->dtype == DENDRITE_TURBO) return DENDRITE_EDTYPE;
     PendingAppend& pa = p->pending;
@@ -1567,13 +1644,43 @@ int dendrite_append_layer_rope(dendrite_pool* p, int32_t layer, const int32_t* p
     const int32_t n = (int32_t)pa.branches.size();
     RowsCall c{};
     std::vector<uint8_t> depth;
-    DENDRITE_TRY(check_rotation(p, n, pa.n_new, parents, n_trees, K, V, Q, n_q_heads, q_out, rope, 1, c, depth));
+    DENDRITE_TRY(check_rotation(p, n, pa.n_new, parents, n_trees, K, V, Q, n_q_heads, q_out, rope, 1, c, depth, at));
     DENDRITE_TRY(check_not_capturing((cudaStream_t)stream));
     DENDRITE_TRY(append_launch(p, pa.branches.data(), pa.lens.data(), n, pa.n_new, pa.touched, true, K, V, layer, 1, 0,
                                (cudaStream_t)stream, /*meta=*/false, &c));
     pa.layer_done[layer] = 1;
     if (++pa.n_done == p->n_layers) pa.active = false;
     return DENDRITE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dendrite_append_rope(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n_new, const int32_t* parents,
+                         int32_t n_trees, const void* K, const void* V, const void* Q, int32_t n_q_heads, void* q_out,
+                         const dendrite_rope* rope, void* stream) {
+    return append_turned(p, branches, n, n_new, parents, n_trees, nullptr, K, V, Q, n_q_heads, q_out, rope, stream);
+}
+
+int dendrite_append_layer_rope(dendrite_pool* p, int32_t layer, const int32_t* parents, int32_t n_trees,
+                               const void* K, const void* V, const void* Q, int32_t n_q_heads, void* q_out,
+                               const dendrite_rope* rope, void* stream) {
+    return append_layer_turned(p, layer, parents, n_trees, nullptr, K, V, Q, n_q_heads, q_out, rope, stream);
+}
+
+int dendrite_append_rope_at(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t n_new,
+                            const dendrite_positions* at, const void* K, const void* V, const void* Q,
+                            int32_t n_q_heads, void* q_out, const dendrite_rope* rope, void* stream) {
+    if (p && !p->poisoned && !at) return DENDRITE_EINVAL;
+    return append_turned(p, branches, n, n_new, nullptr, 0, at, K, V, Q, n_q_heads, q_out, rope, stream);
+}
+
+int dendrite_append_layer_rope_at(dendrite_pool* p, int32_t layer, const dendrite_positions* at, const void* K,
+                                  const void* V, const void* Q, int32_t n_q_heads, void* q_out,
+                                  const dendrite_rope* rope, void* stream) {
+    if (p && !p->poisoned && !at) return DENDRITE_EINVAL;
+    return append_layer_turned(p, layer, nullptr, 0, at, K, V, Q, n_q_heads, q_out, rope, stream);
 }
 
 int dendrite_pool_layers(dendrite_pool* p, int32_t* n_layers) {

@@ -104,7 +104,10 @@ struct RowsArgs {
     int64_t kv_layer, q_layer;   // elements
     int64_t pool_layer;          // bytes
     DevMeta* meta;
+    const int32_t* at;           // given positions, or null
+    int64_t at_branch, at_token, at_axis;
     uint64_t freq[128];          // turns per position, as a fraction of 2^64
+    uint8_t axis[128];           // given positions: the axis that pair i turns by
 };
 
 // Eight consecutive elements as they are; input rows are read once, through L2
@@ -336,6 +339,7 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                     load(src + c1, y[u]);
                 }
                 if (ROPE && it0 == 0) {   // the angles, while the first rows are on their way
+                    const int32_t* at = a.at + i * a.at_branch + tok * a.at_token;
                     const int32_t pos = L + (a.has_depth ? byte_of(args, 3 * (int64_t)n, (int64_t)(a.one_tree ? 0 : i) * a.n_new + tok) : tok);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
@@ -343,7 +347,11 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                         const bool on = a.interleaved ? (q < 4 ? turn0 : turn1) : turn0;
                         cs[q] = 1.f;
                         sn[q] = 0.f;
-                        if (on) sincos_turns(a.freq[pair & 127] * (uint64_t)(uint32_t)pos, a.m, sn[q], cs[q]);
+                        if (on) {
+                            // (a negative position's product wraps to the negative angle)
+                            const int64_t x = a.at ? (int64_t)__ldg(at + a.axis[pair & 127] * a.at_axis) : (int64_t)pos;
+                            sincos_turns(a.freq[pair & 127] * (uint64_t)x, a.m, sn[q], cs[q]);
+                        }
                     }
                 }
 #pragma unroll
@@ -604,6 +612,158 @@ __global__ void __launch_bounds__(128) k_keep_rows(const __grid_constant__ A arg
     }
 }
 
+// ---------------------------------------------------- forks onto selected rows
+// args, per child (n of each): child, parent, rows kept at the front, length,
+// parent's length, first entry of its list, first block off the free stack,
+// prefix of its items.  An item is a chunk of kShareChunk table entries that
+// the child shares with its parent (copied, a reference each), or one block of
+// its own: CTA x takes items x, x + gridDim.x, ..., for layer y and the heads
+// z, z + gridDim.z, ...  A block's id follows from the free stack's top as it
+// was before the call (every CTA reads it; the last one to finish lowers it), so
+// that nothing waits for a metadata kernel: table entry, count and rows are
+// written by the same CTA.
+//
+// Rows are stored bits, moved 16 bytes a thread with the rows' sources (block
+// and slot, looked up once per row and head into shared memory) ahead of them;
+// a tile's writes are contiguous, its reads are whole rows anywhere.
+struct ForkRowsArgs {
+    int32_t n, bpb, n_kv, n_blocks, uniform, n_items, blocks;
+    int32_t k_words, v_words, k_shift, v_shift;   // 16-byte words of a row, and the power of two at or above
+    int32_t fp8, clear_v, per_head;
+    int64_t k_tile, v_tile, k_layer, v_layer;     // bytes
+    const int32_t* rows;
+    int64_t rows_layer;
+    const int32_t* stack;
+    int32_t* table;
+    int32_t* refcount;
+    char* kp;
+    char* vp;
+    DevMeta* meta;
+};
+
+constexpr int kForkRowsThreads = 256;
+
+template <typename A>
+__global__ void __launch_bounds__(kForkRowsThreads, 6) k_fork_rows(const __grid_constant__ A args, const __grid_constant__ ForkRowsArgs a) {
+    pdl_wait();
+    constexpr int bs = kBlockSize, NT = kForkRowsThreads, U = 4;
+    __shared__ int32_t src_blk[64 * bs];
+    __shared__ uint8_t src_slot[64 * bs];
+    const int32_t t = threadIdx.x;
+    const int64_t n = a.n;
+    const int32_t top = a.meta->top;
+    const bool unclean = a.clear_v && a.meta->unclean;
+    if (__syncthreads_or(a.meta->status)) return;
+    if (a.blocks > top) {   // every CTA finds the same: nothing is written
+        if (t == 0) atomicCAS(&a.meta->status, 0, DENDRITE_ENOMEM);
+        return;
+    }
+    const bool lead = blockIdx.y == 0 && blockIdx.z == 0;
+    for (int32_t item = blockIdx.x; item < a.n_items; item += gridDim.x) {
+        int32_t first;
+        const int32_t i = find_branch(args, 7 * n, a.n, item, a.uniform, first);
+        const int32_t child = args[i], parent = args[n + i], start = args[2 * n + i], len = args[3 * n + i];
+        const int32_t shared = start / bs, chunks = (shared + kShareChunk - 1) / kShareChunk;
+        const int32_t* from = a.table + (int64_t)parent * a.bpb;
+        int32_t* to = a.table + (int64_t)child * a.bpb;
+        if (item - first < chunks) {
+            const int32_t e = (item - first) * kShareChunk + t;
+            if (lead && t < kShareChunk && e < shared) {
+                const int32_t blk = from[e];
+                to[e] = blk;
+                if ((uint32_t)blk < (uint32_t)a.n_blocks) atomicAdd(a.refcount + blk, 1);
+                else atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
+            }
+            continue;
+        }
+        const int32_t j = item - first - chunks;          // owned block
+        const int32_t dst = a.stack[top - 1 - (args[6 * n + i] + j)];
+        if ((uint32_t)dst >= (uint32_t)a.n_blocks) {
+            if (t == 0) atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
+            continue;
+        }
+        if (lead && t == 0) {
+            to[shared + j] = dst;
+            a.refcount[dst] = 1;
+        }
+        const int32_t p0 = (shared + j) * bs, nt = min(bs, len - p0);
+        // where each row comes from (heads z, z + gridDim.z, ... of the tile)
+        const int32_t parent_len = args[4 * n + i];
+        const int32_t* list = a.rows + blockIdx.y * a.rows_layer;
+        const int32_t heads = (a.n_kv - (int)blockIdx.z + (int)gridDim.z - 1) / (int)gridDim.z;
+        const int32_t lists = a.per_head ? heads : 1;
+        __syncthreads();   // the last item's sources have been read
+        for (int32_t e = t; e < lists * bs; e += NT) {
+            const int32_t s = e % bs, p = p0 + s;
+            int32_t blk = -1, r = p;
+            if (s < nt) {
+                if (p >= start) {
+                    const int64_t k = (int64_t)args[5 * n + i] + (p - start);
+                    r = __ldg(list + (a.per_head ? k * a.n_kv + (int)blockIdx.z + (e / bs) * (int)gridDim.z : k));
+                }
+                if ((uint32_t)r < (uint32_t)parent_len) {
+                    blk = __ldcg(from + r / bs);
+                    if ((uint32_t)blk >= (uint32_t)a.n_blocks) {
+                        blk = -1;
+                        atomicCAS(&a.meta->status, 0, DENDRITE_ECORRUPT);
+                    }
+                } else {
+                    atomicCAS(&a.meta->status, 0, DENDRITE_EINVAL);
+                }
+            }
+            src_blk[e] = blk;
+            src_slot[e] = (uint8_t)(r & (bs - 1));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const int32_t words = v ? a.v_words : a.k_words, shift = v ? a.v_shift : a.k_shift;
+            const int64_t tile = v ? a.v_tile : a.k_tile;
+            char* pool = v ? a.vp + blockIdx.y * a.v_layer : a.kp + blockIdx.y * a.k_layer;
+            const int32_t w = t & ((1 << shift) - 1), step = NT >> shift, n_rows = heads * bs;
+            if (w < words) {
+                for (int32_t r0 = t >> shift; r0 < n_rows; r0 += U * step) {
+                    uint4 x[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int32_t r = r0 + u * step;
+                        if (r >= n_rows) continue;
+                        const int32_t e = a.per_head ? r : r % bs, h = (int)blockIdx.z + (r / bs) * (int)gridDim.z;
+                        const int32_t blk = src_blk[e], slot = src_slot[e];
+                        x[u] = make_uint4(0u, 0u, 0u, 0u);
+                        if (blk >= 0)
+                            x[u] = __ldcg(reinterpret_cast<const uint4*>(pool + ((int64_t)blk * a.n_kv + h) * tile) +
+                                          slot * words + (a.fp8 ? w ^ (slot & 7) : w));
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int32_t r = r0 + u * step, s = r % bs;
+                        // (V behind the end stays as it is, or becomes finite)
+                        if (r >= n_rows || (s >= nt && !(v && unclean))) continue;
+                        const int32_t h = (int)blockIdx.z + (r / bs) * (int)gridDim.z;
+                        reinterpret_cast<uint4*>(pool + ((int64_t)dst * a.n_kv + h) * tile)[s * words + (a.fp8 ? w ^ (s & 7) : w)] = x[u];
+                    }
+                }
+            }
+            if (a.fp8)
+                for (int32_t r = t; r < n_rows; r += NT) {
+                    const int32_t s = r % bs, e = a.per_head ? r : s, h = (int)blockIdx.z + (r / bs) * (int)gridDim.z;
+                    if (s < nt && src_blk[e] >= 0)
+                        pool[((int64_t)dst * a.n_kv + h) * tile + bs * kFp8Dim + s] =
+                            pool[((int64_t)src_blk[e] * a.n_kv + h) * tile + bs * kFp8Dim + src_slot[e]];
+                }
+        }
+    }
+    if (t == 0) {
+        __threadfence();
+        const int32_t all = (int32_t)(gridDim.x * gridDim.y * gridDim.z);
+        if (atomicAdd(&a.meta->rows_done, 1) == all - 1) {
+            a.meta->rows_done = 0;
+            a.meta->top = top - a.blocks;
+        }
+    }
+}
+
 // Calls `go` with the argument words: as kernel parameters, or staged.
 template <typename Fill, typename Go>
 int with_words(dendrite_pool* p, size_t words, cudaStream_t s, Fill fill, Go go) {
@@ -634,6 +794,70 @@ unsigned head_splits(const dendrite_pool* p, int64_t tiles, int64_t most, int pe
 }  // namespace
 
 namespace dendrite {
+
+int launch_fork_rows(dendrite_pool* p, const ForkRows& c, cudaStream_t s) {
+    const int32_t bs = p->block_size;
+    const int64_t tiles = p->num_blocks * p->n_kv;
+    ForkRowsArgs a{};
+    a.n = c.n;
+    a.bpb = p->bpb;
+    a.n_kv = p->n_kv;
+    a.n_blocks = (int32_t)p->num_blocks;
+    a.n_items = (int32_t)c.items;
+    a.blocks = (int32_t)c.blocks;
+    a.fp8 = p->dtype == DENDRITE_FP8;
+    a.clear_v = p->dtype == DENDRITE_BF16;
+    a.per_head = c.per_head;
+    a.k_tile = (int64_t)p->layer_bytes / tiles;
+    a.v_tile = (int64_t)p->layer_bytes_v / tiles;
+    a.k_layer = (int64_t)p->layer_bytes;
+    a.v_layer = (int64_t)p->layer_bytes_v;
+    a.k_words = (int32_t)((a.k_tile - (a.fp8 ? bs : 0)) / bs / 16);
+    a.v_words = (int32_t)((a.v_tile - (a.fp8 ? bs : 0)) / bs / 16);
+    while (1 << a.k_shift < a.k_words) ++a.k_shift;
+    while (1 << a.v_shift < a.v_words) ++a.v_shift;
+    a.rows = c.rows;
+    a.rows_layer = c.per_head ? c.total * p->n_kv : 0;
+    a.stack = p->d_stack;
+    a.table = p->d_table;
+    a.refcount = p->d_refcount;
+    a.kp = static_cast<char*>(p->d_k);
+    a.vp = static_cast<char*>(p->d_v);
+    a.meta = p->d_meta;
+    auto items = [&](int32_t i) {
+        const int32_t shared = c.starts[i] / bs;
+        return (shared + kShareChunk - 1) / kShareChunk + (c.starts[i] + c.counts[i] + bs - 1) / bs - shared;
+    };
+    int32_t uniform = items(0);
+    for (int32_t i = 1; i < c.n; ++i)
+        if (items(i) != uniform) uniform = 0;
+    a.uniform = uniform;
+    const size_t n = c.n;
+    auto fill = [&](int32_t* w) {
+        int32_t list = 0, block = 0, item = 0;
+        for (size_t i = 0; i < n; ++i) {
+            w[i] = c.children[i];
+            w[n + i] = c.parents[i];
+            w[2 * n + i] = c.starts[i];
+            w[3 * n + i] = c.starts[i] + c.counts[i];
+            w[4 * n + i] = p->br[c.parents[i]].len;
+            w[5 * n + i] = list;
+            w[6 * n + i] = block;
+            w[7 * n + i] = item;
+            list += c.counts[i];
+            block += (c.starts[i] + c.counts[i] + bs - 1) / bs - c.starts[i] / bs;
+            item += items((int32_t)i);
+        }
+    };
+    // as many CTAs as run at once (each adds one to the count of the finished)
+    const int64_t most = 6 * (int64_t)p->sm_count;
+    const unsigned z = head_splits(p, c.items * p->n_layers, p->n_kv, 6);
+    const dim3 grid((unsigned)std::max<int64_t>(1, std::min(c.items, most / (p->n_layers * (int64_t)z))), (unsigned)p->n_layers, z);
+    return with_words(p, 8 * n, s, fill, [&](auto args) -> int {
+        DENDRITE_CUDA(launch_pdl(k_fork_rows<decltype(args)>, grid, dim3(kForkRowsThreads), 0, s, args, a));
+        return DENDRITE_OK;
+    });
+}
 
 // Captured calls would be replayed with the lengths, tables and staged
 // arguments of the capture: refused.
@@ -741,6 +965,13 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* stage
         }
         a.has_depth = c.depth != nullptr;
         a.one_tree = c.n_trees == 1;
+        if (c.at) {
+            a.at = c.at->at;
+            a.at_branch = c.at->branch_stride;
+            a.at_token = c.at->token_stride;
+            a.at_axis = c.at->axis_stride;
+            std::memcpy(a.axis, c.at->axis, sizeof(a.axis));
+        }
     }
     int32_t uniform = -1;
     for (int32_t i = 0; i < n && uniform != 0; ++i) {

@@ -33,6 +33,7 @@ struct RowsCall {
     const dendrite_rope* rope; // null: rows are stored as they are
     const uint8_t* depth;      // [n_trees][n_new] draft tree depths; null: token j is at length + j
     int32_t n_trees;
+    const dendrite_positions* at;   // positions given with the rows; null: by length (and depth)
 };
 
 // The kernel's argument words: how many the caller has to stage (0: they go as
@@ -41,6 +42,21 @@ struct RowsCall {
 size_t staged_rows_words(const RowsCall& c);
 void fill_rows_words(const RowsCall& c, int32_t block_size, int32_t* words);
 int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* staged, cudaStream_t s);
+
+// Children forked onto selected rows (one launch; see k_fork_rows).  Child i
+// shares the parent's first starts[i] / 16 blocks and owns the rows from there
+// to its length starts[i] + counts[i].
+struct ForkRows {
+    const int32_t *parents, *starts, *counts, *children;
+    int32_t n;
+    const int32_t* rows;   // device: [sum counts], or [n_layers][sum counts][n_kv] where per_head
+    bool per_head;
+    int64_t total;         // sum counts
+    int64_t blocks;        // blocks taken off the free stack
+    int64_t items;         // (child, owned block) pairs and chunks of shared entries
+};
+constexpr int32_t kShareChunk = 256;   // shared table entries an item copies
+int launch_fork_rows(dendrite_pool* p, const ForkRows& c, cudaStream_t s);
 
 // Checks n_trees (1 or n) trees of t drafted tokens (parents[j] in [-1, j)).
 int check_trees(const int32_t* parents, int32_t n_trees, int32_t n, int32_t t);

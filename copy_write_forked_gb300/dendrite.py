@@ -29,6 +29,7 @@ FP32, BF16, TURBO, FP8 = 0, 1, 2, 3
 TURBO_KEY_BYTES, TURBO_VALUE_BYTES = 96, 64
 FP8_TILE_BYTES = 16 * 128 + 16   # 16 slots of 128 codes, then their exponent bytes
 MAX_DRAFT = 64
+MAX_AXES = 4
 ROPE_SCALINGS = ("none", "linear", "ntk", "yarn", "bands")
 
 _LIB = None
@@ -54,6 +55,11 @@ class _Opts(ctypes.Structure):
 class _Rope(ctypes.Structure):
     _fields_ = [("rot_dim", _i32), ("interleaved", _i32), ("reserved", _i32 * 2), ("scale", ctypes.c_double),
                 ("inv_freq", ctypes.c_double * 128)]
+
+
+class _Positions(ctypes.Structure):
+    _fields_ = [("at", _p), ("branch_stride", _i64), ("token_stride", _i64), ("axis_stride", _i64), ("n_axes", _i32),
+                ("reserved", _i32), ("axis", ctypes.c_uint8 * 128)]
 
 
 class _PlanStats(ctypes.Structure):
@@ -85,6 +91,11 @@ _SIGS = {
                            ctypes.c_double, ctypes.c_double],
     "dendrite_append_rope": [_p, _pi32, _i32, _i32, _pi32, _i32, _p, _p, _p, _i32, _p, _p, _p],
     "dendrite_append_layer_rope": [_p, _i32, _pi32, _i32, _p, _p, _p, _i32, _p, _p, _p],
+    "dendrite_append_rope_at": [_p, _pi32, _i32, _i32, ctypes.POINTER(_Positions), _p, _p, _p, _i32, _p, _p, _p],
+    "dendrite_append_layer_rope_at": [_p, _i32, ctypes.POINTER(_Positions), _p, _p, _p, _i32, _p, _p, _p],
+    "dendrite_fork_rows": [_p, _pi32, _pi32, _pi32, _i32, _p, _i32, _pi32, _p],
+    "dendrite_tree_attn_cross": [_p, _i32, _p, _i32, _i32, _pi32, _i32, _p, _p],
+    "dendrite_verify_draft": [_p, _i32, _i32, _pi32, _i32, _p, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p],
     "dendrite_tree_attn_draft": [_p, _i32, _p, _i32, _i32, _pi32, _i32, _pi32, _i32, _p, _p],
     "dendrite_accept_draft": [_p, _pi32, _i32, _i32, _pi32, _pi32, _p],
     "dendrite_read_kv": [_p, _i32, _pi32, _pi32, _pi32, _i32, _p, _p, _p],
@@ -194,12 +205,14 @@ class Rope:
     ``factor``; the last two from ``original_len`` positions, with a ramp
     between ``turns_low`` and ``turns_high`` turns, by default 1 and 32 for
     "yarn", 1 and 4 for "bands").  ``inv_freq``: radians per position of each
-    pair instead; ``scale``: the factor on turned elements."""
+    pair instead; ``scale``: the factor on turned elements.  ``axes``: the axis
+    that each pair turns by, of up to 4 (``[0] * 16 + [1] * 24 + [2] * 24``: time,
+    height and width of images and clips); the appends then take ``positions``."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
                  factor: float = 1.0, original_len: float = 0.0, turns_low: float = 1.0,
                  turns_high: Optional[float] = None, inv_freq: Optional[Sequence[float]] = None,
-                 scale: Optional[float] = None):
+                 scale: Optional[float] = None, axes: Optional[Sequence[int]] = None):
         if scaling not in ROPE_SCALINGS:
             raise DendriteError(-1, f"scaling {scaling!r}")
         self._c = _Rope()
@@ -214,6 +227,13 @@ class Rope:
                 self._c.inv_freq[i] = float(f)
         if scale is not None:
             self._c.scale = float(scale)
+        self.n_axes = 1
+        self._axis = bytes(128)
+        if axes is not None:
+            if len(axes) != self._c.rot_dim // 2 or min(axes) < 0 or max(axes) >= MAX_AXES:
+                raise DendriteError(-1, "axes: one of 0 .. 3 for each pair")
+            self.n_axes = max(axes) + 1
+            self._axis = bytes(axes).ljust(128, b"\0")
         self._ptr = ctypes.addressof(self._c)
 
     @property
@@ -316,6 +336,33 @@ class Pool:
             k += n
         return res
 
+    def fork_rows(self, parents: Sequence[int], starts: Sequence[int], counts: Sequence[int], rows: Optional[torch.Tensor],
+                  stream=None) -> List[int]:
+        """One child per entry of ``parents`` (any branch any number of times), holding that
+        branch's first ``starts[i]`` rows (their whole blocks shared) and ``counts[i]`` listed ones
+        (copied).  ``rows``: int32 CUDA tensor, the children's lists one after the other,
+        ``[sum counts]``, or ``[sum counts][n_kv_heads]`` with a list of each head's own (layers
+        first in a pool of several); any of the parent's row numbers, in any order."""
+        n = len(parents)
+        if len(starts) != n or len(counts) != n:
+            raise DendriteError(-1, "parents / starts / counts length")
+        total, heads = sum(counts), 0
+        if rows is not None:
+            if not rows.is_cuda or rows.dtype != torch.int32 or not rows.is_contiguous() or rows.get_device() != self._dev:
+                raise DendriteError(-1, f"rows must be a contiguous int32 CUDA tensor on cuda:{self._dev}")
+            each = (total, self.n_kv_heads) if self.n_layers == 1 else (self.n_layers, total, self.n_kv_heads)
+            if rows.shape == each:
+                heads = 1
+            elif rows.shape != (total,):
+                raise DendriteError(-1, f"rows shape {tuple(rows.shape)}")
+            if stream is not None:
+                self._other(stream, rows)
+        pa, sa, ca = _arr(parents), _arr(starts), _arr(counts)
+        out = array.array("i", bytes(4 * max(1, n)))
+        _check(lib().dendrite_fork_rows(self._h, _ptr(pa), _ptr(sa), _ptr(ca), n, rows.data_ptr() if total > 0 and rows is not None else None,
+                                        heads, _ptr(out), _stream_ptr(stream, self._dev)), "fork_rows")
+        return out.tolist()[:n]
+
     def fork_each(self, parents: Sequence[int], stream=None) -> List[int]:
         """One child per parent (dendrite_fork_batch with every count 1): the
         children's handles, in the parents' order."""
@@ -346,14 +393,14 @@ class Pool:
             t.record_stream(stream)
         return stream
 
-    def _output(self, shape, stream) -> torch.Tensor:
+    def _output(self, shape, stream, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
         """A new output of a call on ``stream``: that stream's memory (work queued on the current
         one may still use what is free there), kept for the current one too."""
         other = self._other(stream)
         if other is None:
-            return torch.empty(shape, dtype=self.dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
         with torch.cuda.stream(other):
-            out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            out = torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
         out.record_stream(torch.cuda.current_stream(self._dev))
         return out
 
@@ -427,20 +474,50 @@ class Pool:
         out = self._out(Q, out, stream)
         return Q.data_ptr(), nq, out
 
+    def _positions(self, positions, rope, parents, n, n_new, stream) -> Optional[_Positions]:
+        """Given positions as dendrite_positions, or None where they follow from the length."""
+        if positions is None:
+            if rope.n_axes > 1:
+                raise DendriteError(-1, "a rope of several axes needs positions")
+            return None
+        if parents is not None:
+            raise DendriteError(-1, "positions and parents: the positions hold the depths")
+        t = positions
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.get_device() != self._dev:
+            raise DendriteError(-1, f"positions must be an int32 CUDA tensor on cuda:{self._dev}")
+        shape = t.shape
+        if shape != (n, n_new, rope.n_axes) and (rope.n_axes != 1 or shape != (n, n_new)):
+            raise DendriteError(-1, f"positions shape {tuple(shape)}")
+        if stream is not None:
+            self._other(stream, t)
+        st = t.stride()
+        c = _Positions(t.data_ptr(), st[0], st[1], st[2] if len(st) == 3 else 1, rope.n_axes, 0)
+        ctypes.memmove(c.axis, rope._axis, 128)
+        return c
+
     def append_rope(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, rope: Rope,
                     Q: Optional[torch.Tensor] = None, parents=None, out: Optional[torch.Tensor] = None,
-                    stream=None) -> Optional[torch.Tensor]:
+                    stream=None, positions: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
         """:meth:`append_kv` with K turned by its positions; Q
         ``[n_branches][n_new][n_q_heads][head_dim]`` (layers first in a pool of
         several) is turned too and returned (``out`` may be Q).  ``parents``:
         the new tokens are draft trees (int32 ``[n_new]`` for every branch or
-        ``[n_branches][n_new]``, -1 or an earlier index), token j at its depth."""
+        ``[n_branches][n_new]``, -1 or an earlier index), token j at its depth.
+        ``positions``: the tokens' positions instead, an int32 CUDA tensor
+        ``[n_branches][n_new][axes of the rope]`` (``[n_branches][n_new]`` for one
+        axis) of any strides."""
         ks = K.shape
         nb, n_new = len(branches), ks[-3] if len(ks) >= 4 else 0
         lead = () if self.n_layers == 1 else (self.n_layers,)
         qp, nq, out = self._rotated(K, V, rope, Q, out, lead, nb, n_new, stream)
-        keep, pp, nt = _trees(parents, nb, n_new)
+        at = self._positions(positions, rope, parents, nb, n_new, stream)
         ba = _arr(branches)
+        if at is not None:
+            _check(lib().dendrite_append_rope_at(self._h, _ptr(ba), nb, n_new, at, K.data_ptr(), V.data_ptr(), qp, nq,
+                                                 out.data_ptr() if qp is not None else None, rope._ptr,
+                                                 _stream_ptr(stream, self._dev)), "append_rope")
+            return out
+        keep, pp, nt = _trees(parents, nb, n_new)
         _check(lib().dendrite_append_rope(self._h, _ptr(ba), nb, n_new, pp, nt, K.data_ptr(), V.data_ptr(), qp, nq,
                                           out.data_ptr() if qp is not None else None, rope._ptr,
                                           _stream_ptr(stream, self._dev)), "append_rope")
@@ -448,10 +525,16 @@ class Pool:
 
     def append_layer_rope(self, layer: int, K: torch.Tensor, V: torch.Tensor, rope: Rope,
                           Q: Optional[torch.Tensor] = None, parents=None, out: Optional[torch.Tensor] = None,
-                          stream=None) -> Optional[torch.Tensor]:
+                          stream=None, positions: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
         """:meth:`append_layer` with the rotation of :meth:`append_rope`."""
         nb, n_new = (K.shape[0], K.shape[1]) if K.dim() == 4 else (0, 0)
         qp, nq, out = self._rotated(K, V, rope, Q, out, (), nb, n_new, stream)
+        at = self._positions(positions, rope, parents, nb, n_new, stream)
+        if at is not None:
+            _check(lib().dendrite_append_layer_rope_at(self._h, int(layer), at, K.data_ptr(), V.data_ptr(), qp, nq,
+                                                       out.data_ptr() if qp is not None else None, rope._ptr,
+                                                       _stream_ptr(stream, self._dev)), "append_layer_rope")
+            return out
         keep, pp, nt = _trees(parents, nb, n_new)
         _check(lib().dendrite_append_layer_rope(self._h, int(layer), pp, nt, K.data_ptr(), V.data_ptr(), qp, nq,
                                                 out.data_ptr() if qp is not None else None, rope._ptr,
@@ -478,6 +561,69 @@ class Pool:
                                               len(branches), pp, nt, out.data_ptr(), _stream_ptr(stream, self._dev)),
                "tree_attn_draft")
         return out
+
+    def tree_attn_cross(self, Q: torch.Tensor, branches: Sequence[int], out: Optional[torch.Tensor] = None,
+                        stream=None, layer: int = 0) -> torch.Tensor:
+        """Cross attention: Q ``[n_branches][q_len][n_q_heads][head_dim]``, every query sees every
+        row of its branch (another sequence, of any length; zeros where it has none)."""
+        qs, out = self._query(Q, len(branches), out, stream)
+        ba = _arr(branches)
+        _check(lib().dendrite_tree_attn_cross(self._h, int(layer), Q.data_ptr(), qs[2], qs[1], _ptr(ba), len(branches),
+                                              out.data_ptr(), _stream_ptr(stream, self._dev)), "tree_attn_cross")
+        return out
+
+    def _plain(self, t, name: str, dtype: torch.dtype, shape) -> None:
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != self._dev or not t.is_contiguous() or t.shape != shape:
+            raise DendriteError(-1, f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{self._dev}")
+
+    def _vocab_rows(self, t, name: str, n: int, rows: int, dtype: torch.dtype, vocab: int) -> int:
+        """The row stride of [n][rows][vocab] probabilities whose rows follow one another evenly."""
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != self._dev or t.shape != (n, rows, vocab):
+            raise DendriteError(-1, f"{name} must be a {dtype} tensor {(n, rows, vocab)} on cuda:{self._dev}")
+        a, b, c = t.stride()
+        step = b if rows > 1 else a if n > 1 else vocab
+        if (vocab > 1 and c != 1) or (n > 1 and rows > 1 and a != rows * b):
+            raise DendriteError(-1, f"{name} strides {t.stride()}")
+        return max(step, vocab) if n * rows == 1 else step
+
+    def verify_draft(self, tokens: torch.Tensor, target: torch.Tensor, parents, accept: torch.Tensor, sample: torch.Tensor,
+                     draft: Optional[torch.Tensor] = None, out: Optional[Tuple[torch.Tensor, torch.Tensor, torch.Tensor]] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """Verifies drafted tokens (int32 ``[n][n_draft]``, trees as ``parents`` tells) against the
+        target's probabilities ``[n][1 + n_draft][vocab]`` (fp32 or bf16; row 0 after the last
+        accepted token, row 1 + j after node j), with ``accept`` ``[n][n_draft]`` and ``sample``
+        ``[n]`` uniform in [0, 1) (fp32).  ``draft``: what each node's children were drawn from,
+        ``[n][n_draft][vocab]`` (row 0, rows 1 + j of nodes but the last); None: certain drafts.
+        Returns int32 (path ``[n][n_draft]``, padded with -1, its length ``[n]``, next token ``[n]``);
+        ``accept_draft`` takes ``[p[:k] for p, k in zip(path.tolist(), length.tolist())]``."""
+        if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2 or not isinstance(target, torch.Tensor) or target.dim() != 3:
+            raise DendriteError(-1, "tokens must be [n][n_draft], target [n][1 + n_draft][vocab]")
+        n, t = tokens.shape
+        self._plain(tokens, "tokens", torch.int32, (n, t))
+        self._plain(accept, "accept", torch.float32, (n, t))
+        self._plain(sample, "sample", torch.float32, (n,))
+        if target.dtype not in (torch.float32, torch.bfloat16):
+            raise DendriteError(-5, f"target dtype {target.dtype}")
+        vocab = target.shape[2]
+        ps = self._vocab_rows(target, "target", n, 1 + t, target.dtype, vocab)
+        qs = 0 if draft is None else self._vocab_rows(draft, "draft", n, t, target.dtype, vocab)
+        keep, pp, nt = _trees(parents, n, t)
+        if out is None:
+            path = torch.empty(n, t, dtype=torch.int32, device=self.device) if stream is None else self._output((n, t), stream, torch.int32)
+            size, token = (torch.empty(n, dtype=torch.int32, device=self.device) if stream is None else self._output((n,), stream, torch.int32)
+                           for _ in range(2))
+        else:
+            path, size, token = out
+            self._plain(path, "out[0]", torch.int32, (n, t))
+            self._plain(size, "out[1]", torch.int32, (n,))
+            self._plain(token, "out[2]", torch.int32, (n,))
+        if stream is not None:
+            self._other(stream, tokens, target, accept, sample, path, size, token, *(() if draft is None else (draft,)))
+        _check(lib().dendrite_verify_draft(self._h, n, t, pp, nt, tokens.data_ptr(), vocab, _DT[target.dtype], target.data_ptr(), ps,
+                                           None if draft is None else draft.data_ptr(), qs, accept.data_ptr(), sample.data_ptr(),
+                                           path.data_ptr(), size.data_ptr(), token.data_ptr(), _stream_ptr(stream, self._dev)),
+               "verify_draft")
+        return path, size, token
 
     def accept_draft(self, branches: Sequence[int], n_draft: int, keep: Sequence[Sequence[int]], stream=None) -> None:
         """Of each branch's last ``n_draft`` tokens keep the nodes ``keep[i]``

@@ -207,6 +207,34 @@ int dendrite_fork_batch(dendrite_pool* pool, const int32_t* parents, const int32
                         int32_t n_parents, int32_t* out_children, void* stream);
 
 /*
+ * Fork onto selected rows (no counterpart on the pages): a branch thinned out,
+ * copied or put into another order.  Child i is a new branch of starts[i] +
+ * counts[i] rows: the parent's first starts[i] rows, then the parent's row
+ * rows[k] for each k of the child's list.  Whole blocks before starts[i] are
+ * shared as in a fork; every other row of the child is copied, in every layer,
+ * bit for bit (rotated keys keep their angles), into blocks of its own, which
+ * come off the free stack in argument order, then position order.  The parents
+ * stay live and unchanged: freeing them afterwards makes this a compaction.
+ * The child's next row stands at its length; where the positions of its rows
+ * are to go on from the parent's, dendrite_append_rope_at takes them.
+ *   parents:  host int32[n], any branch any number of times.
+ *   starts:   host int32[n], 0 .. the parent's length.
+ *   counts:   host int32[n], >= 0.
+ *   rows:     device int32, the children's lists one after the other:
+ *             [sum counts], or with per_head = 1 [n_layers][sum counts][n_kv_heads],
+ *             where every layer and KV head has its own.  Any rows in [0, the
+ *             parent's length), in any order, any number of times.  An index
+ *             outside that range poisons the pool with DENDRITE_EINVAL when the
+ *             device finds it.  Read in stream order; may be NULL if no row is listed.
+ *   out_children: host int32[n], written before the call returns.
+ * All pool types.  All-or-nothing: with too few free blocks the pool reports
+ * DENDRITE_ENOMEM (sticky).  DENDRITE_EINVAL while a split append is pending and on a
+ * stream that is being captured; DENDRITE_ELIMIT past the table row or the handles.
+ */
+int dendrite_fork_rows(dendrite_pool* pool, const int32_t* parents, const int32_t* starts, const int32_t* counts,
+                       int32_t n, const int32_t* rows, int32_t per_head, int32_t* out_children, void* stream);
+
+/*
  * Append n_new tokens to every branch in `branches` (host int32[n_branches],
  * no duplicates).  K, V: device, [n_branches][n_new][n_kv_heads][head_dim] in
  * the pool dtype, contiguous.
@@ -315,6 +343,36 @@ int dendrite_append_layer_rope(dendrite_pool* pool, int32_t layer, const int32_t
                                const dendrite_rope* rope, void* stream);
 
 /*
+ * dendrite_append_rope and dendrite_append_layer_rope with the rows' positions
+ * given, of one axis or several (time, height and width of an image's or clip's
+ * tokens): pair i turns by at[branch][token][axis[i]] * inv_freq[i].  For rows
+ * whose number is not their position: behind images, in a thinned branch
+ * (dendrite_fork_rows), or turned by several axes.
+ *   at:      device int32; element (i, j, x) at i * branch_stride + j *
+ *            token_stride + x * axis_stride elements (each stride >= 0).  Any
+ *            values, negative ones among them.  In every layer of the call the same.
+ *            Read in stream order; must not overlap q_out.
+ *   n_axes:  1 .. DENDRITE_MAX_AXES.
+ *   axis:    axis[i] < n_axes: the axis of pair i < rot_dim / 2.
+ * Everything else as those calls (a draft tree's positions are part of `at`).
+ */
+#define DENDRITE_MAX_AXES 4
+typedef struct dendrite_positions {
+    const int32_t* at;
+    int64_t branch_stride, token_stride, axis_stride;
+    int32_t n_axes;
+    int32_t reserved;     /* must be zero */
+    uint8_t axis[128];
+} dendrite_positions;
+
+int dendrite_append_rope_at(dendrite_pool* pool, const int32_t* branches, int32_t n_branches, int32_t n_new,
+                            const dendrite_positions* at, const void* K, const void* V, const void* Q,
+                            int32_t n_q_heads, void* q_out, const dendrite_rope* rope, void* stream);
+int dendrite_append_layer_rope_at(dendrite_pool* pool, int32_t layer, const dendrite_positions* at, const void* K,
+                                  const void* V, const void* Q, int32_t n_q_heads, void* q_out,
+                                  const dendrite_rope* rope, void* stream);
+
+/*
  * Tree decode attention (Dendrite article, section 技术深度解析: attention
  * gathers keys and values from the shared ancestor path and the branch's own
  * leaf path).
@@ -376,6 +434,56 @@ int dendrite_tree_attn_decode_layer(dendrite_pool* pool, int32_t layer, const vo
 int dendrite_tree_attn_draft(dendrite_pool* pool, int32_t layer, const void* Q, int32_t n_q_heads, int32_t n_draft,
                              const int32_t* branches, int32_t n_branches, const int32_t* parents, int32_t n_trees,
                              void* out, void* stream);
+
+/*
+ * Cross attention: the same attention with every query seeing every row of its
+ * branch, which holds another sequence (an encoder's states, say) of any length,
+ * shorter than q_len too; rows are masked by nothing but that length.  Several
+ * queries' sequences read one branch through forks of it, which share its blocks.
+ * A branch of no rows gives zeros.
+ *   Q, out: device, [n_branches][q_len][n_q_heads][head_dim].
+ * Layers, types, sharing, the cached plan and errors as
+ * dendrite_tree_attn_decode_layer; DENDRITE_EINVAL on a stream that is being captured.
+ */
+int dendrite_tree_attn_cross(dendrite_pool* pool, int32_t layer, const void* Q, int32_t n_q_heads, int32_t q_len,
+                             const int32_t* branches, int32_t n_branches, void* out, void* stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities from given
+ * random numbers (the verify step of speculative decoding, DSpark blog, section
+ * 第二层, with the drafts of a branch as a tree).  Gives each branch's accepted
+ * path, for dendrite_accept_draft, and its next token, distributed as the target
+ * alone would sample it.  Reads none of the pool's rows.
+ *   n, n_draft: sequences, and drafted tokens of each, 1 .. DENDRITE_MAX_DRAFT.
+ *   parents, n_trees: as for dendrite_append_rope (parents required).
+ *   tokens:  device int32 [n][n_draft].  A token outside [0, vocab) is a padding
+ *            node: never accepted, and as if it were not there.
+ *   target:  device, [n][1 + n_draft] rows of vocab probabilities of type `dtype`
+ *            (DENDRITE_FP32 or DENDRITE_BF16), row_stride elements apart: row 0 after the
+ *            last accepted token, row 1 + j after node j.
+ *   draft:   device, [n][n_draft] rows the same way (row 0, and rows 1 + j of the
+ *            nodes before the last): what the children of a node were drawn from,
+ *            each by itself.  NULL: the drafts are certain (a table's, a greedy
+ *            draft's): q is 1 at the drafted token.
+ *   accept:  device float [n][n_draft], sample: device float [n]: uniform in [0, 1).
+ * From the last accepted token on, the children of the current node are tried
+ * in order.  With w = p, S = 1 and c = 0 at first, child x is accepted where
+ * w(x) > 0 and accept q(x) S < w(x), and becomes the current node; else c += S,
+ * w = max(p - c q, 0) and S = sum w (without draft: x leaves w, S = sum w).
+ * The next token is the least one whose running sum of w passes sample * sum w;
+ * where no weight is left, of p instead; -1 where p has none.  Probabilities that
+ * are not positive and finite count as zero.  Rows need not add up to one exactly;
+ * sums are taken to 2^-44 and better, so the outcome is that of 64-bit arithmetic.
+ *   path: device int32 [n][n_draft], the accepted nodes in order, then -1;
+ *   n_keep: device int32 [n]; next: device int32 [n].  Written.
+ * The outputs may not overlap one another or any input (DENDRITE_EINVAL, as for a
+ * stride below vocab, a misaligned pointer or a stream that is being captured).
+ * DENDRITE_ELIMIT past 2^31 rows or a vocabulary or stride of 2^30.
+ */
+int dendrite_verify_draft(dendrite_pool* pool, int32_t n, int32_t n_draft, const int32_t* parents, int32_t n_trees,
+                          const int32_t* tokens, int32_t vocab, int32_t dtype, const void* target,
+                          int64_t target_stride, const void* draft, int64_t draft_stride, const float* accept,
+                          const float* sample, int32_t* path, int32_t* n_keep, int32_t* next, void* stream);
 
 /*
  * Keeps the accepted nodes of each branch's n_draft drafted tokens (its last
