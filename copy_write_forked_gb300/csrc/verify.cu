@@ -28,6 +28,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "rows.h"
 
@@ -35,7 +36,8 @@ using namespace dendrite;
 
 namespace {
 
-constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32, kVerifyCluster = 8;
+constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32, kVerifyCluster = 16, kHeld = 8;
+constexpr int kDraftSmem = kHeld * kVerifyThreads * 16;
 constexpr int kTreeWordsCap = 1536;   // tree bytes as kernel parameters, four to a word
 
 struct VerifyArgs {
@@ -52,54 +54,186 @@ struct VerifyArgs {
     const DevMeta* meta;
 };
 
-// A sum of two floats, hi + lo.
-struct Pair {
+// A number as the sum of two floats, h + l, with l a rounding error of h (after norm) or a sum of such.
+struct alignas(8) Pair {
     float h, l;
 };
 __device__ __forceinline__ Pair two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
     return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ Pair add(Pair a, Pair b) {
+__device__ __forceinline__ Pair norm(Pair a) { return two_sum(a.h, a.l); }
+__device__ __forceinline__ Pair add(Pair a, Pair b) {   // (not normal: for sums of a few)
     const Pair s = two_sum(a.h, b.h);
-    return two_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+    return {s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))};
 }
-// Inclusive sums over the lanes.
-__device__ __forceinline__ Pair warp_scan(Pair x, int lane) {
+__device__ __forceinline__ Pair product(Pair a, float b) {
+    const float h = __fmul_rn(a.h, b);
+    return norm({h, __fmaf_rn(a.l, b, __fmaf_rn(a.h, b, -h))});
+}
+__device__ __forceinline__ Pair product(Pair a, Pair b) {
+    const float h = __fmul_rn(a.h, b.h);
+    return norm({h, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -h)))});
+}
+// Of normal pairs.
+__device__ __forceinline__ bool less(Pair a, Pair b) { return a.h < b.h || (a.h == b.h && a.l < b.l); }
+__device__ __forceinline__ Pair of_lane(Pair x, int lane) {
+    return {__shfl_sync(0xffffffffu, x.h, lane), __shfl_sync(0xffffffffu, x.l, lane)};
+}
+// Sum over 2^STEPS lanes (in every one of them).
+template <int STEPS>
+__device__ __forceinline__ Pair lanes_sum(Pair x) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1 << (STEPS - 1); o > 0; o >>= 1)
+        x = add(x, Pair{__shfl_xor_sync(0xffffffffu, x.h, o), __shfl_xor_sync(0xffffffffu, x.l, o)});
+    return norm(x);
+}
+// Inclusive sums over 2^STEPS lanes.
+template <int STEPS>
+__device__ __forceinline__ Pair lanes_scan(Pair x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 1 << STEPS; o <<= 1) {
         const Pair y = {__shfl_up_sync(0xffffffffu, x.h, o), __shfl_up_sync(0xffffffffu, x.l, o)};
         if (lane >= o) x = add(y, x);
     }
-    return x;
-}
-__device__ __forceinline__ Pair lane_of(Pair x, int lane) {
-    return {__shfl_sync(0xffffffffu, x.h, lane), __shfl_sync(0xffffffffu, x.l, lane)};
-}
-__device__ __forceinline__ double value(Pair a) { return (double)a.h + (double)a.l; }
-__device__ __forceinline__ Pair pair_of(double x) {
-    const float h = (float)x;
-    return {h, (float)(x - (double)h)};
-}
-__device__ __forceinline__ Pair warp_sum(Pair x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        x = add(x, Pair{__shfl_xor_sync(0xffffffffu, x.h, o), __shfl_xor_sync(0xffffffffu, x.l, o)});
-    return x;
+    return norm(x);
 }
 
 // A probability: what is not positive and finite counts as zero.
 __device__ __forceinline__ float prob(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
+
 __device__ __forceinline__ float load_prob(const float* p) { return prob(__ldg(p)); }
 __device__ __forceinline__ float load_prob(const __nv_bfloat16* p) { return prob(__bfloat162float(__ldg(p))); }
 
-// max(p - c q, 0) to 48 bits: the product's and the difference's errors carried.
+// Two fp32 in a register pair, and their packed arithmetic (each rounded as the scalar instruction rounds).
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pack(float lo, float hi) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpack(f32x2 x) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, pack(-1.f, -1.f), a); }   // a - b, rounded once
+// Two sums side by side: h + l each.
+struct Pair2 {
+    f32x2 h, l;
+};
+__device__ __forceinline__ Pair2 two_sum2(f32x2 a, f32x2 b) {
+    const f32x2 s = add2(a, b), t = sub2(s, a);
+    return {s, add2(sub2(a, sub2(s, t)), sub2(b, t))};
+}
+// Adds w, at most sum.h in size: the short form of two_sum.
+__device__ __forceinline__ void accumulate(Pair2& sum, Pair2 w) {
+    const f32x2 s = add2(sum.h, w.h);
+    sum = {s, add2(sum.l, add2(add2(sub2(sum.h, s), w.h), w.l))};
+}
+__device__ __forceinline__ void accumulate(Pair2& sum, f32x2 w) {
+    const f32x2 s = add2(sum.h, w);
+    sum = {s, add2(sum.l, add2(sub2(sum.h, s), w))};
+}
+
+// max(p - c q, 0) to 48 bits: the product's error and the difference's are carried (the latter by the
+// short form for |p| >= |c q|: where that does not hold the result is zero).  ONE: c is 1.
+struct Factor {
+    f32x2 h, l, minus;   // c, twice each; -c.h
+    __device__ __forceinline__ explicit Factor(Pair c) : h(pack(c.h, c.h)), l(pack(c.l, c.l)), minus(pack(-c.h, -c.h)) {}
+};
+template <bool ONE>
+__device__ __forceinline__ Pair2 residual(f32x2 p, f32x2 q, const Factor& c) {
+    if constexpr (ONE) {   // p - min(p, q)
+        const float2 x = unpack(p), y = unpack(q);
+        const f32x2 m = pack(fminf(x.x, y.x), fminf(x.y, y.y)), s = sub2(p, m);
+        return {s, sub2(sub2(p, s), m)};
+    } else {
+        const f32x2 nph = mul2(c.minus, q), s = add2(p, nph);
+        const f32x2 e = sub2(add2(sub2(p, s), nph), fma2(c.l, q, fma2(c.h, q, nph)));
+        const float2 h = unpack(s), l = unpack(e);
+        return {pack(fmaxf(h.x, 0.f), fmaxf(h.y, 0.f)), pack(h.x > 0.f ? l.x : 0.f, h.y > 0.f ? l.y : 0.f)};
+    }
+}
 __device__ __forceinline__ Pair residual(float p, float q, Pair c) {
-    const float ph = __fmul_rn(c.h, q);
-    const float pl = __fmaf_rn(c.l, q, __fmaf_rn(c.h, q, -ph));
-    Pair d = two_sum(p, -ph);
-    d.l = __fsub_rn(d.l, pl);
-    return __fadd_rn(d.h, d.l) > 0.f ? d : Pair{0.f, 0.f};
+    const Pair2 w = residual<false>(pack(p, 0.f), pack(q, 0.f), Factor(c));
+    return norm({unpack(w.h).x, unpack(w.l).x});
+}
+
+// A row is read in words of 16 bytes that are aligned whatever its address: element e of a row
+// stands at e + skew, with skew = the elements between the aligned address below the row and the row.
+template <typename T>
+constexpr int kPer = 16 / (int)sizeof(T);   // elements of a word
+template <typename T>
+__device__ __forceinline__ uint32_t clean(uint32_t x) {
+    if constexpr (sizeof(T) == 4) {
+        return __float_as_uint(prob(__uint_as_float(x)));
+    } else {
+        __nv_bfloat162 v;
+        memcpy(&v, &x, 4);
+        return x & __hgt2_mask(v, __float2bfloat162_rn(0.f)) & __hlt2_mask(v, __float2bfloat162_rn(INFINITY));
+    }
+}
+// A word at a row's end, or of a row whose words are not aligned: element by element.
+template <typename T>
+__device__ __noinline__ uint4 some(const T* base, int32_t skew, int32_t vocab, int32_t e) {
+    uint32_t x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+            x[j] = e + j >= skew && e + j < skew + vocab ? __ldg(reinterpret_cast<const uint32_t*>(base) + e + j) : 0u;
+        } else {
+            const uint16_t* b = reinterpret_cast<const uint16_t*>(base);
+            const int32_t f = e + 2 * j;
+            const uint32_t lo = f >= skew && f < skew + vocab ? __ldg(b + f) : 0u;
+            const uint32_t hi = f + 1 >= skew && f + 1 < skew + vocab ? __ldg(b + f + 1) : 0u;
+            x[j] = lo | hi << 16;
+        }
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+// The word at e of a row with its elements at [skew, skew + vocab), as probabilities.
+template <typename T>
+__device__ __forceinline__ uint4 word(const T* base, bool aligned, int32_t skew, int32_t vocab, int32_t e) {
+    constexpr int PER = kPer<T>;
+    return aligned && e >= skew && e + PER <= skew + vocab ? __ldg(reinterpret_cast<const uint4*>(base + e)) : some(base, skew, vocab, e);
+}
+template <typename T>
+__device__ __forceinline__ uint4 clean(uint4 w) {
+    return make_uint4(clean<T>(w.x), clean<T>(w.y), clean<T>(w.z), clean<T>(w.w));
+}
+// Elements 2 j, 2 j + 1 of a word.
+template <typename T>
+__device__ __forceinline__ f32x2 two(const uint4& w, int j) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 4) return pack(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+    else return pack(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xffff0000u));
+}
+// Takes element r of a word away, where it has one.
+template <typename T>
+__device__ __forceinline__ void drop(uint4& w, int32_t r) {
+    if (r < 0 || r >= kPer<T>) return;
+    const uint32_t keep = sizeof(T) == 4 ? 0u : r & 1 ? 0x0000ffffu : 0xffff0000u;
+    const int32_t j = sizeof(T) == 4 ? r : r >> 1;
+    if (j == 0) w.x &= keep;
+    if (j == 1) w.y &= keep;
+    if (j == 2) w.z &= keep;
+    if (j == 3) w.w &= keep;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -115,9 +249,18 @@ __device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
     return y;
 }
-__device__ __forceinline__ void store_peer(uint32_t at, uint32_t x) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+__device__ __forceinline__ void store_peer(uint32_t at, Pair x) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(x.h), "f"(x.l) : "memory");
 }
+__device__ __forceinline__ uint32_t load_peer(uint32_t at) {
+    uint32_t x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ void copy_async(uint4* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // The tree as bytes, parent + 1 of each node: kernel parameters, or staged.
 template <int CAP>
@@ -132,38 +275,42 @@ struct GlobalTree {
 
 // What the first CTA of a cluster found about the nodes, the same in every CTA.
 struct Nodes {
-    int32_t status;
     int32_t token[kMaxDraft];   // -1: no such node
     float accept[kMaxDraft], p[kMaxDraft], q[kMaxDraft];
+    uint32_t real[2], first[2];   // bits of the nodes that there are, and that are accepted if they are tried first
+    int32_t status;
     float sample;
 };
 
-// A node's weights: max(p - c q, 0), or p without the refused nodes' tokens.
-template <typename T>
-struct Weights {
-    const T* p;
-    const T* q;          // null: c is zero
-    Pair c;
-    uint64_t refused;    // certain drafts: nodes whose tokens are gone
+// Where the walk of the tree stands: the current node's row, and its residual.  Warp 0's, in
+// shared memory between the passes (in registers it would cost every warp's share of the row some).
+struct Walk {
+    Pair c, S, S_pass;           // w = max(p - c q, 0); its sum; the sum that was last taken over the row
+    uint64_t refused, left;      // certain drafts: refused nodes; children to try
+    uint64_t first;              // nodes that are accepted if they are tried first
+    int32_t cur, kept;
+    bool fresh, stale, last;     // none refused yet; S is not the sum of w; nothing is left to try
 };
 
+// Each thread holds kHeld words of the target's row in registers and as many of the draft's in shared
+// memory.  A share of the row that fits them is read once, however many children of the node are refused.
 template <typename T, bool DRAFT, typename A>
 __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid_constant__ A tree, const __grid_constant__ VerifyArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ uint4 held_q[];   // [kHeld][threads], each thread's own
     __shared__ Nodes nodes;
-    __shared__ int32_t up[kMaxDraft];
-    __shared__ uint32_t kids[kMaxDraft + 1][2];
     __shared__ Pair cta_sum[2][kVerifyCluster];   // every CTA's, of two passes in turn
     __shared__ Pair warp_sums[kVerifyWarps];
+    __shared__ Walk walk;
     __shared__ struct {
-        int32_t done, cur;
+        int32_t done, cur, again;   // again: the row has to be summed
         Pair c;
         uint64_t refused;
     } order;
     __shared__ struct {
         int32_t here, none;   // whether the token is in this CTA's share; no weight at all
-        double before, goal;
+        Pair before, goal;
     } find;
     const int32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int32_t cs = a.cluster, nd = a.n_draft;
@@ -171,18 +318,27 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
     const int64_t i = blockIdx.x / cs;
     const T* P = static_cast<const T*>(a.target) + i * (1 + nd) * a.target_stride;
     const T* Q = static_cast<const T*>(a.draft) + i * nd * a.draft_stride;
-    if (cs > 1) cluster_arrive();   // (the others have to have begun before their memory is written)
-    // the nodes: gathered by the first CTA, given to the others
-    if (t < 2 * (kMaxDraft + 1)) kids[t >> 1][t & 1] = 0;
-    if (t < nd) up[t] = tree((a.one_tree ? 0 : i * nd) + t);
+    // the nodes: gathered by the first CTA, fetched by the others
+    // the rows that node t, and (warp 0, which walks) node 32 + t hang on
+    const int32_t up = t < nd ? tree((a.one_tree ? 0 : i * nd) + t) : -1;
+    const int32_t up1 = warp == 0 && 32 + lane < nd ? tree((a.one_tree ? 0 : i * nd) + 32 + lane) : -1;
     if (rank == 0) {
-        if (t < nd) {
-            const int32_t x = __ldg(a.tokens + i * nd + t);
+        if (t < kMaxDraft) {
+            const int32_t x = t < nd ? __ldg(a.tokens + i * nd + t) : -1;
             const bool real = x >= 0 && x < a.vocab;
+            const float u = real ? __ldg(a.accept + i * nd + t) : 0.f;
+            const float p = real ? load_prob(P + up * a.target_stride + x) : 0.f;
+            const float q = !real ? 0.f : DRAFT ? load_prob(Q + up * a.draft_stride + x) : 1.f;
             nodes.token[t] = real ? x : -1;
-            nodes.accept[t] = __ldg(a.accept + i * nd + t);
-            nodes.p[t] = real ? load_prob(P + up[t] * a.target_stride + x) : 0.f;
-            nodes.q[t] = !real ? 0.f : DRAFT ? load_prob(Q + up[t] * a.draft_stride + x) : 1.f;
+            nodes.accept[t] = u;
+            nodes.p[t] = p;
+            nodes.q[t] = q;
+            const uint32_t all = __ballot_sync(0xffffffffu, real);
+            const uint32_t first = __ballot_sync(0xffffffffu, p > 0.f && less(product(Pair{u, 0.f}, q), Pair{p, 0.f}));
+            if (lane == 0) {
+                nodes.real[warp] = all;
+                nodes.first[warp] = first;
+            }
         } else if (t == kMaxDraft) {
             nodes.status = a.meta->status;
             const float u = __ldg(a.sample + i);
@@ -190,139 +346,188 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
         }
     }
     if (cs > 1) {
-        cluster_wait();
-        __syncthreads();
-        if (rank == 0) {
-            constexpr int words = sizeof(Nodes) / 4;
-            for (int32_t e = t; e < words * (cs - 1); e += kVerifyThreads) {
-                const int32_t to = e / words + 1, w = e % words;
-                store_peer(peer(reinterpret_cast<const uint32_t*>(&nodes) + w, to), reinterpret_cast<const uint32_t*>(&nodes)[w]);
-            }
-        }
         cluster_arrive();
         cluster_wait();
-    } else {
-        __syncthreads();
+        constexpr int words = sizeof(Nodes) / 4;
+        static_assert(words <= kVerifyThreads, "a word a thread");
+        if (rank && t < words) reinterpret_cast<uint32_t*>(&nodes)[t] = load_peer(peer(reinterpret_cast<const uint32_t*>(&nodes) + t, 0));
     }
-    if (nodes.status) return;   // (all CTAs of the cluster alike)
-    if (t < nd && nodes.token[t] >= 0) atomicOr(&kids[up[t]][t >> 5], 1u << (t & 31));
     __syncthreads();
+    // (the first CTA is there until the others have fetched: each waits for all once more, or leaves here)
+    if (nodes.status) {
+        if (cs > 1) {
+            cluster_arrive();
+            cluster_wait();
+        }
+        return;
+    }
 
-    // this warp's range of every row
-    const int32_t share = ((a.vocab + cs * kVerifyWarps - 1) / (cs * kVerifyWarps) + 31) & ~31;
-    const int32_t lo = min(a.vocab, (rank * kVerifyWarps + warp) * share), hi = min(a.vocab, lo + share);
+    constexpr int PER = kPer<T>;
+    uint4 hp[kHeld];
+    uint4* const hq = held_q + t;
+    float top = 0.f;                  // the largest held probability of the target
+    int32_t p_row = -1, q_row = -1;   // the rows that are held, where a share fits the registers
 
-    // the walk (warp 0): state of the current node
-    int32_t cur = 0, kept = 0, parity = 0;   // cur: row of the current node
-    double c = 0.0, S = 1.0;
-    bool stale = false;                      // S is not the sum of w yet
-    uint64_t refused = 0, left = 0;          // certain drafts: refused nodes; children to try
-    if (warp == 0) left = (uint64_t)kids[0][1] << 32 | kids[0][0];
-    bool fresh = true;                       // the node has refused none
-    bool last = false, fell_back = false;
+    // the real nodes that hang on a row (warp 0)
+    auto kids = [&](int32_t row) {
+        const uint32_t lo = __ballot_sync(0xffffffffu, up == row) & nodes.real[0], hi = __ballot_sync(0xffffffffu, up1 == row) & nodes.real[1];
+        return (uint64_t)hi << 32 | lo;
+    };
+    if (warp == 0) {
+        const uint64_t left = kids(0);
+        if (lane == 0)
+            walk = Walk{{0.f, 0.f}, {1.f, 0.f}, {0.f, 0.f}, 0, left, (uint64_t)nodes.first[1] << 32 | nodes.first[0], 0, 0, true, false, false};
+        __syncwarp();
+    }
+    bool fell_back = false;
+    int32_t parity = 0;
+    uint64_t counted = 0;   // refused nodes whose tokens the sums are without
 
     for (;;) {
         if (warp == 0) {
-            bool pass = false;
-            while (!last && left && !pass) {
-                const int32_t j = __ffsll((long long)left) - 1;
-                if (stale) {   // the sum first
-                    pass = true;
-                    break;
-                }
-                left &= left - 1;
-                double w = nodes.p[j], asked = (double)nodes.accept[j];
-                if (DRAFT) {
-                    if (!fresh) w = fmax(w - c * (double)nodes.q[j], 0.0);
-                    asked *= (double)nodes.q[j];
-                    if (!fresh) asked *= S;
+            Walk z = walk;
+            __syncwarp();
+            while (!z.last && z.left && !z.stale) {
+                const int32_t j = __ffsll((long long)z.left) - 1;
+                z.left &= z.left - 1;
+                bool ok;
+                Pair w = {nodes.p[j], 0.f};
+                if (z.fresh) {
+                    ok = z.first >> j & 1;
                 } else {
-                    for (uint64_t r = refused; r; r &= r - 1)
-                        if (nodes.token[__ffsll((long long)r) - 1] == nodes.token[j]) w = 0.0;
-                    if (!fresh) asked *= S;
+                    if (DRAFT) w = residual(nodes.p[j], nodes.q[j], z.c);
+                    else
+                        for (uint64_t r = z.refused; r; r &= r - 1)
+                            if (nodes.token[__ffsll((long long)r) - 1] == nodes.token[j]) w.h = 0.f;
+                    ok = w.h > 0.f && less(product(product(Pair{nodes.accept[j], 0.f}, nodes.q[j]), z.S), w);
                 }
-                if (w > 0.0 && asked < w) {
-                    if (rank == 0 && lane == 0) a.path[i * nd + kept] = j;
-                    ++kept;
-                    cur = j + 1;
-                    left = (uint64_t)kids[cur][1] << 32 | kids[cur][0];
-                    c = 0.0;
-                    S = 1.0;
-                    refused = 0;
-                    fresh = true;
+                if (ok) {
+                    if (rank == 0 && lane == 0) a.path[i * nd + z.kept] = j;
+                    ++z.kept;
+                    z.cur = j + 1;
+                    z.left = kids(z.cur);
+                    z.c = {0.f, 0.f};
+                    z.S = {1.f, 0.f};
+                    z.refused = 0;
+                    z.fresh = true;
+                } else if (DRAFT) {
+                    z.c = norm(add(z.c, z.S));
+                    z.fresh = false;
+                    z.stale = true;
                 } else {
-                    if (DRAFT) c += S;
-                    else refused |= 1ull << j;
-                    fresh = false;
-                    stale = true;
+                    // the sum without one more token: a new one only where the subtraction would lose digits
+                    z.S = norm(add(z.S, Pair{-w.h, 0.f}));
+                    z.stale = z.fresh || z.S.h < z.S_pass.h * 0x1p-10f;
+                    z.refused |= 1ull << j;
+                    z.fresh = false;
                 }
             }
-            if (!pass) last = true;
+            z.last = z.last || !z.left;   // (a sum that nothing asks for is the last pass's)
             if (lane == 0) {
-                order.done = last;
-                order.cur = cur;
-                order.c = pair_of(c);
-                order.refused = refused;
+                walk = z;
+                order.done = z.last;
+                order.again = DRAFT || z.fresh || z.stale;   // (else it was, and S went on by subtraction)
+                order.cur = z.cur;
+                order.c = z.c;
+                order.refused = z.refused;
             }
         }
         __syncthreads();
-        const bool fin = order.done != 0;
-        Weights<T> W;
-        W.p = P + order.cur * a.target_stride;
-        W.c = order.c;
-        W.q = DRAFT && W.c.h != 0.f ? Q + order.cur * a.draft_stride : nullptr;
-        W.refused = order.refused;
-        if (fell_back) {
-            W.q = nullptr;
-            W.refused = 0;
+        const bool fin = order.done != 0, again = order.again || fell_back;
+        const int32_t row = order.cur;
+        const Pair pc = fell_back ? Pair{0.f, 0.f} : order.c;
+        const uint64_t gone = fell_back ? 0 : order.refused;
+        const bool with_q = DRAFT && pc.h != 0.f;
+        const T* rp = P + row * a.target_stride;
+        const T* rq = Q + row * a.draft_stride;
+        // this warp's range of the row, in its words' numbering
+        const int32_t skew = (int32_t)((uintptr_t)rp & 15) / (int32_t)sizeof(T), words = (skew + a.vocab + PER - 1) / PER;
+        const int32_t share = (words + cs * kVerifyWarps - 1) / (cs * kVerifyWarps) * PER;
+        const int32_t lo = min(words * PER, (rank * kVerifyWarps + warp) * share), hi = min(words * PER, lo + share);
+        const bool fits = share <= 32 * PER * kHeld;
+        // certain drafts: where the row was summed before, the warps that have lost a token since do it again
+        uint64_t here = 0;   // tokens of this warp's range that are gone
+        for (uint64_t r = gone; r; r &= r - 1) {
+            const int32_t at = nodes.token[__ffsll((long long)r) - 1] + skew;
+            if (at >= lo && at < hi) here |= r & (0 - r);
         }
-        // refused tokens in this warp's range
-        uint64_t mine = 0;
-        if (!DRAFT)
-            for (uint64_t r = W.refused; r; r &= r - 1) {
-                const int32_t x = nodes.token[__ffsll((long long)r) - 1];
-                if (x >= lo && x < hi) mine |= r & (0 - r);
-            }
-        Pair sum = {0.f, 0.f};
-        constexpr int U = 8;
-        for (int32_t e0 = lo + lane; e0 < hi; e0 += 32 * U) {
-            float p[U], q[U];
+        const bool mine = again || (here & ~counted);
+        counted = gone;
+        Pair2 sum2 = {0, 0};
+        const Factor fc(pc);
+        for (int32_t base = mine ? lo : hi; base < hi; base += 32 * PER * kHeld) {
+            const int32_t e0 = base + PER * lane;
+            const bool new_q = with_q && (!fits || q_row != row);
+            if (new_q) {
+                const T* qb = rq - skew;
+                const bool aligned = ((uintptr_t)qb & 15) == 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) p[u] = e0 + 32 * u < hi ? load_prob(W.p + e0 + 32 * u) : 0.f;
-            if (DRAFT && W.q) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) q[u] = e0 + 32 * u < hi ? load_prob(W.q + e0 + 32 * u) : 0.f;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const Pair w = residual(p[u], q[u], W.c), s = two_sum(sum.h, w.h);
-                    sum = {s.h, __fadd_rn(sum.l, __fadd_rn(s.l, w.l))};
+                for (int k = 0; k < kHeld; ++k) {
+                    const int32_t e = e0 + 32 * PER * k;
+                    if (e >= hi) continue;
+                    if (aligned && e >= skew && e + PER <= skew + a.vocab) copy_async(hq + k * kVerifyThreads, qb + e);
+                    else hq[k * kVerifyThreads] = some(qb, skew, a.vocab, e);
                 }
-            } else {
-                if (!DRAFT)
-                    for (uint64_t r = mine; r; r &= r - 1) {
-                        const int32_t x = nodes.token[__ffsll((long long)r) - 1];
+            }
+            if (!fits || p_row != row) {
 #pragma unroll
-                        for (int u = 0; u < U; ++u)
-                            if (e0 + 32 * u == x) p[u] = 0.f;
+                for (int k = 0; k < kHeld; ++k) {
+                    const int32_t e = e0 + 32 * PER * k;
+                    hp[k] = e < hi ? word(rp - skew, true, skew, a.vocab, e) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) hp[k] = clean<T>(hp[k]);
+                top = 0.f;
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k)
+#pragma unroll
+                    for (int j = 0; j < PER / 2; ++j) {
+                        const float2 x = unpack(two<T>(hp[k], j));
+                        top = fmaxf(top, fmaxf(x.x, x.y));
                     }
+            }
+            if (new_q) copies_done();
+            // the sum stands above the largest weight meanwhile, so that each addition is the short form
+            const Pair2 up2 = two_sum2(sum2.h, pack(top, top));
+            sum2 = {up2.h, add2(sum2.l, up2.l)};
+            auto drafted = [&](auto one) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const Pair s = two_sum(sum.h, p[u]);
-                    sum = {s.h, __fadd_rn(sum.l, s.l)};
+                for (int k = 0; k < kHeld; ++k) {
+                    if (e0 + 32 * PER * k >= hi) continue;
+                    uint4 q = hq[k * kVerifyThreads];
+                    if (new_q) hq[k * kVerifyThreads] = q = clean<T>(q);
+#pragma unroll
+                    for (int j = 0; j < PER / 2; ++j) accumulate(sum2, residual<decltype(one)::value>(two<T>(hp[k], j), two<T>(q, j), fc));
+                }
+            };
+            if (DRAFT && with_q) {
+                if (pc.h == 1.f && pc.l == 0.f) drafted(std::true_type());
+                else drafted(std::false_type());
+            } else {
+                for (uint64_t r = here; r; r &= r - 1) {
+                    const int32_t at = nodes.token[__ffsll((long long)r) - 1] + skew - e0;
+#pragma unroll
+                    for (int k = 0; k < kHeld; ++k) drop<T>(hp[k], at - 32 * PER * k);
+                }
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) {
+                    if (e0 + 32 * PER * k >= hi) continue;
+#pragma unroll
+                    for (int j = 0; j < PER / 2; ++j) accumulate(sum2, two<T>(hp[k], j));
                 }
             }
+            const Pair2 down = two_sum2(sum2.h, pack(-top, -top));
+            sum2 = {down.h, add2(sum2.l, down.l)};
         }
-        sum = warp_sum(two_sum(sum.h, sum.l));
-        if (lane == 0) warp_sums[warp] = sum;
+        if (mine) p_row = row;   // (of one node more tokens may go, none come back)
+        if (with_q) q_row = row;
+        const float2 sh = unpack(sum2.h), sl = unpack(sum2.l);
+        const Pair sum = lanes_sum<5>(add(Pair{sh.x, sl.x}, Pair{sh.y, sl.y}));
+        if (mine && lane == 0) warp_sums[warp] = sum;
         __syncthreads();
         if (warp == 0) {
-            Pair x = lane < kVerifyWarps ? warp_sums[lane] : Pair{0.f, 0.f};
-            x = warp_sum(x);
-            if (lane < cs) {
-                const uint32_t at = peer(&cta_sum[parity][rank], lane);
-                store_peer(at, __float_as_uint(x.h));
-                store_peer(at + 4, __float_as_uint(x.l));
-            }
+            const Pair x = lanes_sum<4>(warp_sums[lane & (kVerifyWarps - 1)]);
+            if (lane < cs) store_peer(peer(&cta_sum[parity][rank], lane), x);
         }
         if (cs > 1) {
             cluster_arrive();
@@ -330,65 +535,98 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
         } else {
             __syncthreads();
         }
-        // every CTA's sum, added in the same order in every CTA (fp64 by one warp alone)
+        // every CTA's sum, added in the same order in every CTA
         if (warp == 0) {
-            const Pair incl = warp_scan(lane < cs ? cta_sum[parity][lane] : Pair{0.f, 0.f}, lane);
-            S = value(lane_of(incl, 31));
-            stale = false;
-            const Pair before = lane_of(incl, max(rank - 1, 0)), upto = lane_of(incl, rank);
-            if (fin && lane == 0) {
-                find.goal = (double)nodes.sample * S;
-                find.before = rank ? value(before) : 0.0;
-                find.here = find.goal >= find.before && find.goal < value(upto);
-                find.none = !(S > 0.0);
+            const Pair incl = lanes_scan<4>(lane < cs ? cta_sum[parity][lane] : Pair{0.f, 0.f}, lane);
+            const Pair S = of_lane(incl, 15), before = of_lane(incl, max(rank - 1, 0)), upto = of_lane(incl, rank);
+            if (lane == 0) {
+                walk.S = walk.S_pass = S;
+                walk.stale = false;
+                if (fin) {
+                    find.goal = product(S, nodes.sample);
+                    find.before = rank ? before : Pair{0.f, 0.f};
+                    find.here = !less(find.goal, find.before) && less(find.goal, upto);
+                    find.none = !(S.h > 0.f);
+                }
             }
+            __syncwarp();
         }
         parity ^= 1;
         if (!fin) continue;
         __syncthreads();
         if (find.none) {
-            if (fell_back || (!W.q && !W.refused)) {   // p has no weight
+            if (fell_back || (!with_q && !gone)) {   // p has no weight
                 if (rank == 0 && t == 0) a.next[i] = -1;
                 break;
             }
             fell_back = true;
+            p_row = -1;
             __syncthreads();
             continue;
         }
         if (!find.here) break;
         // the warp, then the lanes' runs, then the token
-        const Pair ws = lane < kVerifyWarps ? warp_sums[lane] : Pair{0.f, 0.f}, wi = warp_scan(ws, lane);
-        const double goal = find.goal;
+        const Pair ws = lane < kVerifyWarps ? warp_sums[lane] : Pair{0.f, 0.f}, wi = lanes_scan<4>(ws, lane);
+        const Pair goal = find.goal, start = find.before;
         const uint32_t with = __ballot_sync(0xffffffffu, ws.h > 0.f);
-        const uint32_t past = __ballot_sync(0xffffffffu, ws.h > 0.f && goal < find.before + value(wi));
+        const uint32_t past = __ballot_sync(0xffffffffu, ws.h > 0.f && less(goal, norm(add(start, wi))));
         // (rounding apart, some warp's end is past the goal)
         if (warp != (past ? __ffs(past) - 1 : 31 - __clz(with))) break;
-        const double from = find.before + (warp ? value(lane_of(wi, warp - 1)) : 0.0);
-        const int32_t run = (hi - lo + 31) / 32, r0 = min(hi, lo + lane * run), r1 = min(hi, r0 + run);
-        auto weight = [&](int32_t e) {
-            const float p = load_prob(W.p + e);
-            if (W.q) return residual(p, load_prob(W.q + e), W.c);
-            for (uint64_t r = mine; r; r &= r - 1)
-                if (nodes.token[__ffsll((long long)r) - 1] == e) return Pair{0.f, 0.f};
-            return Pair{p, 0.f};
+        const Pair from = warp ? norm(add(start, of_lane(wi, warp - 1))) : start;
+        const int32_t run = ((hi - lo) / PER + 31) / 32 * PER, r0 = min(hi, lo + lane * run), r1 = min(hi, r0 + run);
+        constexpr int U = 8;
+        auto weights = [&](int32_t e, Pair (&w)[U]) {   // of the U elements from e on, in the words' numbering
+            float p[U], q[U];
+            const int32_t r = e - skew;
+#pragma unroll
+            for (int u = 0; u < U; ++u) p[u] = e + u < r1 && r + u >= 0 && r + u < a.vocab ? load_prob(rp + r + u) : 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                q[u] = with_q && e + u < r1 && r + u >= 0 && r + u < a.vocab ? load_prob(rq + r + u) : 0.f;
+            for (uint64_t g = here; g; g &= g - 1) {
+                const int32_t x = nodes.token[__ffsll((long long)g) - 1];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (r + u == x) p[u] = 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; u += 2) {
+                Pair2 x = {pack(p[u], p[u + 1]), 0};
+                if (with_q) x = residual<false>(x.h, pack(q[u], q[u + 1]), fc);
+                const float2 h = unpack(x.h), l = unpack(x.l);
+                w[u] = {h.x, l.x};
+                w[u + 1] = {h.y, l.y};
+            }
         };
-        Pair x = {0.f, 0.f};
-        for (int32_t e = r0; e < r1; ++e) x = add(x, weight(e));
-        const Pair incl = warp_scan(x, lane);
+        Pair x = {0.f, 0.f}, w[U];
+        for (int32_t e = r0; e < r1; e += U) {
+            weights(e, w);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Pair s = two_sum(x.h, w[u].h);
+                x = {s.h, __fadd_rn(x.l, __fadd_rn(s.l, w[u].l))};
+            }
+        }
+        x = norm(x);
+        const Pair incl = lanes_scan<5>(x, lane);
         // the first lane whose end passes the goal, or the last one with weight
         const uint32_t has = __ballot_sync(0xffffffffu, x.h > 0.f);
-        const uint32_t over = __ballot_sync(0xffffffffu, x.h > 0.f && goal < from + value(incl));
+        const uint32_t over = __ballot_sync(0xffffffffu, x.h > 0.f && less(goal, norm(add(from, incl))));
         const int32_t pick = over ? __ffs(over) - 1 : 31 - __clz(has);
+        const Pair ahead = of_lane(incl, max(pick - 1, 0));
         if (lane == pick) {
-            const double base = from + (value(incl) - value(x));
-            Pair s = {0.f, 0.f};
+            Pair s = pick ? add(from, ahead) : from;
             int32_t token = -1;
-            for (int32_t e = r0; e < r1; ++e) {
-                const Pair w = weight(e);
-                if (!(w.h > 0.f)) continue;
-                s = add(s, w);
-                token = e;
-                if (goal < base + value(s)) break;
+            bool found = false;
+            for (int32_t e = r0; e < r1 && !found; e += U) {
+                weights(e, w);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (found || !(w[u].h > 0.f)) continue;
+                    s = norm(add(s, w[u]));
+                    token = e + u - skew;
+                    found = less(goal, s);
+                }
             }
             a.next[i] = token;
         }
@@ -396,15 +634,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
     }
     // (the loop ends after the last exchange of every CTA: none writes to another any more)
     if (rank == 0 && warp == 0) {
+        const int32_t kept = walk.kept;
         for (int32_t j = kept + lane; j < nd; j += 32) a.path[i * nd + j] = -1;
         if (lane == 0) a.n_keep[i] = kept;
     }
 }
 
-// CTAs per sequence: enough for two CTAs an SM, at least 4,096 tokens each.
+// CTAs per sequence: as many as are resident at once (two an SM), at least 2,048 tokens each.
 int verify_cluster(const dendrite_pool* p, int32_t n, int32_t vocab) {
     int cs = 1;
-    while (cs < kVerifyCluster && (int64_t)n * cs < 2 * (int64_t)p->sm_count && vocab > 4096 * cs) cs *= 2;
+    while (cs < kVerifyCluster && (int64_t)n * cs <= p->sm_count && vocab > 2048 * cs) cs *= 2;
     return cs;
 }
 
@@ -413,6 +652,7 @@ int launch_verify(const A& tree, const VerifyArgs& a, int32_t n, cudaStream_t s)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)n * a.cluster));
     cfg.blockDim = dim3(kVerifyThreads);
+    cfg.dynamicSmemBytes = a.draft ? kDraftSmem : 0;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -422,9 +662,14 @@ int launch_verify(const A& tree, const VerifyArgs& a, int32_t n, cudaStream_t s)
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    if (a.draft) DENDRITE_CUDA(cudaLaunchKernelEx(&cfg, k_verify_draft<T, true, A>, tree, a));
-    else DENDRITE_CUDA(cudaLaunchKernelEx(&cfg, k_verify_draft<T, false, A>, tree, a));
-    return DENDRITE_OK;
+    auto go = [&](auto* fn) -> int {
+        // (more than 8 CTAs a cluster, and more shared memory, have to be asked for)
+        if (a.cluster > 8) DENDRITE_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+        if (a.draft) DENDRITE_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kDraftSmem));
+        DENDRITE_CUDA(cudaLaunchKernelEx(&cfg, fn, tree, a));
+        return DENDRITE_OK;
+    };
+    return a.draft ? go(k_verify_draft<T, true, A>) : go(k_verify_draft<T, false, A>);
 }
 
 struct Span {
