@@ -413,6 +413,8 @@ void pack_segments(const FoldParams& fp, int32_t pack_pct, int32_t n_nodes, cons
 // Attention (attn.cu)
 int attn_setup(dendrite_pool* p);      // tensor maps, occupancy
 void attn_teardown(dendrite_pool* p);
+// Verification (verify.cu): its kernels' attributes, on the current device
+int verify_setup();
 
 }  // namespace dendrite
 

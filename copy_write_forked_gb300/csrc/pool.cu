@@ -1362,7 +1362,7 @@ int pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads, int3
         (int64_t)max_branches * bpb, p->d_meta);
     if (cudaGetLastError() != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
         return fail(cuda_err(cudaErrorUnknown));
-    if ((rc = attn_setup(p)) != DENDRITE_OK) return fail(rc);
+    if ((rc = attn_setup(p)) != DENDRITE_OK || (rc = verify_setup()) != DENDRITE_OK) return fail(rc);
     p->br.assign(max_branches, Branch());
     p->free_handles.reserve(max_branches);
     for (int32_t h = max_branches - 1; h >= 0; --h) p->free_handles.push_back(h);

@@ -663,13 +663,27 @@ int launch_verify(const A& tree, const VerifyArgs& a, int32_t n, cudaStream_t s)
     cfg.attrs = at;
     cfg.numAttrs = 2;
     auto go = [&](auto* fn) -> int {
-        // (more than 8 CTAs a cluster, and more shared memory, have to be asked for)
-        if (a.cluster > 8) DENDRITE_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-        if (a.draft) DENDRITE_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kDraftSmem));
         DENDRITE_CUDA(cudaLaunchKernelEx(&cfg, fn, tree, a));
         return DENDRITE_OK;
     };
     return a.draft ? go(k_verify_draft<T, true, A>) : go(k_verify_draft<T, false, A>);
+}
+
+// More than 8 CTAs a cluster, and the shared memory, have to be asked for.
+template <typename T, typename A>
+int setup_one() {
+    auto allow = [](auto* fn, bool draft) -> int {
+        DENDRITE_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+        if (draft) DENDRITE_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kDraftSmem));
+        return DENDRITE_OK;
+    };
+    DENDRITE_TRY(allow(k_verify_draft<T, true, A>, true));
+    return allow(k_verify_draft<T, false, A>, false);
+}
+template <typename A>
+int setup_types() {
+    DENDRITE_TRY((setup_one<float, A>()));
+    return setup_one<__nv_bfloat16, A>();
 }
 
 struct Span {
@@ -677,6 +691,16 @@ struct Span {
 };
 
 }  // namespace
+
+namespace dendrite {
+
+int verify_setup() {
+    DENDRITE_TRY(setup_types<ParamTree<64>>());
+    DENDRITE_TRY(setup_types<ParamTree<kTreeWordsCap>>());
+    return setup_types<GlobalTree>();
+}
+
+}  // namespace dendrite
 
 extern "C" int dendrite_verify_draft(dendrite_pool* p, int32_t n, int32_t n_draft, const int32_t* parents, int32_t n_trees,
                                      const int32_t* tokens, int32_t vocab, int32_t dtype, const void* target,

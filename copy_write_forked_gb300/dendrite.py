@@ -11,6 +11,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -57,9 +58,7 @@ class _Rope(ctypes.Structure):
                 ("inv_freq", ctypes.c_double * 128)]
 
 
-class _Positions(ctypes.Structure):
-    _fields_ = [("at", _p), ("branch_stride", _i64), ("token_stride", _i64), ("axis_stride", _i64), ("n_axes", _i32),
-                ("reserved", _i32), ("axis", ctypes.c_uint8 * 128)]
+_POSITIONS = struct.Struct("@Pqqqii128s")   # dendrite_positions
 
 
 class _PlanStats(ctypes.Structure):
@@ -91,8 +90,8 @@ _SIGS = {
                            ctypes.c_double, ctypes.c_double],
     "dendrite_append_rope": [_p, _pi32, _i32, _i32, _pi32, _i32, _p, _p, _p, _i32, _p, _p, _p],
     "dendrite_append_layer_rope": [_p, _i32, _pi32, _i32, _p, _p, _p, _i32, _p, _p, _p],
-    "dendrite_append_rope_at": [_p, _pi32, _i32, _i32, ctypes.POINTER(_Positions), _p, _p, _p, _i32, _p, _p, _p],
-    "dendrite_append_layer_rope_at": [_p, _i32, ctypes.POINTER(_Positions), _p, _p, _p, _i32, _p, _p, _p],
+    "dendrite_append_rope_at": [_p, _pi32, _i32, _i32, _p, _p, _p, _p, _i32, _p, _p, _p],
+    "dendrite_append_layer_rope_at": [_p, _i32, _p, _p, _p, _p, _i32, _p, _p, _p],
     "dendrite_fork_rows": [_p, _pi32, _pi32, _pi32, _i32, _p, _i32, _pi32, _p],
     "dendrite_tree_attn_cross": [_p, _i32, _p, _i32, _i32, _pi32, _i32, _p, _p],
     "dendrite_verify_draft": [_p, _i32, _i32, _pi32, _i32, _p, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p],
@@ -474,8 +473,8 @@ class Pool:
         out = self._out(Q, out, stream)
         return Q.data_ptr(), nq, out
 
-    def _positions(self, positions, rope, parents, n, n_new, stream) -> Optional[_Positions]:
-        """Given positions as dendrite_positions, or None where they follow from the length."""
+    def _positions(self, positions, rope, parents, n, n_new, stream) -> Optional[bytes]:
+        """Given positions as a dendrite_positions, or None where they follow from the length."""
         if positions is None:
             if rope.n_axes > 1:
                 raise DendriteError(-1, "a rope of several axes needs positions")
@@ -491,9 +490,7 @@ class Pool:
         if stream is not None:
             self._other(stream, t)
         st = t.stride()
-        c = _Positions(t.data_ptr(), st[0], st[1], st[2] if len(st) == 3 else 1, rope.n_axes, 0)
-        ctypes.memmove(c.axis, rope._axis, 128)
-        return c
+        return _POSITIONS.pack(t.data_ptr(), st[0], st[1], st[2] if len(st) == 3 else 1, rope.n_axes, 0, rope._axis)
 
     def append_rope(self, branches: Sequence[int], K: torch.Tensor, V: torch.Tensor, rope: Rope,
                     Q: Optional[torch.Tensor] = None, parents=None, out: Optional[torch.Tensor] = None,
@@ -580,11 +577,12 @@ class Pool:
         """The row stride of [n][rows][vocab] probabilities whose rows follow one another evenly."""
         if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != self._dev or t.shape != (n, rows, vocab):
             raise DendriteError(-1, f"{name} must be a {dtype} tensor {(n, rows, vocab)} on cuda:{self._dev}")
+        if t.is_contiguous():
+            return vocab
         a, b, c = t.stride()
-        step = b if rows > 1 else a if n > 1 else vocab
         if (vocab > 1 and c != 1) or (n > 1 and rows > 1 and a != rows * b):
-            raise DendriteError(-1, f"{name} strides {t.stride()}")
-        return max(step, vocab) if n * rows == 1 else step
+            raise DendriteError(-1, f"{name} strides {(a, b, c)}")
+        return b if rows > 1 else a if n > 1 else vocab
 
     def verify_draft(self, tokens: torch.Tensor, target: torch.Tensor, parents, accept: torch.Tensor, sample: torch.Tensor,
                      draft: Optional[torch.Tensor] = None, out: Optional[Tuple[torch.Tensor, torch.Tensor, torch.Tensor]] = None,
@@ -602,16 +600,17 @@ class Pool:
         self._plain(tokens, "tokens", torch.int32, (n, t))
         self._plain(accept, "accept", torch.float32, (n, t))
         self._plain(sample, "sample", torch.float32, (n,))
-        if target.dtype not in (torch.float32, torch.bfloat16):
-            raise DendriteError(-5, f"target dtype {target.dtype}")
-        vocab = target.shape[2]
-        ps = self._vocab_rows(target, "target", n, 1 + t, target.dtype, vocab)
-        qs = 0 if draft is None else self._vocab_rows(draft, "draft", n, t, target.dtype, vocab)
+        dtype, vocab = target.dtype, target.shape[2]
+        if dtype is not torch.float32 and dtype is not torch.bfloat16:
+            raise DendriteError(-5, f"target dtype {dtype}")
+        ps = self._vocab_rows(target, "target", n, 1 + t, dtype, vocab)
+        qs = 0 if draft is None else self._vocab_rows(draft, "draft", n, t, dtype, vocab)
         keep, pp, nt = _trees(parents, n, t)
-        if out is None:
-            path = torch.empty(n, t, dtype=torch.int32, device=self.device) if stream is None else self._output((n, t), stream, torch.int32)
-            size, token = (torch.empty(n, dtype=torch.int32, device=self.device) if stream is None else self._output((n,), stream, torch.int32)
-                           for _ in range(2))
+        if out is None and stream is None:
+            path = torch.empty_like(tokens)
+            size, token = torch.empty_like(sample, dtype=torch.int32), torch.empty_like(sample, dtype=torch.int32)
+        elif out is None:
+            path, size, token = (self._output(shape, stream, torch.int32) for shape in ((n, t), (n,), (n,)))
         else:
             path, size, token = out
             self._plain(path, "out[0]", torch.int32, (n, t))
@@ -619,7 +618,7 @@ class Pool:
             self._plain(token, "out[2]", torch.int32, (n,))
         if stream is not None:
             self._other(stream, tokens, target, accept, sample, path, size, token, *(() if draft is None else (draft,)))
-        _check(lib().dendrite_verify_draft(self._h, n, t, pp, nt, tokens.data_ptr(), vocab, _DT[target.dtype], target.data_ptr(), ps,
+        _check(lib().dendrite_verify_draft(self._h, n, t, pp, nt, tokens.data_ptr(), vocab, _DT[dtype], target.data_ptr(), ps,
                                            None if draft is None else draft.data_ptr(), qs, accept.data_ptr(), sample.data_ptr(),
                                            path.data_ptr(), size.data_ptr(), token.data_ptr(), _stream_ptr(stream, self._dev)),
                "verify_draft")
