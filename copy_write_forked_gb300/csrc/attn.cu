@@ -1253,6 +1253,68 @@ __global__ void __launch_bounds__(256, 3) k_attn_merge_grouped(const AttnArgs a)
     }
 }
 
+// Direct plans (cross attention): the units split over CTAs, CTA (split unit, 32 of its rows),
+// four rows a warp.  A row's partials are its unit's chunks, so nothing is looked up per row:
+// 114,688 rows of which the general merge found each one's only partial took 95 us.
+__global__ void __launch_bounds__(256) k_attn_merge_splits(const AttnArgs a) {
+    pdl_trigger();
+    const AttnPlanDev& pl = a.plan;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const AttnUnit U = pl.units[pl.splits[blockIdx.x]];
+    const int r0 = (int)blockIdx.y * 32 + warp * 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (r0 >= U.n_rows || *reinterpret_cast<volatile const int32_t*>(&a.meta->status)) return;
+    constexpr int R = 4, V = 2;   // rows and chunks whose loads are in flight together
+    float M[R], L[R];
+    float4 acc[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        M[i] = -INFINITY;
+        L[i] = 0.f;
+        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int k0 = 0; k0 < U.nchunks; k0 += V) {
+        float2 ml[V][R];
+        float4 x[V][R];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool on = k0 + v < U.nchunks && r0 + i < U.n_rows;
+                const int64_t row = (int64_t)U.prow_base + (int64_t)(k0 + v) * U.n_rows + r0 + i;
+                ml[v][i] = on ? __ldcg(a.part_ml + row) : make_float2(-INFINITY, 0.f);
+                x[v][i] = on ? __ldcg(reinterpret_cast<const float4*>(a.part_acc + row * D) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float m = M[i];
+#pragma unroll
+            for (int v = 0; v < V; ++v) m = fmaxf(m, ml[v][i].x);
+            const float ref = m == -INFINITY ? 0.f : m, sc = exp2f(M[i] - ref);
+            M[i] = m;
+            L[i] *= sc;
+            acc[i] = make_float4(acc[i].x * sc, acc[i].y * sc, acc[i].z * sc, acc[i].w * sc);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float w = exp2f(ml[v][i].x - ref);
+                L[i] = fmaf(w, ml[v][i].y, L[i]);
+                acc[i].x = fmaf(w, x[v][i].x, acc[i].x);
+                acc[i].y = fmaf(w, x[v][i].y, acc[i].y);
+                acc[i].z = fmaf(w, x[v][i].z, acc[i].z);
+                acc[i].w = fmaf(w, x[v][i].w, acc[i].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (r0 + i >= U.n_rows) break;
+        const float inv = 1.f / L[i];
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (int64_t)unit_row(pl, U, r0 + i).q_row * D + 4 * lane;
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+    }
+}
+
 // ============================================================ host planning
 // A segment as the unit expansion reads it (host or device): its units are
 // unit_base + kv head * ngroups + row group, its tiles (class numbering)
@@ -1579,6 +1641,8 @@ struct HostPlan {
     std::vector<ExtraTile> pxt;      // the planner's extra tiles of packed segments
     std::vector<AttnXTile> xtiles;   // the same for the kernels (branch handles)
     std::vector<uint64_t> masks;     // draft trees: drafted tokens each query sees
+    std::vector<int32_t> splits;     // direct plans: units split over CTAs
+    bool direct = false;             // see AttnPlanDev::direct
     std::vector<SegPlan> segplan;
     PlanHeader hdr{};
     bool device = false;       // units and CTA split left to the device
@@ -1586,7 +1650,7 @@ struct HostPlan {
     void clear() {   // keeps capacity: plans are rebuilt whenever the tree changes; the unit and
                      // member arrays keep their size too (build_plan resizes and fills them in place)
         segs.clear(); cta_begin.clear(); cta_unit.clear(); segplan.clear(); device = false; small_packed = false;
-        pxt.clear(); xtiles.clear(); masks.clear();
+        pxt.clear(); xtiles.clear(); masks.clear(); splits.clear(); direct = false;
         tc_cta_begin.clear(); tc_cta_unit.clear(); path_off.clear(); path.clear(); cuts.clear();
         tiles = unique_tiles = 0;
         n_tc_units = 0;
@@ -2054,7 +2118,7 @@ int encode_pool_map(dendrite_pool* p, void* base, unsigned char* out) {
 // counts, which k_plan_expand writes when the plan is expanded on the device
 // (only the prefix before them is then uploaded).
 enum PlanSection {
-    SEC_SEGS, SEC_MEMBERS, SEC_PATH_OFF, SEC_PATH, SEC_SEGPLAN, SEC_HEADER, SEC_XTILES, SEC_MASKS,
+    SEC_SEGS, SEC_MEMBERS, SEC_PATH_OFF, SEC_PATH, SEC_SEGPLAN, SEC_HEADER, SEC_XTILES, SEC_MASKS, SEC_SPLITS,
     SEC_UNITS, SEC_CTA_BEGIN, SEC_CTA_UNIT, SEC_TC_BEGIN, SEC_TC_UNIT, SEC_COUNTS, kPlanSections
 };
 constexpr int kPlanDeviceSection = SEC_UNITS;
@@ -2065,6 +2129,7 @@ size_t plan_layout(const HostPlan& hp, size_t (&off)[kPlanSections + 1]) {
         hp.device ? hp.segplan.size() * sizeof(SegPlan) : 0,
         hp.device ? sizeof(PlanHeader) : 0,
         hp.xtiles.size() * sizeof(AttnXTile), hp.masks.size() * sizeof(uint64_t),
+        hp.splits.size() * 4,
         hp.units.size() * sizeof(AttnUnit),   hp.cta_begin.size() * 4,
         hp.cta_unit.size() * 4,               hp.tc_cta_begin.size() * 4,
         hp.tc_cta_unit.size() * 4,            hp.device ? 4 * sizeof(int32_t) : 0};
@@ -2092,6 +2157,7 @@ void plan_pack(const HostPlan& hp, const size_t (&off)[kPlanSections + 1], char*
     put(SEC_PATH, hp.path.data(), hp.path.size() * 4);
     put(SEC_XTILES, hp.xtiles.data(), hp.xtiles.size() * sizeof(AttnXTile));
     put(SEC_MASKS, hp.masks.data(), hp.masks.size() * sizeof(uint64_t));
+    put(SEC_SPLITS, hp.splits.data(), hp.splits.size() * 4);
     if (hp.device) {
         put(SEC_SEGPLAN, hp.segplan.data(), hp.segplan.size() * sizeof(SegPlan));
         put(SEC_HEADER, &hp.hdr, sizeof(PlanHeader));
@@ -2119,6 +2185,9 @@ AttnPlanDev plan_view(const HostPlan& hp, const size_t (&off)[kPlanSections + 1]
     v.tc_cta_unit = reinterpret_cast<const int32_t*>(d + off[SEC_TC_UNIT]);
     v.counts = hp.device ? reinterpret_cast<const int32_t*>(d + off[SEC_COUNTS]) : nullptr;
     v.masks = hp.masks.empty() ? nullptr : reinterpret_cast<const uint64_t*>(d + off[SEC_MASKS]);
+    v.splits = reinterpret_cast<const int32_t*>(d + off[SEC_SPLITS]);
+    v.n_splits = (int32_t)hp.splits.size();
+    v.direct = hp.direct;
     v.back = cross ? 0 : q_len;
     v.step = cross || v.masks ? 0 : 1;
     v.packed = hp.small_packed ? 1 : 0;
@@ -2153,6 +2222,7 @@ AttnPlanDev plan_rebase(AttnPlanDev v, const char* from, const char* to) {
     mv(v.xtiles);
     if (v.counts) mv(v.counts);
     if (v.masks) mv(v.masks);
+    mv(v.splits);
     return v;
 }
 
@@ -2173,6 +2243,17 @@ int launch_plan_expand(dendrite_pool* p, char* d, const size_t* off, int32_t n_u
     DENDRITE_CUDA(launch_pdl(k_plan_expand, dim3((unsigned)std::max(1, (n_units + kExpandUnits - 1) / kExpandUnits)),
                              dim3(kExpandThreads), (size_t)n_segs * 16, s, x));
     return DENDRITE_OK;
+}
+
+// Cross attention: whether the tcgen05 kernel may write the rows of whole units out itself, and
+// which units it does not run whole (AttnPlanDev::direct).
+void find_direct(const dendrite_pool* p, HostPlan& hp, int32_t n) {
+    if ((p->dtype != DENDRITE_BF16 && p->dtype != DENDRITE_FP8) || hp.device || hp.n_tc_units != (int32_t)hp.units.size()) return;
+    for (int32_t i = 0; i < n; ++i)
+        if (hp.path_off[i + 1] - hp.path_off[i] > 1) return;
+    hp.direct = true;
+    for (int32_t u = 0; u < (int32_t)hp.units.size(); ++u)
+        if (hp.units[u].nchunks > 1) hp.splits.push_back(u);
 }
 
 // Each query's drafted tokens: bit b of masks[i][j] is set if node b is node j
@@ -2276,7 +2357,10 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
     }
     prof_end(p, T_ATTN_PARTIAL, s);
     prof_begin(p, T_ATTN_MERGE, s);
-    {
+    if (a.plan.direct) {
+        if (a.plan.n_splits > 0)
+            DENDRITE_CUDA(launch_pdl(k_attn_merge_splits, dim3((unsigned)a.plan.n_splits, kMaxUnitRowsTc / 32), dim3(256), 0, s, a));
+    } else {
         // after a join from the side stream the merge is an ordinary launch:
         // its dependence is on an event, not on the previous kernel alone
         auto mlaunch = [&](auto kernel, unsigned g) -> cudaError_t {
@@ -2605,10 +2689,11 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
             if (!grow) hp.clear();
         }
         if (grow) {
-            DENDRITE_TRY(build_units(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, true));
+            DENDRITE_TRY(build_units(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, !cross));
         } else {
-            DENDRITE_TRY(build_plan(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, true));
+            DENDRITE_TRY(build_plan(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, !cross));
         }
+        if (cross) find_direct(p, hp, n);
         if (parents) draft_masks(parents, n_trees, n, q_len, hp.masks);
         size_t off[kPlanSections + 1];
         const size_t b = plan_layout(hp, off);
@@ -2706,6 +2791,14 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
     a.part_acc = p->d_partial;
     a.part_ml = reinterpret_cast<float2*>(p->d_partial + p->partial_rows_cap * p->head_dim);
     if (!began) prof_begin(p, T_ATTN_TOTAL, s);
+    if (a.plan.direct) {   // no kernel writes the rows of branches without rows: zeros, a run of them at a time
+        const size_t each = (size_t)q_len * n_q_heads * p->head_dim * p->elt;
+        for (int32_t i = 0, end; i < n; i = end) {
+            for (end = i; end < n && p->br[branches[end]].len == 0; ++end) {}
+            if (end > i) DENDRITE_CUDA(cudaMemsetAsync(static_cast<char*>(out) + i * each, 0, (end - i) * each, s));
+            else ++end;
+        }
+    }
     return launch_attention(p, layer, a, s);
 }
 

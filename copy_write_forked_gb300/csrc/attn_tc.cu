@@ -519,6 +519,14 @@ __device__ __forceinline__ void convert_tiles(const AttnArgs& a, unsigned char* 
     }
 }
 
+// Eight values times inv as 16 bytes of bf16.
+__device__ __forceinline__ uint4 out_words(const uint32_t* v, float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = pack_bf16(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The row tiles of a unit's chunk of nst stages, 8-bit pools.  A unit of up to
 // 128 rows is split along its tokens instead: both groups of softmax warps hold
 // its rows, group r takes the stages k with k % 2 = r, and the two (m, l, O) are
@@ -651,7 +659,8 @@ __device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint3
 // F8: an 8-bit pool's blocks (tmK and tmV unused).
 // CUT: bf16, some branch was rolled back into a block, where V rows may stand behind
 // its end (8-bit pools' V is cleared there as it is converted, in every call).
-template <bool DRAFT, bool F8, bool CUT>
+// WHOLE: direct plans (cross attention), whose units that one CTA runs whole are written out here.
+template <bool DRAFT, bool F8, bool CUT, bool WHOLE>
 __global__ void __launch_bounds__(TcLayout<F8>::THREADS, 1)
 k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const AttnArgs a) {
@@ -1224,6 +1233,10 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 const float mine = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
                 const float other = o.x == -INFINITY ? 0.f : ex2_approx(o.x - m);
                 const uint32_t tl_o = tmem + ((uint32_t)(sub * 32) << 16) + (r ^ 1) * 256;
+                const bool whole = WHOLE && U.nchunks == 1;
+                const float sum = l * mine + o.y * other, inv = 1.f / sum;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+                if (whole && valid) out += (int64_t)unit_row(pl, U, row).q_row * D;
 #pragma unroll 1
                 for (int c0 = r * (D / 2); c0 < (r + 1) * (D / 2); c0 += 32) {
                     uint32_t v[32], w[32];
@@ -1231,7 +1244,13 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     tmem_ld32(tl_o + c0, w);
                     tmem_wait_ld(v);
                     reg_tie(w);
-                    if (valid) {
+                    if (valid && whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __float_as_uint(__uint_as_float(v[i]) * mine + __uint_as_float(w[i]) * other);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(out + c0 + i) = out_words(v + i, inv);
+                    } else if (valid) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             float4 x;
@@ -1243,7 +1262,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                         }
                     }
                 }
-                if (valid && r == 0) a.part_ml[prow] = make_float2(m, l * mine + o.y * other);
+                if (valid && !whole && r == 0) a.part_ml[prow] = make_float2(m, sum);
                 // neither accumulator is written again, nor its (m, l), before both groups are done
                 tc_fence_before();
                 __syncwarp();
@@ -1256,18 +1275,26 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 ++u;
                 continue;
             }
+            const bool whole = WHOLE && U.nchunks == 1;   // no other partial: O / l is the output row
+            const float inv = 1.f / l;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+            if (whole && valid) out += (int64_t)unit_row(pl, U, row).q_row * D;
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t v[32];
                 tmem_ld32(tl + c0, v);
                 tmem_wait_ld(v);
-                if (valid) {
+                if (valid && whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *reinterpret_cast<uint4*>(out + c0 + i) = out_words(v + i, inv);
+                } else if (valid) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
-            if (valid) a.part_ml[prow] = make_float2(m_ref, l);
+            if (valid && !whole) a.part_ml[prow] = make_float2(m_ref, l);
             tc_fence_before();
             t = cend;
             ++u;
@@ -1285,9 +1312,9 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
 namespace dendrite {
 
-template <bool DRAFT, bool F8, bool CUT>
+template <bool DRAFT, bool F8, bool CUT, bool WHOLE = false>
 static int setup_one() {
-    constexpr auto fn = k_attn_partial_tc<DRAFT, F8, CUT>;
+    constexpr auto fn = k_attn_partial_tc<DRAFT, F8, CUT, WHOLE>;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLayout<F8>::SMEM) != cudaSuccess)
         return DENDRITE_ECUDA;
     int occ = 0;
@@ -1301,8 +1328,11 @@ static int setup_one() {
 int attn_tc_setup(bool f8) {
     if (f8) {
         DENDRITE_TRY((setup_one<false, true, false>()));
+        DENDRITE_TRY((setup_one<false, true, false, true>()));
         return setup_one<true, true, false>();
     }
+    DENDRITE_TRY((setup_one<false, false, false, true>()));
+    DENDRITE_TRY((setup_one<false, false, true, true>()));
     DENDRITE_TRY((setup_one<false, false, false>()));
     DENDRITE_TRY((setup_one<true, false, false>()));
     DENDRITE_TRY((setup_one<false, false, true>()));
@@ -1312,8 +1342,9 @@ int attn_tc_setup(bool f8) {
 template <bool F8, bool CUT>
 static void launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, cudaStream_t s) {
     using Y = TcLayout<F8>;
-    if (a.plan.masks) k_attn_partial_tc<true, F8, CUT><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
-    else k_attn_partial_tc<false, F8, CUT><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
+    if (a.plan.masks) k_attn_partial_tc<true, F8, CUT, false><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
+    else if (a.plan.direct) k_attn_partial_tc<false, F8, CUT, true><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
+    else k_attn_partial_tc<false, F8, CUT, false><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
 }
 
 int launch_attn_tc(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, bool f8, cudaStream_t s) {

@@ -149,6 +149,10 @@ struct AttnPlanDev {
     const uint64_t* masks;         // [n_queried][q_len] drafted tokens each query sees (draft trees), or null
     int32_t back, step;            // query j of a branch of len rows sees positions < len - back + (j + 1) step:
                                    // causal q_len, 1; draft trees q_len, 0 (and their masks); cross attention 0, 0
+    // Cross attention whose branches each read one segment, all on the tcgen05 kernel: a unit that one
+    // CTA runs whole writes its rows out itself, and only the units split over CTAs are merged.
+    const int32_t* splits;         // [n_splits] units split over CTAs
+    int32_t direct, n_splits;
     int32_t packed;                // some unit reads extra tiles (the mma.sync kernel then needs its tile info)
 };
 
