@@ -821,14 +821,14 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // 0.5 % of a verification call and lost 1.2 % of the stress step, where
         // memory is the bound.
         auto one = [] {
-            if constexpr (DRAFT) return elect_one();
+            if constexpr (DRAFT || WHOLE) return elect_one();
             return true;
         };
         auto wait = [&](uint32_t wb, uint32_t parity) {
-            if constexpr (DRAFT) return warp_wait(wb, parity, abortp, a.meta);
+            if constexpr (DRAFT || WHOLE) return warp_wait(wb, parity, abortp, a.meta);
             return thread_wait(wb, parity, abortp, a.meta);
         };
-        if (DRAFT || lane == 0) {
+        if (DRAFT || WHOLE || lane == 0) {
             const uint32_t sQ = base + OFF_Q + my_r * TC_QTILE;
             int32_t g = 0, js = 0, qc = 0;
             bool ok = true, any = false;
@@ -894,7 +894,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                             mbar_arrive(bar(B_V_EMPTY + slot));
                         }
                     }
-                    if constexpr (DRAFT) __syncwarp();
+                    if constexpr (DRAFT || WHOLE) __syncwarp();
                 }
                 g += nst;
                 t = cend;
@@ -1129,7 +1129,13 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 // row max of the raw scores (eight independent chains), then
                 // in base-2 units (the scale is positive)
                 float mx;
-                {
+                if constexpr (WHOLE) {
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2)
+                        m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], __float_as_uint(s[i]), __float_as_uint(s[i + 1]));
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+                } else {
                     float m8[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) m8[j] = s[j];
@@ -1170,7 +1176,18 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 // P = 2^(s * scale - m_ref) in bf16; the row sum is taken over
                 // the rounded values (eight independent chains)
                 uint32_t pk[32];
-                {
+                if constexpr (WHOLE) {   // the same sums, two to an instruction
+                    const f32x2 scale2 = pair(a.scale_log2, a.scale_log2), nref2 = pair(nref, nref);
+                    f32x2 l2[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const f32x2 x = fma2(pair(s[2 * i], s[2 * i + 1]), scale2, nref2);
+                        pk[i] = pack_bf16(ex2_approx(low(x)), ex2_approx(high(x)));
+                        l2[i & 3] = add2(l2[i & 3], pair(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u)));
+                    }
+                    const f32x2 ls = add2(add2(l2[0], l2[1]), add2(l2[2], l2[3]));
+                    l += low(ls) + high(ls);
+                } else {
                     float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
