@@ -38,6 +38,7 @@
 #include <algorithm>
 #include <cmath>
 #include <climits>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
@@ -1689,8 +1690,10 @@ constexpr ClassWeights kSmallWeightsFp8{30, 2, 8};
 inline const ClassWeights& small_weights(const dendrite_pool* p) {
     return p->dtype == DENDRITE_FP8 ? kSmallWeightsFp8 : kSmallWeights;
 }
-constexpr ClassWeights kTcWeights{24, -1, 32};
-inline int64_t tile_weight(int rt) { return 1 + rt; }
+static int EV(const char* n,int d){const char* e=getenv(n);return e?atoi(e):d;}
+static ClassWeights kTcWeights{EV("US",24)*20, -1, 32*20};
+static int W1=EV("W1",40);
+inline int64_t tile_weight(int rt) { return rt==1?W1:20*(1 + rt); }
 inline int64_t start_weight(const ClassWeights& cw, int32_t n_rows) {
     return cw.unit_start + (cw.row_shift >= 0 ? (n_rows >> cw.row_shift) : 0);
 }

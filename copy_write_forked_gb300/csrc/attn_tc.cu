@@ -132,9 +132,13 @@ struct TcLayout {
     static constexpr int OFF_XHELD = OFF_XINFO + TC_ROWTILES * kMaxTcExtraTiles * 8;
     // F8: (m, l) of the rows of a split unit, per group
     static constexpr int OFF_ML = OFF_XHELD + TC_ROWTILES * kMaxTcExtraTiles;
+    // WHOLE, bf16: 32 rows of 64 bytes of each softmax warp, on their way out (row stride 80 bytes)
+    static constexpr int OFF_OUT = (OFF_ML + (F8 ? TC_ROWTILES * 128 * 8 : 0) + 15) & ~15;
+    static constexpr int OUT_WARP = 32 * 80;
     static constexpr int SMEM = 1024 + OFF_ML + (F8 ? TC_ROWTILES * 128 * 8 : 0);
+    static constexpr int SMEM_WHOLE = F8 ? SMEM : 1024 + OFF_OUT + 8 * OUT_WARP;
 };
-static_assert(TcLayout<false>::SMEM <= 227 * 1024 - 64 && TcLayout<true>::SMEM <= 227 * 1024 - 64,
+static_assert(TcLayout<false>::SMEM_WHOLE <= 227 * 1024 - 64 && TcLayout<true>::SMEM <= 227 * 1024 - 64,
               "shared memory budget");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float RESCALE_THRESHOLD = 8.f;
@@ -309,13 +313,22 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     }
     return ok;
 }
+// The same, looking for a while before it reads the clock and the abort flag: every look that they delay
+// lengthens the chain of a stage (S, its softmax, P V, S again), which is what bounds direct plans.
+__device__ __forceinline__ bool eager_wait(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
+    bool ok = false;
+    for (int i = 0; i < 128 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return warp_wait(bar, parity, abortp, meta);
+}
 // The same by a call where the first look does not settle it, for the 8-bit
 // pools' kernel, whose roles have to share the instruction cache.
 __device__ __noinline__ bool long_wait(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
     return thread_wait(bar, parity, abortp, meta);
 }
-template <bool F8>
+template <bool F8, bool WHOLE = false>
 __device__ __forceinline__ bool warp_wait_(uint32_t bar, uint32_t parity, volatile int* abortp, DevMeta* meta) {
+    if constexpr (!F8 && WHOLE) return eager_wait(bar, parity, abortp, meta);
     if constexpr (!F8) return warp_wait(bar, parity, abortp, meta);
     return __all_sync(0xffffffffu, mbar_test(bar, parity) || long_wait(bar, parity, abortp, meta));
 }
@@ -825,11 +838,13 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             return true;
         };
         auto wait = [&](uint32_t wb, uint32_t parity) {
-            if constexpr (DRAFT || WHOLE) return warp_wait(wb, parity, abortp, a.meta);
+            if constexpr (WHOLE) return eager_wait(wb, parity, abortp, a.meta);
+            if constexpr (DRAFT) return warp_wait(wb, parity, abortp, a.meta);
             return thread_wait(wb, parity, abortp, a.meta);
         };
         if (DRAFT || WHOLE || lane == 0) {
             const uint32_t sQ = base + OFF_Q + my_r * TC_QTILE;
+            const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(base + OFF_K, 16, 1024), dv = sdesc(base + OFF_V, TC_HALF, 1024);
             int32_t g = 0, js = 0, qc = 0;
             bool ok = true, any = false;
             int32_t t = t_begin, u = u0;
@@ -856,7 +871,17 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                             const uint32_t stage = base + OFF_K + slot * TC_RING_STAGE;
                             const uint32_t id = idesc_bf16(128, 16 * ntiles, 0, 0);
                             const uint32_t dS = tmem + my_r * 256 + 128 + b * 64;
-                            if (one()) {
+                            if constexpr (WHOLE) {   // descriptors by one addition each
+                                if (one()) {
+                                    const uint64_t dK = sdesc_at(dk, slot * TC_RING_STAGE);
+#pragma unroll
+                                    for (int kk = 0; kk < 8; ++kk)
+                                        umma_bf16(dS, sdesc_at(dq, (kk >> 2) * 16384 + (kk & 3) * 32),
+                                                  sdesc_at(dK, (kk >> 2) * TC_HALF + (kk & 3) * 32), id, kk > 0);
+                                    umma_commit(bar(B_S_FULL + 2 * my_r + b));
+                                    umma_commit(bar(B_K_EMPTY + slot));
+                                }
+                            } else if (one()) {
 #pragma unroll
                                 for (int kk = 0; kk < 8; ++kk) {
                                     const uint32_t qoff = (kk >> 2) * 16384 + (kk & 3) * 32;
@@ -881,7 +906,17 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                             const uint32_t vst = base + OFF_V + slot * TC_RING_STAGE;
                             const uint32_t id = idesc_bf16(128, 128, 0, 1);
                             const uint32_t tP = tmem + my_r * 256 + 128 + b * 64;   // 16 tokens per 8 columns
-                            if (one()) {
+                            if constexpr (WHOLE) {
+                                if (one()) {
+                                    const uint64_t dV = sdesc_at(dv, slot * TC_RING_STAGE);
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        if (kk < ntiles)
+                                            umma_bf16_ta(tmem + my_r * 256, tP + kk * 8, sdesc_at(dV, kk * 2048), id, kk > 0 || k > 0);
+                                    umma_commit(bar(B_PV_DONE + 2 * my_r + b));
+                                    umma_commit(bar(B_V_EMPTY + slot));
+                                }
+                            } else if (one()) {
                                 for (int kk = 0; kk < ntiles; ++kk)
                                     umma_bf16_ta(tmem + my_r * 256, tP + kk * 8, sdesc(vst + kk * 2048, TC_HALF, 1024),
                                                  id, kk > 0 || k > 0);
@@ -931,6 +966,30 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             const int row = row_of(V);
             const bool v_ok = row < V.n_rows;
             const AttnRow RR = v_ok ? unit_row(pl, V, row) : AttnRow{0, 0};
+            if constexpr (WHOLE && !F8) {
+                // two rows an instruction (sixteen lanes each), so that a request covers whole lines: a row
+                // a lane, 16 bytes at a time, took 4,000 cycles for the 256 rows
+                const int32_t from = v_ok ? RR.q_row : -1;
+                const int ch = lane & 15;
+#pragma unroll
+                for (int i0 = 0; i0 < 16; i0 += 8) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int32_t q_row = __shfl_sync(0xffffffffu, from, 2 * (i0 + i) + (lane >> 4));
+                        v[i] = q_row >= 0 ? __ldg(reinterpret_cast<const uint4*>(Q + (int64_t)q_row * D) + ch) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int tr = sub * 32 + 2 * (i0 + i) + (lane >> 4);
+                        *reinterpret_cast<uint4*>(sQ + (ch >> 3) * 16384 + tr * 128 + (((ch & 7) ^ (tr & 7)) << 4)) = v[i];
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_Q_FULL + r));
+                return RR;
+            }
             const uint4* q = reinterpret_cast<const uint4*>(Q + (int64_t)RR.q_row * D);
 #pragma unroll
             for (int ch = 0; ch < 16; ++ch) {
@@ -987,13 +1046,23 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + r) : "memory");
             }
+            if constexpr (WHOLE && !F8) {   // the next chunk's Q, on its way to L2 meanwhile
+                if (u + 1 < pl.n_units && cend < t_end) {
+                    const AttnUnit& V = pl.units[u + 1];
+                    if (row_of(V) < V.n_rows) {
+                        const char* q = reinterpret_cast<const char*>(Q + (int64_t)unit_row(pl, V, row_of(V)).q_row * D);
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128));
+                    }
+                }
+            }
             const int32_t k0 = F8 && tiles.split ? r : 0, k_step = F8 && tiles.split ? 2 : 1;
             float m_ref = -INFINITY, l = 0.f;
             for (int32_t k = k0; k < nst && ok; k += k_step, ++js) {
                 const int32_t st = t + 4 * k;
                 const int ntiles = min(4, cend - st);
                 const int b = js & 1;
-                ok = warp_wait_<F8>(bar(B_S_FULL + 2 * r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
+                ok = warp_wait_<F8, WHOLE>(bar(B_S_FULL + 2 * r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
                 if (!ok) break;
                 tc_fence_after();
                 if ((DRAFT || F8) && row - lane >= U.n_rows) {
@@ -1230,7 +1299,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
             g += nst;
             // chunk done: O after the last PV -> partial row
-            ok = warp_wait_<F8>(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u, abortp, a.meta);
+            ok = warp_wait_<F8, WHOLE>(bar(B_PV_DONE + 2 * r + ((js - 1) & 1)), (uint32_t)((js - 1) >> 1) & 1u, abortp, a.meta);
             if (!ok) break;
             tc_fence_after();
             const int32_t prow = U.prow_base + (c - U.cfirst) * U.n_rows + row;
@@ -1294,6 +1363,48 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
             const bool whole = WHOLE && U.nchunks == 1;   // no other partial: O / l is the output row
             const float inv = 1.f / l;
+            if constexpr (WHOLE && !F8) {
+                // 64 bytes of each of the warp's rows at a time through shared memory, so that a store
+                // covers whole sectors of eight rows
+                unsigned char* box = sm + Y::OFF_OUT + (warp - Y::SOFTMAX_WARP0) * Y::OUT_WARP;
+                const int32_t to = !valid ? -1 : whole ? unit_row(pl, U, row).q_row : prow;
+                char* base_out = whole ? static_cast<char*>(a.out) : reinterpret_cast<char*>(a.part_acc);
+                const int32_t row_bytes = whole ? D * 2 : D * 4;
+                auto send = [&](const uint4 (&x)[4], int32_t at) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + lane * 80 + i * 16) = x[i];
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 8 * i + (lane >> 2);
+                        const int32_t out_row = __shfl_sync(0xffffffffu, to, rr);
+                        const uint4 y = *reinterpret_cast<const uint4*>(box + rr * 80 + (lane & 3) * 16);
+                        if (out_row >= 0)
+                            *reinterpret_cast<uint4*>(base_out + (int64_t)out_row * row_bytes + at + (lane & 3) * 16) = y;
+                    }
+                    __syncwarp();
+                };
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tl + c0, v);
+                    tmem_wait_ld(v);
+                    if (whole) {
+                        send({out_words(v, inv), out_words(v + 8, inv), out_words(v + 16, inv), out_words(v + 24, inv)}, c0 * 2);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 16)
+                            send({make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]), make_uint4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]),
+                                  make_uint4(v[i + 8], v[i + 9], v[i + 10], v[i + 11]), make_uint4(v[i + 12], v[i + 13], v[i + 14], v[i + 15])},
+                                 (c0 + i) * 4);
+                    }
+                }
+                if (valid && !whole) a.part_ml[prow] = make_float2(m_ref, l);
+                tc_fence_before();
+                t = cend;
+                ++u;
+                continue;
+            }
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
             if (whole && valid) out += (int64_t)unit_row(pl, U, row).q_row * D;
 #pragma unroll 1
@@ -1332,10 +1443,11 @@ namespace dendrite {
 template <bool DRAFT, bool F8, bool CUT, bool WHOLE = false>
 static int setup_one() {
     constexpr auto fn = k_attn_partial_tc<DRAFT, F8, CUT, WHOLE>;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLayout<F8>::SMEM) != cudaSuccess)
+    constexpr int smem = WHOLE ? TcLayout<F8>::SMEM_WHOLE : TcLayout<F8>::SMEM;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return DENDRITE_ECUDA;
     int occ = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, TcLayout<F8>::THREADS, TcLayout<F8>::SMEM) !=
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, TcLayout<F8>::THREADS, smem) !=
             cudaSuccess ||
         occ != 1)
         return DENDRITE_ECUDA;   // the kernel's 512 TMEM columns need exactly one CTA per SM
@@ -1360,7 +1472,7 @@ template <bool F8, bool CUT>
 static void launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int n_ctas, cudaStream_t s) {
     using Y = TcLayout<F8>;
     if (a.plan.masks) k_attn_partial_tc<true, F8, CUT, false><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
-    else if (a.plan.direct) k_attn_partial_tc<false, F8, CUT, true><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
+    else if (a.plan.direct) k_attn_partial_tc<false, F8, CUT, true><<<n_ctas, Y::THREADS, Y::SMEM_WHOLE, s>>>(mk, mv, a);
     else k_attn_partial_tc<false, F8, CUT, false><<<n_ctas, Y::THREADS, Y::SMEM, s>>>(mk, mv, a);
 }
 
