@@ -38,7 +38,6 @@
 #include <algorithm>
 #include <cmath>
 #include <climits>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
@@ -1643,6 +1642,7 @@ struct HostPlan {
     std::vector<AttnXTile> xtiles;   // the same for the kernels (branch handles)
     std::vector<uint64_t> masks;     // draft trees: drafted tokens each query sees
     std::vector<int32_t> splits;     // direct plans: units split over CTAs
+    bool cross = false;              // cross attention (set per call)
     bool direct = false;             // see AttnPlanDev::direct
     std::vector<SegPlan> segplan;
     PlanHeader hdr{};
@@ -1677,6 +1677,7 @@ struct ClassWeights {
     int64_t unit_start;
     int32_t row_shift;         // a unit start also weighs n_rows >> row_shift (-1: no row term)
     int64_t min_per_cta;       // smallest total weight worth a CTA of its own
+    int32_t tile1 = 2, tile2 = 3;   // a tile of a unit with one row tile, and with two
 };
 constexpr ClassWeights kSmallWeights{10, 2, 8};
 // 8-bit pools' small kernel reads a tile in half the time (88 SM ns) and starts a
@@ -1690,10 +1691,13 @@ constexpr ClassWeights kSmallWeightsFp8{30, 2, 8};
 inline const ClassWeights& small_weights(const dendrite_pool* p) {
     return p->dtype == DENDRITE_FP8 ? kSmallWeightsFp8 : kSmallWeights;
 }
-static int EV(const char* n,int d){const char* e=getenv(n);return e?atoi(e):d;}
-static ClassWeights kTcWeights{EV("US",24)*20, -1, 32*20};
-static int W1=EV("W1",40);
-inline int64_t tile_weight(int rt) { return rt==1?W1:20*(1 + rt); }
+constexpr ClassWeights kTcWeights{24, -1, 32};
+// Direct plans (cross attention on the tcgen05 kernel alone), in halves of that: the work is the
+// stages' chains rather than HBM, so one row tile takes nearly what two take, and a start (Q, the
+// way out) 27 tiles.  16 prompts of 448 tokens over 1,500 states 129 -> 125 us, 4 of 515 with 4 heads a kv
+// head over 6,404 (units of 256 rows and of 12) 216 -> 205.
+constexpr ClassWeights kTcDirectWeights{160, -1, 64, 5, 6};
+inline int64_t tile_weight(const ClassWeights& cw, int rt) { return rt == 1 ? cw.tile1 : rt == 2 ? cw.tile2 : 1 + rt; }
 inline int64_t start_weight(const ClassWeights& cw, int32_t n_rows) {
     return cw.unit_start + (cw.row_shift >= 0 ? (n_rows >> cw.row_shift) : 0);
 }
@@ -1723,7 +1727,7 @@ void partition_class(HostPlan& hp, int32_t u_lo, int32_t u_hi, int64_t T, int64_
         for (int32_t ui = u_lo; ui < u_hi; ++ui) {
             const AttnUnit& U = hp.units[ui];
             const int64_t nb = U.n_blk;
-            const int64_t tw = tile_weight(U.rt);
+            const int64_t tw = tile_weight(cw_, U.rt);
             const int64_t us = start_weight(cw_, U.n_rows);
             const int64_t uw = us + nb * tw;
             while (c < C0 && target < cw + uw) {
@@ -1910,6 +1914,10 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
         n_members_total += sg.n_members;
     }
     if (n_units_total >= (size_t)INT32_MAX / 2) return DENDRITE_ELIMIT;
+    const bool direct = hp.cross && bf16 && std::all_of(hp.psegs.begin(), hp.psegs.end(), [&](const Segment& sg) {
+        return tc_on && sg.n_members == 1 && RM > hp.tc_rows;
+    });
+    const ClassWeights& tcw = direct ? kTcDirectWeights : kTcWeights;
     // By default only plans whose host expansion rivals the kernels' work go
     // to the device: many units (the expansion's cost) of few tiles each (the
     // kernels' work).  Elsewhere the host expansion hides behind the device's
@@ -1929,7 +1937,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
     int64_t n_rows = 0;
     for (int pass = 0; pass < 2; ++pass) {
         PlanClass& pc = hp.hdr.cls[pass];
-        const ClassWeights& cwt = pass == 0 ? kTcWeights : small_weights(p);
+        const ClassWeights& cwt = pass == 0 ? tcw : small_weights(p);
         pc = PlanClass{};
         pc.u_lo = n_unit;
         pc.s_lo = (int32_t)hp.segplan.size();
@@ -1977,8 +1985,8 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
             }
             sp.row_base = (int32_t)n_rows;
             sp.wbase = weight;
-            sp.w_full = (int32_t)(start_weight(cwt, group_rows) + (int64_t)S.n_blk * tile_weight(sp.rt_full));
-            sp.w_last = (int32_t)(start_weight(cwt, sp.rows_last) + (int64_t)S.n_blk * tile_weight(sp.rt_last));
+            sp.w_full = (int32_t)(start_weight(cwt, group_rows) + (int64_t)S.n_blk * tile_weight(cwt, sp.rt_full));
+            sp.w_last = (int32_t)(start_weight(cwt, sp.rows_last) + (int64_t)S.n_blk * tile_weight(cwt, sp.rt_last));
             hp.segplan.push_back(sp);
             const int64_t units = (int64_t)nkv * S.ngroups;
             n_unit += (int32_t)units;
@@ -2004,7 +2012,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
                 max_ctas = std::min(max_ctas, (p->sm_count - n) * p->attn_ctas_per_sm);
             }
         }
-        ct.c0 = ct.u_hi > ct.u_lo ? class_ctas(ct.weight, max_tc_ctas, kTcWeights) : 0;
+        ct.c0 = ct.u_hi > ct.u_lo ? class_ctas(ct.weight, max_tc_ctas, tcw) : 0;
         cs.c0 = cs.u_hi > cs.u_lo ? class_ctas(cs.weight, max_ctas, small_weights(p)) : 0;
     }
     if (n_rows >= INT32_MAX / 2) return DENDRITE_ELIMIT;
@@ -2046,7 +2054,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
                 }
             }
         }
-        partition_class(hp, 0, hp.n_tc_units, hp.hdr.cls[0].tiles, hp.hdr.cls[0].weight, max_tc_ctas, kTcWeights,
+        partition_class(hp, 0, hp.n_tc_units, hp.hdr.cls[0].tiles, hp.hdr.cls[0].weight, max_tc_ctas, tcw,
                         hp.tc_cta_begin, hp.tc_cta_unit);
         partition_class(hp, hp.n_tc_units, (int32_t)hp.units.size(), hp.hdr.cls[1].tiles, hp.hdr.cls[1].weight,
                         max_ctas, small_weights(p), hp.cta_begin, hp.cta_unit);
@@ -2642,6 +2650,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
         static thread_local HostPlan hp;
         hp.clear();
         hp.tc_rows = parents ? p->tc_min_rows_draft : p->tc_min_rows;
+        hp.cross = cross;
         if (grow) {
             hp.psegs = pc.segs;
             hp.seg_members = pc.seg_members;
@@ -2900,6 +2909,7 @@ extern "C" int dendrite_tree_attn_decode_noalloc(dendrite_pool* p, const void* Q
     static thread_local HostPlan hp;
     hp.clear();
     hp.tc_rows = p->tc_min_rows;
+    hp.cross = false;
     DENDRITE_TRY(build_plan(p, branches, n, q_len, n_q_heads, p->sm_count * p->attn_ctas_per_sm, tc_ctas(p), hp,
                             false));
     // scratch layout: plan sections, then partial acc rows, then partial (m, l)

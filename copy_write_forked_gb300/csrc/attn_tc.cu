@@ -878,8 +878,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                                     for (int kk = 0; kk < 8; ++kk)
                                         umma_bf16(dS, sdesc_at(dq, (kk >> 2) * 16384 + (kk & 3) * 32),
                                                   sdesc_at(dK, (kk >> 2) * TC_HALF + (kk & 3) * 32), id, kk > 0);
-                                    umma_commit(bar(B_S_FULL + 2 * my_r + b));
-                                    umma_commit(bar(B_K_EMPTY + slot));
+                                    umma_commit(bar(B_S_FULL + 2 * my_r + b));   // (the softmax gives the K slot back)
                                 }
                             } else if (one()) {
 #pragma unroll
@@ -1065,6 +1064,8 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 ok = warp_wait_<F8, WHOLE>(bar(B_S_FULL + 2 * r + b), (uint32_t)(js >> 1) & 1u, abortp, a.meta);
                 if (!ok) break;
                 tc_fence_after();
+                // (a commit takes its issuer some 150 cycles, an arrival next to nothing)
+                if (WHOLE && !F8 && sub == 0 && lane == 0) mbar_arrive(bar(B_K_EMPTY + (g + k) % TC_NSTAGE));
                 if ((DRAFT || F8) && row - lane >= U.n_rows) {
                     // a warp without a row of the unit: its rows of Q are zero,
                     // hence of S, which is zero as P too; it only passes the buffer on
