@@ -300,7 +300,14 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
     char* vp = a.vp + blockIdx.y * a.pool_layer;
     const int64_t tile_bytes = FP8 ? kFp8TileBytes : (int64_t)bs * dim * (int)sizeof(T);
     if (__any_sync(0xffffffffu, status)) return;   // a whole warp leaves: shuffles below
-    for (int32_t t = blockIdx.x; t < a.n_tiles; t += gridDim.x) {
+    // this CTA's share of all tiles' rows (tile after tile, each its K, V and Q heads)
+    const int64_t all = (int64_t)a.n_tiles * n_rows;
+    int64_t at_row = all * blockIdx.x / gridDim.x;
+    const int64_t end_row = all * (blockIdx.x + 1) / gridDim.x;
+    for (int32_t t = (int32_t)(at_row / n_rows); at_row < end_row; ++t) {
+        const int32_t row0 = (int32_t)(at_row - (int64_t)t * n_rows);
+        const int32_t row1 = (int32_t)min((int64_t)n_rows, row0 + (end_row - at_row));
+        at_row += row1 - row0;
         int32_t first;
         const int32_t i = find_branch(args, 2 * (int64_t)n, n, t, a.uniform, first);
         const int32_t L = args[n + i];
@@ -324,14 +331,14 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
             const int32_t tok = lblk * bs + slot - L;       // 0 .. n_new - 1
             const int64_t in_row = (int64_t)i * a.n_new + tok;
             const int64_t kv_at = in_row * a.n_kv * dim, q_at = in_row * a.nq * dim;
-            const int32_t n_iter = (n_rows + rstep * (int)gridDim.z - 1) / (rstep * (int)gridDim.z);
+            const int32_t n_iter = (row1 - row0 + rstep - 1) / rstep;
             float cs[8], sn[8];
             for (int32_t it0 = 0; it0 < n_iter; it0 += U) {
                 Chunk<T> x[U], y[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int32_t rr = ((it0 + u) * (int)gridDim.z + (int)blockIdx.z) * rstep + r0;
-                    if (!live || rr >= n_rows) continue;
+                    const int32_t rr = row0 + (it0 + u) * rstep + r0;
+                    if (!live || rr >= row1) continue;
                     const T* src = rr < a.n_kv       ? K + kv_at + rr * dim
                                    : rr < 2 * a.n_kv ? V + kv_at + (rr - a.n_kv) * dim
                                                      : Q + q_at + (rr - 2 * a.n_kv) * dim;
@@ -356,8 +363,8 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int32_t rr = ((it0 + u) * (int)gridDim.z + (int)blockIdx.z) * rstep + r0;
-                    const bool act = live && rr < n_rows;
+                    const int32_t rr = row0 + (it0 + u) * rstep + r0;
+                    const bool act = live && rr < row1;
                     const int32_t kind = rr < a.n_kv ? 0 : rr < 2 * a.n_kv ? 1 : 2;   // K, V, Q
                     const int32_t h = rr - (kind == 0 ? 0 : kind == 1 ? a.n_kv : 2 * a.n_kv);
                     float f[8], g[8];
@@ -432,14 +439,14 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
         }
         // bf16: V behind the branch's new end becomes finite
         if (!FP8 && sizeof(T) == 2 && unclean)
-            for (int32_t h = blockIdx.z; h < a.n_kv; h += gridDim.z) {
+            for (int32_t h = max(0, row0 - a.n_kv); h < min(a.n_kv, row1 - a.n_kv); ++h) {
                 uint4* to = reinterpret_cast<uint4*>(vp + ((int64_t)dst * a.n_kv + h) * tile_bytes);
                 for (int32_t w = s1 * (dim / 8) + threadIdx.x; w < bs * (dim / 8); w += 128) to[w] = make_uint4(0u, 0u, 0u, 0u);
             }
         // the valid slots of a copied-on-write tail, stored rows as they are
         if (csrc >= 0 && s0 > 0) {
             const int32_t words = FP8 ? kFp8Dim / 16 : dim * (int)sizeof(T) / 16;
-            for (int32_t r = blockIdx.z; r < 2 * a.n_kv; r += gridDim.z) {
+            for (int32_t r = row0; r < min(row1, 2 * a.n_kv); ++r) {
                 char* pool = r < a.n_kv ? kp : vp;
                 const int32_t h = r < a.n_kv ? r : r - a.n_kv;
                 const char* from = pool + ((int64_t)csrc * a.n_kv + h) * tile_bytes;
@@ -984,10 +991,13 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* stage
     int32_t lanes = 128 / (a.dim / 16), tp = 1;
     while (lanes & (lanes - 1)) lanes &= lanes - 1;
     while (tp < lanes && tp < std::min(n_new, bs)) tp *= 2;
-    // (rotating rows: as many as run at once, for each CTA makes the angles anew:
-    // 32 x 16 tokens of 48 heads 8 us, and 10 with 8 an SM)
-    const unsigned z = head_splits(p, c.touched * c.n_layers_in, (n_rows + lanes / tp - 1) / (lanes / tp), c.rope ? 4 : 8);
-    const dim3 grid((unsigned)std::min<int64_t>(c.touched, (int64_t)p->sm_count * 64), (unsigned)c.n_layers_in, z);
+    // As many CTAs as run at once, the rows shared out evenly among them, or one for as many rows as it
+    // takes at a time where those are fewer (of more, each makes the angles anew: 32 x 16 tokens of 48
+    // heads 8 us, and 10 with 8 an SM; with one CTA per tile 12,432 tokens of 36 heads into an
+    // 8-bit pool, 1.3 waves of them, took VIDEO us).
+    const int64_t resident = (c.rope ? 4 : 8) * (int64_t)p->sm_count;
+    const int64_t parts = c.touched * ((n_rows + lanes / tp - 1) / (lanes / tp));
+    const dim3 grid((unsigned)std::max<int64_t>(1, std::min(parts, resident / c.n_layers_in)), (unsigned)c.n_layers_in);
     auto go = [&](auto args) -> int {
         using A = decltype(args);
         if (p->dtype == DENDRITE_FP8 && !c.rope)
