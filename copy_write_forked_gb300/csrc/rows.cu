@@ -651,7 +651,7 @@ struct ForkRowsArgs {
 constexpr int kForkRowsThreads = 256;
 
 template <typename A>
-__global__ void __launch_bounds__(kForkRowsThreads, 6) k_fork_rows(const __grid_constant__ A args, const __grid_constant__ ForkRowsArgs a) {
+__global__ void __launch_bounds__(kForkRowsThreads, 8) k_fork_rows(const __grid_constant__ A args, const __grid_constant__ ForkRowsArgs a) {
     pdl_wait();
     constexpr int bs = kBlockSize, NT = kForkRowsThreads, U = 4;
     __shared__ int32_t src_blk[64 * bs];
@@ -857,8 +857,8 @@ int launch_fork_rows(dendrite_pool* p, const ForkRows& c, cudaStream_t s) {
         }
     };
     // as many CTAs as run at once (each adds one to the count of the finished)
-    const int64_t most = 6 * (int64_t)p->sm_count;
-    const unsigned z = head_splits(p, c.items * p->n_layers, p->n_kv, 6);
+    const int64_t most = 8 * (int64_t)p->sm_count;
+    const unsigned z = head_splits(p, c.items * p->n_layers, p->n_kv, 8);
     const dim3 grid((unsigned)std::max<int64_t>(1, std::min(c.items, most / (p->n_layers * (int64_t)z))), (unsigned)p->n_layers, z);
     return with_words(p, 8 * n, s, fill, [&](auto args) -> int {
         DENDRITE_CUDA(launch_pdl(k_fork_rows<decltype(args)>, grid, dim3(kForkRowsThreads), 0, s, args, a));
