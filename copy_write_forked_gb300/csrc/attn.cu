@@ -2263,8 +2263,14 @@ void find_direct(const dendrite_pool* p, HostPlan& hp, int32_t n) {
     for (int32_t i = 0; i < n; ++i)
         if (hp.path_off[i + 1] - hp.path_off[i] > 1) return;
     hp.direct = true;
-    for (int32_t u = 0; u < (int32_t)hp.units.size(); ++u)
-        if (hp.units[u].nchunks > 1) hp.splits.push_back(u);
+    hp.partial_rows = 0;   // only those units have partial rows
+    for (int32_t u = 0; u < (int32_t)hp.units.size(); ++u) {
+        AttnUnit& U = hp.units[u];
+        U.prow_base = (int32_t)hp.partial_rows;
+        if (U.nchunks == 1) continue;
+        hp.splits.push_back(u);
+        hp.partial_rows += (size_t)U.nchunks * U.n_rows;
+    }
 }
 
 // Each query's drafted tokens: bit b of masks[i][j] is set if node b is node j
