@@ -219,6 +219,13 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
     return d;
 }
 // The largest of three (a NaN counts for nothing, as in fmaxf).
+// Adds a pair's two bf16 to two fp32 sums.
+__device__ __forceinline__ void add_bf16(float& a, float& b, uint32_t x) {
+    uint16_t lo, hi;
+    asm("mov.b32 {%0, %1}, %2;" : "=h"(lo), "=h"(hi) : "r"(x));
+    asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(a) : "h"(lo));
+    asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(b) : "h"(hi));
+}
 __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
@@ -1025,7 +1032,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             const int row = row_of(U);
             const bool valid = row < U.n_rows;
             const AttnRow R = staged_u == u ? staged_R : stage_q(U);
-            if (!F8 && U.n_blk > U.n_shared) {
+            if (!F8 && !WHOLE && U.n_blk > U.n_shared) {   // (no unit of a direct plan is packed)
                 // a packed unit: its extra tiles' logical blocks, member masks
                 // and held tokens into shared memory, once every warp of the row tile
                 // is done with the previous unit's (the plan keeps them to
@@ -1156,7 +1163,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 // mask stage columns past the chunk and positions the row does
                 // not see (only stages some row of the warp does not fully see)
                 const int32_t ti0 = st - U.tile_off;
-                if (ti0 + ntiles <= U.n_shared) {
+                if (WHOLE || ti0 + ntiles <= U.n_shared) {
                     const int32_t vis = min(ntiles * BS, R.limit - (U.blk_start + ti0) * BS);
                     if (!__all_sync(0xffffffffu, vis >= TC_TOK)) {
                         if constexpr (DRAFT) {
@@ -1248,15 +1255,14 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 uint32_t pk[32];
                 if constexpr (WHOLE) {   // the same sums, two to an instruction
                     const f32x2 scale2 = pair(a.scale_log2, a.scale_log2), nref2 = pair(nref, nref);
-                    f32x2 l2[4] = {0, 0, 0, 0};
+                    float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const f32x2 x = fma2(pair(s[2 * i], s[2 * i + 1]), scale2, nref2);
                         pk[i] = pack_bf16(ex2_approx(low(x)), ex2_approx(high(x)));
-                        l2[i & 3] = add2(l2[i & 3], pair(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u)));
+                        add_bf16(l8[(2 * i) & 7], l8[(2 * i + 1) & 7], pk[i]);
                     }
-                    const f32x2 ls = add2(add2(l2[0], l2[1]), add2(l2[2], l2[3]));
-                    l += low(ls) + high(ls);
+                    l += ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
                 } else {
                     float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
