@@ -2259,7 +2259,9 @@ int launch_plan_expand(dendrite_pool* p, char* d, const size_t* off, int32_t n_u
 // Cross attention: whether the tcgen05 kernel may write the rows of whole units out itself, and
 // which units it does not run whole (AttnPlanDev::direct).
 void find_direct(const dendrite_pool* p, HostPlan& hp, int32_t n) {
-    if ((p->dtype != DENDRITE_BF16 && p->dtype != DENDRITE_FP8) || hp.device || hp.n_tc_units != (int32_t)hp.units.size()) return;
+    if ((p->dtype != DENDRITE_BF16 && p->dtype != DENDRITE_FP8) || hp.device || !hp.xtiles.empty() ||
+        hp.n_tc_units != (int32_t)hp.units.size())
+        return;
     for (int32_t i = 0; i < n; ++i)
         if (hp.path_off[i + 1] - hp.path_off[i] > 1) return;
     hp.direct = true;
