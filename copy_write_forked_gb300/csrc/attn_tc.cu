@@ -680,6 +680,20 @@ __device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint3
 // CUT: bf16, some branch was rolled back into a block, where V rows may stand behind
 // its end (8-bit pools' V is cleared there as it is converted, in every call).
 // WHOLE: direct plans (cross attention), whose units that one CTA runs whole are written out here.
+// Nothing there waits for HBM (256 rows a unit, several units a KV head through L2), so the roles' chains
+// and instructions are what a stage takes, 1,700 cycles of which the products need 1,280 (S with N = 64
+// reads its operands from shared memory for longer than it multiplies).  4 prompts of 515 tokens, 32
+// heads, over 6,404 states (215 GFLOP): 176 us, 1.2 PFLOP/s, tensor pipe 57 %; 16 prompts of 448, 16
+// heads, over 1,500 (86 GFLOP, a unit starts every 24 stages): 102 us.  On the way there, as whole calls:
+//   - partial rows for every unit and the general merge: 248 / 229 us
+//   - rows of whole units written here, split units merged by unit: 238 / 138
+//   - elected issuers, packed fp32 arithmetic: 216 / 130
+//   - tiles and starts weighed by what they take here: 205 / 124
+//   - Q in and rows out in whole lines, Q on its way to L2 a unit ahead, descriptors by additions: 193 / 120
+//   - K slots given back by the softmax, row sums by mixed additions: 188 / 115
+// Tried there and left: S in one buffer and P in two of its own, so that S is issued a stage ahead (196 /
+// 120: the softmax warps then all compute at once, and have more waits), a quarter of the exponentials as
+// polynomials (209 / 122: instructions are short, not the SFU).
 template <bool DRAFT, bool F8, bool CUT, bool WHOLE>
 __global__ void __launch_bounds__(TcLayout<F8>::THREADS, 1)
 k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,

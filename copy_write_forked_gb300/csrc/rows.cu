@@ -4,7 +4,8 @@
 // rotary positions and the 8-bit quantisation, so that a row is read once and
 // written once.
 //
-// Rotary positions.  Pair i of a head (elements (i, i + r/2), or (2 i, 2 i + 1)
+// Rotary positions.  (Given positions turn a pair by the one of its axis; else a token's is its
+// branch's length and its place.)  Pair i of a head (elements (i, i + r/2), or (2 i, 2 i + 1)
 // when interleaved; r = rot_dim) turns by a = position * inv_freq[i]:
 //     y1 = m (x1 cos a - x2 sin a),   y2 = m (x2 cos a + x1 sin a).
 // The angle is kept in turns, as a 64-bit fixed-point fraction: position *
@@ -632,7 +633,11 @@ __global__ void __launch_bounds__(128) k_keep_rows(const __grid_constant__ A arg
 //
 // Rows are stored bits, moved 16 bytes a thread with the rows' sources (block
 // and slot, looked up once per row and head into shared memory) ahead of them;
-// a tile's writes are contiguous, its reads are whole rows anywhere.
+// a tile's writes are contiguous, its reads are whole rows anywhere.  Bound by HBM:
+// 16 x 2,048 rows of 8 heads in bf16, each head its own: 45 us for 268 MB (6.0 TB/s); 32 x 4,000
+// 8-bit rows of 8 heads: 99 us at 6.0 TB/s, 600 MB for 528 (the exponent bytes, and tiles
+// whose ends share a sector).  Six CTAs an SM: 50 and 105 us; fewer with more loads in flight
+// each: more.
 struct ForkRowsArgs {
     int32_t n, bpb, n_kv, n_blocks, uniform, n_items, blocks;
     int32_t k_words, v_words, k_shift, v_shift;   // 16-byte words of a row, and the power of two at or above
@@ -993,8 +998,8 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* stage
     while (tp < lanes && tp < std::min(n_new, bs)) tp *= 2;
     // As many CTAs as run at once, the rows shared out evenly among them, or one for as many rows as it
     // takes at a time where those are fewer (of more, each makes the angles anew: 32 x 16 tokens of 48
-    // heads 8 us, and 10 with 8 an SM; with one CTA per tile 12,432 tokens of 36 heads into an
-    // 8-bit pool, 1.3 waves of them, took VIDEO us).
+    // heads 8 us, and 10 with 8 an SM; one CTA per tile, 1.3 waves of them, took 56 us for 12,432
+    // tokens of 36 heads into an 8-bit pool that take 50 this way).
     const int64_t resident = (c.rope ? 4 : 8) * (int64_t)p->sm_count;
     const int64_t parts = c.touched * ((n_rows + lanes / tp - 1) / (lanes / tp));
     const dim3 grid((unsigned)std::max<int64_t>(1, std::min(parts, resident / c.n_layers_in)), (unsigned)c.n_layers_in);

@@ -21,7 +21,24 @@
 // Sums decide which token a number falls to, and a vocabulary of 2^17 tokens puts
 // borders 2^-17 apart: fp32 sums would move some.  They are held as pairs of
 // floats (48 bits) with the error of every addition and product carried along,
-// fp64 adds being 1/64 of the fp32 rate here.
+// fp64 adds being 1/64 of the fp32 rate here (with fp64 in the walk and in the
+// joins of the sums a pass took 12 us where it takes 5).
+//
+// What bounds it is the chain of a sequence's passes: the gather (two dependent
+// loads), one pass over the last node's rows, and one for every second and later
+// refusal at a node.  A pass that finds its rows held takes some 8,000 cycles where
+// all SMs work on two CTAs (4,000 sums, 2,000 exchange between the CTAs, 2,000
+// walk), 2 us alone.  32 trees of 24 nodes, 128,256 tokens in fp32, six passes in
+// the longest: 45 us (33 MB that have to be read: 5 us); 256 sequences of 7 certain
+// drafts, 50,257 tokens in bf16: 31 us (26 MB); one of 5 in a row, 32,000 tokens: 14 us
+// (16 CTAs).  On the way there, in these cases:
+//   - rows read anew in every pass, an element a load, sums joined in fp64: 97 / 93 us
+//   - 16-byte words, held between passes, 16 CTAs a sequence in two waves: 55 / 79
+//   - as many CTAs a sequence as fit one wave, packed fp32 pairs without fp64: 49 / 40
+//   - certain drafts' sums by subtraction, only warps that lost a token anew: 47 / 36
+//   - short additions below the largest weight: 45 / 31
+// Half the threads a CTA and twice the CTAs: 45 / 33, and 28 us in place of 23 where
+// every sequence takes one pass.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -318,10 +335,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
     const int64_t i = blockIdx.x / cs;
     const T* P = static_cast<const T*>(a.target) + i * (1 + nd) * a.target_stride;
     const T* Q = static_cast<const T*>(a.draft) + i * nd * a.draft_stride;
-    // the nodes: gathered by the first CTA, fetched by the others
     // the rows that node t, and (warp 0, which walks) node 32 + t hang on
     const int32_t up = t < nd ? tree((a.one_tree ? 0 : i * nd) + t) : -1;
     const int32_t up1 = warp == 0 && 32 + lane < nd ? tree((a.one_tree ? 0 : i * nd) + 32 + lane) : -1;
+    // the nodes: gathered by the first CTA, fetched by the others
     if (rank == 0) {
         if (t < kMaxDraft) {
             const int32_t x = t < nd ? __ldg(a.tokens + i * nd + t) : -1;
@@ -517,7 +534,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
                 }
             }
             const Pair2 down = two_sum2(sum2.h, pack(-top, -top));
-            sum2 = {down.h, add2(sum2.l, down.l)};
+            sum2 = two_sum2(down.h, add2(sum2.l, down.l));
         }
         if (mine) p_row = row;   // (of one node more tokens may go, none come back)
         if (with_q) q_row = row;
