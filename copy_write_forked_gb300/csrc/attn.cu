@@ -183,7 +183,7 @@ __device__ __forceinline__ void merge_row_wide(const AttnArgs& a, int32_t o, int
     }
     wait_partials(waited);
     if (*reinterpret_cast<volatile const int32_t*>(&a.meta->status)) return;
-    const float inv = pbeg == pend ? 0.f : 1.f / L;   // (cross attention to a branch of no rows: zeros)
+    const float inv = 1.f / L;
     float y[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
     if (a.tq_signs) {
         // compressed pools: the partials live in the rotated space; rotate
@@ -1087,7 +1087,7 @@ __global__ void __launch_bounds__(256, WIDE ? 2 : 1) k_attn_merge(const AttnArgs
     }
     wait_partials(waited);
     if (*reinterpret_cast<volatile const int32_t*>(&a.meta->status)) return;
-    const float inv = pbeg == pend ? 0.f : 1.f / L;
+    const float inv = 1.f / L;
     if constexpr (WIDE) {
         T* dst = static_cast<T*>(a.out) + (int64_t)o * D + 4 * lane;
         if constexpr (sizeof(T) == 2) {
@@ -1239,7 +1239,7 @@ __global__ void __launch_bounds__(256, 3) k_attn_merge_grouped(const AttnArgs a)
     if (*reinterpret_cast<volatile const int32_t*>(&a.meta->status)) return;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
-        const float inv = pbeg == pend ? 0.f : 1.f / L[i];
+        const float inv = 1.f / L[i];
         const int64_t o = ((int64_t)qi * pl.q_len + j) * pl.n_q_heads + h * G + g0 + i;
         T* dst = static_cast<T*>(a.out) + o * D + 4 * lane;
         if constexpr (sizeof(T) == 2) {
@@ -2811,7 +2811,8 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
     a.part_acc = p->d_partial;
     a.part_ml = reinterpret_cast<float2*>(p->d_partial + p->partial_rows_cap * p->head_dim);
     if (!began) prof_begin(p, T_ATTN_TOTAL, s);
-    if (a.plan.direct) {   // no kernel writes the rows of branches without rows: zeros, a run of them at a time
+    DENDRITE_TRY(launch_attention(p, layer, a, s));
+    if (cross) {   // branches without rows: zeros, a run of them at a time (the merge leaves 0 / 0 there, or nothing)
         const size_t each = (size_t)q_len * n_q_heads * p->head_dim * p->elt;
         for (int32_t i = 0, end; i < n; i = end) {
             for (end = i; end < n && p->br[branches[end]].len == 0; ++end) {}
@@ -2819,7 +2820,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
             else ++end;
         }
     }
-    return launch_attention(p, layer, a, s);
+    return DENDRITE_OK;
 }
 
 }  // namespace
