@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "attn_common.cuh"
+#include "attn_f32.h"
 #include "attn_fp8.h"
 #include "rows.h"
 #include "turbo.h"
@@ -1315,6 +1316,40 @@ __global__ void __launch_bounds__(256) k_attn_merge_splits(const AttnArgs a) {
     }
 }
 
+// The same for fp32 (any head_dim), a row a warp.
+__global__ void __launch_bounds__(256) k_attn_merge_splits_f32(const AttnArgs a) {
+    pdl_trigger();
+    const AttnPlanDev& pl = a.plan;
+    const int lane = threadIdx.x & 31, r = (int)blockIdx.y * 8 + (threadIdx.x >> 5), d = a.head_dim;
+    const AttnUnit U = pl.units[pl.splits[blockIdx.x]];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (r >= U.n_rows || *reinterpret_cast<volatile const int32_t*>(&a.meta->status)) return;
+    const int64_t first = (int64_t)U.prow_base + r;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k = lane; k < U.nchunks; k += 32) M = fmaxf(M, __ldcg(a.part_ml + first + (int64_t)k * U.n_rows).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.f : M;
+    for (int k = 0; k < U.nchunks; ++k) {
+        const int64_t row = first + (int64_t)k * U.n_rows;
+        const float2 ml = __ldcg(a.part_ml + row);
+        const float w = exp2f(ml.x - ref);
+        L = fmaf(w, ml.y, L);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (4 * (lane + 32 * j) < d) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_acc + row * d) + lane + 32 * j);
+                acc[j] = make_float4(fmaf(w, x.x, acc[j].x), fmaf(w, x.y, acc[j].y), fmaf(w, x.z, acc[j].z), fmaf(w, x.w, acc[j].w));
+            }
+    }
+    const float inv = 1.f / L;
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + (int64_t)unit_row(pl, U, r).q_row * d);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (4 * (lane + 32 * j) < d) dst[lane + 32 * j] = make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
+}
+
 // ============================================================ host planning
 // A segment as the unit expansion reads it (host or device): its units are
 // unit_base + kv head * ngroups + row group, its tiles (class numbering)
@@ -1643,6 +1678,7 @@ struct HostPlan {
     std::vector<uint64_t> masks;     // draft trees: drafted tokens each query sees
     std::vector<int32_t> splits;     // direct plans: units split over CTAs
     bool cross = false;              // cross attention (set per call)
+    int32_t tiled = 0;               // see AttnPlanDev::tiled
     bool direct = false;             // see AttnPlanDev::direct
     std::vector<SegPlan> segplan;
     PlanHeader hdr{};
@@ -1688,7 +1724,10 @@ constexpr ClassWeights kSmallWeights{10, 2, 8};
 // -> 346; single contexts of any length unchanged.  20 gives 80 us, 40 to 60 62 to 65
 // but more elsewhere.
 constexpr ClassWeights kSmallWeightsFp8{30, 2, 8};
-inline const ClassWeights& small_weights(const dendrite_pool* p) {
+// The tiled fp32 kernel takes the same for a unit of few rows as for a full one.
+constexpr ClassWeights kF32TiledWeights{8, -1, 8};
+inline const ClassWeights& small_weights(const dendrite_pool* p, const HostPlan& hp) {
+    if (hp.tiled) return kF32TiledWeights;
     return p->dtype == DENDRITE_FP8 ? kSmallWeightsFp8 : kSmallWeights;
 }
 constexpr ClassWeights kTcWeights{24, -1, 32};
@@ -1766,7 +1805,8 @@ void partition_class(HostPlan& hp, int32_t u_lo, int32_t u_hi, int64_t T, int64_
 
 int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_len, int32_t nq, int max_ctas,
                 int max_tc_ctas, HostPlan& hp, bool allow_device);
-int unit_rows_small(const dendrite_pool* p);
+void choose_tiled(const dendrite_pool* p, int32_t q_len, int32_t rows_per_member, HostPlan& hp);
+int unit_rows_small(const dendrite_pool* p, const HostPlan& hp);
 
 // max_ctas: CTAs of the mma.sync/fp32 kernel; max_tc_ctas: of the tcgen05
 // kernel (0 when it is not used).  The segments (after folding) are left in
@@ -1776,7 +1816,6 @@ int build_plan(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_l
     const int32_t G = nq / p->n_kv, nkv = p->n_kv;
     const int32_t RM = q_len * G;
     const bool bf16 = p->dtype == DENDRITE_BF16;
-    const int small_rows = unit_rows_small(p);
     const bool tc_on = max_tc_ctas > 0 && p->tc_min_rows >= 0;
     const int32_t n_nodes = (int32_t)p->nodes.size();
     hp.parent.resize(n_nodes);
@@ -1791,6 +1830,8 @@ int build_plan(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_l
     for (int32_t i = 0; i < n; ++i) hp.queried[i] = p->br[branches[i]].node;
     plan_segments(n_nodes, hp.parent.data(), hp.fork_len.data(), hp.len.data(), p->block_size, hp.queried.data(), n,
                   hp.psegs, hp.seg_members);
+    choose_tiled(p, q_len, RM, hp);
+    const int small_rows = unit_rows_small(p, hp);
     // distinct tiles: the sharing segments before folding read each (block,
     // kv head) pair once
     for (const Segment& sg : hp.psegs) hp.unique_tiles += (int64_t)sg.block_count * nkv;
@@ -1812,10 +1853,24 @@ int32_t class_ctas(int64_t weight, int max_ctas, const ClassWeights& cw) {
     return (int32_t)std::max<int64_t>(1, std::min<int64_t>(max_ctas, (weight + cw.min_per_cta - 1) / cw.min_per_cta));
 }
 
+// fp32 cross attention: the fewest rows per unit that hold those of the largest segment
+// (16 branches of 700 tokens, d = 128, a kv head's rows 4, 16, 64: 16 rows a unit 71, 75, 195 us, 32 63, 64,
+// 119, 64 90, 91, 96, 128 148, 149, 154, the row-by-row kernel 134, 289, 967).  A single query takes the
+// decode call's kernel: what the two calls return is the same to the bit, as for the other element types.
+void choose_tiled(const dendrite_pool* p, int32_t q_len, int32_t rows_per_member, HostPlan& hp) {
+    hp.tiled = 0;
+    if (!hp.cross || p->dtype != DENDRITE_FP32 || q_len == 1) return;
+    int64_t most = 0;
+    for (const Segment& sg : hp.psegs) most = std::max(most, (int64_t)sg.n_members * rows_per_member);
+    hp.tiled = kF32TiledMinRows;
+    while (hp.tiled < most && hp.tiled < f32_tiled_max_rows(p->head_dim)) hp.tiled *= 2;
+}
+
 // Rows per unit of the mma.sync (bf16: 4 row tiles of 16) or compressed
 // (64: the CTA decodes each tile once for its four warps' row tiles) partial
-// kernels, and of the fp32 kernel (16).
-int unit_rows_small(const dendrite_pool* p) {
+// kernels, and of the fp32 kernels (16, or what choose_tiled found).
+int unit_rows_small(const dendrite_pool* p, const HostPlan& hp) {
+    if (hp.tiled) return hp.tiled;
     switch (p->dtype) {
         case DENDRITE_BF16: return kMaxUnitRowsBf16;
         case DENDRITE_TURBO: return kMaxUnitRowsTurbo;
@@ -1896,7 +1951,9 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
     const int32_t G = nq / p->n_kv, nkv = p->n_kv;
     const int32_t RM = q_len * G;
     const bool bf16 = p->dtype == DENDRITE_BF16;
-    const int small_rows = unit_rows_small(p);
+    const int small_rows = unit_rows_small(p, hp);
+    if (hp.tiled) max_ctas = p->sm_count * attn_f32_tiled_ctas(hp.tiled, p->f32_tiled_ctas_per_sm);
+    const ClassWeights& smallw = small_weights(p, hp);
     const bool tc_on = max_tc_ctas > 0 && p->tc_min_rows >= 0;
     // Segments, their members and their units (kv head major, then row
     // group), tensor-core segments first: pass 0 takes the segments read by
@@ -1937,7 +1994,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
     int64_t n_rows = 0;
     for (int pass = 0; pass < 2; ++pass) {
         PlanClass& pc = hp.hdr.cls[pass];
-        const ClassWeights& cwt = pass == 0 ? tcw : small_weights(p);
+        const ClassWeights& cwt = pass == 0 ? tcw : smallw;
         pc = PlanClass{};
         pc.u_lo = n_unit;
         pc.s_lo = (int32_t)hp.segplan.size();
@@ -1962,7 +2019,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
                 const int32_t qi = hp.seg_members[sg.member_offset + k];
                 mp[n_mem++] = AttnMember{qi, p->br[branches[qi]].len};
             }
-            auto rt_of = [&](int32_t rows) { return tc ? (rows + 127) / 128 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4; };
+            auto rt_of = [&](int32_t rows) { return tc ? (rows + 127) / 128 : hp.tiled || rows <= 16 ? 1 : rows <= 32 ? 2 : 4; };
             SegPlan sp;
             sp.unit_base = S.unit_base;
             sp.ngroups = S.ngroups;
@@ -2013,7 +2070,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
             }
         }
         ct.c0 = ct.u_hi > ct.u_lo ? class_ctas(ct.weight, max_tc_ctas, tcw) : 0;
-        cs.c0 = cs.u_hi > cs.u_lo ? class_ctas(cs.weight, max_ctas, small_weights(p)) : 0;
+        cs.c0 = cs.u_hi > cs.u_lo ? class_ctas(cs.weight, max_ctas, smallw) : 0;
     }
     if (n_rows >= INT32_MAX / 2) return DENDRITE_ELIMIT;
     hp.hdr.n_units = n_unit;
@@ -2057,7 +2114,7 @@ int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_
         partition_class(hp, 0, hp.n_tc_units, hp.hdr.cls[0].tiles, hp.hdr.cls[0].weight, max_tc_ctas, tcw,
                         hp.tc_cta_begin, hp.tc_cta_unit);
         partition_class(hp, hp.n_tc_units, (int32_t)hp.units.size(), hp.hdr.cls[1].tiles, hp.hdr.cls[1].weight,
-                        max_ctas, small_weights(p), hp.cta_begin, hp.cta_unit);
+                        max_ctas, smallw, hp.cta_begin, hp.cta_unit);
         // partial rows per unit
         size_t prow = 0;
         for (AttnUnit& U : hp.units) {
@@ -2199,6 +2256,7 @@ AttnPlanDev plan_view(const HostPlan& hp, const size_t (&off)[kPlanSections + 1]
     v.splits = reinterpret_cast<const int32_t*>(d + off[SEC_SPLITS]);
     v.n_splits = (int32_t)hp.splits.size();
     v.direct = hp.direct;
+    v.tiled = hp.tiled;
     v.back = cross ? 0 : q_len;
     v.step = cross || v.masks ? 0 : 1;
     v.packed = hp.small_packed ? 1 : 0;
@@ -2259,9 +2317,9 @@ int launch_plan_expand(dendrite_pool* p, char* d, const size_t* off, int32_t n_u
 // Cross attention: whether the tcgen05 kernel may write the rows of whole units out itself, and
 // which units it does not run whole (AttnPlanDev::direct).
 void find_direct(const dendrite_pool* p, HostPlan& hp, int32_t n) {
-    if ((p->dtype != DENDRITE_BF16 && p->dtype != DENDRITE_FP8) || hp.device || !hp.xtiles.empty() ||
-        hp.n_tc_units != (int32_t)hp.units.size())
-        return;
+    const bool one_kernel = hp.tiled || ((p->dtype == DENDRITE_BF16 || p->dtype == DENDRITE_FP8) &&
+                                         hp.n_tc_units == (int32_t)hp.units.size());
+    if (!one_kernel || hp.device || !hp.xtiles.empty()) return;
     for (int32_t i = 0; i < n; ++i)
         if (hp.path_off[i + 1] - hp.path_off[i] > 1) return;
     hp.direct = true;
@@ -2365,6 +2423,8 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
         DENDRITE_TRY(launch_turbo_partials(a, a.Q, n_out_rows, p->d_tq_signs, p->d_tq_S, p->d_tq_qs, s));
     } else if (f8) {
         DENDRITE_TRY(launch_attn_fp8(a, false, s));
+    } else if (a.plan.tiled) {
+        DENDRITE_TRY(launch_attn_f32_tiled(a, s));
     } else if (a.plan.n_ctas > 0) {
         if (bf16) {
             const MmaKernel k = mma_kernel(a);
@@ -2377,7 +2437,9 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
     prof_end(p, T_ATTN_PARTIAL, s);
     prof_begin(p, T_ATTN_MERGE, s);
     if (a.plan.direct) {
-        if (a.plan.n_splits > 0)
+        if (a.plan.n_splits > 0 && !out16)
+            DENDRITE_CUDA(launch_pdl(k_attn_merge_splits_f32, dim3((unsigned)a.plan.n_splits, (unsigned)a.plan.tiled / 8), dim3(256), 0, s, a));
+        else if (a.plan.n_splits > 0)
             DENDRITE_CUDA(launch_pdl(k_attn_merge_splits, dim3((unsigned)a.plan.n_splits, kMaxUnitRowsTc / 32), dim3(256), 0, s, a));
     } else {
         // after a join from the side stream the merge is an ordinary launch:
@@ -2518,6 +2580,7 @@ int attn_setup(dendrite_pool* p) {
         int occ = 0;
         DENDRITE_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k_attn_partial_f32, 128, sm));
         p->attn_ctas_per_sm = std::max(1, occ);
+        DENDRITE_TRY(attn_f32_tiled_setup(p->head_dim, p->f32_tiled_ctas_per_sm));
     }
     return DENDRITE_OK;
 }
@@ -2659,6 +2722,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
         hp.clear();
         hp.tc_rows = parents ? p->tc_min_rows_draft : p->tc_min_rows;
         hp.cross = cross;
+        hp.tiled = 0;
         if (grow) {
             hp.psegs = pc.segs;
             hp.seg_members = pc.seg_members;
@@ -2709,6 +2773,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
             if (!grow) hp.clear();
         }
         if (grow) {
+            choose_tiled(p, q_len, q_len * (n_q_heads / p->n_kv), hp);
             DENDRITE_TRY(build_units(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, !cross));
         } else {
             DENDRITE_TRY(build_plan(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, !cross));
@@ -2919,6 +2984,7 @@ extern "C" int dendrite_tree_attn_decode_noalloc(dendrite_pool* p, const void* Q
     hp.clear();
     hp.tc_rows = p->tc_min_rows;
     hp.cross = false;
+    hp.tiled = 0;
     DENDRITE_TRY(build_plan(p, branches, n, q_len, n_q_heads, p->sm_count * p->attn_ctas_per_sm, tc_ctas(p), hp,
                             false));
     // scratch layout: plan sections, then partial acc rows, then partial (m, l)

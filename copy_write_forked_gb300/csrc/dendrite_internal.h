@@ -149,10 +149,11 @@ struct AttnPlanDev {
     const uint64_t* masks;         // [n_queried][q_len] drafted tokens each query sees (draft trees), or null
     int32_t back, step;            // query j of a branch of len rows sees positions < len - back + (j + 1) step:
                                    // causal q_len, 1; draft trees q_len, 0 (and their masks); cross attention 0, 0
-    // Cross attention whose branches each read one segment, all on the tcgen05 kernel: a unit that one
+    // Cross attention whose branches each read one segment, all on the tcgen05 (fp32: tiled) kernel: a unit that one
     // CTA runs whole writes its rows out itself, and only the units split over CTAs are merged.
     const int32_t* splits;         // [n_splits] units split over CTAs
     int32_t direct, n_splits;
+    int32_t tiled;                 // fp32 cross attention on the tiled kernel: rows per unit; 0: not on it
     int32_t packed;                // some unit reads extra tiles (the mma.sync kernel then needs its tile info)
 };
 
@@ -286,6 +287,7 @@ struct dendrite_pool {
     int device = 0;
     int sm_count = 0;
     int attn_ctas_per_sm = 1;
+    int f32_tiled_ctas_per_sm[4] = {1, 1, 1, 1};   // of its kernels for 16, 32, 64 and 128 rows
     int32_t tc_min_rows = dendrite::kTcMinRowsDefault;   // < 0: tensor-core attention kernel off
     int32_t tc_min_rows_draft = dendrite::kTcMinRowsDraft;   // the same, for draft trees
     int32_t tc_sms = 0;   // SMs of the tcgen05 kernel beside the mma.sync one (0: estimated, -1: no split)

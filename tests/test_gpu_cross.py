@@ -273,3 +273,43 @@ def test_a_step_with_images_thinning_drafts_and_an_encoder():
     self_pool.sync()
     self_pool.close()
     c.pool.close()
+
+
+@pytest.mark.parametrize("dim", range(32, 257, 32))
+def test_row_counts_of_fp32_pools(dim):
+    """Units of 16, 32, 64 and 128 rows, filled, just passed and in pieces, over ends on both sides of 32 tokens."""
+    c = Case("fp32", [1, 31, 32, 33, 500], 2, 1, dim=dim)
+    for q_len in (2, 16, 17, 32, 33, 64, 65, 130):
+        c.attend(c.br, q_len)
+    c.pool.close()
+
+
+def test_fp32_rows_of_several_branches_in_one_unit():
+    """Forks of one length share units whose rows end at different positions of a shared block once they are cut."""
+    c = Case("fp32", [700], 1, 3)
+    kids = c.pool.fork(c.br[0], 9)
+    c.pool.truncate(kids, [700, 699, 689, 688, 673, 672, 300, 17, 0])
+    for q_len in (2, 5, 11, 40):
+        c.attend(kids, q_len)
+    c.append(kids, 3)
+    c.attend(kids, 5)
+    c.pool.close()
+
+
+def test_what_stands_behind_the_end_touches_nothing_in_fp32():
+    c = Case("fp32", [40, 40], 1, 4)
+    bad = torch.full((2, 7, 1, 128), float("nan"), device="cuda")
+    c.pool.append_kv(c.br, bad, bad)
+    kid = c.pool.fork(c.br[0], 1)[0]      # still holds those rows, in the blocks that the first branch reads
+    c.pool.truncate(c.br, [40, 33])
+    for q_len in (2, 20, 100):
+        c.attend(c.br, q_len)
+        q = c.rows(3, q_len, 4)
+        out = R.f64(c.pool.tree_attn_cross(q, [c.br[0], kid, c.br[1]]))
+        assert np.isnan(out[1]).all() and np.isfinite(out[[0, 2]]).all()
+        for i, b in ((0, c.br[0]), (2, c.br[1])):
+            n = c.pool.branch_len(b)
+            K, V = (R.f64(x) for x in c.pool.read_kv([b], [0], [n]))
+            ref = R.attention(R.f64(q[i]), K, V, np.ones((q_len, n), bool))
+            assert (np.abs(out[i] - ref[0]) <= R.attention_bound("fp32", *ref)).all()
+    c.pool.close()
