@@ -218,7 +218,6 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// The largest of three (a NaN counts for nothing, as in fmaxf).
 // Adds a pair's two bf16 to two fp32 sums.
 __device__ __forceinline__ void add_bf16(float& a, float& b, uint32_t x) {
     uint16_t lo, hi;
@@ -226,6 +225,7 @@ __device__ __forceinline__ void add_bf16(float& a, float& b, uint32_t x) {
     asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(a) : "h"(lo));
     asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(b) : "h"(hi));
 }
+// The largest of three (a NaN counts for nothing, as in fmaxf).
 __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));

@@ -379,6 +379,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
         return;
     }
 
+    // (before the passes' exchanges: whoever finds a token writes it after this)
+    if (rank == 0 && t == 0) a.next[i] = -1;
+
     constexpr int PER = kPer<T>;
     uint4 hp[kHeld];
     uint4* const hq = held_q + t;
@@ -561,6 +564,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
                 walk.stale = false;
                 if (fin) {
                     find.goal = product(S, nodes.sample);
+                    // (of the least numbers a part rounds to the whole, which no token would pass; S.l is zero there)
+                    if (S.h > 0.f && !less(find.goal, S)) find.goal = {__uint_as_float(__float_as_uint(S.h) - 1), 0.f};
                     find.before = rank ? before : Pair{0.f, 0.f};
                     find.here = !less(find.goal, find.before) && less(find.goal, upto);
                     find.none = !(S.h > 0.f);
@@ -572,10 +577,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
         if (!fin) continue;
         __syncthreads();
         if (find.none) {
-            if (fell_back || (!with_q && !gone)) {   // p has no weight
-                if (rank == 0 && t == 0) a.next[i] = -1;
-                break;
-            }
+            if (fell_back || (!with_q && !gone)) break;   // p has no weight
             fell_back = true;
             p_row = -1;
             __syncthreads();

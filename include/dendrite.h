@@ -472,9 +472,10 @@ int dendrite_tree_attn_cross(dendrite_pool* pool, int32_t layer, const void* Q, 
  * w = max(p - c q, 0) and S = sum w (without draft: x leaves w, S = sum w).
  * The next token is the least one whose running sum of w passes sample * sum w;
  * where no weight is left, of p instead; -1 where p has none.  Probabilities that
- * are not positive and finite count as zero.  Rows need not add up to one exactly.
- * Sums are held in 48 bits: the outcome is that of 64-bit arithmetic but where a
- * number is within some 2^-40 of a border.
+ * are not positive and finite count as zero.  Rows need not add up to one exactly (-1
+ * where the sum is past the largest fp32).  Sums are held in 48 bits: the outcome is
+ * that of 64-bit arithmetic but where a number is within some 2^-40 of a border (of sums
+ * below 2^-100, whose last bits fp32 does not hold, within 2^-149).
  *   path: device int32 [n][n_draft], the accepted nodes in order, then -1;
  *   n_keep: device int32 [n]; next: device int32 [n].  Written.
  * The outputs may not overlap one another or any input (DENDRITE_EINVAL, as for a

@@ -254,3 +254,39 @@ def test_refusals(pool):
     empty = pool.verify_draft(tokens[:0], p[:0], torch.zeros(0, 5, dtype=torch.int32), accept[:0], sample[:0])
     assert [x.numel() for x in empty] == [0, 0, 0]
     pool.sync()
+
+
+@pytest.mark.parametrize("vocab", [5, 70000])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_least_weights_still_give_a_token(pool, vocab, kind):
+    """One weight of the type's least positive number: its token, however near one the sample is (sample times the
+    weight rounds to the weight itself)."""
+    least = 2.0 ** (-149 if kind == "fp32" else -133)
+    samples = [0.0, 0.5, 1 - 2.0 ** -24]
+    n = len(samples)
+    for at in (0, 3, vocab - 1):
+        p = torch.zeros(n, 2, vocab, device="cuda", dtype=TYPES[kind])
+        p[:, 0, at] = least
+        tokens, accept = torch.full((n, 1), -1, dtype=torch.int32, device="cuda"), torch.zeros(n, 1, device="cuda")
+        out = tuple(torch.full(s, 7, dtype=torch.int32, device="cuda") for s in ((n, 1), (n,), (n,)))
+        _, size, token = pool.verify_draft(tokens, p, [-1], accept, torch.tensor(samples, device="cuda"), out=out)
+        assert size.tolist() == [0] * n and token.tolist() == [at] * n
+
+
+@pytest.mark.parametrize("certain", [False, True])
+def test_small_rows(pool, certain):
+    """Rows that add up to 2^-90: the digits that the sums keep are all there."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    tokens, p, trees, accept, sample, q = _case(3, 6, 500, "fp32", certain, g, seed=11)
+    _check(pool, (tokens, p * 2.0 ** -90, trees, accept, sample, None if q is None else q * 2.0 ** -90))
+
+
+@pytest.mark.parametrize("vocab", [6, 30000])
+def test_rows_past_the_largest_float(pool, vocab):
+    """The sum of such a row is no number: -1, and nothing else is touched."""
+    p = torch.full((2, 2, vocab), 1.0 / vocab, device="cuda")
+    p[0, 0] = 3e38
+    tokens, accept = torch.full((2, 1), -1, dtype=torch.int32, device="cuda"), torch.zeros(2, 1, device="cuda")
+    out = tuple(torch.full(s, 7, dtype=torch.int32, device="cuda") for s in ((2, 1), (2,), (2,)))
+    path, size, token = pool.verify_draft(tokens, p, [-1], accept, torch.tensor([0.5, 0.0], device="cuda"), out=out)
+    assert size.tolist() == [0, 0] and token.tolist() == [-1, 0] and path.eq(-1).all()
