@@ -1805,7 +1805,7 @@ void partition_class(HostPlan& hp, int32_t u_lo, int32_t u_hi, int64_t T, int64_
 
 int build_units(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_len, int32_t nq, int max_ctas,
                 int max_tc_ctas, HostPlan& hp, bool allow_device);
-void choose_tiled(const dendrite_pool* p, int32_t q_len, int32_t rows_per_member, HostPlan& hp);
+void choose_tiled(const dendrite_pool* p, int32_t rows_per_member, HostPlan& hp);
 int unit_rows_small(const dendrite_pool* p, const HostPlan& hp);
 
 // max_ctas: CTAs of the mma.sync/fp32 kernel; max_tc_ctas: of the tcgen05
@@ -1830,7 +1830,7 @@ int build_plan(dendrite_pool* p, const int32_t* branches, int32_t n, int32_t q_l
     for (int32_t i = 0; i < n; ++i) hp.queried[i] = p->br[branches[i]].node;
     plan_segments(n_nodes, hp.parent.data(), hp.fork_len.data(), hp.len.data(), p->block_size, hp.queried.data(), n,
                   hp.psegs, hp.seg_members);
-    choose_tiled(p, q_len, RM, hp);
+    choose_tiled(p, RM, hp);
     const int small_rows = unit_rows_small(p, hp);
     // distinct tiles: the sharing segments before folding read each (block,
     // kv head) pair once
@@ -1854,12 +1854,11 @@ int32_t class_ctas(int64_t weight, int max_ctas, const ClassWeights& cw) {
 }
 
 // fp32 cross attention: the fewest rows per unit that hold those of the largest segment
-// (16 branches of 700 tokens, d = 128, a kv head's rows 4, 16, 64: 16 rows a unit 71, 75, 195 us, 32 63, 64,
-// 119, 64 90, 91, 96, 128 148, 149, 154, the row-by-row kernel 134, 289, 967).  A single query takes the
-// decode call's kernel: what the two calls return is the same to the bit, as for the other element types.
-void choose_tiled(const dendrite_pool* p, int32_t q_len, int32_t rows_per_member, HostPlan& hp) {
+// (32 branches of 1,500 tokens, one row a kv head: 79 us in units of 4 rows, 123 of 16; 16 of 700, 16 rows a kv
+// head: 64 us in units of 32 rows, 91 of 64, 149 of 128, and 64 rows: 119, 96 and 154).
+void choose_tiled(const dendrite_pool* p, int32_t rows_per_member, HostPlan& hp) {
     hp.tiled = 0;
-    if (!hp.cross || p->dtype != DENDRITE_FP32 || q_len == 1) return;
+    if (!hp.cross || p->dtype != DENDRITE_FP32) return;
     int64_t most = 0;
     for (const Segment& sg : hp.psegs) most = std::max(most, (int64_t)sg.n_members * rows_per_member);
     hp.tiled = kF32TiledMinRows;
@@ -2438,7 +2437,7 @@ int launch_attention(dendrite_pool* p, int32_t layer, const AttnArgs& a, cudaStr
     prof_begin(p, T_ATTN_MERGE, s);
     if (a.plan.direct) {
         if (a.plan.n_splits > 0 && !out16)
-            DENDRITE_CUDA(launch_pdl(k_attn_merge_splits_f32, dim3((unsigned)a.plan.n_splits, (unsigned)a.plan.tiled / 8), dim3(256), 0, s, a));
+            DENDRITE_CUDA(launch_pdl(k_attn_merge_splits_f32, dim3((unsigned)a.plan.n_splits, (unsigned)(a.plan.tiled + 7) / 8), dim3(256), 0, s, a));
         else if (a.plan.n_splits > 0)
             DENDRITE_CUDA(launch_pdl(k_attn_merge_splits, dim3((unsigned)a.plan.n_splits, kMaxUnitRowsTc / 32), dim3(256), 0, s, a));
     } else {
@@ -2773,7 +2772,7 @@ int attn_call(dendrite_pool* p, int32_t layer, const void* Q, int32_t n_q_heads,
             if (!grow) hp.clear();
         }
         if (grow) {
-            choose_tiled(p, q_len, q_len * (n_q_heads / p->n_kv), hp);
+            choose_tiled(p, q_len * (n_q_heads / p->n_kv), hp);
             DENDRITE_TRY(build_units(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, !cross));
         } else {
             DENDRITE_TRY(build_plan(p, branches, n, q_len, n_q_heads, max_ctas, tc_ctas(p), hp, !cross));

@@ -287,7 +287,7 @@ struct dendrite_pool {
     int device = 0;
     int sm_count = 0;
     int attn_ctas_per_sm = 1;
-    int f32_tiled_ctas_per_sm[4] = {1, 1, 1, 1};   // of its kernels for 16, 32, 64 and 128 rows
+    int f32_tiled_ctas_per_sm[6] = {1, 1, 1, 1, 1, 1};   // of its kernels for 4, 8, 16, 32, 64 and 128 rows
     int32_t tc_min_rows = dendrite::kTcMinRowsDefault;   // < 0: tensor-core attention kernel off
     int32_t tc_min_rows_draft = dendrite::kTcMinRowsDraft;   // the same, for draft trees
     int32_t tc_sms = 0;   // SMs of the tcgen05 kernel beside the mma.sync one (0: estimated, -1: no split)

@@ -89,7 +89,16 @@ def test_a_single_query_is_the_decode_call(kind):
     for q_len in (1, 8):
         q, out = c.attend(c.br, q_len)
         causal = c.pool.tree_attn_decode(q, c.br)
-        assert torch.equal(out[:, -1:], causal[:, -1:]) if q_len == 1 else not torch.equal(out, causal)
+        if q_len == 1 and kind == "fp32":
+            # two kernels, two orders of the sums: with |out - x| <= b (checked by attend) and |causal - x| <= b for
+            # the exact x and its bound b, |out - causal| <= |out - x| + |x - causal| <= 2 b
+            for i, b in enumerate(c.br):
+                n = c.pool.branch_len(b)
+                K, V = (R.f64(x) for x in c.pool.read_kv([b], [0], [n]))
+                ref = R.attention(R.f64(q[i]), K, V, np.ones((1, n), bool))
+                assert (np.abs(R.f64(out[i]) - R.f64(causal[i])) <= 2 * R.attention_bound(kind, *ref)).all()
+        else:
+            assert torch.equal(out[:, -1:], causal[:, -1:]) if q_len == 1 else not torch.equal(out, causal)
         again = c.pool.tree_attn_cross(q, c.br)
         assert torch.equal(again, out)
         trees = list(range(-1, q_len - 1))
@@ -277,9 +286,9 @@ def test_a_step_with_images_thinning_drafts_and_an_encoder():
 
 @pytest.mark.parametrize("dim", range(32, 257, 32))
 def test_row_counts_of_fp32_pools(dim):
-    """Units of 16, 32, 64 and 128 rows, filled, just passed and in pieces, over ends on both sides of 32 tokens."""
+    """Units of 4, 8, .. 128 rows, filled, just passed and in pieces, over ends on both sides of 32 tokens."""
     c = Case("fp32", [1, 31, 32, 33, 500], 2, 1, dim=dim)
-    for q_len in (2, 16, 17, 32, 33, 64, 65, 130):
+    for q_len in (1, 2, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65, 130):
         c.attend(c.br, q_len)
     c.pool.close()
 
@@ -289,7 +298,7 @@ def test_fp32_rows_of_several_branches_in_one_unit():
     c = Case("fp32", [700], 1, 3)
     kids = c.pool.fork(c.br[0], 9)
     c.pool.truncate(kids, [700, 699, 689, 688, 673, 672, 300, 17, 0])
-    for q_len in (2, 5, 11, 40):
+    for q_len in (1, 2, 5, 11, 40):
         c.attend(kids, q_len)
     c.append(kids, 3)
     c.attend(kids, 5)
@@ -302,7 +311,7 @@ def test_what_stands_behind_the_end_touches_nothing_in_fp32():
     c.pool.append_kv(c.br, bad, bad)
     kid = c.pool.fork(c.br[0], 1)[0]      # still holds those rows, in the blocks that the first branch reads
     c.pool.truncate(c.br, [40, 33])
-    for q_len in (2, 20, 100):
+    for q_len in (1, 2, 20, 100):
         c.attend(c.br, q_len)
         q = c.rows(3, q_len, 4)
         out = R.f64(c.pool.tree_attn_cross(q, [c.br[0], kid, c.br[1]]))
