@@ -988,26 +988,19 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             const AttnRow RR = v_ok ? unit_row(pl, V, row) : AttnRow{0, 0};
             if constexpr (WHOLE && !F8) {
                 // two rows an instruction (sixteen lanes each), so that a request covers whole lines: a row
-                // a lane, 16 bytes at a time, took 4,000 cycles for the 256 rows
+                // a lane, 16 bytes at a time, took 4,000 cycles for the 256 rows.  On their way while the
+                // previous unit's rows go out (q_there)
                 const int32_t from = v_ok ? RR.q_row : -1;
                 const int ch = lane & 15;
 #pragma unroll
-                for (int i0 = 0; i0 < 16; i0 += 8) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int32_t q_row = __shfl_sync(0xffffffffu, from, 2 * (i0 + i) + (lane >> 4));
-                        v[i] = q_row >= 0 ? __ldg(reinterpret_cast<const uint4*>(Q + (int64_t)q_row * D) + ch) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int tr = sub * 32 + 2 * (i0 + i) + (lane >> 4);
-                        *reinterpret_cast<uint4*>(sQ + (ch >> 3) * 16384 + tr * 128 + (((ch & 7) ^ (tr & 7)) << 4)) = v[i];
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    const int32_t q_row = __shfl_sync(0xffffffffu, from, 2 * i + (lane >> 4));
+                    const int tr = sub * 32 + 2 * i + (lane >> 4);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     smem_u32(sQ + (ch >> 3) * 16384 + tr * 128 + (((ch & 7) ^ (tr & 7)) << 4))),
+                                 "l"(reinterpret_cast<const uint4*>(Q + (int64_t)max(q_row, 0) * D) + ch), "r"(q_row >= 0 ? 16 : 0)
+                                 : "memory");
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_Q_FULL + r));
                 return RR;
             }
             const uint4* q = reinterpret_cast<const uint4*>(Q + (int64_t)RR.q_row * D);
@@ -1025,6 +1018,15 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         int32_t js = 0;
         bool ok = true;
         int32_t t = t_begin, u = u0;
+        // WHOLE: the tile's Q is there, and S may be issued
+        auto q_there = [&] {
+            if constexpr (WHOLE && !F8) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_Q_FULL + r));
+            }
+        };
         int32_t staged_u = -1;      // unit whose Q is already in the tile
         AttnRow staged_R{0, 0};
         uint32_t joined = 0;        // phase of the joins of split units
@@ -1045,7 +1047,9 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
             const int row = row_of(U);
             const bool valid = row < U.n_rows;
-            const AttnRow R = staged_u == u ? staged_R : stage_q(U);
+            const bool staged = staged_u == u;
+            const AttnRow R = staged ? staged_R : stage_q(U);
+            if (!staged) q_there();
             if (!F8 && !WHOLE && U.n_blk > U.n_shared) {   // (no unit of a direct plan is packed)
                 // a packed unit: its extra tiles' logical blocks, member masks
                 // and held tokens into shared memory, once every warp of the row tile
@@ -1303,6 +1307,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
             if (!ok) break;
             // the next chunk this row tile works on: stage its Q now
+            bool coming;
             {
                 int32_t t2 = cend, u2 = u + 1;
                 while (t2 < t_end) {
@@ -1317,6 +1322,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     staged_R = stage_q(pl.units[u2]);
                     staged_u = u2;
                 }
+                coming = t2 < t_end;
             }
             g += nst;
             // chunk done: O after the last PV -> partial row
@@ -1410,6 +1416,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     uint32_t v[32];
                     tmem_ld32(tl + c0, v);
                     tmem_wait_ld(v);
+                    if (c0 == D / 2 && coming) q_there();
                     if (whole) {
                         send({out_words(v, inv), out_words(v + 8, inv), out_words(v + 16, inv), out_words(v + 24, inv)}, c0 * 2);
                     } else {
@@ -1448,6 +1455,7 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             t = cend;
             ++u;
         }
+        if (WHOLE && !F8) asm volatile("cp.async.wait_all;" ::: "memory");   // (an aborted unit's)
     }
 
     tc_fence_before();
