@@ -1254,7 +1254,8 @@ __global__ void __launch_bounds__(256, 3) k_attn_merge_grouped(const AttnArgs a)
     }
 }
 
-// Direct plans (cross attention): the units split over CTAs, CTA (split unit, 32 of its rows),
+// Direct plans (cross attention): the units split over CTAs (bf16: over more than two, the others
+// being joined by the tcgen05 kernel), CTA (split unit, 32 of its rows),
 // four rows a warp.  A row's partials are its unit's chunks, so nothing is looked up per row:
 // 114,688 rows of which the general merge found each one's only partial took 95 us.
 __global__ void __launch_bounds__(256) k_attn_merge_splits(const AttnArgs a) {
@@ -2327,7 +2328,7 @@ void find_direct(const dendrite_pool* p, HostPlan& hp, int32_t n) {
         AttnUnit& U = hp.units[u];
         U.prow_base = (int32_t)hp.partial_rows;
         if (U.nchunks == 1) continue;
-        hp.splits.push_back(u);
+        if (p->dtype != DENDRITE_BF16 || U.nchunks > 2) hp.splits.push_back(u);   // (two: joined where the second ends)
         hp.partial_rows += (size_t)U.nchunks * U.n_rows;
     }
 }
@@ -2487,6 +2488,7 @@ AttnArgs attn_args(const dendrite_pool* p, int32_t layer, const void* Q, void* o
     a.pool_k = reinterpret_cast<const float*>(static_cast<const char*>(p->d_k) + (size_t)layer * p->layer_bytes);
     a.pool_v = reinterpret_cast<const float*>(static_cast<const char*>(p->d_v) + (size_t)layer * p->layer_bytes_v);
     a.tq_signs = p->dtype == DENDRITE_TURBO ? p->d_tq_signs : nullptr;
+    a.joins = p->d_joins;
     a.meta = p->d_meta;
     a.bpb = p->bpb;
     a.n_kv = p->n_kv;

@@ -71,6 +71,7 @@ struct AttnArgs {
     const float* pool_v;
     float* part_acc;       // [partial rows][head_dim]
     float2* part_ml;       // [partial rows] (m, l)
+    int32_t* joins;        // [SMs][8] direct bf16 plans: meetings of a unit's two chunks, by its first CTA and warp; zero between calls
     DevMeta* meta;
     int32_t bpb;
     int32_t n_kv;

@@ -683,7 +683,7 @@ __device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint3
 // Nothing there waits for HBM (256 rows a unit, several units a KV head through L2), so the roles' chains
 // and instructions are what a stage takes, 1,700 cycles of which the products need 1,280 (S with N = 64
 // reads its operands from shared memory for longer than it multiplies).  4 prompts of 515 tokens, 32
-// heads, over 6,404 states (215 GFLOP): 176 us, 1.2 PFLOP/s, tensor pipe 57 %; 16 prompts of 448, 16
+// heads, over 6,404 states (215 GFLOP): 178 us, 1.2 PFLOP/s, tensor pipe 57 %; 16 prompts of 448, 16
 // heads, over 1,500 (86 GFLOP, a unit starts every 24 stages): 102 us.  On the way there, as whole calls:
 //   - partial rows for every unit and the general merge: 248 / 229 us
 //   - rows of whole units written here, split units merged by unit: 238 / 138
@@ -691,6 +691,8 @@ __device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint3
 //   - tiles and starts weighed by what they take here: 205 / 124
 //   - Q in and rows out in whole lines, Q on its way to L2 a unit ahead, descriptors by additions: 193 / 120
 //   - K slots given back by the softmax, row sums by mixed additions: 188 / 115
+//   - the next unit's Q copied while rows go out: 183 / 106
+//   - units of two chunks joined where the second ends, no merge behind: 180 / 104
 // Tried there and left: S in one buffer and P in two of its own, so that S is issued a stage ahead (196 /
 // 120: the softmax warps then all compute at once, and have more waits), a quarter of the exponentials as
 // polynomials (209 / 122: instructions are short, not the SFU).
@@ -1394,9 +1396,9 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 // 64 bytes of each of the warp's rows at a time through shared memory, so that a store
                 // covers whole sectors of eight rows
                 unsigned char* box = sm + Y::OFF_OUT + (warp - Y::SOFTMAX_WARP0) * Y::OUT_WARP;
-                const int32_t to = !valid ? -1 : whole ? unit_row(pl, U, row).q_row : prow;
+                int32_t to = !valid ? -1 : whole ? unit_row(pl, U, row).q_row : prow;
                 char* base_out = whole ? static_cast<char*>(a.out) : reinterpret_cast<char*>(a.part_acc);
-                const int32_t row_bytes = whole ? D * 2 : D * 4;
+                int32_t row_bytes = whole ? D * 2 : D * 4;
                 auto send = [&](const uint4 (&x)[4], int32_t at) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + lane * 80 + i * 16) = x[i];
@@ -1411,12 +1413,22 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     }
                     __syncwarp();
                 };
+                // a unit of two chunks: each warp's rows are joined by the CTA that ends second, which has its
+                // own in TMEM yet; none waits for the other.  (The one with the second chunk does it first of
+                // all, the other last.)  Sums are in the chunks' order, whoever makes them
+                const bool two = U.nchunks == 2, later = c != U.cfirst;
+                int32_t* met = a.joins + U.cfirst * 8 + (warp - Y::SOFTMAX_WARP0);
+                int32_t other = 0;   // the other's partial rows are there
+                if (two) other = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(met, 0) : 0, 0);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = 0; c0 < (other ? 0 : D); c0 += 32) {
                     uint32_t v[32];
                     tmem_ld32(tl + c0, v);
                     tmem_wait_ld(v);
-                    if (c0 == D / 2 && coming) q_there();
+                    if (c0 == D / 2 && coming) {
+                        q_there();
+                        coming = false;
+                    }
                     if (whole) {
                         send({out_words(v, inv), out_words(v + 8, inv), out_words(v + 16, inv), out_words(v + 24, inv)}, c0 * 2);
                     } else {
@@ -1427,7 +1439,72 @@ k_attn_partial_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                                  (c0 + i) * 4);
                     }
                 }
-                if (valid && !whole) a.part_ml[prow] = make_float2(m_ref, l);
+                if (valid && !whole && !other) a.part_ml[prow] = make_float2(m_ref, l);
+                if (two && !other) {
+                    __threadfence();
+                    __syncwarp();
+                    other = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(met, 1) : 0, 0);
+                }
+                if (two && other) {
+                    __threadfence();
+                    const int64_t there = (int64_t)U.prow_base + (later ? 0 : U.n_rows) + row;
+                    const float2 o = valid ? __ldcg(a.part_ml + there) : make_float2(-INFINITY, 0.f);
+                    const float m = fmaxf(m_ref, o.x), ref = m == -INFINITY ? 0.f : m;
+                    const float w = exp2f(m_ref - ref), w_o = exp2f(o.x - ref);
+                    const float w0 = later ? w_o : w, w1 = later ? w : w_o;
+                    const float inv2 = 1.f / (later ? fmaf(w1, l, w0 * o.y) : fmaf(w1, o.y, w0 * l));
+                    to = valid ? unit_row(pl, U, row).q_row : -1;
+                    base_out = static_cast<char*>(a.out);
+                    row_bytes = D * 2;
+                    // the other's rows 64 bytes at a time, eight rows a load (a row a lane: 16 us more), through the
+                    // same box; the next 128 are on their way meanwhile
+                    const int32_t from = valid ? (int32_t)there : -1;
+                    float4 next[2][4];
+                    auto load = [&](int32_t c0, float4 (&to)[4]) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int32_t at = __shfl_sync(0xffffffffu, from, 8 * i + (lane >> 2));
+                            to[i] = at >= 0 ? __ldcg(reinterpret_cast<const float4*>(a.part_acc + (int64_t)at * D + c0) + (lane & 3))
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                    };
+                    load(0, next[0]);
+                    load(16, next[1]);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<float4*>(box + (8 * i + (lane >> 2)) * 80 + (lane & 3) * 16) = next[half][i];
+                            __syncwarp();
+                            if (c0 + 32 < D) load(c0 + 32 + 16 * half, next[half]);
+                            float x[16];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 y = *reinterpret_cast<const float4*>(box + lane * 80 + i * 16);
+                                x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
+                            }
+                            __syncwarp();
+                            if (half == 0) {
+                                tmem_ld32(tl + c0, v);
+                                tmem_wait_ld(v);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float own = __uint_as_float(v[16 * half + i]);
+                                v[16 * half + i] = __float_as_uint(later ? fmaf(w1, own, w0 * x[i]) : fmaf(w1, x[i], w0 * own));
+                            }
+                        }
+                        if (c0 == D / 2 && coming) {
+                            q_there();
+                            coming = false;
+                        }
+                        send({out_words(v, inv2), out_words(v + 8, inv2), out_words(v + 16, inv2), out_words(v + 24, inv2)}, c0 * 2);
+                    }
+                    if (lane == 0) atomicExch(met, 0);   // as the next call expects it
+                }
                 tc_fence_before();
                 t = cend;
                 ++u;

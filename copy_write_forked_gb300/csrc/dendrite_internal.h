@@ -150,8 +150,9 @@ struct AttnPlanDev {
     int32_t back, step;            // query j of a branch of len rows sees positions < len - back + (j + 1) step:
                                    // causal q_len, 1; draft trees q_len, 0 (and their masks); cross attention 0, 0
     // Cross attention whose branches each read one segment, all on the tcgen05 (fp32: tiled) kernel: a unit that one
-    // CTA runs whole writes its rows out itself, and only the units split over CTAs are merged.
-    const int32_t* splits;         // [n_splits] units split over CTAs
+    // CTA runs whole writes its rows out itself, and only the units split over CTAs are merged (bf16: over
+    // more than two; the second of two joins them).
+    const int32_t* splits;         // [n_splits] units that are merged
     int32_t direct, n_splits;
     int32_t tiled;                 // fp32 cross attention on the tiled kernel: rows per unit; 0: not on it
     int32_t packed;                // some unit reads extra tiles (the mma.sync kernel then needs its tile info)
@@ -305,6 +306,7 @@ struct dendrite_pool {
     int32_t* d_holders = nullptr;    // [num_blocks] holders of a shared tail within one append
     int32_t* d_last = nullptr;       // [num_blocks] last holder index within one append
     int32_t* d_released = nullptr;   // bitmap of the blocks a free released (word k: ids 32 k ..)
+    int32_t* d_joins = nullptr;      // AttnArgs::joins
     int32_t* d_call_i32 = nullptr;   // [4 * max_branches] per-call scratch (offsets, cow sources)
 
     // layers: layer l's K pool starts at d_k + l * layer_bytes, its V pool at

@@ -1340,6 +1340,8 @@ int pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv_heads, int3
         cudaMalloc(&p->d_released, nb4) != cudaSuccess ||
         cudaMalloc(&p->d_table, (size_t)max_branches * bpb * 4) != cudaSuccess ||
         cudaMalloc(&p->d_call_i32, (size_t)max_branches * 4 * 4) != cudaSuccess ||
+        cudaMalloc(&p->d_joins, (size_t)p->sm_count * 8 * 4) != cudaSuccess ||
+        cudaMemset(p->d_joins, 0, (size_t)p->sm_count * 8 * 4) != cudaSuccess ||
         cudaMalloc(&p->d_meta, sizeof(DevMeta)) != cudaSuccess)
         return fail(cuda_err(cudaErrorMemoryAllocation));
     if ((rc = p->staging.init(4u << 20)) != DENDRITE_OK) return fail(rc);
@@ -1394,7 +1396,7 @@ int dendrite_pool_destroy(dendrite_pool* p) {
     attn_teardown(p);
     p->staging.destroy();
     void* bufs[] = {p->d_k, p->d_v, p->d_refcount, p->d_stack, p->d_holders, p->d_last,
-                    p->d_released, p->d_table, p->d_call_i32, p->d_meta, p->d_tq_signs, p->d_tq_S};
+                    p->d_released, p->d_table, p->d_call_i32, p->d_joins, p->d_meta, p->d_tq_signs, p->d_tq_S};
     for (void* b : bufs)
         if (b) cudaFree(b);
     for (int k = 0; k < T_COUNT; ++k)

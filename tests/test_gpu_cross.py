@@ -322,3 +322,17 @@ def test_what_stands_behind_the_end_touches_nothing_in_fp32():
             ref = R.attention(R.f64(q[i]), K, V, np.ones((q_len, n), bool))
             assert (np.abs(out[i] - ref[0]) <= R.attention_bound("fp32", *ref)).all()
     c.pool.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,q_len", [(13, 64), (25, 65), (19, 10)])
+def test_units_shared_by_two_ctas(kind, n, q_len):
+    """About as many units as CTAs, so that most CTAs end inside a unit that the next one began: their rows are joined,
+    the same way whichever ends first, and every later call finds the counts of their meetings as the first did."""
+    c = Case(kind, [300 - 7 * i for i in range(n)], 8, 4, seed=n)
+    q, out = c.attend(c.br, q_len)
+    for _ in range(20):
+        assert torch.equal(c.pool.tree_attn_cross(q, c.br), out)
+    c.append(c.br, 9)
+    c.attend(c.br, q_len)
+    c.pool.close()
