@@ -122,6 +122,9 @@ __device__ __forceinline__ void load(const T* p, Chunk<T>& x) {
 #pragma unroll
     for (int k = 0; k < (int)(sizeof(T) / 2); ++k) x.w[k] = __ldcg(reinterpret_cast<const uint4*>(p) + k);
 }
+__device__ __forceinline__ void copy_row(uint4* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
 template <typename T>
 __device__ __forceinline__ void store(T* p, const Chunk<T>& x) {
 #pragma unroll
@@ -263,16 +266,21 @@ __device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
 // tree depths as bytes.
 // T: the rows' type; FP8: the blocks hold 8-bit rows (else rows of T); ROPE:
 // keys and queries turn (else every row is stored as it is).
-// Rows go through a thread U at a time, loads first.  Rotating rows of 16 bits:
-// four, at four CTAs an SM (three or six at a time lost 1 to 5 %, two at six CTAs
-// 17 %).  Rows that are only quantised: two, at eight CTAs (32,768 tokens of 8
-// heads appended and read back 94.9 us, against 98.7 with four at five CTAs and
-// 104 with one at twelve).
+// Rows go through a thread U at a time, loads first.  Rotating rows of 16 bits come through shared
+// memory, U of them behind the U that are worked on, one after the other, at four CTAs an SM: 12,432
+// tokens of 36 heads into an 8-bit pool, read back, 66.7 us, 16,396 of 48 in bf16 101 (U = 4; 2, 3, 5, 6:
+// 68.4, 67.5, 69.1, 69.9 and 104.6; 101.2, 104.6, 105.4, 105.7; three CTAs 69.6 / 103.5, five 70.3 /
+// 107.7; four rows at a time in registers, each batch's loads waited for, 75.1 / 104.4).  Rotating fp32 rows: in registers, two at a time (16,396 of 48:
+// 181 us; through shared memory 227).  Rows that are only quantised: two, at eight CTAs (32,768
+// tokens of 8 heads appended and read back 94.9 us, against 98.7 with four at five CTAs and 104 with
+// one at twelve).
 template <typename T, bool FP8, bool ROPE, typename A>
 __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_constant__ A args, const __grid_constant__ RowsArgs a) {
     pdl_wait();
     constexpr int bs = kBlockSize;
-    constexpr int U = ROPE && sizeof(T) == 2 ? 4 : 2;
+    constexpr bool RING = ROPE && sizeof(T) == 2;
+    constexpr int U = RING && FP8 ? 4 : 2, XN = RING ? 1 : U;
+    __shared__ uint4 ring[RING ? 2 * U * 2 * 128 : 1];   // rows on their way: each thread's own words
     const int32_t n = a.n, dim = a.dim;
     const int32_t items = dim >> 4;                     // threads per row
     const int32_t lanes = 128 / items;                  // rows in flight, cut to a power of two
@@ -334,17 +342,37 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
             const int64_t kv_at = in_row * a.n_kv * dim, q_at = in_row * a.nq * dim;
             const int32_t n_iter = (row1 - row0 + rstep - 1) / rstep;
             float cs[8], sn[8];
-            for (int32_t it0 = 0; it0 < n_iter; it0 += U) {
-                Chunk<T> x[U], y[U];
+            Chunk<T> xs[XN], ys[XN];
+            auto source = [&](int32_t rr) {
+                return rr < a.n_kv       ? K + kv_at + rr * dim
+                       : rr < 2 * a.n_kv ? V + kv_at + (rr - a.n_kv) * dim
+                                         : Q + q_at + (rr - 2 * a.n_kv) * dim;
+            };
+            auto ahead = [&](int32_t it0, int b) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int32_t rr = row0 + (it0 + u) * rstep + r0;
                     if (!live || rr >= row1) continue;
-                    const T* src = rr < a.n_kv       ? K + kv_at + rr * dim
-                                   : rr < 2 * a.n_kv ? V + kv_at + (rr - a.n_kv) * dim
-                                                     : Q + q_at + (rr - 2 * a.n_kv) * dim;
-                    load(src + c0, x[u]);
-                    load(src + c1, y[u]);
+                    const T* src = source(rr);
+                    copy_row(&ring[(b * U + u) * 256 + threadIdx.x], src + c0);
+                    copy_row(&ring[(b * U + u) * 256 + 128 + threadIdx.x], src + c1);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            if constexpr (RING) ahead(0, 0);
+            int b = 0;
+            for (int32_t it0 = 0; it0 < n_iter; it0 += U, b ^= 1) {
+                if constexpr (RING) {
+                    ahead(it0 + U, b ^ 1);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int32_t rr = row0 + (it0 + u) * rstep + r0;
+                        if (!live || rr >= row1) continue;
+                        const T* src = source(rr);
+                        load(src + c0, xs[u]);
+                        load(src + c1, ys[u]);
+                    }
                 }
                 if (ROPE && it0 == 0) {   // the angles, while the first rows are on their way
                     const int32_t* at = a.at + i * a.at_branch + tok * a.at_token;
@@ -362,18 +390,24 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                         }
                     }
                 }
-#pragma unroll
+                if constexpr (RING) asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll XN
                 for (int u = 0; u < U; ++u) {
                     const int32_t rr = row0 + (it0 + u) * rstep + r0;
                     const bool act = live && rr < row1;
+                    Chunk<T>&x = xs[RING ? 0 : u], &y = ys[RING ? 0 : u];
+                    if (RING && act) {
+                        x.w[0] = ring[(b * U + u) * 256 + threadIdx.x];
+                        y.w[0] = ring[(b * U + u) * 256 + 128 + threadIdx.x];
+                    }
                     const int32_t kind = rr < a.n_kv ? 0 : rr < 2 * a.n_kv ? 1 : 2;   // K, V, Q
                     const int32_t h = rr - (kind == 0 ? 0 : kind == 1 ? a.n_kv : 2 * a.n_kv);
                     float f[8], g[8];
                     uint32_t top = 0;
                     const bool turns = ROPE && act && kind != 1;
                     if (turns) {
-                        to_float(x[u], f);
-                        to_float(y[u], g);
+                        to_float(x, f);
+                        to_float(y, g);
                         if (a.interleaved) {
                             if (turn0) {
 #pragma unroll
@@ -400,14 +434,14 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                             }
                         }
                         if (!FP8 || kind == 2) {
-                            from_float(f, x[u]);
-                            from_float(g, y[u]);
+                            from_float(f, x);
+                            from_float(g, y);
                         }
                     }
                     if constexpr (FP8) {
                         if (act && kind != 2) {
                             if (turns) top = max(top_bits(f), top_bits(g));
-                            else top = max(top_bits(x[u]), top_bits(y[u]));
+                            else top = max(top_bits(x), top_bits(y));
                         }
                         // the row's largest element: its eight threads are eight neighbouring lanes
 #pragma unroll
@@ -417,12 +451,12 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                     char* tile = (kind == 0 ? kp : vp) + ((int64_t)dst * a.n_kv + (kind == 2 ? 0 : h)) * tile_bytes;
                     if (kind == 2) {
                         T* out = q_out + q_at + h * dim;
-                        store(out + c0, x[u]);
-                        store(out + c1, y[u]);
+                        store(out + c0, x);
+                        store(out + c1, y);
                     } else if constexpr (FP8) {
                         if (!turns) {
-                            to_float(x[u], f);
-                            to_float(y[u], g);
+                            to_float(x, f);
+                            to_float(y, g);
                         }
                         const uint32_t e = fp8_exponent(top);
                         *reinterpret_cast<uint2*>(tile + fp8_at(slot, c0)) = fp8_codes(f, e);
@@ -430,10 +464,10 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                         if (item == 0) tile[bs * kFp8Dim + slot] = (char)e;
                     } else {
                         T* out = reinterpret_cast<T*>(tile) + slot * dim;
-                        store(out + c0, x[u]);
-                        store(out + c1, y[u]);
+                        store(out + c0, x);
+                        store(out + c1, y);
                         if constexpr (sizeof(T) == 2)   // (fp32 attention reads no row that nothing sees)
-                            if (kind == 1 && max(top_bits(x[u]), top_bits(y[u])) >= 0x7f800000u) a.meta->unclean = 1;
+                            if (kind == 1 && max(top_bits(x), top_bits(y)) >= 0x7f800000u) a.meta->unclean = 1;
                     }
                 }
             }
@@ -1002,7 +1036,12 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* stage
     // tokens of 36 heads into an 8-bit pool that take 50 this way).
     const int64_t resident = (c.rope ? 4 : 8) * (int64_t)p->sm_count;
     const int64_t parts = c.touched * ((n_rows + lanes / tp - 1) / (lanes / tp));
-    const dim3 grid((unsigned)std::max<int64_t>(1, std::min(parts, resident / c.n_layers_in)), (unsigned)c.n_layers_in);
+    int64_t ctas = std::max<int64_t>(1, std::min(parts, resident / c.n_layers_in));
+    // (fp32 is bound by HBM, which a last wave of at least half the CTAs fills too: one per tile there, 16,396
+    // tokens of 48 heads, 1.7 waves, 181 us, 190 shared out; 12,432, 1.3 waves, 167 and 152)
+    const int64_t tiles = c.touched * c.n_layers_in;
+    if (p->dtype == DENDRITE_FP32 && tiles > resident && tiles % resident * 2 > resident) ctas = c.touched;
+    const dim3 grid((unsigned)ctas, (unsigned)c.n_layers_in);
     auto go = [&](auto args) -> int {
         using A = decltype(args);
         if (p->dtype == DENDRITE_FP8 && !c.rope)
