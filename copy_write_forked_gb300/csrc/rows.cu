@@ -1033,7 +1033,7 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* stage
     // As many CTAs as run at once, the rows shared out evenly among them, or one for as many rows as it
     // takes at a time where those are fewer (of more, each makes the angles anew: 32 x 16 tokens of 48
     // heads 8 us, and 10 with 8 an SM; one CTA per tile, 1.3 waves of them, took 56 us for 12,432
-    // tokens of 36 heads into an 8-bit pool that take 50 this way).
+    // tokens of 36 heads into an 8-bit pool that took 50 this way).
     const int64_t resident = (c.rope ? 4 : 8) * (int64_t)p->sm_count;
     const int64_t parts = c.touched * ((n_rows + lanes / tp - 1) / (lanes / tp));
     int64_t ctas = std::max<int64_t>(1, std::min(parts, resident / c.n_layers_in));
