@@ -557,17 +557,26 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
         }
         // every CTA's sum, added in the same order in every CTA
         if (warp == 0) {
-            const Pair incl = lanes_scan<4>(lane < cs ? cta_sum[parity][lane] : Pair{0.f, 0.f}, lane);
-            const Pair S = of_lane(incl, 15), before = of_lane(incl, max(rank - 1, 0)), upto = of_lane(incl, rank);
+            const Pair own = lane < cs ? cta_sum[parity][lane] : Pair{0.f, 0.f}, incl = lanes_scan<4>(own, lane);
+            const Pair S = of_lane(incl, 15);
             if (lane == 0) {
                 walk.S = walk.S_pass = S;
                 walk.stale = false;
-                if (fin) {
-                    find.goal = product(S, nodes.sample);
-                    // (of the least numbers a part rounds to the whole, which no token would pass; S.l is zero there)
-                    if (S.h > 0.f && !less(find.goal, S)) find.goal = {__uint_as_float(__float_as_uint(S.h) - 1), 0.f};
+            }
+            if (fin) {
+                Pair goal = product(S, nodes.sample);
+                // (of the least numbers a part rounds to the whole, which no token would pass; S.l is zero there)
+                if (S.h > 0.f && !less(goal, S)) goal = {__uint_as_float(__float_as_uint(S.h) - 1), 0.f};
+                // The CTA: of those with weight the first whose end passes the goal, or the last.  (Ends are rounded, each
+                // in an order of its own, so one may lie behind the next: two CTAs could hold the goal between theirs, or
+                // one without weight.)
+                const uint32_t with = __ballot_sync(0xffffffffu, own.h > 0.f);
+                const uint32_t past = __ballot_sync(0xffffffffu, own.h > 0.f && less(goal, incl));
+                const Pair before = of_lane(incl, max(rank - 1, 0));
+                if (lane == 0) {
+                    find.goal = goal;
                     find.before = rank ? before : Pair{0.f, 0.f};
-                    find.here = !less(find.goal, find.before) && less(find.goal, upto);
+                    find.here = rank == (past ? __ffs(past) - 1 : 31 - __clz(with));
                     find.none = !(S.h > 0.f);
                 }
             }
