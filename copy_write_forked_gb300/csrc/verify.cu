@@ -36,7 +36,9 @@
 //   - 16-byte words, held between passes, 16 CTAs a sequence in two waves: 55 / 79
 //   - as many CTAs a sequence as fit one wave, packed fp32 pairs without fp64: 49 / 40
 //   - certain drafts' sums by subtraction, only warps that lost a token anew: 47 / 36
-//   - short additions below the largest weight: 45 / 31
+//   - short additions of a row's own weights, below the largest of them: 45 / 31
+//   - residuals added by whole two_sums (beside a probability that the draft has too they would lose digits
+//     that a pair of their own holds), the largest weight taken of what is left, two bf16 at a time: 44 / 31
 // Half the threads a CTA and twice the CTAs: 45 / 33, and 28 us in place of 23 where
 // every sequence takes one pass.
 #include <cuda_bf16.h>
@@ -158,12 +160,13 @@ __device__ __forceinline__ Pair2 two_sum2(f32x2 a, f32x2 b) {
     const f32x2 s = add2(a, b), t = sub2(s, a);
     return {s, add2(sub2(a, sub2(s, t)), sub2(b, t))};
 }
-// Adds w, at most sum.h in size: the short form of two_sum.
+// Adds w, of any size.
 __device__ __forceinline__ void accumulate(Pair2& sum, Pair2 w) {
-    const f32x2 s = add2(sum.h, w.h);
-    sum = {s, add2(sum.l, add2(add2(sub2(sum.h, s), w.h), w.l))};
+    const Pair2 s = two_sum2(sum.h, w.h);
+    sum = {s.h, add2(sum.l, add2(s.l, w.l))};
 }
-__device__ __forceinline__ void accumulate(Pair2& sum, f32x2 w) {
+// Adds w, at most sum.h in size: the short form of two_sum.
+__device__ __forceinline__ void accumulate_below(Pair2& sum, f32x2 w) {
     const f32x2 s = add2(sum.h, w);
     sum = {s, add2(sum.l, add2(sub2(sum.h, s), w))};
 }
@@ -240,6 +243,26 @@ __device__ __forceinline__ f32x2 two(const uint4& w, int j) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
     if constexpr (sizeof(T) == 4) return pack(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
     else return pack(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xffff0000u));
+}
+// The largest element of words of probabilities.
+template <typename T, int N>
+__device__ __forceinline__ float largest(const uint4 (&w)[N]) {
+    if constexpr (sizeof(T) == 4) {
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            top = fmaxf(top, fmaxf(fmaxf(__uint_as_float(w[k].x), __uint_as_float(w[k].y)), fmaxf(__uint_as_float(w[k].z), __uint_as_float(w[k].w))));
+        return top;
+    } else {   // (two at a time as they are: unpacked, they would stay in registers for the sum)
+        __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            __nv_bfloat162 x[4];
+            memcpy(x, &w[k], 16);
+            top = __hmax2(top, __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3])));
+        }
+        return fmaxf(__low2float(top), __high2float(top));
+    }
 }
 // Takes element r of a word away, where it has one.
 template <typename T>
@@ -385,7 +408,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
     constexpr int PER = kPer<T>;
     uint4 hp[kHeld];
     uint4* const hq = held_q + t;
-    float top = 0.f;                  // the largest held probability of the target
     int32_t p_row = -1, q_row = -1;   // the rows that are held, where a share fits the registers
 
     // the real nodes that hang on a row (warp 0)
@@ -497,19 +519,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
                 }
 #pragma unroll
                 for (int k = 0; k < kHeld; ++k) hp[k] = clean<T>(hp[k]);
-                top = 0.f;
-#pragma unroll
-                for (int k = 0; k < kHeld; ++k)
-#pragma unroll
-                    for (int j = 0; j < PER / 2; ++j) {
-                        const float2 x = unpack(two<T>(hp[k], j));
-                        top = fmaxf(top, fmaxf(x.x, x.y));
-                    }
             }
             if (new_q) copies_done();
-            // the sum stands above the largest weight meanwhile, so that each addition is the short form
-            const Pair2 up2 = two_sum2(sum2.h, pack(top, top));
-            sum2 = {up2.h, add2(sum2.l, up2.l)};
             auto drafted = [&](auto one) {
 #pragma unroll
                 for (int k = 0; k < kHeld; ++k) {
@@ -523,21 +534,27 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
             if (DRAFT && with_q) {
                 if (pc.h == 1.f && pc.l == 0.f) drafted(std::true_type());
                 else drafted(std::false_type());
+                sum2 = two_sum2(sum2.h, sum2.l);
             } else {
                 for (uint64_t r = here; r; r &= r - 1) {
                     const int32_t at = nodes.token[__ffsll((long long)r) - 1] + skew - e0;
 #pragma unroll
                     for (int k = 0; k < kHeld; ++k) drop<T>(hp[k], at - 32 * PER * k);
                 }
+                // The sum stands above the largest weight meanwhile, so that each addition is the short form.  Not the
+                // largest probability: the sum's last digits are as far below what it stands on as a pair's are.
+                const float top = largest<T>(hp);
+                const Pair2 up2 = two_sum2(sum2.h, pack(top, top));
+                sum2 = {up2.h, add2(sum2.l, up2.l)};
 #pragma unroll
                 for (int k = 0; k < kHeld; ++k) {
                     if (e0 + 32 * PER * k >= hi) continue;
 #pragma unroll
-                    for (int j = 0; j < PER / 2; ++j) accumulate(sum2, two<T>(hp[k], j));
+                    for (int j = 0; j < PER / 2; ++j) accumulate_below(sum2, two<T>(hp[k], j));
                 }
+                const Pair2 down = two_sum2(sum2.h, pack(-top, -top));
+                sum2 = two_sum2(down.h, add2(sum2.l, down.l));
             }
-            const Pair2 down = two_sum2(sum2.h, pack(-top, -top));
-            sum2 = two_sum2(down.h, add2(sum2.l, down.l));
         }
         if (mine) p_row = row;   // (of one node more tokens may go, none come back)
         if (with_q) q_row = row;
@@ -634,8 +651,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
                 const Pair s = two_sum(x.h, w[u].h);
                 x = {s.h, __fadd_rn(x.l, __fadd_rn(s.l, w[u].l))};
             }
+            x = norm(x);
         }
-        x = norm(x);
         const Pair incl = lanes_scan<5>(x, lane);
         // the first lane whose end passes the goal, or the last one with weight
         const uint32_t has = __ballot_sync(0xffffffffu, x.h > 0.f);

@@ -473,9 +473,11 @@ int dendrite_tree_attn_cross(dendrite_pool* pool, int32_t layer, const void* Q, 
  * The next token is the least one whose running sum of w passes sample * sum w;
  * where no weight is left, of p instead; -1 where p has none.  Probabilities that
  * are not positive and finite count as zero.  Rows need not add up to one exactly (-1
- * where the sum is past the largest fp32).  Sums are held in 48 bits: the outcome is
- * that of 64-bit arithmetic but where a number is within some 2^-40 of a border (of sums
- * below 2^-100, whose last bits fp32 does not hold, within 2^-149).
+ * where the sum and its largest term together are past the largest fp32).  Sums are held in
+ * 48 bits: the outcome is that of exact arithmetic but where a number is within some 2^-40
+ * of a border, relative to what is left (the residual's S, however small a part of the row it is;
+ * of sums below 2^-100, whose last bits fp32 does not hold, within 2^-149).  From the second refusal of
+ * drafts with probabilities on, where p and c q of 48 bits nearly cancel: within some 2^-44 c / S of it.
  *   path: device int32 [n][n_draft], the accepted nodes in order, then -1;
  *   n_keep: device int32 [n]; next: device int32 [n].  Written.
  * The outputs may not overlap one another or any input (DENDRITE_EINVAL, as for a
