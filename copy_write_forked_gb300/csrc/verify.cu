@@ -328,7 +328,7 @@ struct Walk {
     Pair c, S, S_pass;           // w = max(p - c q, 0); its sum; the sum that was last taken over the row
     uint64_t refused, left;      // certain drafts: refused nodes; children to try
     uint64_t first;              // nodes that are accepted if they are tried first
-    int32_t cur, kept;
+    int32_t cur, kept, lost;     // lost: tokens that S went without since S_pass
     bool fresh, stale, last;     // none refused yet; S is not the sum of w; nothing is left to try
 };
 
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
     if (warp == 0) {
         const uint64_t left = kids(0);
         if (lane == 0)
-            walk = Walk{{0.f, 0.f}, {1.f, 0.f}, {0.f, 0.f}, 0, left, (uint64_t)nodes.first[1] << 32 | nodes.first[0], 0, 0, true, false, false};
+            walk = Walk{{0.f, 0.f}, {1.f, 0.f}, {0.f, 0.f}, 0, left, (uint64_t)nodes.first[1] << 32 | nodes.first[0], 0, 0, 0, true, false, false};
         __syncwarp();
     }
     bool fell_back = false;
@@ -457,9 +457,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
                     z.fresh = false;
                     z.stale = true;
                 } else {
-                    // the sum without one more token: a new one only where the subtraction would lose digits
+                    // the sum without one more token: a new one only where subtractions would lose digits (each is off
+                    // by 2^-49 of the last sum at most, so S by 2^-41 of itself)
                     z.S = norm(add(z.S, Pair{-w.h, 0.f}));
-                    z.stale = z.fresh || z.S.h < z.S_pass.h * 0x1p-10f;
+                    ++z.lost;
+                    z.stale = z.fresh || z.S.h < z.S_pass.h * (0x1p-8f * (float)z.lost);
                     z.refused |= 1ull << j;
                     z.fresh = false;
                 }
@@ -579,6 +581,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
             if (lane == 0) {
                 walk.S = walk.S_pass = S;
                 walk.stale = false;
+                walk.lost = 0;
             }
             if (fin) {
                 Pair goal = product(S, nodes.sample);

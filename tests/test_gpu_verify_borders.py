@@ -234,3 +234,29 @@ def test_drafts_near_the_target(pool, kind, near, n, vocab):
     for i in range(0, n, 5 if n > 100 else 1):
         want, nxt = verified(target[i].tolist(), draft[i].tolist(), tokens[i].tolist(), [-1] * t, accept[i].tolist(), sample[i].item())
         assert (path[i].tolist()[:size[i]], token[i].item()) == (want, nxt), i
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [200, 6])
+def test_many_refusals_of_certain_drafts(pool, kind, n):
+    """Sixty-three refused tokens, most of them of digits that a sum of one does not hold, leave some 2^-8.5 of the row;
+    the last child's number is 2^-38 of that beside its border."""
+    rng = random.Random(5)
+    p, expect = np.zeros((n, VOCAB)), []
+    tokens = torch.zeros(n, 64, dtype=torch.int32)
+    digits = lambda x: float(torch.tensor(x).to(TYPES[kind]))   # noqa: E731
+    for i in range(n):
+        side = 1 if rng.random() < 0.5 else -1
+        w = Fraction(rng.randrange(2 ** (BITS[kind] - 1), 2 ** BITS[kind])) * Fraction(2) ** (-BITS[kind] - 9)
+        d = Fraction(2) ** -38 * Fraction(2) ** math.frexp(float(2 * w))[1]
+        rest = _pieces(w - 2 * side * d, BITS[kind])      # all that is left: 2 (w - side d)
+        at = rng.sample(range(VOCAB), 64 + len(rest))
+        lost = [2.0 ** (-26 if kind == "fp32" else -43) * rng.uniform(1, 4) for _ in range(56)] + [rng.uniform(0.05, 0.25) for _ in range(7)]
+        p[i, at[:63]] = [digits(x) for x in lost]
+        p[i, at[63]] = w
+        p[i, at[64:]] = rest
+        tokens[i] = torch.tensor(at[:64])
+        expect.append(([63], -1) if side > 0 else ([], min(at[64:])))
+    accept = torch.full((n, 64), 1 - 2.0 ** -24)
+    accept[:, 63] = 0.5
+    _run(pool, kind, tokens, p, None, accept, torch.zeros(n), expect)
