@@ -105,6 +105,7 @@ struct RowsArgs {
     int64_t kv_layer, q_layer;   // elements
     int64_t pool_layer;          // bytes
     DevMeta* meta;
+    int32_t share_tiles, share_rows, share_more;   // rows of a CTA (k_append_rows)
     const int32_t* at;           // given positions, or null
     int64_t at_branch, at_token, at_axis;
     uint64_t freq[128];          // turns per position, as a fraction of 2^64
@@ -265,7 +266,7 @@ __device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
 // args: branch[n], length[n], prefix of touched blocks[n], then the draft
 // tree depths as bytes.
 // T: the rows' type; FP8: the blocks hold 8-bit rows (else rows of T); ROPE:
-// keys and queries turn (else every row is stored as it is).
+// keys and queries turn (else every row is stored as it is); AT: by given positions.
 // Rows go through a thread U at a time, loads first.  Rotating rows of 16 bits come through shared
 // memory, U of them behind the U that are worked on, one after the other, at four CTAs an SM: 12,432
 // tokens of 36 heads into an 8-bit pool, read back, 66.7 us, 16,396 of 48 in bf16 101 (U = 4; 2, 3, 5, 6:
@@ -274,7 +275,7 @@ __device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
 // 181 us; through shared memory 227).  Rows that are only quantised: two, at eight CTAs (32,768
 // tokens of 8 heads appended and read back 94.9 us, against 98.7 with four at five CTAs and 104 with
 // one at twelve).
-template <typename T, bool FP8, bool ROPE, typename A>
+template <typename T, bool FP8, bool ROPE, bool AT, typename A>
 __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_constant__ A args, const __grid_constant__ RowsArgs a) {
     pdl_wait();
     constexpr int bs = kBlockSize;
@@ -309,14 +310,23 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
     char* vp = a.vp + blockIdx.y * a.pool_layer;
     const int64_t tile_bytes = FP8 ? kFp8TileBytes : (int64_t)bs * dim * (int)sizeof(T);
     if (__any_sync(0xffffffffu, status)) return;   // a whole warp leaves: shuffles below
-    // this CTA's share of all tiles' rows (tile after tile, each its K, V and Q heads)
-    const int64_t all = (int64_t)a.n_tiles * n_rows;
-    int64_t at_row = all * blockIdx.x / gridDim.x;
-    const int64_t end_row = all * (blockIdx.x + 1) / gridDim.x;
-    for (int32_t t = (int32_t)(at_row / n_rows); at_row < end_row; ++t) {
-        const int32_t row0 = (int32_t)(at_row - (int64_t)t * n_rows);
-        const int32_t row1 = (int32_t)min((int64_t)n_rows, row0 + (end_row - at_row));
-        at_row += row1 - row0;
+    // This CTA's share of all tiles' rows (tile after tile, each its K, V and Q heads): CTA x of C begins at row x all / C,
+    // all / C being share_tiles tiles, share_rows rows and share_more C-ths of a row.
+    const uint32_t x = blockIdx.x;
+    uint32_t off = x * (uint32_t)a.share_rows, more = 0;
+    if (a.share_more) {
+        const uint32_t before = x * (uint32_t)a.share_more / gridDim.x;
+        more = (x + 1) * (uint32_t)a.share_more / gridDim.x - before;
+        off += before;
+    }
+    int32_t t = (int32_t)(x * (uint32_t)a.share_tiles), row0 = 0, row1;
+    if (off) {
+        t += (int32_t)(off / (uint32_t)n_rows);
+        row0 = (int32_t)(off % (uint32_t)n_rows);
+    }
+    int64_t left = (int64_t)a.share_tiles * n_rows + a.share_rows + more;
+    for (; left > 0; left -= row1 - row0, row0 = 0, ++t) {
+        row1 = (int32_t)min((int64_t)n_rows, row0 + left);
         int32_t first;
         const int32_t i = find_branch(args, 2 * (int64_t)n, n, t, a.uniform, first);
         const int32_t L = args[n + i];
@@ -375,7 +385,7 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                     }
                 }
                 if (ROPE && it0 == 0) {   // the angles, while the first rows are on their way
-                    const int32_t* at = a.at + i * a.at_branch + tok * a.at_token;
+                    const int32_t* at = AT ? a.at + i * a.at_branch + tok * a.at_token : nullptr;
                     const int32_t pos = L + (a.has_depth ? byte_of(args, 3 * (int64_t)n, (int64_t)(a.one_tree ? 0 : i) * a.n_new + tok) : tok);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
@@ -385,8 +395,10 @@ __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_
                         sn[q] = 0.f;
                         if (on) {
                             // (a negative position's product wraps to the negative angle)
-                            const int64_t x = a.at ? (int64_t)__ldg(at + a.axis[pair & 127] * a.at_axis) : (int64_t)pos;
-                            sincos_turns(a.freq[pair & 127] * (uint64_t)x, a.m, sn[q], cs[q]);
+                            if constexpr (AT)
+                                sincos_turns(a.freq[pair & 127] * (uint64_t)(int64_t)__ldg(at + a.axis[pair & 127] * a.at_axis), a.m, sn[q], cs[q]);
+                            else
+                                sincos_turns(a.freq[pair & 127] * (uint64_t)(uint32_t)pos, a.m, sn[q], cs[q]);
                         }
                     }
                 }
@@ -1032,26 +1044,45 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* stage
     while (tp < lanes && tp < std::min(n_new, bs)) tp *= 2;
     // As many CTAs as run at once, the rows shared out evenly among them, or one for as many rows as it
     // takes at a time where those are fewer (of more, each makes the angles anew: 32 x 16 tokens of 48
-    // heads 8 us, and 10 with 8 an SM; one CTA per tile, 1.3 waves of them, took 56 us for 12,432
-    // tokens of 36 heads into an 8-bit pool that took 50 this way).
+    // heads 8 us, and 10 with 8 an SM); in whole parts of a tile where that leaves at most a fifth of the CTAs out
+    // (a CTA whose share crosses a tile's end starts twice: 4 branches x 16 tokens of 16 heads in 32 layers 18 -> 15 us).
+    // Where the tiles alone are more than run at once, one CTA per tile if the waves of them are full
+    // enough: to 70 % and more, in bf16 85.  One per tile against shared out, bf16, 8-bit and fp32 pools, us: 1.1 waves
+    // (10,500 tokens of 48 heads) 67 / 57, 67 / 55, 118 / 107; 1.3 waves 71 / 65, 71 / 64, 126 / 126; 2.01 waves 101 / 95,
+    // 100 / 91, 180 / 184; 1.55 waves 76 / 74, 75 / 73, 133 / 147; 1.7 waves (16,396 tokens turned by three axes)
+    // 103 / 101 in bf16, of 48 heads alone 79 / 79, 76 / 78, 139 / 158; 1.86 waves 83 / 88, 80 / 84, 151 / 173; 2.6 waves
+    // 115 / 122, 110 / 117, 208 / 236; 4.4 waves 175 / 189, 166 / 184, 330 / 370.  Tiles of little work, whose
+    // start counts, one per tile or part of one whatever the waves: one token of 32 branches in 32 layers (1.7
+    // waves) 16 / 20, 17 / 22, 20 / 21.
     const int64_t resident = (c.rope ? 4 : 8) * (int64_t)p->sm_count;
-    const int64_t parts = c.touched * ((n_rows + lanes / tp - 1) / (lanes / tp));
-    int64_t ctas = std::max<int64_t>(1, std::min(parts, resident / c.n_layers_in));
-    // (fp32 is bound by HBM, which a last wave of at least half the CTAs fills too: one per tile there, 16,396
-    // tokens of 48 heads, 1.7 waves, 181 us, 190 shared out; 12,432, 1.3 waves, 167 and 152)
-    const int64_t tiles = c.touched * c.n_layers_in;
-    if (p->dtype == DENDRITE_FP32 && tiles > resident && tiles % resident * 2 > resident) ctas = c.touched;
+    const int64_t turns = (n_rows + lanes / tp - 1) / (lanes / tp);   // of a full tile
+    const int64_t tiles = c.touched * c.n_layers_in, waves = (tiles + resident - 1) / resident;
+    int64_t ctas = std::max<int64_t>(1, std::min(c.touched * turns, resident / c.n_layers_in));
+    const int64_t parts = ctas / c.touched * c.touched, full = p->dtype == DENDRITE_BF16 ? 85 : 70;
+    if (turns < 8) ctas = c.touched * head_splits(p, tiles, turns, c.rope ? 4 : 8);
+    else if (tiles > resident) ctas = tiles * 100 < waves * resident * full ? ctas : c.touched;
+    else if (parts * 5 >= ctas * 4) ctas = parts;
+    if (ctas > 0xffff || ctas * n_rows > INT32_MAX) ctas = c.touched;   // (a CTA's first row is found in 32 bits)
+    const int64_t share = c.touched * n_rows / ctas;
+    a.share_tiles = (int32_t)(share / n_rows);
+    a.share_rows = (int32_t)(share % n_rows);
+    a.share_more = (int32_t)(c.touched * n_rows % ctas);
     const dim3 grid((unsigned)ctas, (unsigned)c.n_layers_in);
     auto go = [&](auto args) -> int {
         using A = decltype(args);
-        if (p->dtype == DENDRITE_FP8 && !c.rope)
-            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, false, A>, grid, dim3(128), 0, s, args, a));
-        else if (p->dtype == DENDRITE_FP8)
-            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, true, A>, grid, dim3(128), 0, s, args, a));
-        else if (p->dtype == DENDRITE_BF16)
-            DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, false, true, A>, grid, dim3(128), 0, s, args, a));
-        else
-            DENDRITE_CUDA(launch_pdl(k_append_rows<float, false, true, A>, grid, dim3(128), 0, s, args, a));
+        auto rope = [&](auto at) -> int {
+            constexpr bool AT = decltype(at)::value;
+            if (p->dtype == DENDRITE_FP8)
+                DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, true, AT, A>, grid, dim3(128), 0, s, args, a));
+            else if (p->dtype == DENDRITE_BF16)
+                DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, false, true, AT, A>, grid, dim3(128), 0, s, args, a));
+            else
+                DENDRITE_CUDA(launch_pdl(k_append_rows<float, false, true, AT, A>, grid, dim3(128), 0, s, args, a));
+            return DENDRITE_OK;
+        };
+        if (c.at) return rope(std::true_type());
+        if (c.rope) return rope(std::false_type());
+        DENDRITE_CUDA(launch_pdl(k_append_rows<__nv_bfloat16, true, false, false, A>, grid, dim3(128), 0, s, args, a));
         return DENDRITE_OK;
     };
     if (staged) return go(GlobalWords{staged});
