@@ -171,8 +171,10 @@ __device__ __forceinline__ void accumulate_below(Pair2& sum, f32x2 w) {
     sum = {s, add2(sum.l, add2(sub2(sum.h, s), w))};
 }
 
-// max(p - c q, 0) to 48 bits: the product's error and the difference's are carried (the latter by the
-// short form for |p| >= |c q|: where that does not hold the result is zero).  ONE: c is 1.
+// max(p - c q, 0), p and c q to 48 bits: the product's error and the difference's are carried (the latter by the
+// short form for |p| >= |c q|: where that does not hold the result is zero, or the difference is exact).  What is
+// left may be below the last digit of either, so the sign is that of both parts' sum; the high part may be the
+// smaller one, or negative.  ONE: c is 1, and the result exact and normal.
 struct Factor {
     f32x2 h, l, minus;   // c, twice each; -c.h
     __device__ __forceinline__ explicit Factor(Pair c) : h(pack(c.h, c.h)), l(pack(c.l, c.l)), minus(pack(-c.h, -c.h)) {}
@@ -186,8 +188,8 @@ __device__ __forceinline__ Pair2 residual(f32x2 p, f32x2 q, const Factor& c) {
     } else {
         const f32x2 nph = mul2(c.minus, q), s = add2(p, nph);
         const f32x2 e = sub2(add2(sub2(p, s), nph), fma2(c.l, q, fma2(c.h, q, nph)));
-        const float2 h = unpack(s), l = unpack(e);
-        return {pack(fmaxf(h.x, 0.f), fmaxf(h.y, 0.f)), pack(h.x > 0.f ? l.x : 0.f, h.y > 0.f ? l.y : 0.f)};
+        const float2 h = unpack(s), l = unpack(e), x = unpack(add2(s, e));
+        return {pack(x.x > 0.f ? h.x : 0.f, x.y > 0.f ? h.y : 0.f), pack(x.x > 0.f ? l.x : 0.f, x.y > 0.f ? l.y : 0.f)};
     }
 }
 __device__ __forceinline__ Pair residual(float p, float q, Pair c) {
@@ -642,8 +644,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
                 Pair2 x = {pack(p[u], p[u + 1]), 0};
                 if (with_q) x = residual<false>(x.h, pack(q[u], q[u + 1]), fc);
                 const float2 h = unpack(x.h), l = unpack(x.l);
-                w[u] = {h.x, l.x};
-                w[u + 1] = {h.y, l.y};
+                w[u] = norm({h.x, l.x});
+                w[u + 1] = norm({h.y, l.y});
             }
         };
         Pair x = {0.f, 0.f}, w[U];

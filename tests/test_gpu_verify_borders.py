@@ -260,3 +260,64 @@ def test_many_refusals_of_certain_drafts(pool, kind, n):
     accept = torch.full((n, 64), 1 - 2.0 ** -24)
     accept[:, 63] = 0.5
     _run(pool, kind, tokens, p, None, accept, torch.zeros(n), expect)
+
+
+def _outcome(p, q, tokens, accept, sample):
+    """A star's outcome in rational arithmetic, and whether every number is farther from its border than the sums are
+    documented to be off: 2^-40 of what is left, 2^-44 c / S from the second refusal on."""
+    exact = lambda row: [Fraction(x) for x in row]   # noqa: E731
+    p, q = exact(p), exact(q)
+    w, S, c, clear = p, Fraction(1), Fraction(0), True
+    off = lambda: max(Fraction(1, 2 ** 40), Fraction(1, 2 ** 44) * c / S if c > 1 else Fraction(0))   # noqa: E731
+    for j, x in enumerate(tokens):
+        asked = Fraction(accept[j]) * q[x] * S
+        if w[x] > 0 or c > 1:
+            clear &= abs(asked - w[x]) > off() * max(asked, w[x])
+        if w[x] > 0 and asked < w[x]:
+            return ([j], None), clear
+        c += S
+        w = [max(a - c * b, Fraction(0)) for a, b in zip(p, q)]
+        S = sum(w)
+        if S == 0 or off() > Fraction(1, 8):
+            return (None, None), False
+    goal, run, at = Fraction(sample) * S, Fraction(0), None
+    for k, x in enumerate(w):
+        run += x
+        clear &= abs(run - goal) > off() * S
+        if at is None and run > goal:
+            at = k
+    return ([], at), clear
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [2, 3, 17, 300])
+@pytest.mark.parametrize("near", [1.0, 2.0 ** -4, 2.0 ** -10, 2.0 ** -17])
+def test_residuals_below_the_last_digit_of_their_row(pool, kind, vocab, near):
+    """Refusal after refusal a residual shrinks under the last digit of p and c q, which fp32 differences do not hold."""
+    g = torch.Generator().manual_seed(vocab)
+    n, t = 200, 6
+    logits = 2 * torch.randn(n, vocab, generator=g)
+    p = torch.softmax(logits, -1).to(TYPES[kind])
+    q = torch.softmax(logits + near * torch.randn(n, vocab, generator=g), -1).to(TYPES[kind])
+    target, draft = torch.zeros(n, 1 + t, vocab, dtype=p.dtype), torch.zeros(n, t, vocab, dtype=p.dtype)
+    target[:, 0], draft[:, 0] = p, q
+    ratio = q.float() / p.float().clamp(min=1e-30)
+    tokens = ratio.argmax(-1, keepdim=True).expand(n, t).clone()            # refused
+    accept = torch.full((n, t), 1 - 2.0 ** -24)
+    for i in range(n):
+        if i % (t + 1):   # behind one refusal or more the token that is left longest
+            tokens[i, i % (t + 1):] = ratio[i].argmin()
+            accept[i, i % (t + 1):] = torch.rand(t - i % (t + 1), generator=g)
+    tokens = tokens.int()
+    sample = torch.rand(n, generator=g)
+    path, size, token = pool.verify_draft(tokens.cuda(), target.cuda(), [-1] * t, accept.cuda(), sample.cuda(), draft=draft.cuda())
+    pool.sync()
+    checked = 0
+    for i in range(n):
+        (want, nxt), clear = _outcome(p[i].tolist(), q[i].tolist(), tokens[i].tolist(), accept[i].tolist(), sample[i].item())
+        if not clear:
+            continue
+        checked += 1
+        assert path[i].tolist()[:size[i]] == want, i
+        assert nxt is None or token[i].item() == nxt, i
+    assert checked > 20
