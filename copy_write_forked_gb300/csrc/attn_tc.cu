@@ -683,7 +683,8 @@ __device__ __noinline__ bool rescale_rows(bool need, float d, uint32_t tl, uint3
 // Nothing there waits for HBM (256 rows a unit, several units a KV head through L2), so the roles' chains
 // and instructions are what a stage takes, 1,700 cycles of which the products need 1,280 (S with N = 64
 // reads its operands from shared memory for longer than it multiplies).  4 prompts of 515 tokens, 32
-// heads, over 6,404 states (215 GFLOP): 178 us, 1.2 PFLOP/s, tensor pipe 57 %; 16 prompts of 448, 16
+// heads, over 6,404 states (215 GFLOP): 178 us, 1.2 PFLOP/s, tensor pipe 57 % (whole calls 180 to 188 us on
+// different GPUs of this kind); 16 prompts of 448, 16
 // heads, over 1,500 (86 GFLOP, a unit starts every 24 stages): 102 us.  On the way there, as whole calls:
 //   - partial rows for every unit and the general merge: 248 / 229 us
 //   - rows of whole units written here, split units merged by unit: 238 / 138

@@ -268,13 +268,14 @@ __device__ __forceinline__ int32_t fp8_at(int32_t s, int32_t d) {
 // T: the rows' type; FP8: the blocks hold 8-bit rows (else rows of T); ROPE:
 // keys and queries turn (else every row is stored as it is); AT: by given positions.
 // Rows go through a thread U at a time, loads first.  Rotating rows of 16 bits come through shared
-// memory, U of them behind the U that are worked on, one after the other, at four CTAs an SM: 12,432
-// tokens of 36 heads into an 8-bit pool, read back, 66.7 us, 16,396 of 48 in bf16 101 (U = 4; 2, 3, 5, 6:
-// 68.4, 67.5, 69.1, 69.9 and 104.6; 101.2, 104.6, 105.4, 105.7; three CTAs 69.6 / 103.5, five 70.3 /
-// 107.7; four rows at a time in registers, each batch's loads waited for, 75.1 / 104.4).  Rotating fp32 rows: in registers, two at a time (16,396 of 48:
-// 181 us; through shared memory 227).  Rows that are only quantised: two, at eight CTAs (32,768
-// tokens of 8 heads appended and read back 94.9 us, against 98.7 with four at five CTAs and 104 with
-// one at twelve).
+// memory, U of them behind the U that are worked on, one after the other, at four CTAs an SM:
+//   into 8-bit blocks U = 4: 12,432 tokens of 36 heads, read back, 66.7 us (U = 2: 68.4, 3: 67.5, 5: 69.1, 6: 69.9;
+//     three CTAs an SM 69.6, five 70.3; four rows at a time in registers, each batch's loads waited for, 75.1);
+//   into bf16 blocks U = 2: 16,396 tokens of 48 heads, read back, 101.2 us (U = 3, 4, 5, 6: 104.6 to 105.7; three
+//     CTAs an SM 103.5, five 107.7; in registers 104.4).
+// Rotating fp32 rows: in registers, two at a time (16,396 of 48: 181 us; through shared memory 227).  Rows that are
+// only quantised: two, at eight CTAs (32,768 tokens of 8 heads appended and read back 94.9 us, against 98.7
+// with four at five CTAs and 104 with one at twelve).
 template <typename T, bool FP8, bool ROPE, bool AT, typename A>
 __global__ void __launch_bounds__(128, ROPE ? 4 : 8) k_append_rows(const __grid_constant__ A args, const __grid_constant__ RowsArgs a) {
     pdl_wait();

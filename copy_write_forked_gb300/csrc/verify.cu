@@ -29,8 +29,8 @@
 // refusal at a node.  A pass that finds its rows held takes some 8,000 cycles where
 // all SMs work on two CTAs (4,000 sums, 2,000 exchange between the CTAs, 2,000
 // walk), 2 us alone.  32 trees of 24 nodes, 128,256 tokens in fp32, six passes in
-// the longest: 45 us (33 MB that have to be read: 5 us); 256 sequences of 7 certain
-// drafts, 50,257 tokens in bf16: 31 us (26 MB); one of 5 in a row, 32,000 tokens: 14 us
+// the longest: 44 us (33 MB that have to be read: 5 us); 256 sequences of 7 certain
+// drafts, 50,257 tokens in bf16: 30 us (26 MB); one of 5 in a row, 32,000 tokens: 14 us
 // (16 CTAs).  On the way there, in these cases:
 //   - rows read anew in every pass, an element a load, sums joined in fp64: 97 / 93 us
 //   - 16-byte words, held between passes, 16 CTAs a sequence in two waves: 55 / 79
@@ -38,9 +38,11 @@
 //   - certain drafts' sums by subtraction, only warps that lost a token anew: 47 / 36
 //   - short additions of a row's own weights, below the largest of them: 45 / 31
 //   - residuals added by whole two_sums (beside a probability that the draft has too they would lose digits
-//     that a pair of their own holds), the largest weight taken of what is left, two bf16 at a time: 44 / 31
+//     that a pair of their own holds), the largest weight taken of what is left, two bf16 at a time: 44 / 30
 // Half the threads a CTA and twice the CTAs: 45 / 33, and 28 us in place of 23 where
 // every sequence takes one pass.
+// Draft rows that lie otherwise in their 16 bytes than the target's (vocabularies of odd sizes) are loaded
+// element by element: 32 sequences of 7 drafts, 50,257 tokens, fp32 33.7 us (50,256: 32.4), bf16 32.8 (31.3).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) k_verify_draft(const __grid
     }
 }
 
-// CTAs per sequence: as many as are resident at once (two an SM), at least 2,048 tokens each.
+// CTAs per sequence: as many as are resident at once (two an SM), more than 1,024 tokens each.
 int verify_cluster(const dendrite_pool* p, int32_t n, int32_t vocab) {
     int cs = 1;
     while (cs < kVerifyCluster && (int64_t)n * cs <= p->sm_count && vocab > 2048 * cs) cs *= 2;

@@ -440,7 +440,8 @@ int dendrite_tree_attn_draft(dendrite_pool* pool, int32_t layer, const void* Q, 
  * branch, which holds another sequence (an encoder's states, say) of any length,
  * shorter than q_len too; rows are masked by nothing but that length.  Several
  * queries' sequences read one branch through forks of it, which share its blocks.
- * A branch of no rows gives zeros.
+ * A branch of no rows gives zeros.  A pool keeps one plan: where these calls take turns with
+ * decode calls, states in a pool of their own leave both plans as they are.
  *   Q, out: device, [n_branches][q_len][n_q_heads][head_dim].
  * Layers, types, sharing, the cached plan and errors as
  * dendrite_tree_attn_decode_layer; DENDRITE_EINVAL on a stream that is being captured.
