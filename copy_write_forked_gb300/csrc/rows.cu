@@ -92,7 +92,7 @@ __device__ __forceinline__ int32_t find_branch(const A& args, int64_t off, int32
 }
 
 struct RowsArgs {
-    int32_t n, n_new, bpb, n_kv, nq, dim, rot, interleaved, n_blocks, uniform, n_tiles, has_depth, one_tree;
+    int32_t n, n_new, bpb, n_kv, nq, dim, rot, interleaved, n_blocks, uniform, has_depth, one_tree;
     float m;
     const int32_t* table;
     const int32_t* call;    // the metadata kernel's scratch: copy-on-write sources at [n, 2 n)
@@ -998,7 +998,6 @@ int launch_append_rows(dendrite_pool* p, const RowsCall& c, const int32_t* stage
     a.nq = c.Q ? c.n_q_heads : 0;
     a.dim = p->head_dim;
     a.n_blocks = (int32_t)p->num_blocks;
-    a.n_tiles = (int32_t)c.touched;
     a.table = p->d_table;
     a.call = p->d_call_i32;
     a.K = c.K;
